@@ -374,6 +374,103 @@ mk_status mk_launch_step(mk_ctx* c, const int32_t* tokens, const int32_t* pos, f
  * 5 tagged-data poll (counter, seen, wanted: -1, tag seen, tag wanted). */
 mk_status mk_ctx_status(mk_ctx* c, int32_t* info);
 
+/* ------------------------------------------------------------------------------------------------
+ * Prompt operators: the building blocks of mk_prefill, also callable by themselves on the current
+ * CUDA device.  They are asynchronous on `stream` (a cudaStream_t, NULL = legacy default stream),
+ * allocate nothing and synchronise nothing, so they can be captured into a CUDA graph; what they
+ * take from host memory (argument structs, lengths) is read before the call returns.  `status`
+ * (where an argument struct has it) is an optional DEVICE int32 that receives an mk_status when the
+ * device meets an error (it is left alone otherwise; the caller zeroes it first). */
+typedef enum { MK_BF16 = 0, MK_F32 = 1 } mk_dtype;
+typedef enum {
+    MK_ACT_NONE = 0,
+    MK_ACT_SILU = 1,     /* y / (1 + exp(-y))                                                 */
+    MK_ACT_GELU = 2,     /* y (1 + erf(y / sqrt 2)) / 2                                       */
+    MK_ACT_SWIGLU = 3    /* silu(gate) * up: w has 2 n rows, the n gate rows then the n up rows */
+} mk_activation;
+
+/* out[r][j] = act(sum_i x[r][i] w[j][i] + bias[j]) + residual[r][j]
+ *  rows, n, k     tokens, output features, input features; rows may be 0 (nothing is done); k a
+ *                 multiple of 8; n any
+ *  x              bf16, row r at x + r * x_stride elements (x_stride a multiple of 8, >= k)
+ *  w              bf16 row-major [n, k] ([2 n, k] for MK_ACT_SWIGLU)
+ *  bias           bf16 [n] ([2 n] for MK_ACT_SWIGLU), or NULL
+ *  residual       of residual_dtype, row r at residual + r * residual_stride elements (0: one row
+ *                 for every token), or NULL
+ *  out            of out_dtype, row r at out + r * out_stride elements (out_stride >= n).  It may
+ *                 be the residual itself (the same pointer, stride and type) but overlap neither
+ *                 x, w, bias nor any other part of the residual
+ * x and w are 16-byte aligned, the others aligned to their element.  Sums, bias, activation and
+ * residual are taken in fp32 and rounded once.  Errors: MK_ERR_ARG, MK_ERR_CUDA;
+ * status: MK_ERR_TIMEOUT (a wait inside the kernel ran out; out is then not valid). */
+typedef struct {
+    int32_t rows, n, k, activation;
+    const void* x;
+    int64_t x_stride;
+    const void* w;
+    const void* bias;
+    const void* residual;
+    int64_t residual_stride;
+    int32_t residual_dtype, out_dtype;
+    void* out;
+    int64_t out_stride;
+    int32_t* status;
+} mk_linear_args;
+mk_status mk_linear(const mk_linear_args* a, void* stream);
+
+/* Attention of query tokens over a KV cache of mk_kv / mk_kv_pages (the caches mk_bind and
+ * mk_bind_paged take), one layer of it.  Sequence b has q_lens[b] query tokens, the last ones of
+ * its kv_lens[b] positions: its i-th token stands at t = kv_lens[b] - q_lens[b] + i and sees the
+ * cached positions p <= t (its own K/V row is in the cache before the call) that its window leaves:
+ * every one with window 0, else those with p > t - window or p < sinks.  Query head h reads KV head
+ * h / (n_q_heads / n_kv_heads).
+ *   out[token][h] = sum_p softmax_p(scale q[token][h] . K[p]) V[p]
+ * A token without a visible position (t < 0: more query tokens than positions) gets zeros.
+ *  q, out         bf16; sequences back to back, token r's heads at q + r * q_stride elements
+ *                 ([n_q_heads, head_dim], q_stride a multiple of 8, 16-byte aligned); out
+ *                 likewise.  out does not overlap q or the cache.  Tokens past the last sequence
+ *                 are not touched.
+ *  q_lens,        HOST int32[batch], each >= 0; kv_lens[b] <= max_seq
+ *  kv_lens
+ *  kv, layer      the cache and the layer to read; positions a token does not see are never used,
+ *                 whatever they hold, apart from this: a position that one token of a block of 128 / (n_q_heads
+ *                 / n_kv_heads) neighbouring tokens sees must hold finite values
+ *  max_seq        positions per (sequence, head) of a contiguous cache, or the most positions a
+ *                 sequence of a paged cache may have (max_blocks * block_size >= max_seq)
+ *  pages          NULL: contiguous.  Else mk_kv_pages with block_size a multiple of 8; a table
+ *                 entry outside [0, n_blocks) is not followed: its positions count as not visible
+ *                 and status receives MK_ERR_BOUNDS
+ *  shared_prefix  the first shared_prefix positions are the same for every sequence and are read
+ *                 once, for all of them together, through sequence 0's rows (or its table row).
+ *                 Needs window 0 and kv_lens[b] - q_lens[b] >= shared_prefix wherever
+ *                 q_lens[b] > 0.  0: none
+ *  scale          finite, positive; 0: 1 / sqrt(head_dim)
+ * head_dim 32, 64 or 128; n_q_heads / n_kv_heads at most 8; batch at most MK_ATTEND_MAX_BATCH.
+ * Scores, softmax and sums are in fp32; the softmax weights are rounded to bf16 for their product
+ * with V.  workspace: mk_attend_workspace(a) bytes of device memory, 256-byte aligned (NULL if 0);
+ * calls that may overlap need workspaces of their own.  Errors: MK_ERR_ARG, MK_ERR_CAPACITY (the
+ * workspace is too small), MK_ERR_CUDA; status: MK_ERR_BOUNDS, MK_ERR_TIMEOUT. */
+#define MK_ATTEND_MAX_BATCH 256
+typedef struct {
+    int32_t n_q_heads, n_kv_heads, head_dim, batch;
+    const int32_t* q_lens;
+    const int32_t* kv_lens;
+    const void* q;
+    int64_t q_stride;
+    void* out;
+    int64_t out_stride;
+    const mk_kv* kv;
+    const mk_kv_pages* pages;
+    int32_t layer, max_seq;
+    int32_t window, sinks, shared_prefix;
+    float scale;
+    int32_t* status;
+} mk_attend_args;
+/* Workspace bytes of mk_attend for these arguments (0 where they are not valid; pointers are not
+ * read but for the lengths). */
+size_t mk_attend_workspace(const mk_attend_args* a);
+mk_status mk_attend(const mk_attend_args* a, void* workspace, size_t workspace_bytes, void* stream);
+
 /* Number of SMs of the current CUDA device (the natural sm_count), or MK_ERR_CUDA. */
 mk_status mk_device_sm_count(int32_t* out);
 

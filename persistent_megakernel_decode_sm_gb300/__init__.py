@@ -10,6 +10,9 @@ High level:
     dec = Decoder(sched, weights, kv)             # allocates counters/scratch with torch, mk_bind
     nxt = dec.step(tokens, pos, logits)           # mk_decode_step (synchronous)
     dec.launch(tokens, pos, logits, next_dev)     # mk_launch_step (asynchronous)
+Prompt operators (asynchronous on torch's current stream of the tensors' device):
+    y = linear(x, w, bias, activation, residual)  # mk_linear
+    o = attend(q, kv, q_lens, kv_lens, window=..) # mk_attend
 """
 from __future__ import annotations
 
@@ -31,13 +34,16 @@ MK_OK, MK_ERR_ARG, MK_ERR_CAPACITY, MK_ERR_RESOURCES, MK_ERR_CUDA, MK_ERR_TIMEOU
 STATUS_NAMES = ["MK_OK", "MK_ERR_ARG", "MK_ERR_CAPACITY", "MK_ERR_RESOURCES", "MK_ERR_CUDA", "MK_ERR_TIMEOUT",
                 "MK_ERR_OPCODE", "MK_ERR_BOUNDS", "MK_ERR_POISONED"]
 SYNC_TAGS, SYNC_COUNTERS = 0, 1   # mk_sync_mode
+BF16, F32 = 0, 1                  # mk_dtype
+ACTIVATIONS = {None: 0, "silu": 1, "gelu": 2, "swiglu": 3}   # mk_activation
+ATTEND_MAX_BATCH = 256            # MK_ATTEND_MAX_BATCH
 
 EXPORTS = ["mk_build_schedule", "mk_schedule_queues", "mk_schedule_counters", "mk_schedule_patch",
            "mk_scratch_bytes", "mk_schedule_free", "mk_bind", "mk_set_timeout", "mk_decode_step",
            "mk_launch_step", "mk_ctx_status", "mk_device_sm_count", "mk_last_error", "mk_unbind", "mk_set_trace",
            "mk_decode_step_static", "mk_set_sync", "mk_decode_steps", "mk_bind_paged", "mk_schedule_attn_chunk",
            "mk_decode_persistent_start", "mk_decode_persistent_stop", "mk_decode_persistent_progress",
-           "mk_decode_persistent_wait", "mk_rebind_schedule"]
+           "mk_decode_persistent_wait", "mk_rebind_schedule", "mk_linear", "mk_attend", "mk_attend_workspace"]
 
 
 class MkError(RuntimeError):
@@ -77,6 +83,23 @@ class mk_kv_pages(ctypes.Structure):
 
 
 _I32P = ctypes.POINTER(ctypes.c_int32)
+
+
+class mk_linear_args(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("rows", "n", "k", "activation")] + \
+               [("x", _P), ("x_stride", ctypes.c_int64), ("w", _P), ("bias", _P), ("residual", _P),
+                ("residual_stride", ctypes.c_int64), ("residual_dtype", ctypes.c_int32), ("out_dtype", ctypes.c_int32),
+                ("out", _P), ("out_stride", ctypes.c_int64), ("status", _P)]
+
+
+class mk_attend_args(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("n_q_heads", "n_kv_heads", "head_dim", "batch")] + \
+               [("q_lens", _I32P), ("kv_lens", _I32P), ("q", _P), ("q_stride", ctypes.c_int64), ("out", _P),
+                ("out_stride", ctypes.c_int64), ("kv", ctypes.POINTER(mk_kv)), ("pages", ctypes.POINTER(mk_kv_pages))] + \
+               [(n, ctypes.c_int32) for n in ("layer", "max_seq", "window", "sinks", "shared_prefix")] + \
+               [("scale", ctypes.c_float), ("status", _P)]
+
+
 lib.mk_build_schedule.restype = ctypes.c_int
 lib.mk_build_schedule.argtypes = [ctypes.POINTER(mk_model_cfg), ctypes.c_int32, ctypes.POINTER(mk_sched_opts),
                                   ctypes.POINTER(_P)]
@@ -127,6 +150,12 @@ lib.mk_set_trace.restype = ctypes.c_int
 lib.mk_set_trace.argtypes = [_P, _P]
 lib.mk_set_sync.restype = ctypes.c_int
 lib.mk_set_sync.argtypes = [_P, ctypes.c_int32]
+lib.mk_linear.restype = ctypes.c_int
+lib.mk_linear.argtypes = [ctypes.POINTER(mk_linear_args), _P]
+lib.mk_attend_workspace.restype = ctypes.c_size_t
+lib.mk_attend_workspace.argtypes = [ctypes.POINTER(mk_attend_args)]
+lib.mk_attend.restype = ctypes.c_int
+lib.mk_attend.argtypes = [ctypes.POINTER(mk_attend_args), _P, ctypes.c_size_t, _P]
 lib.mk_unbind.restype = None
 lib.mk_unbind.argtypes = [_P]
 
@@ -378,3 +407,157 @@ class Decoder:
         info = (ctypes.c_int32 * 8)()
         st = lib.mk_ctx_status(self.handle, info)
         return st, list(info)
+
+
+# ---- prompt operators ------------------------------------------------------------------------
+
+def _op_tensor(t, name, dtypes, device, dim=2):
+    """The checks every operand passes: a CUDA tensor of one of `dtypes` on `device` whose last
+    dimension is contiguous."""
+    if not t.is_cuda or t.device != device:
+        raise ValueError(f"{name} must be a CUDA tensor on {device}")
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name} must be one of {dtypes}, not {t.dtype}")
+    if t.dim() != dim:
+        raise ValueError(f"{name} must have {dim} dimensions, not {t.dim()}")
+    if t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name}: its last dimension must be contiguous")
+    return t
+
+
+def _op_status(status, device):
+    import torch
+    if status is None:
+        return None
+    _op_tensor(status, "status", (torch.int32,), device, dim=1)
+    if status.numel() < 1:
+        raise ValueError("status must hold one int32")
+    return status.data_ptr()
+
+
+def _on_device(device, call):
+    """Runs call(stream) with `device` current and torch's current stream of it."""
+    import torch
+    if torch.cuda.current_device() == device.index:
+        return _check(call(torch.cuda.current_stream(device).cuda_stream))
+    with torch.cuda.device(device):
+        return _check(call(torch.cuda.current_stream(device).cuda_stream))
+
+
+def linear(x, weight, bias=None, activation: Optional[str] = None, residual=None, out=None, out_dtype=None, status=None):
+    """mk_linear: act(x @ weight.T + bias) + residual, in fp32, rounded once to the output's type.
+
+    x [rows, k] bf16 (rows may be strided by a multiple of 8 elements), weight [n, k] bf16
+    contiguous -- [2 n, k] with activation "swiglu": n gate rows, then n up rows, silu(gate) * up --
+    bias bf16 [n] ([2 n]), residual bf16 or fp32 [rows, n] (or an expanded row).  activation: None,
+    "silu", "gelu" (the erf form) or "swiglu".  out: a bf16 or fp32 [rows, n] tensor, which may be
+    the residual itself; by default one of out_dtype (bf16) is allocated.  Returns out."""
+    import torch
+    bf, f32 = torch.bfloat16, torch.float32
+    dev = x.device
+    _op_tensor(x, "x", (bf,), dev)
+    _op_tensor(weight, "weight", (bf,), dev)
+    if activation not in ACTIVATIONS:
+        raise ValueError(f"activation {activation!r}: expected one of {list(ACTIVATIONS)}")
+    if not weight.is_contiguous():
+        raise ValueError("weight must be contiguous")
+    rows, k = x.shape
+    n = weight.shape[0]
+    if weight.shape[1] != k:
+        raise ValueError(f"weight {tuple(weight.shape)} does not take rows of {k}")
+    if bias is not None and (_op_tensor(bias, "bias", (bf,), dev, dim=1).shape[0] != n or not bias.is_contiguous()):
+        raise ValueError(f"bias must be contiguous, of {n} elements")
+    if activation == "swiglu":
+        if n % 2:
+            raise ValueError("swiglu takes an even number of weight rows: gate rows, then up rows")
+        n //= 2
+    if out is None:
+        out = torch.empty((rows, n), dtype=out_dtype or bf, device=dev)
+    elif out_dtype is not None and out.dtype != out_dtype:
+        raise ValueError(f"out is {out.dtype}, out_dtype {out_dtype}")
+    _op_tensor(out, "out", (bf, f32), dev)
+    if out.shape != (rows, n):
+        raise ValueError(f"out must be [{rows}, {n}], not {tuple(out.shape)}")
+    if residual is not None and _op_tensor(residual, "residual", (bf, f32), dev).shape != (rows, n):
+        raise ValueError(f"residual must be [{rows}, {n}], not {tuple(residual.shape)}")
+    a = mk_linear_args(rows, n, k, ACTIVATIONS[activation], x.data_ptr(), x.stride(0), weight.data_ptr(),
+                       None if bias is None else bias.data_ptr(), None if residual is None else residual.data_ptr(),
+                       0 if residual is None else residual.stride(0),
+                       F32 if residual is not None and residual.dtype == f32 else BF16, F32 if out.dtype == f32 else BF16,
+                       out.data_ptr(), out.stride(0), _op_status(status, dev))
+    _on_device(dev, lambda stream: lib.mk_linear(ctypes.byref(a), stream))
+    return out
+
+
+def attend(q, kv, q_lens: Sequence[int], kv_lens: Sequence[int], layer: int = 0, window: int = 0, sinks: int = 0,
+           shared_prefix: int = 0, scale: Optional[float] = None, pages=None, out=None, workspace=None, status=None):
+    """mk_attend: attention of query tokens over one layer of a KV cache.
+
+    q [tokens, n_q_heads, head_dim] bf16: the sequences' query tokens back to back, q_lens[b] of
+    sequence b, which are the last of its kv_lens[b] positions (their K/V rows already in the
+    cache).  kv, pages: the cache as Decoder takes it -- kv.k / kv.v [batch, layers, kv heads, max_seq,
+    head_dim], or the pool [layers, kv heads, n_blocks * block_size, head_dim] with
+    pages = (block_table, block_size, n_blocks).  A token at position t sees positions p <= t; with a
+    window those with p > t - window or p < sinks.  shared_prefix: the first positions, the same
+    for every sequence, read once through sequence 0.  out: bf16, shaped like q (allocated by
+    default); workspace: at least attend_workspace bytes (allocated by default).  Returns out."""
+    import torch
+    bf = torch.bfloat16
+    dev = q.device
+    _op_tensor(q, "q", (bf,), dev, dim=3)
+    tokens, nq, d = q.shape
+    batch = len(q_lens)
+    if len(kv_lens) != batch:
+        raise ValueError("q_lens and kv_lens must have the same length")
+    ql, kvl = (ctypes.c_int32 * max(batch, 1))(*q_lens), (ctypes.c_int32 * max(batch, 1))(*kv_lens)
+    if sum(ql) > tokens:
+        raise ValueError(f"q holds {tokens} tokens, q_lens add up to {sum(ql)}")
+    if out is None:
+        out = torch.empty((tokens, nq, d), dtype=bf, device=dev)
+    elif _op_tensor(out, "out", (bf,), dev, dim=3).shape != q.shape:
+        raise ValueError("out must have q's shape")
+    for t, name in ((q, "q"), (out, "out")):
+        if nq > 1 and t.stride(1) != d:
+            raise ValueError(f"{name}: a token's heads must be contiguous")
+    k, v = kv.k, kv.v
+    dims = 5 if pages is None else 4
+    _op_tensor(k, "kv.k", (bf,), dev, dim=dims)
+    _op_tensor(v, "kv.v", (bf,), dev, dim=dims)
+    if k.shape != v.shape or k.stride() != v.stride() or k.shape[-1] != d or k.stride(-2) != d:
+        raise ValueError("kv.k and kv.v must be alike, with contiguous [positions, head_dim] rows of q's head_dim")
+    st = k.stride()
+    layers, nkv, positions = k.shape[-4], k.shape[-3], k.shape[-2]
+    if not 0 <= layer < layers:
+        raise ValueError(f"layer {layer} of {layers}")
+    if pages is None:
+        if k.shape[0] < batch:
+            raise ValueError(f"the cache holds {k.shape[0]} sequences, q_lens name {batch}")
+        c_kv, c_pages = mk_kv(k.data_ptr(), v.data_ptr(), st[0], st[1], st[2]), None
+    else:
+        table, block_size, n_blocks = pages
+        _op_tensor(table, "the block table", (torch.int32,), dev)
+        if table.shape[0] < batch or not table.is_contiguous():
+            raise ValueError(f"the block table must be contiguous, with a row for each of {batch} sequences")
+        if positions < int(n_blocks) * int(block_size):
+            raise ValueError(f"the pool holds {positions} positions a head, {n_blocks} blocks of {block_size} need more")
+        c_kv = mk_kv(k.data_ptr(), v.data_ptr(), 0, st[0], st[1])
+        c_pages = mk_kv_pages(table.data_ptr(), int(block_size), table.shape[1], int(n_blocks))
+        positions = table.shape[1] * int(block_size)
+    a = mk_attend_args(nq, nkv, d, batch, ql, kvl, q.data_ptr(), q.stride(0), out.data_ptr(), out.stride(0),
+                       ctypes.pointer(c_kv), None if c_pages is None else ctypes.pointer(c_pages), layer, positions,
+                       window, sinks, shared_prefix, 0.0 if scale is None else scale, _op_status(status, dev))
+    if scale is not None and not scale > 0:
+        raise ValueError("scale must be positive")
+
+    def call(stream):
+        ws = workspace
+        need = int(lib.mk_attend_workspace(ctypes.byref(a)))
+        if ws is None and need:
+            ws = torch.empty(need, dtype=torch.uint8, device=dev)
+        if ws is not None and (ws.device != dev or not ws.is_contiguous()):
+            raise ValueError(f"workspace must be contiguous, on {dev}")
+        return lib.mk_attend(ctypes.byref(a), None if ws is None else ws.data_ptr(),
+                             0 if ws is None else ws.numel() * ws.element_size(), stream)
+
+    _on_device(dev, call)
+    return out

@@ -1,10 +1,12 @@
 """Builds libmk.so (the C-ABI library) in-tree with nvcc for sm_103a.
 
-Three translation units compiled in parallel and linked into one shared library:
+Translation units compiled in parallel and linked into one shared library:
   csrc/mk_sched.cpp  host scheduler
   csrc/mk_api.cu     binding, launch and status (host)
   csrc/mk_kernel.cu  the persistent megakernel (batch-1 instances) and the RoPE table kernel (device)
   csrc/mk_kernel_batch.cu  the batch > 1 instance of the same kernel source (tensor-core matvec tiles)
+  csrc/mk_linear.cu  the linear map with a fused epilogue (prompt path)
+  csrc/mk_attend.cu  attention of query tokens over the KV cache (prompt path)
 """
 from __future__ import annotations
 
@@ -20,7 +22,8 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libmk.so")
 BUILD_DIR = os.path.join(HERE, "_build")
-SOURCES = ["mk_sched.cpp", "mk_api.cu", "mk_kernel.cu", "mk_kernel_batch.cu"]
+SOURCES = ["mk_sched.cpp", "mk_api.cu", "mk_kernel.cu", "mk_kernel_batch.cu", "mk_linear.cu", "mk_attend.cu"]
+HEADERS = ["mk_internal.h", "mk_ops.h"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -33,7 +36,7 @@ def _nvcc() -> str:
 
 def _inputs() -> List[str]:
     files = [os.path.join(CSRC, s) for s in SOURCES]
-    files += [os.path.join(CSRC, "mk_internal.h"), os.path.join(INCLUDE, "mk.h"), __file__]
+    files += [os.path.join(CSRC, h) for h in HEADERS] + [os.path.join(INCLUDE, "mk.h"), __file__]
     return files
 
 
@@ -57,7 +60,7 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
         cmd = [nvcc, *common, *ARCH, "-lineinfo", "-c", os.path.join(CSRC, src), "-o", obj]
         if src.endswith(".cpp"):
             cmd = [nvcc, *common, "-x", "c++", "-c", os.path.join(CSRC, src), "-o", obj]
-        if ptxas_info and src == "mk_kernel.cu":
+        if ptxas_info and src in ("mk_kernel.cu", "mk_linear.cu", "mk_attend.cu"):
             cmd.insert(1, "-Xptxas=-v")
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:

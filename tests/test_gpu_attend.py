@@ -1,0 +1,262 @@
+"""mk_attend against its definition in 64 bits: head layouts, lengths from none to many tiles, windows
+and sinks, ragged batches, paged caches, shared prefixes, what masked places hold, strides, streams
+and graphs.  The tolerance is derived in attend_reference."""
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+if not torch.cuda.is_available():
+    pytest.skip("needs a CUDA GPU", allow_module_level=True)
+
+import persistent_megakernel_decode_sm_gb300 as mk  # noqa: E402
+from attend_reference import attend_reference  # noqa: E402
+from workload import KVCache  # noqa: E402
+
+BF = torch.bfloat16
+
+
+def randn(shape, seed, std=1.0):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return (torch.randn(shape, generator=g, device="cuda") * std).to(BF)
+
+
+def cache(batch, nkv, d, max_seq, layers=1, seed=0):
+    shape = (batch, layers, nkv, max_seq, d)
+    return KVCache(randn(shape, seed + 1), randn(shape, seed + 2))
+
+
+def pool(batch, nkv, d, max_seq, block, layers=1, seed=0, spare=3):
+    """A paged cache: (kv, pages) with blocks in shuffled order."""
+    per = -(-max_seq // block)
+    n = batch * per + spare
+    table = torch.randperm(n, generator=torch.Generator().manual_seed(seed))[:batch * per].reshape(batch, per)
+    shape = (layers, nkv, n * block, d)
+    return KVCache(randn(shape, seed + 1), randn(shape, seed + 2)), (table.to(device="cuda", dtype=torch.int32), block, n)
+
+
+def check(q, kv, q_lens, kv_lens, out=None, **kw):
+    want, bound = attend_reference(q, kv, q_lens, kv_lens, **kw)
+    got = mk.attend(q, kv, q_lens, kv_lens, out=out, **kw)
+    rows = sum(q_lens)
+    off = (got[:rows].double() - want[:rows]).abs() / bound[:rows]
+    assert torch.isfinite(got[:rows]).all()
+    assert off.numel() == 0 or off.max().item() <= 1, off.max().item()
+    return got
+
+
+@pytest.mark.parametrize("d", [32, 64, 128])
+@pytest.mark.parametrize("nkv,group", [(1, 1), (2, 2), (1, 3), (2, 4), (1, 5), (1, 6), (1, 7), (2, 8)])
+def test_head_layouts(d, nkv, group):
+    kv = cache(2, nkv, d, 300)
+    check(randn((1 + 70, nkv * group, d), 5, 1.5), kv, [1, 70], [300, 211])
+
+
+@pytest.mark.parametrize("q_len,kv_len", [(1, 1), (1, 2), (2, 2), (1, 127), (1, 128), (1, 129), (1, 1000), (16, 16), (17, 128),
+                                          (31, 131), (32, 256), (33, 257), (64, 640), (129, 129), (130, 513), (400, 400)])
+@pytest.mark.parametrize("d", [32, 64, 128])
+def test_lengths(q_len, kv_len, d):
+    check(randn((q_len, 4, d), 5, 1.5), cache(1, 1, d, kv_len), [q_len], [kv_len])
+
+
+@pytest.mark.parametrize("window,sinks", [(1, 0), (1, 1), (5, 0), (5, 3), (64, 4), (127, 0), (128, 128), (130, 64), (300, 150),
+                                          (1000, 4), (40, 1000), (2000, 0)])
+@pytest.mark.parametrize("q_len,kv_len", [(1, 700), (40, 700), (300, 700), (700, 700)])
+def test_windows(window, sinks, q_len, kv_len):
+    check(randn((q_len, 8, 64), 5, 1.5), cache(1, 2, 64, 704), [q_len], [kv_len], window=window, sinks=sinks)
+
+
+@pytest.mark.parametrize("window,sinks", [(0, 0), (70, 3)])
+def test_ragged_batch(window, sinks):
+    q_lens, kv_lens = [1, 0, 37, 200, 1, 3, 0, 129], [1, 17, 300, 200, 513, 3, 0, 400]
+    q = randn((sum(q_lens) + 9, 6, 64), 5, 1.5)
+    kv = cache(8, 2, 64, 520)
+    out = torch.full_like(q, 3.0)
+    check(q, kv, q_lens, kv_lens, out=out, window=window, sinks=sinks)
+    assert (out[sum(q_lens):] == 3).all()          # rows behind the last sequence are left as they were
+
+
+def test_tokens_without_a_visible_position_get_zeros():
+    q_lens, kv_lens = [5, 300, 2], [2, 170, 0]
+    q, kv = randn((307, 4, 64), 5), cache(3, 1, 64, 300)
+    got = check(q, kv, q_lens, kv_lens)
+    assert (got[:3] == 0).all() and (got[5:5 + 130] == 0).all() and (got[305:] == 0).all() and (got[3:5] != 0).any()
+
+
+@pytest.mark.parametrize("window,sinks", [(0, 0), (90, 5)])
+@pytest.mark.parametrize("q_lens,kv_lens", [([1, 1], [200, 333]), ([60, 200], [200, 333])])
+def test_what_masked_places_hold(window, sinks, q_lens, kv_lens):
+    # positions that no token of the call sees hold NaN and infinities: they change nothing
+    kv = cache(2, 2, 64, 384)
+    q = randn((sum(q_lens), 8, 64), 5)
+    clean = mk.attend(q, kv, q_lens, kv_lens, window=window, sinks=sinks)
+    for b in range(2):
+        for t, bad in ((kv.k, float("nan")), (kv.v, float("nan"))):
+            t[b, :, :, kv_lens[b]:] = bad
+        low = kv_lens[b] - q_lens[b] - window + 1
+        if window and low > sinks:
+            kv.k[b, :, :, sinks:low] = float("inf")
+            kv.v[b, :, :, sinks:low] = float("nan")
+    assert torch.equal(mk.attend(q, kv, q_lens, kv_lens, window=window, sinks=sinks), clean)
+
+
+@pytest.mark.parametrize("block", [8, 16, 48, 64, 128, 200, 256, 512])
+@pytest.mark.parametrize("d", [32, 64, 128])
+def test_paged(block, d):
+    kv, pages = pool(3, 2, d, 777, block)
+    q_lens, kv_lens = [1, 90, 3], [777, 400, 129]
+    check(randn((94, 8, d), 5, 1.5), kv, q_lens, kv_lens, pages=pages)
+    check(randn((94, 8, d), 6, 1.5), kv, q_lens, kv_lens, pages=pages, window=150, sinks=9)
+
+
+def test_a_bad_table_entry_is_not_followed():
+    kv, pages = pool(2, 1, 64, 512, 64)
+    q_lens, kv_lens = [2, 40], [512, 500]
+    q = randn((42, 4, 64), 5)
+    for bad in (-1, pages[2], 1 << 30):
+        pages[0][0, 1] = bad
+        pages[0][1, 7] = bad
+        status = torch.zeros(1, dtype=torch.int32, device="cuda")
+        want, bound = attend_reference(q, kv, q_lens, kv_lens, pages=pages)
+        got = mk.attend(q, kv, q_lens, kv_lens, pages=pages, status=status)
+        assert ((got.double() - want).abs() <= bound).all()
+        assert status.item() == mk.MK_ERR_BOUNDS
+
+
+def test_unused_table_entries_may_hold_anything():
+    kv, pages = pool(2, 1, 64, 512, 64)
+    pages[0][0, 4:] = -7
+    pages[0][1, 1:5] = 1 << 29          # between the sinks and the window of every token
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    q = randn((11, 4, 64), 5)
+    got = mk.attend(q, kv, [1, 10], [256, 500], pages=pages, window=100, sinks=3, status=status)
+    want, bound = attend_reference(q, kv, [1, 10], [256, 500], pages=pages, window=100, sinks=3)
+    assert ((got.double() - want).abs() <= bound).all() and status.item() == 0
+
+
+@pytest.mark.parametrize("block", [0, 64, 128])
+@pytest.mark.parametrize("prefix", [1, 100, 128, 1000])
+@pytest.mark.parametrize("q_lens,tails", [([1, 1, 1], [1, 2, 140]), ([1, 0, 33, 7], [1, 0, 200, 7]), ([60] * 9, [60] * 9)])
+def test_shared_prefix(block, prefix, q_lens, tails):
+    kv_lens = [prefix + t for t in tails]
+    batch, top = len(q_lens), max(kv_lens)
+    if block:
+        kv, pages = pool(batch, 2, 64, top, block)
+    else:
+        kv, pages = cache(batch, 2, 64, top), None
+        for b in range(1, batch):          # the prefix is read through sequence 0 alone
+            kv.k[b, :, :, :prefix] = float("nan")
+            kv.v[b, :, :, :prefix] = float("nan")
+    check(randn((sum(q_lens), 8, 64), 5, 1.5), kv, q_lens, kv_lens, shared_prefix=prefix, pages=pages)
+
+
+@pytest.mark.parametrize("d,group", [(32, 1), (64, 3), (128, 8)])
+def test_shared_prefix_heads(d, group):
+    q_lens = [1, 4, 2, 50, 1]
+    kv_lens = [400 + n + 3 * b for b, n in enumerate(q_lens)]
+    check(randn((sum(q_lens), 2 * group, d), 5, 1.5), cache(5, 2, d, 500), q_lens, kv_lens, shared_prefix=400)
+
+
+def test_strides_layers_and_scale():
+    kv = cache(3, 2, 64, 400, layers=3)
+    wide = KVCache(*(torch.full((3, 3, 2, 500, 64), float("nan"), device="cuda", dtype=BF)[:, :, :, :400] for _ in range(2)))
+    wide.k.copy_(kv.k)
+    wide.v.copy_(kv.v)
+    buf = randn((60, 1000), 5, 1.5)
+    q = buf[:, 8:8 + 512].unflatten(1, (8, 64))
+    obuf = torch.full((60, 800), 2.0, device="cuda", dtype=BF)
+    out = obuf[:, 16:16 + 512].unflatten(1, (8, 64))
+    for c in (kv, wide):
+        for layer in (0, 2):
+            got = check(q, c, [10, 50], [400, 123], out=out, layer=layer, scale=0.3)
+            assert (obuf[:, :16] == 2).all() and (obuf[:, 528:] == 2).all()
+    assert torch.equal(got, check(q.contiguous(), kv, [10, 50], [400, 123], layer=2, scale=0.3))
+
+
+def test_sharp_and_flat_softmax():
+    # scores far apart (one weight near 1, the maximum rising along the row) and all alike
+    d = 64
+    kv = cache(1, 1, d, 600)
+    q = randn((64, 4, d), 5, 12.0)
+    check(q, kv, [64], [600])
+    ramp = torch.arange(600, device="cuda") / 20.0
+    kv.k[0, 0, 0] = (ramp[:, None] * torch.ones(d, device="cuda")).to(BF)
+    check(torch.ones((64, 4, d), device="cuda", dtype=BF), kv, [64], [600])
+    check(-torch.ones((64, 4, d), device="cuda", dtype=BF), kv, [64], [600])
+    check(torch.zeros((64, 4, d), device="cuda", dtype=BF), kv, [64], [600])
+
+
+def test_far_positions():
+    # offsets past 2^31 elements: only the window's tail of a long cache is read
+    d, top = 64, (1 << 25) + 700
+    kv = KVCache(torch.zeros((1, 1, 1, top, d), device="cuda", dtype=BF), torch.zeros((1, 1, 1, top, d), device="cuda", dtype=BF))
+    kv.k[0, 0, 0, -1000:] = randn((1000, d), 1)
+    kv.v[0, 0, 0, -1000:] = randn((1000, d), 2)
+    kv.v[0, 0, 0, :4] = 1.0
+    q = randn((30, 4, d), 5)
+    got = mk.attend(q, kv, [30], [top], window=300, sinks=4)
+    near = KVCache(kv.k[:, :, :, -1000:].contiguous(), kv.v[:, :, :, -1000:].contiguous())
+    near.k[0, 0, 0, :4], near.v[0, 0, 0, :4] = 0.0, 1.0
+    want, bound = attend_reference(q, near, [30], [1000], window=300, sinks=4)
+    assert ((got.double() - want).abs() <= bound).all()
+
+
+def test_repeatable_on_streams_and_with_a_given_workspace():
+    kv = cache(4, 2, 64, 3000)
+    q = randn((4, 8, 64), 5)
+    args = (q, kv, [1] * 4, [3000, 1, 2000, 700])
+    a = mk.attend(*args)
+    for _ in range(3):
+        assert torch.equal(mk.attend(*args), a)
+    ws = torch.full((1 << 24,), 0xFF, dtype=torch.uint8, device="cuda")      # whatever it holds
+    assert torch.equal(mk.attend(*args, workspace=ws), a)
+    s = [torch.cuda.Stream() for _ in range(2)]
+    got = []
+    for x in s:
+        x.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(x):
+            got.append(mk.attend(*args))
+    torch.cuda.synchronize()
+    assert torch.equal(got[0], a) and torch.equal(got[1], a)
+
+
+def test_captured_and_replayed():
+    kv, pages = pool(2, 2, 64, 2000, 128)
+    q = randn((5, 8, 64), 5)
+    ws = torch.empty(1 << 24, dtype=torch.uint8, device="cuda")
+    graphs, outs = [], []
+    mk.attend(q, kv, [1, 4], [2000, 1500], pages=pages)
+    torch.cuda.synchronize()
+    for lens in ([2000, 1500], [900, 2000]):          # two graphs, one workspace, replayed in turn
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(mk.attend(q, kv, [1, 4], lens, pages=pages, workspace=ws))
+        graphs.append(g)
+    kv.v.copy_(randn(tuple(kv.v.shape), 77))
+    for g in graphs * 2:
+        g.replay()
+    torch.cuda.synchronize()
+    for lens, o in zip(([2000, 1500], [900, 2000]), outs):
+        assert torch.equal(o, mk.attend(q, kv, [1, 4], lens, pages=pages))
+
+
+def test_refuses_tensors_it_cannot_take():
+    kv, (pk, pages) = cache(2, 2, 64, 100), pool(2, 2, 64, 100, 16)
+    q = randn((3, 8, 64), 5)
+    for bad in (lambda: mk.attend(q.cpu(), kv, [1, 2], [9, 9]), lambda: mk.attend(q.float(), kv, [1, 2], [9, 9]),
+                lambda: mk.attend(q, kv, [1, 2], [9]), lambda: mk.attend(q, kv, [2, 2], [9, 9]),
+                lambda: mk.attend(q, kv, [1, 1, 1], [9, 9, 9]), lambda: mk.attend(q, kv, [1, 2], [9, 9], layer=1),
+                lambda: mk.attend(q, pk, [1, 2], [9, 9]), lambda: mk.attend(q, kv, [1, 2], [9, 9], pages=pages),
+                lambda: mk.attend(q, kv, [1, 2], [9, 9], scale=0.0), lambda: mk.attend(q[:, ::2], kv, [1, 2], [9, 9]),
+                lambda: mk.attend(q, pk, [1, 2], [9, 9], pages=(pages[0], 16, pages[2] + 1)),
+                lambda: mk.attend(q, pk, [1, 2], [9, 9], pages=(pages[0][:1], 16, pages[2])),
+                lambda: mk.attend(q, kv, [1, 2], [9, 9], out=torch.empty_like(q[:2])),
+                lambda: mk.attend(q, KVCache(kv.k, kv.v[:, :, :, :50]), [1, 2], [9, 9])):
+        with pytest.raises(ValueError):
+            bad()
+    for bad in (lambda: mk.attend(q, kv, [1, 2], [9, 101]), lambda: mk.attend(q, kv, [1, 2], [9, 9], out=q),
+                lambda: mk.attend(q, kv, [1, 2], [9, 9], shared_prefix=9),
+                lambda: mk.attend(randn((3, 18, 64), 5), kv, [1, 2], [9, 9])):
+        with pytest.raises(mk.MkError) as e:
+            bad()
+        assert e.value.status == mk.MK_ERR_ARG
