@@ -23,7 +23,7 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libmk.so")
 BUILD_DIR = os.path.join(HERE, "_build")
 SOURCES = ["mk_sched.cpp", "mk_api.cu", "mk_kernel.cu", "mk_kernel_batch.cu", "mk_linear.cu", "mk_attend.cu"]
-HEADERS = ["mk_internal.h", "mk_ops.h"]
+HEADERS = ["mk_internal.h", "mk_ops.h", "mk_sm103.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

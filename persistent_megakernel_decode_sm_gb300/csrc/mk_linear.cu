@@ -1,24 +1,22 @@
 // The linear map of the prompt path: out = act(x w^T + bias) + residual (mk_linear).
 #include "mk_ops.h"
-
-#include <cuda_bf16.h>
+#include "mk_sm103.cuh"
 
 namespace mk {
 
 struct LinearParams {
     int rows, n, k, act;
-    const __nv_bfloat16* x;
-    int64_t x_stride;
-    const __nv_bfloat16* w;
+    int tiles_n, tiles_m, split;   // feature tiles, token tiles; CTAs (one cluster) that share a tile's contraction
     const __nv_bfloat16* bias;
     const void* residual;
     int64_t residual_stride;
     int residual_f32, out_f32;
     void* out;
     int64_t out_stride;
+    int32_t* status;
 };
 
-// bias, activation and residual of one output, in fp32; rounded once by the store
+// y and the up factor of one output, bias included, to the value before the residual, in fp32
 __device__ __forceinline__ float linear_act(int act, float y, float up) {
     switch (act) {
         case MK_ACT_SILU: return y / (1.f + expf(-y));
@@ -27,41 +25,255 @@ __device__ __forceinline__ float linear_act(int act, float y, float up) {
         default: return y;
     }
 }
-
-// One thread per output; 16 x 16 outputs a block, their rows staged 16 inputs at a time.
-__global__ void __launch_bounds__(256) linear_simple_kernel(const LinearParams p) {
-    __shared__ float sx[16][17], sw[16][17], su[16][17];
-    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-    const int j = blockIdx.x * 16 + tx, r = blockIdx.y * 16 + ty;
-    const bool gated = p.act == MK_ACT_SWIGLU;
-    float y = 0.f, u = 0.f;
-    for (int k0 = 0; k0 < p.k; k0 += 16) {
-        const int jl = blockIdx.x * 16 + ty, kk = k0 + tx;
-        sx[ty][tx] = r < p.rows && kk < p.k ? __bfloat162float(p.x[r * p.x_stride + kk]) : 0.f;
-        sw[ty][tx] = jl < p.n && kk < p.k ? __bfloat162float(p.w[int64_t(jl) * p.k + kk]) : 0.f;
-        su[ty][tx] = gated && jl < p.n && kk < p.k ? __bfloat162float(p.w[(int64_t(p.n) + jl) * p.k + kk]) : 0.f;
-        __syncthreads();
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            y = fmaf(sx[ty][i], sw[tx][i], y);
-            if (gated) u = fmaf(sx[ty][i], su[tx][i], u);
-        }
-        __syncthreads();
-    }
-    if (r >= p.rows || j >= p.n) return;
-    if (p.bias) {
-        y += __bfloat162float(p.bias[j]);
-        if (gated) u += __bfloat162float(p.bias[p.n + j]);
-    }
-    y = linear_act(p.act, y, u);
-    if (p.residual) {
-        const int64_t at = r * p.residual_stride + j;
-        y += p.residual_f32 ? static_cast<const float*>(p.residual)[at]
-                            : __bfloat162float(static_cast<const __nv_bfloat16*>(p.residual)[at]);
-    }
+__device__ __forceinline__ float linear_residual(const LinearParams& p, int r, int j) {
+    const int64_t at = r * p.residual_stride + j;
+    return p.residual_f32 ? static_cast<const float*>(p.residual)[at]
+                          : __bfloat162float(static_cast<const __nv_bfloat16*>(p.residual)[at]);
+}
+__device__ __forceinline__ void linear_store(const LinearParams& p, int r, int j, float y) {
     const int64_t at = r * p.out_stride + j;
     if (p.out_f32) static_cast<float*>(p.out)[at] = y;
     else static_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16_rn(y);
+}
+
+// A tile is 128 output features (the MMA's M: rows of w, one per tensor-memory lane) by BN tokens
+// (its N: one accumulator column each), so few tokens cost few columns, a bias belongs to a lane,
+// and a warp's store of one column is 32 neighbouring outputs of a token's row.  SwiGLU holds the
+// gate rows and the up rows of the same features as two accumulators, multiplied in the epilogue.
+// The contraction runs in blocks of 64 through a ring of shared-memory stages.
+constexpr int kLinK = 64;
+template <int BN, bool GATED>
+struct LinearTile {
+    static constexpr int kAccs = GATED ? 2 : 1;
+    static constexpr int kABytes = 128 * kLinK * 2, kBBytes = BN * kLinK * 2;
+    static constexpr int kStageBytes = kAccs * kABytes + kBBytes;
+    static constexpr int kStages = 200 * 1024 / kStageBytes < 10 ? 200 * 1024 / kStageBytes : 10;
+    static constexpr int kBufCols = BN * kAccs;                    // columns of one tile's accumulators
+    static constexpr int kCols = 2 * kBufCols < 32 ? 32 : 2 * kBufCols;   // two tiles: one is written out while the next is summed
+    static constexpr int kSmem = kStages * kStageBytes + 1024;    // (+ alignment of the first stage)
+    static_assert(kCols <= 512 && (kCols & (kCols - 1)) == 0);
+    static_assert(kStages * kStageBytes >= kBufCols * 128 * 4);   // a split tile's partial sums are staged there
+};
+
+// Warp 0: TMA producer.  Warp 1: tensor memory and MMA issue.  Warps 2-5: epilogue, one per 32 lanes.
+template <int BN, bool GATED>
+__global__ void __launch_bounds__(192, 1)
+linear_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x,
+              const __grid_constant__ LinearParams p) {
+    using T = LinearTile<BN, GATED>;
+    extern __shared__ uint8_t raw[];
+    __shared__ uint64_t bars[2 * T::kStages + 5];
+    __shared__ uint32_t tmem_at;
+    __shared__ int abort_flag;
+    volatile int* abort_word = &abort_flag;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t stage0 = (sm::smem(raw) + 1023u) & ~1023u;
+    const uint32_t bar0 = sm::smem(bars);
+    auto full = [&](int s) { return bar0 + 8u * s; };
+    auto empty = [&](int s) { return bar0 + 8u * (T::kStages + s); };
+    auto acc_full = [&](int s) { return bar0 + 8u * (2 * T::kStages + s); };
+    auto acc_empty = [&](int s) { return bar0 + 8u * (2 * T::kStages + 2 + s); };
+    const uint32_t drained = bar0 + 8u * (2 * T::kStages + 4);
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < T::kStages; ++s) { sm::bar_init(full(s), 1); sm::bar_init(empty(s), 1); }
+        for (int s = 0; s < 2; ++s) { sm::bar_init(acc_full(s), 1); sm::bar_init(acc_empty(s), 128); }
+        sm::bar_init(drained, 1);
+        abort_flag = 0;
+        sm::bar_fence_init();
+        sm::tma_prefetch_map(&map_w);
+        sm::tma_prefetch_map(&map_x);
+    }
+    if (warp == 1) sm::tmem_alloc(sm::smem(&tmem_at), T::kCols);
+    sm::tc_fence_before();
+    __syncthreads();
+    sm::tc_fence_after();
+    const uint32_t tmem = tmem_at;
+
+    // this CTA's tiles, and its share [kb0, kb1) of their contraction blocks
+    const int rank = p.split > 1 ? int(sm::cluster_rank()) : 0;
+    const int first = int(blockIdx.x) / p.split, step = int(gridDim.x) / p.split;
+    const int tiles = p.tiles_n * p.tiles_m;
+    const int blocks = (p.k + kLinK - 1) / kLinK;
+    const int kb0 = int(int64_t(blocks) * rank / p.split), kb1 = int(int64_t(blocks) * (rank + 1) / p.split);
+    // neighbouring tiles share their rows of w (and, 16 token tiles further, of x): both stay in L2
+    auto place = [&](int tile, int& n0, int& m0) {
+        const int group = tile / (16 * p.tiles_n), in = tile - group * 16 * p.tiles_n;
+        const int width = min(16, p.tiles_m - group * 16);
+        m0 = (group * 16 + in % width) * BN;
+        n0 = in / width * 128;
+    };
+
+    if (warp == 0) {
+        if (lane == 0) {
+            int it = 0;
+            bool ok = true;
+            for (int tile = first; tile < tiles && ok; tile += step) {
+                int n0, m0;
+                place(tile, n0, m0);
+                for (int kb = kb0; kb < kb1; ++kb, ++it) {
+                    const int s = it % T::kStages;
+                    if (it >= T::kStages && !(ok = sm::bar_wait(empty(s), uint32_t(it / T::kStages - 1) & 1u, abort_word, p.status))) break;
+                    const uint32_t at = stage0 + s * T::kStageBytes;
+                    sm::bar_expect(full(s), T::kStageBytes);
+                    sm::tma_load_2d(at, &map_w, full(s), kb * kLinK, n0);
+                    if (GATED) sm::tma_load_2d(at + T::kABytes, &map_w, full(s), kb * kLinK, p.n + n0);
+                    sm::tma_load_2d(at + T::kAccs * T::kABytes, &map_x, full(s), kb * kLinK, m0);
+                }
+            }
+            if (*abort_word)   // the copies in flight land before the CTA gives its shared memory back
+                for (int i = max(0, it - T::kStages); i < it; ++i) sm::bar_drain(full(i % T::kStages), uint32_t(i / T::kStages) & 1u);
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        if (lane == 0) {
+            constexpr uint32_t idesc = sm::mma_idesc(128, BN);
+            int it = 0, n = 0;
+            bool ok = true;
+            for (int tile = first; tile < tiles && ok; tile += step, ++n) {
+                const int buf = n & 1;
+                if (n >= 2 && !(ok = sm::bar_wait(acc_empty(buf), uint32_t(n / 2 - 1) & 1u, abort_word, p.status))) break;
+                sm::tc_fence_after();
+                const uint32_t d = tmem + buf * T::kBufCols;
+                for (int kb = kb0; kb < kb1; ++kb, ++it) {
+                    const int s = it % T::kStages;
+                    if (!(ok = sm::bar_wait(full(s), uint32_t(it / T::kStages) & 1u, abort_word, p.status))) break;
+                    sm::tc_fence_after();
+                    const uint32_t at = stage0 + s * T::kStageBytes;
+                    const uint64_t a = sm::desc_k_sw128(at), b = sm::desc_k_sw128(at + T::kAccs * T::kABytes);
+#pragma unroll
+                    for (int kk = 0; kk < kLinK / 16; ++kk) {   // (32 bytes along the row: 2 in the descriptor's units)
+                        sm::mma_ss(d, a + 2 * kk, b + 2 * kk, idesc, kb > kb0 || kk > 0);
+                        if (GATED) sm::mma_ss(d + BN, a + (T::kABytes >> 4) + 2 * kk, b + 2 * kk, idesc, kb > kb0 || kk > 0);
+                    }
+                    sm::mma_commit(empty(s));
+                }
+                if (ok) sm::mma_commit(acc_full(buf));
+            }
+            if (*abort_word) { sm::mma_commit(drained); sm::bar_drain(drained, 0); }
+        }
+        __syncwarp();
+    } else {
+        const int quarter = warp & 3, row = quarter * 32 + lane;
+        const uint32_t lanes = uint32_t(quarter * 32) << 16;
+        constexpr int kChunk = BN < 32 ? 16 : 32;
+        int n = 0;
+        for (int tile = first; tile < tiles; tile += step, ++n) {
+            int n0, m0;
+            place(tile, n0, m0);
+            const int buf = n & 1, j = n0 + row;
+            const bool live = j < p.n;
+            const float bias = p.bias && live ? __bfloat162float(p.bias[j]) : 0.f;
+            const float bias_up = GATED && p.bias && live ? __bfloat162float(p.bias[p.n + j]) : 0.f;
+            if (!sm::bar_wait(acc_full(buf), uint32_t(n / 2) & 1u, abort_word, p.status)) break;
+            sm::tc_fence_after();
+            const uint32_t acc = tmem + buf * T::kBufCols + lanes;
+            if (p.split > 1) {
+                // partial sums to this CTA's stages (free: every product has read them): [column][feature]
+                for (int c = 0; c < T::kBufCols; c += 16) {
+                    uint32_t v[16];
+                    sm::tmem_ld16(acc + c, v);
+                    sm::tmem_wait_ld(v);
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        asm volatile("st.shared.b32 [%0], %1;" ::"r"(stage0 + uint32_t(((c + i) * 128 + row) * 4)), "r"(v[i]) : "memory");
+                }
+                break;
+            }
+            const int columns = min(BN, p.rows - m0);
+#pragma unroll 1
+            for (int c = 0; c < columns; c += kChunk) {
+                uint32_t v[kChunk], u[kChunk];
+                if constexpr (kChunk == 32) {
+                    sm::tmem_ld32(acc + c, v);
+                    if constexpr (GATED) sm::tmem_ld32(acc + BN + c, u);
+                } else {
+                    sm::tmem_ld16(acc + c, v);
+                    if constexpr (GATED) sm::tmem_ld16(acc + BN + c, u);
+                }
+                float res[kChunk];
+#pragma unroll
+                for (int i = 0; i < kChunk; ++i) res[i] = p.residual && live && c + i < columns ? linear_residual(p, m0 + c + i, j) : 0.f;
+                sm::tmem_wait_ld(v);
+                if constexpr (GATED) sm::tmem_wait_ld(u);
+                if (live)
+#pragma unroll
+                    for (int i = 0; i < kChunk; ++i)
+                        if (c + i < columns)
+                            linear_store(p, m0 + c + i, j,
+                                         linear_act(p.act, __uint_as_float(v[i]) + bias,
+                                                    GATED ? __uint_as_float(u[i]) + bias_up : 0.f) + res[i]);
+            }
+            sm::tc_fence_before();
+            sm::bar_arrive(acc_empty(buf));
+        }
+    }
+    if (p.split > 1) {
+        // the tile's columns are shared out over the cluster; each is summed over the CTAs in rank order
+        __syncwarp();
+        sm::cluster_sync();
+        if (warp >= 2 && !*abort_word) {
+            int n0, m0;
+            place(first, n0, m0);
+            const int row = (warp & 3) * 32 + lane, j = n0 + row, columns = min(BN, p.rows - m0);
+            if (j < p.n) {
+                const float bias = p.bias ? __bfloat162float(p.bias[j]) : 0.f;
+                const float bias_up = GATED && p.bias ? __bfloat162float(p.bias[p.n + j]) : 0.f;
+                for (int c = rank; c < columns; c += p.split) {
+                    const float res = p.residual ? linear_residual(p, m0 + c, j) : 0.f;
+                    float y = 0.f, u = 0.f;
+                    for (int s = 0; s < p.split; ++s) {
+                        y += sm::cluster_ld(stage0 + uint32_t((c * 128 + row) * 4), s);
+                        if (GATED) u += sm::cluster_ld(stage0 + uint32_t(((BN + c) * 128 + row) * 4), s);
+                    }
+                    linear_store(p, m0 + c, j, linear_act(p.act, y + bias, u + bias_up) + res);
+                }
+            }
+        }
+        __syncwarp();
+        sm::cluster_sync();   // no CTA leaves while a peer reads its partial sums
+    }
+    sm::tc_fence_before();
+    __syncthreads();
+    sm::tc_fence_after();
+    if (warp == 1) sm::tmem_free(tmem, T::kCols);
+}
+
+template <int BN, bool GATED>
+static mk_status linear_launch(const mk_linear_args* a, LinearParams& p, int device, int sms, cudaStream_t stream) {
+    using T = LinearTile<BN, GATED>;
+    static std::atomic<uint64_t> set{0};
+    const void* fn = reinterpret_cast<const void*>(&linear_kernel<BN, GATED>);
+    mk_status st = op_smem(fn, T::kSmem, device, &set);
+    if (st != MK_OK) return st;
+    CUtensorMap map_w, map_x;
+    const int64_t wr = int64_t(p.n) * T::kAccs, xs = p.rows == 1 ? p.k : a->x_stride;
+    const cuuint64_t wd[2] = {cuuint64_t(p.k), cuuint64_t(wr)}, ws[1] = {cuuint64_t(p.k) * 2};
+    const cuuint64_t xd[2] = {cuuint64_t(p.k), cuuint64_t(p.rows)}, xst[1] = {cuuint64_t(xs) * 2};
+    const cuuint32_t wb[2] = {kLinK, 128}, xb[2] = {kLinK, BN};
+    if ((st = op_tensor_map(&map_w, a->w, 2, wd, ws, wb)) != MK_OK) return st;
+    if ((st = op_tensor_map(&map_x, a->x, 2, xd, xst, xb)) != MK_OK) return st;
+    p.tiles_n = (p.n + 127) / 128;
+    p.tiles_m = (p.rows + BN - 1) / BN;
+    const int64_t tiles = int64_t(p.tiles_n) * p.tiles_m;
+    if (tiles > (1 << 30)) return fail(MK_ERR_ARG, "linear: %lld tiles", static_cast<long long>(tiles));
+    // fewer tiles than SMs: the contraction is cut over a cluster (2, 4 or 8 CTAs, at least two
+    // blocks of it each), as far as the SMs go
+    const int blocks = (p.k + kLinK - 1) / kLinK;
+    p.split = 1;
+    while (p.split < 8 && tiles * p.split * 2 <= sms && blocks >= p.split * 4) p.split *= 2;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(unsigned(p.split > 1 ? tiles * p.split : (tiles < sms ? tiles : sms)));
+    cfg.blockDim = dim3(192);
+    cfg.dynamicSmemBytes = T::kSmem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = unsigned(p.split);
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    MK_CK(cudaLaunchKernelEx(&cfg, &linear_kernel<BN, GATED>, map_w, map_x, p));
+    return MK_OK;
 }
 
 static mk_status linear_check(const mk_linear_args* a) {
@@ -105,9 +317,6 @@ extern "C" mk_status mk_linear(const mk_linear_args* a, void* stream) {
     if (st != MK_OK || a->rows == 0) return st;
     LinearParams p{};
     p.rows = a->rows; p.n = a->n; p.k = a->k; p.act = a->activation;
-    p.x = static_cast<const __nv_bfloat16*>(a->x);
-    p.x_stride = a->rows == 1 ? a->k : a->x_stride;
-    p.w = static_cast<const __nv_bfloat16*>(a->w);
     p.bias = static_cast<const __nv_bfloat16*>(a->bias);
     p.residual = a->residual;
     p.residual_stride = a->residual_stride;
@@ -115,7 +324,20 @@ extern "C" mk_status mk_linear(const mk_linear_args* a, void* stream) {
     p.out_f32 = a->out_dtype == MK_F32;
     p.out = a->out;
     p.out_stride = a->out_stride;
-    linear_simple_kernel<<<dim3((a->n + 15) / 16, (a->rows + 15) / 16), 256, 0, static_cast<cudaStream_t>(stream)>>>(p);
-    MK_CK(cudaGetLastError());
-    return MK_OK;
+    p.status = a->status;
+    int device = 0, sms = 0;
+    const mk_status ds = op_device(&device, &sms);
+    if (ds != MK_OK) return ds;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (a->activation == MK_ACT_SWIGLU) {
+        if (p.rows <= 16) return linear_launch<16, true>(a, p, device, sms, s);
+        if (p.rows <= 32) return linear_launch<32, true>(a, p, device, sms, s);
+        if (p.rows <= 64) return linear_launch<64, true>(a, p, device, sms, s);
+        return linear_launch<128, true>(a, p, device, sms, s);
+    }
+    if (p.rows <= 16) return linear_launch<16, false>(a, p, device, sms, s);
+    if (p.rows <= 32) return linear_launch<32, false>(a, p, device, sms, s);
+    if (p.rows <= 64) return linear_launch<64, false>(a, p, device, sms, s);
+    if (p.rows <= 128) return linear_launch<128, false>(a, p, device, sms, s);
+    return linear_launch<256, false>(a, p, device, sms, s);
 }
