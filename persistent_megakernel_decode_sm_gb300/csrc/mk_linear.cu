@@ -2,6 +2,8 @@
 #include "mk_ops.h"
 #include "mk_sm103.cuh"
 
+#include <type_traits>
+
 namespace mk {
 
 struct LinearParams {
@@ -34,6 +36,36 @@ __device__ __forceinline__ void linear_store(const LinearParams& p, int r, int j
     const int64_t at = r * p.out_stride + j;
     if (p.out_f32) static_cast<float*>(p.out)[at] = y;
     else static_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16_rn(y);
+}
+
+// The residuals of 8 tokens r, r + 1, .. of feature j, and their outputs; `left` of them exist
+__device__ __forceinline__ void linear_residuals(const LinearParams& p, int r, int j, int left, float (&res)[8]) {
+    const int64_t at = r * p.residual_stride + j;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) res[i] = 0.f;
+    if (!p.residual) return;
+    if (p.residual_f32) {
+        const float* src = static_cast<const float*>(p.residual) + at;
+#pragma unroll
+        for (int i = 0; i < 8; ++i, src += p.residual_stride)
+            if (i < left) res[i] = *src;
+    } else {
+        const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(p.residual) + at;
+#pragma unroll
+        for (int i = 0; i < 8; ++i, src += p.residual_stride)
+            if (i < left) res[i] = __bfloat162float(*src);
+    }
+}
+template <bool F32>
+__device__ __forceinline__ void linear_stores(const LinearParams& p, int r, int j, int left, const float (&y)[8]) {
+    using Out = std::conditional_t<F32, float, __nv_bfloat16>;
+    Out* dst = static_cast<Out*>(p.out) + (r * p.out_stride + j);
+#pragma unroll
+    for (int i = 0; i < 8; ++i, dst += p.out_stride)
+        if (i < left) {
+            if constexpr (F32) *dst = y[i];
+            else *dst = __float2bfloat16_rn(y[i]);
+        }
 }
 
 // A tile is 128 output features (the MMA's M: rows of w, one per tensor-memory lane) by BN tokens
@@ -222,8 +254,8 @@ linear_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
                     const float res = p.residual ? linear_residual(p, m0 + c, j) : 0.f;
                     float y = 0.f, u = 0.f;
                     for (int s = 0; s < p.split; ++s) {
-                        y += sm::cluster_ld(stage0 + uint32_t((c * 128 + row) * 4), s);
-                        if (GATED) u += sm::cluster_ld(stage0 + uint32_t(((BN + c) * 128 + row) * 4), s);
+                        y += sm::cluster_ld(sm::cluster_addr(stage0 + uint32_t((c * 128 + row) * 4), s));
+                        if (GATED) u += sm::cluster_ld(sm::cluster_addr(stage0 + uint32_t(((BN + c) * 128 + row) * 4), s));
                     }
                     linear_store(p, m0 + c, j, linear_act(p.act, y + bias, u + bias_up) + res);
                 }
@@ -236,6 +268,260 @@ linear_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
     __syncthreads();
     sm::tc_fence_after();
     if (warp == 1) sm::tmem_free(tmem, T::kCols);
+}
+
+// ---- many tokens: CTA pairs ------------------------------------------------------------------
+// A pair of CTAs makes a tile of 256 rows of w by 256 tokens: each CTA stages its 128 rows of w and 128
+// of the tokens, 32 KB for 512 cycles of products.  What limits a CTA by itself is shared
+// memory (128 bytes a cycle for the tiles written and the operands read): 128 x 256 moves 96 + 96
+// bytes a cycle at the full product rate, the pair 64 + 64.  SwiGLU puts 64 gate rows and the same
+// 64 features' up rows into a CTA's 128; their accumulators sit 64 lanes apart and meet in the epilogue
+// through shared memory.
+//
+// The tensor core truncates as it accumulates, an error that grows with the length of the sum
+// (measured at k = 8192 with an fp32 output: 1.5e-6 of its norm, against 7e-7 for plain fp32 sums).  fp32
+// outputs are therefore summed in pieces of kPromote blocks that the epilogue warps add up in registers; a
+// bf16 output rounds a thousand times coarser and takes the whole contraction in one piece.
+constexpr int kPromote = 8;
+template <bool GATED>
+struct PairTile {
+    static constexpr int kRows = GATED ? 64 : 128;          // features of one CTA
+    static constexpr int kHalfBytes = 128 * kLinK * 2;      // a CTA's part of w, and of the tokens
+    static constexpr int kStageBytes = 2 * kHalfBytes;
+    static constexpr int kStages = 6;
+    static constexpr int kExchange = GATED ? 2 * 2 * 8 * 128 * 4 : 0;   // [buffer][column half][8][128] fp32
+    static constexpr int kSmem = kStages * kStageBytes + kExchange + 1024;
+    static_assert(kStages * kStageBytes >= 128 * 256 * 4);  // a split tile's partial sums are staged there
+};
+
+// Warp 0: TMA producer.  Warp 1: tensor memory, MMA issue (even CTA).  Warps 2-9: epilogue, each 32 lanes
+// by 128 of the 256 columns, held in registers.
+template <bool GATED, bool F32>
+__global__ void __launch_bounds__(320, 1)
+linear_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x,
+                   const __grid_constant__ LinearParams p) {
+    using T = PairTile<GATED>;
+    extern __shared__ uint8_t raw[];
+    __shared__ uint64_t bars[2 * T::kStages + 4];
+    __shared__ uint32_t tmem_at;
+    __shared__ int abort_flag;
+    volatile int* abort_word = &abort_flag;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t stage0 = (sm::smem(raw) + 1023u) & ~1023u;
+    const uint32_t bar0 = sm::smem(bars);
+    auto full = [&](int s) { return bar0 + 8u * s; };
+    auto empty = [&](int s) { return bar0 + 8u * (T::kStages + s); };
+    auto acc_full = [&](int s) { return bar0 + 8u * (2 * T::kStages + s); };
+    auto acc_empty = [&](int s) { return bar0 + 8u * (2 * T::kStages + 2 + s); };
+    const int rank = int(sm::cluster_rank()), half = rank & 1, part = rank >> 1;
+    const uint32_t leader = uint32_t(rank & ~1);
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < T::kStages; ++s) { sm::bar_init(full(s), 1); sm::bar_init(empty(s), 1); }
+        for (int s = 0; s < 2; ++s) { sm::bar_init(acc_full(s), 1); sm::bar_init(acc_empty(s), 16); }
+        abort_flag = 0;
+        sm::bar_fence_init();
+        sm::tma_prefetch_map(&map_w);
+        sm::tma_prefetch_map(&map_x);
+    }
+    if (warp == 1) sm::tmem_alloc_pair(sm::smem(&tmem_at), 512);
+    sm::tc_fence_before();
+    __syncthreads();
+    sm::cluster_sync();   // both CTAs' barriers and tensor memory are there
+    sm::tc_fence_after();
+    const uint32_t tmem = tmem_at;
+
+    const int cluster = 2 * p.split;
+    const int first = int(blockIdx.x) / cluster, step = int(gridDim.x) / cluster;
+    const int tiles = p.tiles_n * p.tiles_m;
+    const int blocks = (p.k + kLinK - 1) / kLinK;
+    const int kb0 = int(int64_t(blocks) * part / p.split), kb1 = int(int64_t(blocks) * (part + 1) / p.split);
+    const int piece = F32 ? kPromote : kb1 - kb0;   // blocks summed in tensor memory at a time
+    auto place = [&](int tile, int& n0, int& m0) {
+        const int group = tile / (8 * p.tiles_n), in = tile - group * 8 * p.tiles_n;
+        const int width = min(8, p.tiles_m - group * 8);
+        m0 = (group * 8 + in % width) * 256;
+        n0 = in / width * (2 * T::kRows) + half * T::kRows;
+    };
+
+    if (warp == 0) {
+        if (lane == 0) {
+            int it = 0;
+            bool ok = true;
+            for (int tile = first; tile < tiles && ok; tile += step) {
+                int n0, m0;
+                place(tile, n0, m0);
+                for (int kb = kb0; kb < kb1; ++kb, ++it) {
+                    const int s = it % T::kStages;
+                    if (it >= T::kStages && !(ok = sm::bar_wait(empty(s), uint32_t(it / T::kStages - 1) & 1u, abort_word, p.status))) break;
+                    const uint32_t at = stage0 + s * T::kStageBytes;
+                    if (half == 0) sm::bar_expect(full(s), 2 * T::kStageBytes);   // both CTAs' copies
+                    const uint32_t bar = sm::cluster_addr(full(s), leader);
+                    sm::tma_load_2d_pair(at, &map_w, bar, kb * kLinK, n0);
+                    if (GATED) sm::tma_load_2d_pair(at + T::kHalfBytes / 2, &map_w, bar, kb * kLinK, p.n + n0);
+                    sm::tma_load_2d_pair(at + T::kHalfBytes, &map_x, bar, kb * kLinK, m0 + half * 128);
+                }
+            }
+            // the products' last arrivals on this CTA's barriers come before it leaves
+            for (int i = max(0, it - T::kStages); i < it && ok; ++i)
+                ok = sm::bar_wait(empty(i % T::kStages), uint32_t(i / T::kStages) & 1u, abort_word, p.status);
+            if (*abort_word) {   // the copies in flight land (microseconds) before the CTA leaves
+                const uint64_t t0 = sm::timer_ns();
+                while (sm::timer_ns() - t0 < 10000000ull) {}
+            }
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        if (lane == 0 && half == 0) {
+            constexpr uint32_t idesc = sm::mma_idesc(256, 256);
+            const uint16_t both = uint16_t(3u << leader);
+            int it = 0, n = 0;
+            bool ok = true;
+            for (int tile = first; tile < tiles && ok; tile += step)
+                for (int k0 = kb0; k0 < kb1 && ok; k0 += piece, ++n) {
+                    const int buf = n & 1;
+                    if (n >= 2 && !(ok = sm::bar_wait(acc_empty(buf), uint32_t(n / 2 - 1) & 1u, abort_word, p.status))) break;
+                    sm::tc_fence_after();
+                    const uint32_t d = tmem + buf * 256;
+                    const int k1 = min(k0 + piece, kb1);
+                    for (int kb = k0; kb < k1; ++kb, ++it) {
+                        const int s = it % T::kStages;
+                        if (!(ok = sm::bar_wait(full(s), uint32_t(it / T::kStages) & 1u, abort_word, p.status))) break;
+                        sm::tc_fence_after();
+                        const uint32_t at = stage0 + s * T::kStageBytes;
+                        const uint64_t a = sm::desc_k_sw128(at), b = sm::desc_k_sw128(at + T::kHalfBytes);
+#pragma unroll
+                        for (int kk = 0; kk < kLinK / 16; ++kk)
+                            sm::mma_ss_pair(d, a + 2 * kk, b + 2 * kk, idesc, kb > k0 || kk > 0);
+                        sm::mma_commit_pair(empty(s), both);
+                    }
+                    if (ok) sm::mma_commit_pair(acc_full(buf), both);
+                }
+            if (*abort_word) {   // products in flight end before the tensor memory is freed
+                const uint64_t t0 = sm::timer_ns();
+                while (sm::timer_ns() - t0 < 10000000ull) {}
+            }
+        }
+        __syncwarp();
+    } else {
+        const int quarter = warp & 3, row = quarter * 32 + lane, cols = (warp - 2) / 4 * 128;
+        const uint32_t lanes = uint32_t(quarter * 32) << 16;
+        const bool up_row = GATED && row >= 64;
+        float v[128];   // the thread's row of the tile, its 128 columns
+        int n = 0;
+        bool ok = true;
+        for (int tile = first; tile < tiles && ok; tile += step) {
+            int n0, m0;
+            place(tile, n0, m0);
+            if (F32)
+#pragma unroll
+                for (int i = 0; i < 128; ++i) v[i] = 0.f;
+#pragma unroll 1
+            for (int k0 = kb0; k0 < kb1; k0 += piece, ++n) {
+                const int buf = n & 1;
+                if (!(ok = sm::bar_wait(acc_full(buf), uint32_t(n / 2) & 1u, abort_word, p.status))) break;
+                sm::tc_fence_after();
+                const uint32_t acc = tmem + buf * 256 + cols + lanes;
+#pragma unroll
+                for (int c = 0; c < 128; c += 16) {
+                    uint32_t t[16];
+                    sm::tmem_ld16(acc + c, t);
+                    sm::tmem_wait_ld(t);
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        if (F32) v[c + i] += __uint_as_float(t[i]);
+                        else v[c + i] = __uint_as_float(t[i]);
+                    }
+                }
+                sm::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) sm::bar_arrive_cluster(sm::cluster_addr(acc_empty(buf), leader));
+            }
+            if (!ok) break;
+            if (p.split > 1) {   // partial sums to this CTA's stages (every product has read them): [column][row]
+#pragma unroll
+                for (int i = 0; i < 128; ++i)
+                    asm volatile("st.shared.f32 [%0], %1;" ::"r"(stage0 + uint32_t(((cols + i) * 128 + row) * 4)), "f"(v[i]) : "memory");
+                break;
+            }
+            const int j = n0 + (GATED ? row & 63 : row);
+            const bool live = j < p.n;
+            const int jb = up_row ? p.n + j : j;   // (bias rows: gate rows, then up rows)
+            const float bias = p.bias && live ? __bfloat162float(p.bias[jb]) : 0.f;
+            // 8 columns a step.  SwiGLU: 16 columns, of which the gate row keeps 0-7 and receives their up
+            // values from its up row, which keeps 8-15 and receives their gate values; two buffers take turns
+            constexpr int kStep = GATED ? 16 : 8;
+#pragma unroll
+            for (int c = 0; c < 128; c += kStep) {
+                const int m = m0 + cols + c + (up_row ? 8 : 0), left = live ? p.rows - m : 0;
+                if (m0 + cols + c >= p.rows) break;   // (the same for both warps of an exchange: they share cols)
+                float y[8], res[8];
+                linear_residuals(p, m, j, left, res);
+                if constexpr (GATED) {
+                    const uint32_t at = stage0 + T::kStages * T::kStageBytes + uint32_t(((c / 16 & 1) * 2 + cols / 128) * (8 * 128 * 4));
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        asm volatile("st.shared.f32 [%0], %1;" ::"r"(at + uint32_t((i * 128 + row) * 4)),
+                                     "f"((up_row ? v[c + i] : v[c + 8 + i]) + bias) : "memory");
+                    asm volatile("bar.sync %0, 64;" ::"r"(1 + cols / 128 * 2 + (quarter & 1)) : "memory");
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        float got;
+                        asm volatile("ld.shared.f32 %0, [%1];" : "=f"(got) : "r"(at + uint32_t((i * 128 + (row ^ 64)) * 4)) : "memory");
+                        const float own = (up_row ? v[c + 8 + i] : v[c + i]) + bias;
+                        y[i] = linear_act(MK_ACT_SWIGLU, up_row ? got : own, up_row ? own : got) + res[i];
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) y[i] = linear_act(p.act, v[c + i] + bias, 0.f) + res[i];
+                }
+                linear_stores<F32>(p, m, j, left, y);
+            }
+        }
+    }
+    if (p.split > 1) {
+        // the tile's columns are shared out over the pairs; each is summed in order of the contraction
+        __syncwarp();
+        sm::cluster_sync();
+        if (warp >= 2 && !*abort_word) {
+            int n0, m0;
+            place(first, n0, m0);
+            const int t = threadIdx.x - 64, row = t % T::kRows, j = n0 + row;
+            constexpr int kGroups = 256 / T::kRows;
+            const int width = 256 / p.split, c1 = min(width * (part + 1), p.rows - m0);
+            if (j < p.n) {
+                const float bias = p.bias ? __bfloat162float(p.bias[j]) : 0.f;
+                const float bias_up = GATED && p.bias ? __bfloat162float(p.bias[p.n + j]) : 0.f;
+                for (int c = width * part + t / T::kRows; c < c1; c += 8 * kGroups) {
+                    float y[8], u[8], res[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const int m = m0 + c + i * kGroups;
+                        y[i] = u[i] = 0.f;
+                        res[i] = p.residual && c + i * kGroups < c1 ? linear_residual(p, m, j) : 0.f;
+                    }
+                    for (int s = 0; s < p.split; ++s) {
+                        const uint32_t peer = sm::cluster_addr(stage0, uint32_t(2 * s + half));
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const uint32_t at = peer + uint32_t((min(c + i * kGroups, 255) * 128 + row) * 4);
+                            y[i] += sm::cluster_ld(at);
+                            if (GATED) u[i] += sm::cluster_ld(at + 64 * 4);
+                        }
+                    }
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        if (c + i * kGroups < c1)
+                            linear_store(p, m0 + c + i * kGroups, j, linear_act(p.act, y[i] + bias, u[i] + bias_up) + res[i]);
+                }
+            }
+        }
+        __syncwarp();
+    }
+    sm::tc_fence_before();
+    __syncthreads();
+    sm::cluster_sync();   // no CTA leaves while a peer may still reach its shared memory
+    sm::tc_fence_after();
+    if (warp == 1) sm::tmem_free_pair(tmem, 512);
 }
 
 template <int BN, bool GATED>
@@ -273,6 +559,54 @@ static mk_status linear_launch(const mk_linear_args* a, LinearParams& p, int dev
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     MK_CK(cudaLaunchKernelEx(&cfg, &linear_kernel<BN, GATED>, map_w, map_x, p));
+    return MK_OK;
+}
+
+template <bool GATED, bool F32>
+static mk_status linear_launch_pair(const mk_linear_args* a, LinearParams& p, int device, int sms, cudaStream_t stream) {
+    using T = PairTile<GATED>;
+    static std::atomic<uint64_t> set{0};
+    static std::atomic<int> resident[64];   // clusters of 2 that run at once, per device
+    const void* fn = reinterpret_cast<const void*>(&linear_pair_kernel<GATED, F32>);
+    mk_status st = op_smem(fn, T::kSmem, device, &set);
+    if (st != MK_OK) return st;
+    CUtensorMap map_w, map_x;
+    const int64_t wr = int64_t(p.n) * (GATED ? 2 : 1);
+    const cuuint64_t wd[2] = {cuuint64_t(p.k), cuuint64_t(wr)}, ws[1] = {cuuint64_t(p.k) * 2};
+    const cuuint64_t xd[2] = {cuuint64_t(p.k), cuuint64_t(p.rows)}, xst[1] = {cuuint64_t(a->x_stride) * 2};
+    const cuuint32_t wb[2] = {kLinK, T::kRows}, xb[2] = {kLinK, 128};
+    if ((st = op_tensor_map(&map_w, a->w, 2, wd, ws, wb)) != MK_OK) return st;
+    if ((st = op_tensor_map(&map_x, a->x, 2, xd, xst, xb)) != MK_OK) return st;
+    p.tiles_n = (p.n + 2 * T::kRows - 1) / (2 * T::kRows);
+    p.tiles_m = (p.rows + 255) / 256;
+    const int64_t tiles = int64_t(p.tiles_n) * p.tiles_m;
+    if (tiles > (1 << 28)) return fail(MK_ERR_ARG, "linear: %lld tiles", static_cast<long long>(tiles));
+    const int blocks = (p.k + kLinK - 1) / kLinK;
+    p.split = 1;
+    while (p.split < 4 && tiles * p.split * 4 <= sms && blocks >= p.split * 4) p.split *= 2;
+    cudaLaunchConfig_t cfg{};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = unsigned(2 * p.split);
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.gridDim = dim3(unsigned(2 * p.split));
+    cfg.blockDim = dim3(320);
+    cfg.dynamicSmemBytes = T::kSmem;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int64_t clusters = tiles;
+    if (p.split == 1) {   // a persistent grid of the pairs that fit the device at once
+        int fit = resident[device].load();
+        if (!fit) {
+            MK_CK(cudaOccupancyMaxActiveClusters(&fit, fn, &cfg));
+            if (fit < 1) return fail(MK_ERR_RESOURCES, "linear: a pair of CTAs cannot be resident");
+            resident[device].store(fit);
+        }
+        clusters = tiles < fit ? tiles : fit;
+    }
+    cfg.gridDim = dim3(unsigned(2 * p.split * clusters));
+    MK_CK(cudaLaunchKernelEx(&cfg, &linear_pair_kernel<GATED, F32>, map_w, map_x, p));
     return MK_OK;
 }
 
@@ -333,11 +667,12 @@ extern "C" mk_status mk_linear(const mk_linear_args* a, void* stream) {
         if (p.rows <= 16) return linear_launch<16, true>(a, p, device, sms, s);
         if (p.rows <= 32) return linear_launch<32, true>(a, p, device, sms, s);
         if (p.rows <= 64) return linear_launch<64, true>(a, p, device, sms, s);
-        return linear_launch<128, true>(a, p, device, sms, s);
+        if (p.rows <= 128) return linear_launch<128, true>(a, p, device, sms, s);
+        return p.out_f32 ? linear_launch_pair<true, true>(a, p, device, sms, s) : linear_launch_pair<true, false>(a, p, device, sms, s);
     }
     if (p.rows <= 16) return linear_launch<16, false>(a, p, device, sms, s);
     if (p.rows <= 32) return linear_launch<32, false>(a, p, device, sms, s);
     if (p.rows <= 64) return linear_launch<64, false>(a, p, device, sms, s);
     if (p.rows <= 128) return linear_launch<128, false>(a, p, device, sms, s);
-    return linear_launch<256, false>(a, p, device, sms, s);
+    return p.out_f32 ? linear_launch_pair<false, true>(a, p, device, sms, s) : linear_launch_pair<false, false>(a, p, device, sms, s);
 }
