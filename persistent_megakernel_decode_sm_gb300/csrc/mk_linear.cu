@@ -27,45 +27,67 @@ __device__ __forceinline__ float linear_act(int act, float y, float up) {
         default: return y;
     }
 }
-__device__ __forceinline__ float linear_residual(const LinearParams& p, int r, int j) {
-    const int64_t at = r * p.residual_stride + j;
-    return p.residual_f32 ? static_cast<const float*>(p.residual)[at]
-                          : __bfloat162float(static_cast<const __nv_bfloat16*>(p.residual)[at]);
-}
-__device__ __forceinline__ void linear_store(const LinearParams& p, int r, int j, float y) {
-    const int64_t at = r * p.out_stride + j;
-    if (p.out_f32) static_cast<float*>(p.out)[at] = y;
-    else static_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16_rn(y);
-}
-
-// The residuals of 8 tokens r, r + 1, .. of feature j, and their outputs; `left` of them exist
-__device__ __forceinline__ void linear_residuals(const LinearParams& p, int r, int j, int left, float (&res)[8]) {
-    const int64_t at = r * p.residual_stride + j;
+// The residuals of the tokens r, r + 1, .. of feature j, of which `left` exist (zeros where not wanted)
+template <int N>
+__device__ __forceinline__ void linear_residuals(const LinearParams& p, bool wanted, int r, int j, int left, float (&res)[N], int step = 1) {
+    const int64_t at = r * p.residual_stride + j, by = p.residual_stride * step;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) res[i] = 0.f;
-    if (!p.residual) return;
+    for (int i = 0; i < N; ++i) res[i] = 0.f;
+    if (!p.residual || !wanted) return;
     if (p.residual_f32) {
         const float* src = static_cast<const float*>(p.residual) + at;
 #pragma unroll
-        for (int i = 0; i < 8; ++i, src += p.residual_stride)
-            if (i < left) res[i] = *src;
+        for (int i = 0; i < N; ++i, src += by)
+            if (i * step < left) res[i] = *src;
     } else {
         const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(p.residual) + at;
 #pragma unroll
-        for (int i = 0; i < 8; ++i, src += p.residual_stride)
-            if (i < left) res[i] = __bfloat162float(*src);
+        for (int i = 0; i < N; ++i, src += by)
+            if (i * step < left) res[i] = __bfloat162float(*src);
     }
 }
+// What the sums of a thread's columns start from: the bias and, where no activation comes between,
+// the residual (in one of the CTAs that share the contraction)
+template <int N>
+__device__ __forceinline__ void linear_begin(const LinearParams& p, int r, int j, int left, bool mine, bool plain, float bias, float (&v)[N]) {
+    linear_residuals<N>(p, mine && plain, r, j, left, v);
+    if (mine)
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] += bias;
+}
 template <bool F32>
-__device__ __forceinline__ void linear_stores(const LinearParams& p, int r, int j, int left, const float (&y)[8]) {
+__device__ __forceinline__ void linear_stores(const LinearParams& p, int r, int j, int left, const float (&y)[8], int step = 1) {
     using Out = std::conditional_t<F32, float, __nv_bfloat16>;
     Out* dst = static_cast<Out*>(p.out) + (r * p.out_stride + j);
+    const int64_t by = p.out_stride * step;
 #pragma unroll
-    for (int i = 0; i < 8; ++i, dst += p.out_stride)
-        if (i < left) {
+    for (int i = 0; i < 8; ++i, dst += by)
+        if (i * step < left) {
             if constexpr (F32) *dst = y[i];
             else *dst = __float2bfloat16_rn(y[i]);
         }
+}
+// 8 columns c, c + STEP, .. (below c1) of a split tile: the partial sums of `split` CTAs (ranks
+// by * s + at), staged as [column][128 rows], added in order; the up sums lie `up_bytes` further
+template <int STEP, bool GATED, bool F32>
+__device__ __forceinline__ void linear_join(const LinearParams& p, uint32_t stage0, uint32_t up_bytes, int split, int by, int at,
+                                            int m0, int c, int c1, int row, int j) {
+    float y[8], u[8], res[8];
+    linear_residuals<8>(p, GATED || p.act != MK_ACT_NONE, m0 + c, j, c1 - c, res, STEP);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) y[i] = u[i] = 0.f;
+    for (int s = 0; s < split; ++s) {
+        const uint32_t peer = sm::cluster_addr(stage0, uint32_t(by * s + at));
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {   // (a column past c1 reads one below it: every address is inside the stages)
+            const uint32_t src = peer + uint32_t((min(c + i * STEP, c1 - 1) * 128 + row) * 4);
+            y[i] += sm::cluster_ld(src);
+            if (GATED) u[i] += sm::cluster_ld(src + up_bytes);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) y[i] = linear_act(GATED ? MK_ACT_SWIGLU : p.act, y[i], u[i]) + res[i];
+    linear_stores<F32>(p, m0 + c, j, c1 - c, y, STEP);
 }
 
 // A tile is 128 output features (the MMA's M: rows of w, one per tensor-memory lane) by BN tokens
@@ -73,7 +95,13 @@ __device__ __forceinline__ void linear_stores(const LinearParams& p, int r, int 
 // and a warp's store of one column is 32 neighbouring outputs of a token's row.  SwiGLU holds the
 // gate rows and the up rows of the same features as two accumulators, multiplied in the epilogue.
 // The contraction runs in blocks of 64 through a ring of shared-memory stages.
+//
+// The tensor core truncates as it accumulates, an error that grows with the length of the sum
+// (measured at k = 8192 with an fp32 output: 1.5e-6 of its norm, against 7e-7 for plain fp32 sums).  fp32
+// outputs are therefore summed in pieces of kPromote blocks that the epilogue warps add up in registers
+// (3.4e-7); a bf16 output rounds a thousand times coarser and takes the whole contraction in one piece.
 constexpr int kLinK = 64;
+constexpr int kPromote = 8;
 template <int BN, bool GATED>
 struct LinearTile {
     static constexpr int kAccs = GATED ? 2 : 1;
@@ -83,13 +111,15 @@ struct LinearTile {
     static constexpr int kBufCols = BN * kAccs;                    // columns of one tile's accumulators
     static constexpr int kCols = 2 * kBufCols < 32 ? 32 : 2 * kBufCols;   // two tiles: one is written out while the next is summed
     static constexpr int kSmem = kStages * kStageBytes + 1024;    // (+ alignment of the first stage)
+    static constexpr int kWarps = BN >= 64 ? 8 : 4;               // epilogue warps: 32 lanes by kWidth columns each
+    static constexpr int kWidth = BN / (kWarps / 4);
     static_assert(kCols <= 512 && (kCols & (kCols - 1)) == 0);
     static_assert(kStages * kStageBytes >= kBufCols * 128 * 4);   // a split tile's partial sums are staged there
 };
 
-// Warp 0: TMA producer.  Warp 1: tensor memory and MMA issue.  Warps 2-5: epilogue, one per 32 lanes.
-template <int BN, bool GATED>
-__global__ void __launch_bounds__(192, 1)
+// Warp 0: TMA producer.  Warp 1: tensor memory and MMA issue.  The others: epilogue.
+template <int BN, bool GATED, bool F32>
+__global__ void __launch_bounds__(64 + 32 * LinearTile<BN, GATED>::kWarps, 1)
 linear_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x,
               const __grid_constant__ LinearParams p) {
     using T = LinearTile<BN, GATED>;
@@ -108,7 +138,7 @@ linear_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
     const uint32_t drained = bar0 + 8u * (2 * T::kStages + 4);
     if (threadIdx.x == 0) {
         for (int s = 0; s < T::kStages; ++s) { sm::bar_init(full(s), 1); sm::bar_init(empty(s), 1); }
-        for (int s = 0; s < 2; ++s) { sm::bar_init(acc_full(s), 1); sm::bar_init(acc_empty(s), 128); }
+        for (int s = 0; s < 2; ++s) { sm::bar_init(acc_full(s), 1); sm::bar_init(acc_empty(s), T::kWarps); }
         sm::bar_init(drained, 1);
         abort_flag = 0;
         sm::bar_fence_init();
@@ -120,6 +150,8 @@ linear_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
     __syncthreads();
     sm::tc_fence_after();
     const uint32_t tmem = tmem_at;
+    sm::pdl_trigger();
+    sm::pdl_wait();
 
     // this CTA's tiles, and its share [kb0, kb1) of their contraction blocks
     const int rank = p.split > 1 ? int(sm::cluster_rank()) : 0;
@@ -127,12 +159,10 @@ linear_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
     const int tiles = p.tiles_n * p.tiles_m;
     const int blocks = (p.k + kLinK - 1) / kLinK;
     const int kb0 = int(int64_t(blocks) * rank / p.split), kb1 = int(int64_t(blocks) * (rank + 1) / p.split);
-    // neighbouring tiles share their rows of w (and, 16 token tiles further, of x): both stay in L2
+    const int piece = F32 ? kPromote : kb1 - kb0;   // blocks summed in tensor memory at a time
     auto place = [&](int tile, int& n0, int& m0) {
-        const int group = tile / (16 * p.tiles_n), in = tile - group * 16 * p.tiles_n;
-        const int width = min(16, p.tiles_m - group * 16);
-        m0 = (group * 16 + in % width) * BN;
-        n0 = in / width * 128;
+        n0 = tile / p.tiles_m * 128;
+        m0 = tile % p.tiles_m * BN;
     };
 
     if (warp == 0) {
@@ -161,82 +191,94 @@ linear_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
             constexpr uint32_t idesc = sm::mma_idesc(128, BN);
             int it = 0, n = 0;
             bool ok = true;
-            for (int tile = first; tile < tiles && ok; tile += step, ++n) {
-                const int buf = n & 1;
-                if (n >= 2 && !(ok = sm::bar_wait(acc_empty(buf), uint32_t(n / 2 - 1) & 1u, abort_word, p.status))) break;
-                sm::tc_fence_after();
-                const uint32_t d = tmem + buf * T::kBufCols;
-                for (int kb = kb0; kb < kb1; ++kb, ++it) {
-                    const int s = it % T::kStages;
-                    if (!(ok = sm::bar_wait(full(s), uint32_t(it / T::kStages) & 1u, abort_word, p.status))) break;
+            for (int tile = first; tile < tiles && ok; tile += step)
+                for (int k0 = kb0; k0 < kb1 && ok; k0 += piece, ++n) {
+                    const int buf = n & 1;
+                    if (n >= 2 && !(ok = sm::bar_wait(acc_empty(buf), uint32_t(n / 2 - 1) & 1u, abort_word, p.status))) break;
                     sm::tc_fence_after();
-                    const uint32_t at = stage0 + s * T::kStageBytes;
-                    const uint64_t a = sm::desc_k_sw128(at), b = sm::desc_k_sw128(at + T::kAccs * T::kABytes);
+                    const uint32_t d = tmem + buf * T::kBufCols;
+                    const int k1 = min(k0 + piece, kb1);
+                    for (int kb = k0; kb < k1; ++kb, ++it) {
+                        const int s = it % T::kStages;
+                        if (!(ok = sm::bar_wait(full(s), uint32_t(it / T::kStages) & 1u, abort_word, p.status))) break;
+                        sm::tc_fence_after();
+                        const uint32_t at = stage0 + s * T::kStageBytes;
+                        const uint64_t a = sm::desc_k_sw128(at), b = sm::desc_k_sw128(at + T::kAccs * T::kABytes);
 #pragma unroll
-                    for (int kk = 0; kk < kLinK / 16; ++kk) {   // (32 bytes along the row: 2 in the descriptor's units)
-                        sm::mma_ss(d, a + 2 * kk, b + 2 * kk, idesc, kb > kb0 || kk > 0);
-                        if (GATED) sm::mma_ss(d + BN, a + (T::kABytes >> 4) + 2 * kk, b + 2 * kk, idesc, kb > kb0 || kk > 0);
+                        for (int kk = 0; kk < kLinK / 16; ++kk) {   // (32 bytes along the row: 2 in the descriptor's units)
+                            sm::mma_ss(d, a + 2 * kk, b + 2 * kk, idesc, kb > k0 || kk > 0);
+                            if (GATED) sm::mma_ss(d + BN, a + (T::kABytes >> 4) + 2 * kk, b + 2 * kk, idesc, kb > k0 || kk > 0);
+                        }
+                        sm::mma_commit(empty(s));
                     }
-                    sm::mma_commit(empty(s));
+                    if (ok) sm::mma_commit(acc_full(buf));
                 }
-                if (ok) sm::mma_commit(acc_full(buf));
-            }
             if (*abort_word) { sm::mma_commit(drained); sm::bar_drain(drained, 0); }
         }
         __syncwarp();
     } else {
-        const int quarter = warp & 3, row = quarter * 32 + lane;
+        const int quarter = warp & 3, row = quarter * 32 + lane, cols = (warp - 2) / 4 * T::kWidth;
         const uint32_t lanes = uint32_t(quarter * 32) << 16;
-        constexpr int kChunk = BN < 32 ? 16 : 32;
+        const bool plain = !GATED && p.act == MK_ACT_NONE;
+        float v[T::kWidth], u[GATED ? T::kWidth : 1];   // the thread's feature, its columns
         int n = 0;
-        for (int tile = first; tile < tiles; tile += step, ++n) {
+        bool ok = true;
+        for (int tile = first; tile < tiles && ok; tile += step) {
             int n0, m0;
             place(tile, n0, m0);
-            const int buf = n & 1, j = n0 + row;
-            const bool live = j < p.n;
-            const float bias = p.bias && live ? __bfloat162float(p.bias[j]) : 0.f;
-            const float bias_up = GATED && p.bias && live ? __bfloat162float(p.bias[p.n + j]) : 0.f;
-            if (!sm::bar_wait(acc_full(buf), uint32_t(n / 2) & 1u, abort_word, p.status)) break;
-            sm::tc_fence_after();
-            const uint32_t acc = tmem + buf * T::kBufCols + lanes;
+            const int j = n0 + row, left = j < p.n ? p.rows - m0 - cols : 0;
+            // bias, and without an activation the residual, enter the sums first: their loads are hidden
+            linear_begin<T::kWidth>(p, m0 + cols, j, left, rank == 0, plain, p.bias && j < p.n ? __bfloat162float(p.bias[j]) : 0.f, v);
+            if (GATED) {
+                const float b = rank == 0 && p.bias && j < p.n ? __bfloat162float(p.bias[p.n + j]) : 0.f;
+#pragma unroll
+                for (int i = 0; i < T::kWidth; ++i) u[GATED ? i : 0] = b;
+            }
+#pragma unroll 1
+            for (int k0 = kb0; k0 < kb1; k0 += piece, ++n) {
+                const int buf = n & 1;
+                if (!(ok = sm::bar_wait(acc_full(buf), uint32_t(n / 2) & 1u, abort_word, p.status))) break;
+                sm::tc_fence_after();
+                const uint32_t acc = tmem + buf * T::kBufCols + cols + lanes;
+#pragma unroll
+                for (int c = 0; c < T::kWidth; c += 16) {
+                    uint32_t t[16];
+                    sm::tmem_ld16(acc + c, t);
+                    sm::tmem_wait_ld(t);
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) v[c + i] += __uint_as_float(t[i]);
+                    if (GATED) {
+                        sm::tmem_ld16(acc + BN + c, t);
+                        sm::tmem_wait_ld(t);
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) u[GATED ? c + i : 0] += __uint_as_float(t[i]);
+                    }
+                }
+                sm::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) sm::bar_arrive(acc_empty(buf));
+            }
+            if (!ok) break;
             if (p.split > 1) {
                 // partial sums to this CTA's stages (free: every product has read them): [column][feature]
-                for (int c = 0; c < T::kBufCols; c += 16) {
-                    uint32_t v[16];
-                    sm::tmem_ld16(acc + c, v);
-                    sm::tmem_wait_ld(v);
 #pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        asm volatile("st.shared.b32 [%0], %1;" ::"r"(stage0 + uint32_t(((c + i) * 128 + row) * 4)), "r"(v[i]) : "memory");
+                for (int i = 0; i < T::kWidth; ++i) {
+                    asm volatile("st.shared.f32 [%0], %1;" ::"r"(stage0 + uint32_t(((cols + i) * 128 + row) * 4)), "f"(v[i]) : "memory");
+                    if (GATED)
+                        asm volatile("st.shared.f32 [%0], %1;" ::"r"(stage0 + uint32_t(((BN + cols + i) * 128 + row) * 4)),
+                                     "f"(u[GATED ? i : 0]) : "memory");
                 }
                 break;
             }
-            const int columns = min(BN, p.rows - m0);
-#pragma unroll 1
-            for (int c = 0; c < columns; c += kChunk) {
-                uint32_t v[kChunk], u[kChunk];
-                if constexpr (kChunk == 32) {
-                    sm::tmem_ld32(acc + c, v);
-                    if constexpr (GATED) sm::tmem_ld32(acc + BN + c, u);
-                } else {
-                    sm::tmem_ld16(acc + c, v);
-                    if constexpr (GATED) sm::tmem_ld16(acc + BN + c, u);
-                }
-                float res[kChunk];
 #pragma unroll
-                for (int i = 0; i < kChunk; ++i) res[i] = p.residual && live && c + i < columns ? linear_residual(p, m0 + c + i, j) : 0.f;
-                sm::tmem_wait_ld(v);
-                if constexpr (GATED) sm::tmem_wait_ld(u);
-                if (live)
+            for (int c = 0; c < T::kWidth; c += 8) {
+                if (c >= p.rows - m0 - cols) break;
+                float y[8], res[8];
+                linear_residuals(p, !plain, m0 + cols + c, j, left - c, res);
 #pragma unroll
-                    for (int i = 0; i < kChunk; ++i)
-                        if (c + i < columns)
-                            linear_store(p, m0 + c + i, j,
-                                         linear_act(p.act, __uint_as_float(v[i]) + bias,
-                                                    GATED ? __uint_as_float(u[i]) + bias_up : 0.f) + res[i]);
+                for (int i = 0; i < 8; ++i) y[i] = linear_act(GATED ? MK_ACT_SWIGLU : p.act, v[c + i], GATED ? u[GATED ? c + i : 0] : 0.f) + res[i];
+                linear_stores<F32>(p, m0 + cols + c, j, left - c, y);
             }
-            sm::tc_fence_before();
-            sm::bar_arrive(acc_empty(buf));
         }
     }
     if (p.split > 1) {
@@ -246,20 +288,12 @@ linear_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
         if (warp >= 2 && !*abort_word) {
             int n0, m0;
             place(first, n0, m0);
-            const int row = (warp & 3) * 32 + lane, j = n0 + row, columns = min(BN, p.rows - m0);
-            if (j < p.n) {
-                const float bias = p.bias ? __bfloat162float(p.bias[j]) : 0.f;
-                const float bias_up = GATED && p.bias ? __bfloat162float(p.bias[p.n + j]) : 0.f;
-                for (int c = rank; c < columns; c += p.split) {
-                    const float res = p.residual ? linear_residual(p, m0 + c, j) : 0.f;
-                    float y = 0.f, u = 0.f;
-                    for (int s = 0; s < p.split; ++s) {
-                        y += sm::cluster_ld(sm::cluster_addr(stage0 + uint32_t((c * 128 + row) * 4), s));
-                        if (GATED) u += sm::cluster_ld(sm::cluster_addr(stage0 + uint32_t(((BN + c) * 128 + row) * 4), s));
-                    }
-                    linear_store(p, m0 + c, j, linear_act(p.act, y + bias, u + bias_up) + res);
-                }
-            }
+            const int t = threadIdx.x - 64, row = t & 127, j = n0 + row;
+            constexpr int kGroups = T::kWarps / 4;
+            const int c1 = min(BN * (rank + 1) / p.split, p.rows - m0);
+            if (j < p.n)
+                for (int c = BN * rank / p.split + t / 128; c < c1; c += 8 * kGroups)
+                    linear_join<kGroups, GATED, F32>(p, stage0, BN * 128 * 4, p.split, 1, 0, m0, c, c1, row, j);
         }
         __syncwarp();
         sm::cluster_sync();   // no CTA leaves while a peer reads its partial sums
@@ -277,12 +311,6 @@ linear_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
 // bytes a cycle at the full product rate, the pair 64 + 64.  SwiGLU puts 64 gate rows and the same
 // 64 features' up rows into a CTA's 128; their accumulators sit 64 lanes apart and meet in the epilogue
 // through shared memory.
-//
-// The tensor core truncates as it accumulates, an error that grows with the length of the sum
-// (measured at k = 8192 with an fp32 output: 1.5e-6 of its norm, against 7e-7 for plain fp32 sums).  fp32
-// outputs are therefore summed in pieces of kPromote blocks that the epilogue warps add up in registers; a
-// bf16 output rounds a thousand times coarser and takes the whole contraction in one piece.
-constexpr int kPromote = 8;
 template <bool GATED>
 struct PairTile {
     static constexpr int kRows = GATED ? 64 : 128;          // features of one CTA
@@ -329,6 +357,8 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
     sm::cluster_sync();   // both CTAs' barriers and tensor memory are there
     sm::tc_fence_after();
     const uint32_t tmem = tmem_at;
+    sm::pdl_trigger();
+    sm::pdl_wait();
 
     const int cluster = 2 * p.split;
     const int first = int(blockIdx.x) / cluster, step = int(gridDim.x) / cluster;
@@ -405,16 +435,18 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
     } else {
         const int quarter = warp & 3, row = quarter * 32 + lane, cols = (warp - 2) / 4 * 128;
         const uint32_t lanes = uint32_t(quarter * 32) << 16;
-        const bool up_row = GATED && row >= 64;
+        const bool up_row = GATED && row >= 64, plain = !GATED && p.act == MK_ACT_NONE;
         float v[128];   // the thread's row of the tile, its 128 columns
         int n = 0;
         bool ok = true;
         for (int tile = first; tile < tiles && ok; tile += step) {
             int n0, m0;
             place(tile, n0, m0);
-            if (F32)
-#pragma unroll
-                for (int i = 0; i < 128; ++i) v[i] = 0.f;
+            const int j = n0 + (GATED ? row & 63 : row);
+            const bool live = j < p.n;
+            const int jb = up_row ? p.n + j : j;   // (bias rows: gate rows, then up rows)
+            linear_begin<128>(p, m0 + cols, j, live ? p.rows - m0 - cols : 0, part == 0, plain,
+                              p.bias && live ? __bfloat162float(p.bias[jb]) : 0.f, v);
 #pragma unroll 1
             for (int k0 = kb0; k0 < kb1; k0 += piece, ++n) {
                 const int buf = n & 1;
@@ -427,10 +459,7 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
                     sm::tmem_ld16(acc + c, t);
                     sm::tmem_wait_ld(t);
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        if (F32) v[c + i] += __uint_as_float(t[i]);
-                        else v[c + i] = __uint_as_float(t[i]);
-                    }
+                    for (int i = 0; i < 16; ++i) v[c + i] += __uint_as_float(t[i]);
                 }
                 sm::tc_fence_before();
                 __syncwarp();
@@ -443,10 +472,6 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
                     asm volatile("st.shared.f32 [%0], %1;" ::"r"(stage0 + uint32_t(((cols + i) * 128 + row) * 4)), "f"(v[i]) : "memory");
                 break;
             }
-            const int j = n0 + (GATED ? row & 63 : row);
-            const bool live = j < p.n;
-            const int jb = up_row ? p.n + j : j;   // (bias rows: gate rows, then up rows)
-            const float bias = p.bias && live ? __bfloat162float(p.bias[jb]) : 0.f;
             // 8 columns a step.  SwiGLU: 16 columns, of which the gate row keeps 0-7 and receives their up
             // values from its up row, which keeps 8-15 and receives their gate values; two buffers take turns
             constexpr int kStep = GATED ? 16 : 8;
@@ -455,24 +480,24 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
                 const int m = m0 + cols + c + (up_row ? 8 : 0), left = live ? p.rows - m : 0;
                 if (m0 + cols + c >= p.rows) break;   // (the same for both warps of an exchange: they share cols)
                 float y[8], res[8];
-                linear_residuals(p, m, j, left, res);
+                linear_residuals<8>(p, !plain, m, j, left, res);
                 if constexpr (GATED) {
                     const uint32_t at = stage0 + T::kStages * T::kStageBytes + uint32_t(((c / 16 & 1) * 2 + cols / 128) * (8 * 128 * 4));
 #pragma unroll
                     for (int i = 0; i < 8; ++i)
                         asm volatile("st.shared.f32 [%0], %1;" ::"r"(at + uint32_t((i * 128 + row) * 4)),
-                                     "f"((up_row ? v[c + i] : v[c + 8 + i]) + bias) : "memory");
+                                     "f"(up_row ? v[c + i] : v[c + 8 + i]) : "memory");
                     asm volatile("bar.sync %0, 64;" ::"r"(1 + cols / 128 * 2 + (quarter & 1)) : "memory");
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
                         float got;
                         asm volatile("ld.shared.f32 %0, [%1];" : "=f"(got) : "r"(at + uint32_t((i * 128 + (row ^ 64)) * 4)) : "memory");
-                        const float own = (up_row ? v[c + 8 + i] : v[c + i]) + bias;
+                        const float own = up_row ? v[c + 8 + i] : v[c + i];
                         y[i] = linear_act(MK_ACT_SWIGLU, up_row ? got : own, up_row ? own : got) + res[i];
                     }
                 } else {
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) y[i] = linear_act(p.act, v[c + i] + bias, 0.f) + res[i];
+                    for (int i = 0; i < 8; ++i) y[i] = linear_act(p.act, v[c + i], 0.f) + res[i];
                 }
                 linear_stores<F32>(p, m, j, left, y);
             }
@@ -487,33 +512,10 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
             place(first, n0, m0);
             const int t = threadIdx.x - 64, row = t % T::kRows, j = n0 + row;
             constexpr int kGroups = 256 / T::kRows;
-            const int width = 256 / p.split, c1 = min(width * (part + 1), p.rows - m0);
-            if (j < p.n) {
-                const float bias = p.bias ? __bfloat162float(p.bias[j]) : 0.f;
-                const float bias_up = GATED && p.bias ? __bfloat162float(p.bias[p.n + j]) : 0.f;
-                for (int c = width * part + t / T::kRows; c < c1; c += 8 * kGroups) {
-                    float y[8], u[8], res[8];
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const int m = m0 + c + i * kGroups;
-                        y[i] = u[i] = 0.f;
-                        res[i] = p.residual && c + i * kGroups < c1 ? linear_residual(p, m, j) : 0.f;
-                    }
-                    for (int s = 0; s < p.split; ++s) {
-                        const uint32_t peer = sm::cluster_addr(stage0, uint32_t(2 * s + half));
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const uint32_t at = peer + uint32_t((min(c + i * kGroups, 255) * 128 + row) * 4);
-                            y[i] += sm::cluster_ld(at);
-                            if (GATED) u[i] += sm::cluster_ld(at + 64 * 4);
-                        }
-                    }
-#pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        if (c + i * kGroups < c1)
-                            linear_store(p, m0 + c + i * kGroups, j, linear_act(p.act, y[i] + bias, u[i] + bias_up) + res[i]);
-                }
-            }
+            const int width0 = 256 * part / p.split, c1 = min(256 * (part + 1) / p.split, p.rows - m0);
+            if (j < p.n)
+                for (int c = width0 + t / T::kRows; c < c1; c += 8 * kGroups)
+                    linear_join<kGroups, GATED, F32>(p, stage0, 64 * 4, p.split, 2, half, m0, c, c1, row, j);
         }
         __syncwarp();
     }
@@ -524,11 +526,62 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
     if (warp == 1) sm::tmem_free_pair(tmem, 512);
 }
 
-template <int BN, bool GATED>
-static mk_status linear_launch(const mk_linear_args* a, LinearParams& p, int device, int sms, cudaStream_t stream) {
+// A launch: clusters of one shape, dependent on the kernel before it only from pdl_wait on
+struct LinearLaunch {
+    cudaLaunchConfig_t c{};
+    cudaLaunchAttribute attr[2];
+    LinearLaunch(int threads, int bytes, cudaStream_t stream) {
+        c.blockDim = dim3(unsigned(threads));
+        c.dynamicSmemBytes = size_t(bytes);
+        c.stream = stream;
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[1].val.programmaticStreamSerializationAllowed = 1;
+        c.attrs = attr;
+        c.numAttrs = 2;
+        shape(1, 1);
+    }
+    LinearLaunch(const LinearLaunch&) = delete;
+    void shape(int cluster, int64_t clusters) {
+        attr[0].val.clusterDim.x = unsigned(cluster);
+        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+        c.gridDim = dim3(unsigned(cluster * clusters));
+    }
+};
+
+// Over how many units of `unit` CTAs each (a cluster holds them) a tile's contraction is cut: the
+// count with the least time by rounds of the clusters that run at once, each round the blocks of one
+// unit at `cycles` plus a fixed part (set-up, epilogue), and the exchange of the partial sums
+// between units.  Clusters of 8 leave SMs out (15 run at once on 152 SMs, 36 of 4, 76 of 2): 16 tiles
+// over 8 CTAs each took two rounds, 46.7 us against 38.8 with 4 (512 x 2048 x 8192).
+static mk_status linear_split(const void* fn, LinearLaunch& cfg, std::atomic<int> (&resident)[8], int unit, int most, int64_t tiles,
+                              int blocks, int cycles, int least, int* split) {
+    int64_t best = INT64_MAX;
+    for (int s = 1; s <= most && unit * s <= 8; ++s) {
+        if (s > 1 && blocks < s * least) break;
+        int fit = resident[s - 1].load();
+        if (!fit) {
+            cfg.shape(unit * s, 1);
+            MK_CK(cudaOccupancyMaxActiveClusters(&fit, fn, &cfg.c));
+            if (fit < 1) fit = s > 1 ? -1 : 0;
+            if (!fit) return fail(MK_ERR_RESOURCES, "linear: its CTAs cannot be resident");
+            resident[s - 1].store(fit);
+        }
+        if (fit < 0) break;
+        const int64_t rounds = (tiles + fit - 1) / fit;
+        const int64_t t = rounds * (int64_t((blocks + s - 1) / s) * cycles + 6000) + (s > 1 ? 1500 + 500 * s : 0);
+        if (t < best) { best = t; *split = s; }
+    }
+    return MK_OK;
+}
+
+template <int BN, bool GATED, bool F32>
+static mk_status linear_launch_one(const mk_linear_args* a, LinearParams& p, int device, int sms, cudaStream_t stream) {
     using T = LinearTile<BN, GATED>;
+    constexpr int kLinCycles = BN * (GATED ? 4 : 2) < 384 ? 384 : BN * (GATED ? 4 : 2);   // a block: its bytes, or its products
     static std::atomic<uint64_t> set{0};
-    const void* fn = reinterpret_cast<const void*>(&linear_kernel<BN, GATED>);
+    static std::atomic<int> resident[64][8];
+    const void* fn = reinterpret_cast<const void*>(&linear_kernel<BN, GATED, F32>);
     mk_status st = op_smem(fn, T::kSmem, device, &set);
     if (st != MK_OK) return st;
     CUtensorMap map_w, map_x;
@@ -542,31 +595,22 @@ static mk_status linear_launch(const mk_linear_args* a, LinearParams& p, int dev
     p.tiles_m = (p.rows + BN - 1) / BN;
     const int64_t tiles = int64_t(p.tiles_n) * p.tiles_m;
     if (tiles > (1 << 30)) return fail(MK_ERR_ARG, "linear: %lld tiles", static_cast<long long>(tiles));
-    // fewer tiles than SMs: the contraction is cut over a cluster (2, 4 or 8 CTAs, at least two
-    // blocks of it each), as far as the SMs go
+    // fewer tiles than SMs: the contraction is cut over a cluster, two blocks of it each at least
     const int blocks = (p.k + kLinK - 1) / kLinK;
+    LinearLaunch cfg(64 + 32 * T::kWarps, T::kSmem, stream);
     p.split = 1;
-    while (p.split < 8 && tiles * p.split * 2 <= sms && blocks >= p.split * 4) p.split *= 2;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(unsigned(p.split > 1 ? tiles * p.split : (tiles < sms ? tiles : sms)));
-    cfg.blockDim = dim3(192);
-    cfg.dynamicSmemBytes = T::kSmem;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = unsigned(p.split);
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    MK_CK(cudaLaunchKernelEx(&cfg, &linear_kernel<BN, GATED>, map_w, map_x, p));
+    if (tiles * 2 <= sms)
+        if ((st = linear_split(fn, cfg, resident[device], 1, 8, tiles, blocks, kLinCycles, 2, &p.split)) != MK_OK) return st;
+    cfg.shape(p.split, p.split > 1 ? tiles : (tiles < sms ? tiles : sms));
+    MK_CK(cudaLaunchKernelEx(&cfg.c, &linear_kernel<BN, GATED, F32>, map_w, map_x, p));
     return MK_OK;
 }
 
 template <bool GATED, bool F32>
-static mk_status linear_launch_pair(const mk_linear_args* a, LinearParams& p, int device, int sms, cudaStream_t stream) {
+static mk_status linear_launch_pair(const mk_linear_args* a, LinearParams& p, int device, cudaStream_t stream) {
     using T = PairTile<GATED>;
     static std::atomic<uint64_t> set{0};
-    static std::atomic<int> resident[64];   // clusters of 2 that run at once, per device
+    static std::atomic<int> resident[64][8];
     const void* fn = reinterpret_cast<const void*>(&linear_pair_kernel<GATED, F32>);
     mk_status st = op_smem(fn, T::kSmem, device, &set);
     if (st != MK_OK) return st;
@@ -582,32 +626,18 @@ static mk_status linear_launch_pair(const mk_linear_args* a, LinearParams& p, in
     const int64_t tiles = int64_t(p.tiles_n) * p.tiles_m;
     if (tiles > (1 << 28)) return fail(MK_ERR_ARG, "linear: %lld tiles", static_cast<long long>(tiles));
     const int blocks = (p.k + kLinK - 1) / kLinK;
-    p.split = 1;
-    while (p.split < 4 && tiles * p.split * 4 <= sms && blocks >= p.split * 4) p.split *= 2;
-    cudaLaunchConfig_t cfg{};
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = unsigned(2 * p.split);
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    cfg.gridDim = dim3(unsigned(2 * p.split));
-    cfg.blockDim = dim3(320);
-    cfg.dynamicSmemBytes = T::kSmem;
-    cfg.stream = stream;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    int64_t clusters = tiles;
-    if (p.split == 1) {   // a persistent grid of the pairs that fit the device at once
-        int fit = resident[device].load();
-        if (!fit) {
-            MK_CK(cudaOccupancyMaxActiveClusters(&fit, fn, &cfg));
-            if (fit < 1) return fail(MK_ERR_RESOURCES, "linear: a pair of CTAs cannot be resident");
-            resident[device].store(fit);
-        }
-        clusters = tiles < fit ? tiles : fit;
-    }
-    cfg.gridDim = dim3(unsigned(2 * p.split * clusters));
-    MK_CK(cudaLaunchKernelEx(&cfg, &linear_pair_kernel<GATED, F32>, map_w, map_x, p));
+    LinearLaunch cfg(320, T::kSmem, stream);
+    if ((st = linear_split(fn, cfg, resident[device], 2, 4, tiles, blocks, 512, 2, &p.split)) != MK_OK) return st;
+    const int fit = resident[device][p.split - 1].load();
+    cfg.shape(2 * p.split, p.split > 1 || tiles < fit ? tiles : fit);   // (a persistent grid of the pairs that run at once)
+    MK_CK(cudaLaunchKernelEx(&cfg.c, &linear_pair_kernel<GATED, F32>, map_w, map_x, p));
     return MK_OK;
+}
+
+template <int BN, bool GATED>
+static mk_status linear_launch(const mk_linear_args* a, LinearParams& p, int device, int sms, cudaStream_t stream) {
+    return p.out_f32 ? linear_launch_one<BN, GATED, true>(a, p, device, sms, stream)
+                     : linear_launch_one<BN, GATED, false>(a, p, device, sms, stream);
 }
 
 static mk_status linear_check(const mk_linear_args* a) {
@@ -668,11 +698,11 @@ extern "C" mk_status mk_linear(const mk_linear_args* a, void* stream) {
         if (p.rows <= 32) return linear_launch<32, true>(a, p, device, sms, s);
         if (p.rows <= 64) return linear_launch<64, true>(a, p, device, sms, s);
         if (p.rows <= 128) return linear_launch<128, true>(a, p, device, sms, s);
-        return p.out_f32 ? linear_launch_pair<true, true>(a, p, device, sms, s) : linear_launch_pair<true, false>(a, p, device, sms, s);
+        return p.out_f32 ? linear_launch_pair<true, true>(a, p, device, s) : linear_launch_pair<true, false>(a, p, device, s);
     }
     if (p.rows <= 16) return linear_launch<16, false>(a, p, device, sms, s);
     if (p.rows <= 32) return linear_launch<32, false>(a, p, device, sms, s);
     if (p.rows <= 64) return linear_launch<64, false>(a, p, device, sms, s);
     if (p.rows <= 128) return linear_launch<128, false>(a, p, device, sms, s);
-    return p.out_f32 ? linear_launch_pair<false, true>(a, p, device, sms, s) : linear_launch_pair<false, false>(a, p, device, sms, s);
+    return p.out_f32 ? linear_launch_pair<false, true>(a, p, device, s) : linear_launch_pair<false, false>(a, p, device, s);
 }

@@ -180,6 +180,13 @@ __device__ __forceinline__ void mma_commit_pair(uint32_t bar, uint16_t ranks) { 
                  "h"(ranks) : "memory");
 }
 
+// ---- programmatic dependent launch -----------------------------------------------------------------
+// A kernel launched with the attribute starts while the one before it on the stream drains; it sets
+// itself up, then waits here until that one is done and its writes are visible.  The trigger lets
+// the kernel after it do the same.
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 // ---- clusters ------------------------------------------------------------------------------------
 __device__ __forceinline__ uint32_t cluster_rank() {
     uint32_t r;
