@@ -436,7 +436,7 @@ mk_status mk_linear(const mk_linear_args* a, void* stream);
  *                 whatever they hold, apart from this: a position that one token of a block of 128 / (n_q_heads
  *                 / n_kv_heads) neighbouring tokens sees must hold finite values
  *  max_seq        positions per (sequence, head) of a contiguous cache, or the most positions a
- *                 sequence of a paged cache may have (max_blocks * block_size >= max_seq)
+ *                 sequence of a paged cache may have (max_blocks * block_size >= max_seq); <= 2^30
  *  pages          NULL: contiguous.  Else mk_kv_pages with block_size a multiple of 8; a table
  *                 entry outside [0, n_blocks) is not followed: its positions count as not visible
  *                 and status receives MK_ERR_BOUNDS

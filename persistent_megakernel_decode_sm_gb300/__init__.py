@@ -16,8 +16,10 @@ Prompt operators (asynchronous on torch's current stream of the tensors' device)
 """
 from __future__ import annotations
 
+import array
 import ctypes
 import os
+import struct
 from typing import List, Optional, Sequence
 
 import numpy as np
@@ -151,11 +153,11 @@ lib.mk_set_trace.argtypes = [_P, _P]
 lib.mk_set_sync.restype = ctypes.c_int
 lib.mk_set_sync.argtypes = [_P, ctypes.c_int32]
 lib.mk_linear.restype = ctypes.c_int
-lib.mk_linear.argtypes = [ctypes.POINTER(mk_linear_args), _P]
+lib.mk_linear.argtypes = [_P, _P]   # (a packed mk_linear_args)
 lib.mk_attend_workspace.restype = ctypes.c_size_t
-lib.mk_attend_workspace.argtypes = [ctypes.POINTER(mk_attend_args)]
+lib.mk_attend_workspace.argtypes = [_P]
 lib.mk_attend.restype = ctypes.c_int
-lib.mk_attend.argtypes = [ctypes.POINTER(mk_attend_args), _P, ctypes.c_size_t, _P]
+lib.mk_attend.argtypes = [_P, _P, ctypes.c_size_t, _P]
 lib.mk_unbind.restype = None
 lib.mk_unbind.argtypes = [_P]
 
@@ -410,38 +412,55 @@ class Decoder:
 
 
 # ---- prompt operators ------------------------------------------------------------------------
+# A call's host time counts beside kernels of a few microseconds, so the argument structs are packed
+# in one go (native alignment, the layouts of mk_linear_args and mk_attend_args).
 
-def _op_tensor(t, name, dtypes, device, dim=2):
-    """The checks every operand passes: a CUDA tensor of one of `dtypes` on `device` whose last
-    dimension is contiguous."""
-    if not t.is_cuda or t.device != device:
-        raise ValueError(f"{name} must be a CUDA tensor on {device}")
+_LINEAR_ARGS = struct.Struct("@4iPqPPPq2iPqP")
+_ATTEND_ARGS = struct.Struct("@4iPPPqPqPP5ifP")
+_KV_ARGS, _PAGES_ARGS = struct.Struct("@PPqqq"), struct.Struct("@Piii")
+assert _LINEAR_ARGS.size == ctypes.sizeof(mk_linear_args) and _ATTEND_ARGS.size == ctypes.sizeof(mk_attend_args)
+assert _KV_ARGS.size == ctypes.sizeof(mk_kv)
+
+
+def _operand(t, name, dtypes, device, dim):
+    """(shape, strides) of an operand: a CUDA tensor of one of `dtypes` on `device` (an ordinal) with
+    `dim` dimensions, the last one contiguous."""
+    shape, strides = t.shape, t.stride()
     if t.dtype not in dtypes:
         raise ValueError(f"{name} must be one of {dtypes}, not {t.dtype}")
-    if t.dim() != dim:
-        raise ValueError(f"{name} must have {dim} dimensions, not {t.dim()}")
-    if t.shape[-1] > 1 and t.stride(-1) != 1:
+    if not t.is_cuda or t.get_device() != device:
+        raise ValueError(f"{name} must be a CUDA tensor on the first operand's device, not on {t.device}")
+    if len(shape) != dim:
+        raise ValueError(f"{name} must have {dim} dimensions, not {len(shape)}")
+    if strides[-1] != 1 and shape[-1] > 1:
         raise ValueError(f"{name}: its last dimension must be contiguous")
-    return t
+    return shape, strides
 
 
-def _op_status(status, device):
-    import torch
+def _address(data: bytes) -> int:
+    return ctypes.cast(data, _P).value
+
+
+def _status_ptr(status, device):
     if status is None:
-        return None
-    _op_tensor(status, "status", (torch.int32,), device, dim=1)
-    if status.numel() < 1:
+        return 0
+    import torch
+    if _operand(status, "status", (torch.int32,), device, 1)[0][0] < 1:
         raise ValueError("status must hold one int32")
     return status.data_ptr()
 
 
-def _on_device(device, call):
-    """Runs call(stream) with `device` current and torch's current stream of it."""
+def _launch(device: int, call, *args):
+    """call(*args, stream) with `device` current and torch's current stream of it."""
     import torch
-    if torch.cuda.current_device() == device.index:
-        return _check(call(torch.cuda.current_stream(device).cuda_stream))
-    with torch.cuda.device(device):
-        return _check(call(torch.cuda.current_stream(device).cuda_stream))
+    stream = torch._C._cuda_getCurrentRawStream(device)
+    if torch._C._cuda_getDevice() == device:
+        st = call(*args, stream)
+    else:
+        with torch.cuda.device(device):
+            st = call(*args, stream)
+    if st:
+        _check(st)
 
 
 def linear(x, weight, bias=None, activation: Optional[str] = None, residual=None, out=None, out_dtype=None, status=None):
@@ -454,38 +473,42 @@ def linear(x, weight, bias=None, activation: Optional[str] = None, residual=None
     the residual itself; by default one of out_dtype (bf16) is allocated.  Returns out."""
     import torch
     bf, f32 = torch.bfloat16, torch.float32
-    dev = x.device
-    _op_tensor(x, "x", (bf,), dev)
-    _op_tensor(weight, "weight", (bf,), dev)
-    if activation not in ACTIVATIONS:
+    dev = x.get_device()
+    (rows, k), xs = _operand(x, "x", (bf,), dev, 2)
+    (n, wk), ws = _operand(weight, "weight", (bf,), dev, 2)
+    act = ACTIVATIONS.get(activation, -1)
+    if act < 0:
         raise ValueError(f"activation {activation!r}: expected one of {list(ACTIVATIONS)}")
-    if not weight.is_contiguous():
-        raise ValueError("weight must be contiguous")
-    rows, k = x.shape
-    n = weight.shape[0]
-    if weight.shape[1] != k:
-        raise ValueError(f"weight {tuple(weight.shape)} does not take rows of {k}")
-    if bias is not None and (_op_tensor(bias, "bias", (bf,), dev, dim=1).shape[0] != n or not bias.is_contiguous()):
-        raise ValueError(f"bias must be contiguous, of {n} elements")
-    if activation == "swiglu":
+    if wk != k or (ws[0] != k and n > 1):
+        raise ValueError(f"weight {tuple(weight.shape)} must be contiguous, with rows of {k}")
+    if bias is not None and _operand(bias, "bias", (bf,), dev, 1)[0][0] != n:
+        raise ValueError(f"bias must have {n} elements")
+    if act == 3:
         if n % 2:
             raise ValueError("swiglu takes an even number of weight rows: gate rows, then up rows")
         n //= 2
     if out is None:
-        out = torch.empty((rows, n), dtype=out_dtype or bf, device=dev)
-    elif out_dtype is not None and out.dtype != out_dtype:
-        raise ValueError(f"out is {out.dtype}, out_dtype {out_dtype}")
-    _op_tensor(out, "out", (bf, f32), dev)
-    if out.shape != (rows, n):
-        raise ValueError(f"out must be [{rows}, {n}], not {tuple(out.shape)}")
-    if residual is not None and _op_tensor(residual, "residual", (bf, f32), dev).shape != (rows, n):
-        raise ValueError(f"residual must be [{rows}, {n}], not {tuple(residual.shape)}")
-    a = mk_linear_args(rows, n, k, ACTIVATIONS[activation], x.data_ptr(), x.stride(0), weight.data_ptr(),
-                       None if bias is None else bias.data_ptr(), None if residual is None else residual.data_ptr(),
-                       0 if residual is None else residual.stride(0),
-                       F32 if residual is not None and residual.dtype == f32 else BF16, F32 if out.dtype == f32 else BF16,
-                       out.data_ptr(), out.stride(0), _op_status(status, dev))
-    _on_device(dev, lambda stream: lib.mk_linear(ctypes.byref(a), stream))
+        out = torch.empty((rows, n), dtype=out_dtype or bf, device=x.device)
+        if out.dtype is not bf and out.dtype is not f32:
+            raise ValueError(f"out_dtype must be torch.bfloat16 or torch.float32, not {out_dtype}")
+        os = n
+    else:
+        if out_dtype is not None and out.dtype != out_dtype:
+            raise ValueError(f"out is {out.dtype}, out_dtype {out_dtype}")
+        shape, os = _operand(out, "out", (bf, f32), dev, 2)
+        os = os[0]
+        if shape[0] != rows or shape[1] != n:
+            raise ValueError(f"out must be [{rows}, {n}], not {tuple(shape)}")
+    rp = rs = rt = 0
+    if residual is not None:
+        shape, rs = _operand(residual, "residual", (bf, f32), dev, 2)
+        if shape[0] != rows or shape[1] != n:
+            raise ValueError(f"residual must be [{rows}, {n}], not {tuple(shape)}")
+        rp, rs, rt = residual.data_ptr(), rs[0], F32 if residual.dtype is f32 else BF16
+    _launch(dev, lib.mk_linear,
+            _LINEAR_ARGS.pack(rows, n, k, act, x.data_ptr(), xs[0], weight.data_ptr(), 0 if bias is None else bias.data_ptr(),
+                              rp, rs, rt, F32 if out.dtype is f32 else BF16, out.data_ptr(), os,
+                              0 if status is None else _status_ptr(status, dev)))
     return out
 
 
@@ -503,61 +526,62 @@ def attend(q, kv, q_lens: Sequence[int], kv_lens: Sequence[int], layer: int = 0,
     default); workspace: at least attend_workspace bytes (allocated by default).  Returns out."""
     import torch
     bf = torch.bfloat16
-    dev = q.device
-    _op_tensor(q, "q", (bf,), dev, dim=3)
-    tokens, nq, d = q.shape
+    dev = q.get_device()
+    (tokens, nq, d), qs = _operand(q, "q", (bf,), dev, 3)
     batch = len(q_lens)
     if len(kv_lens) != batch:
         raise ValueError("q_lens and kv_lens must have the same length")
-    ql, kvl = (ctypes.c_int32 * max(batch, 1))(*q_lens), (ctypes.c_int32 * max(batch, 1))(*kv_lens)
-    if sum(ql) > tokens:
-        raise ValueError(f"q holds {tokens} tokens, q_lens add up to {sum(ql)}")
-    if out is None:
-        out = torch.empty((tokens, nq, d), dtype=bf, device=dev)
-    elif _op_tensor(out, "out", (bf,), dev, dim=3).shape != q.shape:
-        raise ValueError("out must have q's shape")
-    for t, name in ((q, "q"), (out, "out")):
-        if nq > 1 and t.stride(1) != d:
-            raise ValueError(f"{name}: a token's heads must be contiguous")
-    k, v = kv.k, kv.v
-    dims = 5 if pages is None else 4
-    _op_tensor(k, "kv.k", (bf,), dev, dim=dims)
-    _op_tensor(v, "kv.v", (bf,), dev, dim=dims)
-    if k.shape != v.shape or k.stride() != v.stride() or k.shape[-1] != d or k.stride(-2) != d:
-        raise ValueError("kv.k and kv.v must be alike, with contiguous [positions, head_dim] rows of q's head_dim")
-    st = k.stride()
-    layers, nkv, positions = k.shape[-4], k.shape[-3], k.shape[-2]
-    if not 0 <= layer < layers:
-        raise ValueError(f"layer {layer} of {layers}")
-    if pages is None:
-        if k.shape[0] < batch:
-            raise ValueError(f"the cache holds {k.shape[0]} sequences, q_lens name {batch}")
-        c_kv, c_pages = mk_kv(k.data_ptr(), v.data_ptr(), st[0], st[1], st[2]), None
-    else:
-        table, block_size, n_blocks = pages
-        _op_tensor(table, "the block table", (torch.int32,), dev)
-        if table.shape[0] < batch or not table.is_contiguous():
-            raise ValueError(f"the block table must be contiguous, with a row for each of {batch} sequences")
-        if positions < int(n_blocks) * int(block_size):
-            raise ValueError(f"the pool holds {positions} positions a head, {n_blocks} blocks of {block_size} need more")
-        c_kv = mk_kv(k.data_ptr(), v.data_ptr(), 0, st[0], st[1])
-        c_pages = mk_kv_pages(table.data_ptr(), int(block_size), table.shape[1], int(n_blocks))
-        positions = table.shape[1] * int(block_size)
-    a = mk_attend_args(nq, nkv, d, batch, ql, kvl, q.data_ptr(), q.stride(0), out.data_ptr(), out.stride(0),
-                       ctypes.pointer(c_kv), None if c_pages is None else ctypes.pointer(c_pages), layer, positions,
-                       window, sinks, shared_prefix, 0.0 if scale is None else scale, _op_status(status, dev))
+    if sum(q_lens) > tokens:
+        raise ValueError(f"q holds {tokens} tokens, q_lens add up to {sum(q_lens)}")
     if scale is not None and not scale > 0:
         raise ValueError("scale must be positive")
-
-    def call(stream):
-        ws = workspace
-        need = int(lib.mk_attend_workspace(ctypes.byref(a)))
-        if ws is None and need:
-            ws = torch.empty(need, dtype=torch.uint8, device=dev)
-        if ws is not None and (ws.device != dev or not ws.is_contiguous()):
-            raise ValueError(f"workspace must be contiguous, on {dev}")
-        return lib.mk_attend(ctypes.byref(a), None if ws is None else ws.data_ptr(),
-                             0 if ws is None else ws.numel() * ws.element_size(), stream)
-
-    _on_device(dev, call)
+    if out is None:
+        out, os = torch.empty((tokens, nq, d), dtype=bf, device=q.device), (nq * d, d)
+    else:
+        shape, os = _operand(out, "out", (bf,), dev, 3)
+        if shape != q.shape:
+            raise ValueError("out must have q's shape")
+    if nq > 1 and (qs[1] != d or os[1] != d):
+        raise ValueError("q and out: a token's heads must be contiguous")
+    k, v = kv.k, kv.v
+    dims = 5 if pages is None else 4
+    shape, ks = _operand(k, "kv.k", (bf,), dev, dims)
+    vshape, vs = _operand(v, "kv.v", (bf,), dev, dims)
+    if shape != vshape or ks != vs or shape[-1] != d or (ks[-2] != d and shape[-2] > 1):
+        raise ValueError("kv.k and kv.v must be alike, with contiguous [positions, head_dim] rows of q's head_dim")
+    layers, nkv, positions = shape[-4:-1]
+    if not 0 <= layer < layers:
+        raise ValueError(f"layer {layer} of {layers}")
+    c_pages = None
+    if pages is None:
+        if shape[0] < batch:
+            raise ValueError(f"the cache holds {shape[0]} sequences, q_lens name {batch}")
+        c_kv = _KV_ARGS.pack(k.data_ptr(), v.data_ptr(), ks[0], ks[1], ks[2])
+    else:
+        table, block_size, n_blocks = pages
+        tshape, ts = _operand(table, "the block table", (torch.int32,), dev, 2)
+        if tshape[0] < batch or (ts[0] != tshape[1] and tshape[0] > 1):
+            raise ValueError(f"the block table must be contiguous, with a row for each of {batch} sequences")
+        if positions < n_blocks * block_size:
+            raise ValueError(f"the pool holds {positions} positions a head, {n_blocks} blocks of {block_size} need more")
+        c_kv = _KV_ARGS.pack(k.data_ptr(), v.data_ptr(), 0, ks[0], ks[1])
+        c_pages = _PAGES_ARGS.pack(table.data_ptr(), block_size, tshape[1], n_blocks)
+        positions = tshape[1] * block_size
+    lens = array.array("i", q_lens)
+    lens.extend(kv_lens)
+    at = lens.buffer_info()[0]
+    # (bytes objects keep their contents at a fixed address while they live)
+    a = _ATTEND_ARGS.pack(nq, nkv, d, batch, at, at + 4 * batch, q.data_ptr(), qs[0], out.data_ptr(), os[0],
+                          _address(c_kv), 0 if c_pages is None else _address(c_pages), layer, min(positions, 1 << 30),
+                          window, sinks, shared_prefix, scale or 0.0, 0 if status is None else _status_ptr(status, dev))
+    need = lib.mk_attend_workspace(a)
+    ws, size = 0, 0
+    if workspace is not None:
+        if not workspace.is_cuda or workspace.get_device() != dev or not workspace.is_contiguous():
+            raise ValueError("workspace must be contiguous, on q's device")
+        ws, size = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    elif need:
+        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        ws, size = workspace.data_ptr(), need
+    _launch(dev, lib.mk_attend, a, ws, size)
     return out

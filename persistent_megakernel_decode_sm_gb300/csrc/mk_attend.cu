@@ -1,73 +1,476 @@
 // Attention of query tokens over one layer of the decode KV cache (mk_attend): causal, an optional
 // sliding window with sinks, an optional prefix shared by the batch.
 #include "mk_ops.h"
+#include "mk_sm103.cuh"
 
-#include <cuda_bf16.h>
-
+#include <algorithm>
 #include <climits>
 #include <cmath>
 
 namespace mk {
 
-struct AttendSeq {
-    int32_t q0, n, len, pad;   // first query token, query tokens, positions
+// ---- work -----------------------------------------------------------------------------------------
+// A segment is a run of query tokens over a range of positions: one sequence, or (the shared prefix)
+// every token over sequence 0's first positions.  It is cut into items: a block of at most 128 rows --
+// neighbouring tokens by the query heads of one KV head, so grouped heads share the K/V they read --
+// times a share of the key tiles the block sees (`splits` shares).  An output row whose tokens have one share
+// is written by its item; else the items leave (o, m, l) in the workspace and attend_merge_kernel joins them.
+struct AttendSeg {
+    int32_t q0, n;         // first query token, tokens
+    int32_t pos0;          // position of the first token; kNoCausal: every token sees every key of the segment
+    int32_t key0, key1;    // positions [key0, key1)
+    int32_t cache;         // the sequence whose cache rows (or table row) are read
+    int32_t splits, item0; // shares of the key tiles; items of the segments before
+    int32_t part0;         // first row group of its parts in the workspace (units of n_q_heads rows)
 };
+constexpr int32_t kNoCausal = INT_MIN;
+constexpr int kKeys = 128;     // key tile
+constexpr int kBlockRows = 128;
 
-struct AttendParams {
-    int nq, nkv, group, d, batch, tokens;
-    const __nv_bfloat16* q;
-    int64_t q_stride;
+struct AttendCommon {
+    int32_t nq, nkv, group, block_tokens;   // block_tokens: query tokens of a block, 128 / group
+    int32_t tokens, segs, prefix_seg;       // prefix_seg: 1 where segment 0 is the shared prefix
+    int32_t window, sinks;
+    float scale_log2;                       // scale / ln 2
+    const int32_t* table;                   // paged: [batch][max_blocks]
+    int32_t block, max_blocks, n_blocks, box;   // box: positions one copy takes (a power of two that divides block)
     __nv_bfloat16* out;
     int64_t out_stride;
-    const __nv_bfloat16* k;   // the layer's cache
-    const __nv_bfloat16* v;
-    int64_t batch_stride, head_stride;
-    const int32_t* table;     // paged: [batch][max_blocks]
-    int block, max_blocks, n_blocks;
-    int window, sinks, prefix;
-    float scale;
+    float* part_o;                          // [row][d], then per row (m, l)
+    float2* part_ml;
     int32_t* status;
-    AttendSeq seq[MK_ATTEND_MAX_BATCH];
+};
+template <int SEGS>
+struct AttendParams : AttendCommon {
+    AttendSeg seg[SEGS];
 };
 
-// One warp per (token, head): one pass over the visible positions with a running maximum and sum.
-__global__ void __launch_bounds__(128) attend_simple_kernel(const __grid_constant__ AttendParams p) {
+// The key tiles a block of queries at positions [t0, t1] of a segment sees, in two ranges of positions:
+// [0, sink_end) and [low, end)
+struct KeyRange {
+    int sink_end, low, end;
+    int sink_tiles, first, count;   // tiles of the sinks, first tile of the window, tiles in all
+    __device__ __forceinline__ KeyRange(const AttendSeg& s, int t0, int t1, int window, int sinks) {
+        const bool causal = s.pos0 != kNoCausal;
+        end = causal ? min(t1 + 1, s.key1) : s.key1;
+        low = window ? max(t0 - window + 1, s.key0) : s.key0;
+        sink_end = window ? min(sinks, end) : 0;
+        if (sink_end >= low) { sink_end = 0; low = s.key0; }   // they meet: one range
+        sink_tiles = (sink_end + kKeys - 1) / kKeys;
+        first = max(low / kKeys, sink_tiles);
+        count = end > low ? sink_tiles + max(0, (end + kKeys - 1) / kKeys - first) : 0;
+    }
+    __device__ __forceinline__ int tile(int i) const { return i < sink_tiles ? i : first + i - sink_tiles; }
+    __device__ __forceinline__ bool whole(int k0, int n) const {   // every position of [k0, k0 + n) is seen by some query
+        return (k0 >= low && k0 + n <= end) || k0 + n <= sink_end;
+    }
+    __device__ __forceinline__ bool any(int k0, int n) const { return k0 < sink_end || (k0 + n > low && k0 < end); }
+    __device__ __forceinline__ bool has(int k) const { return k < sink_end || (k >= low && k < end); }
+};
+
+template <int D>
+struct AttendTile {
+    static constexpr int kSub = D < 64 ? D : 64;                // elements of a swizzled row
+    static constexpr int kSubs = D / kSub;
+    static constexpr int kRowBytes = kSub * 2;
+    static constexpr int kTileBytes = kKeys * D * 2;            // 128 rows of q, K or V
+    static constexpr int kKStages = D == 128 ? 1 : 3, kVStages = D == 128 ? 1 : 2;
+    static constexpr int kSmem = kTileBytes * (1 + kKStages + kVStages) + 1024;
+    // tensor memory: scores, output, softmax weights (two bf16 a column; at D = 128 over the scores' columns)
+    static constexpr int kS = 0, kO = 128, kP = D == 128 ? 0 : 192;
+    static constexpr bool kShareSP = D == 128;
+    static constexpr int kFlags = 8;                            // ring of the copies' skip masks
+};
+
+__device__ __forceinline__ float exp2_approx(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+// One pass over the key tiles: S = q K^T on the tensor cores into tensor memory, one thread per row turns its 128
+// scores into weights exp2(scale_log2 (s - m)) with a running reference m, writes them back as bf16, and
+// O += P V runs with P read from tensor memory.  m follows the row's maximum only when that rises by more
+// than 8 (in powers of two): until then weights stay below 2^8, and O need not be rescaled.  Two CTAs
+// share an SM, so one's products run while the other's threads are at their exponentials.
+// Warps 0-3: softmax, a row per thread.  Warp 4: TMA producer.  Warp 5: tensor memory and MMA issue.
+template <int D, int SEGS>
+__global__ void __launch_bounds__(192, 2)
+attend_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
+              const __grid_constant__ CUtensorMap map_v, const __grid_constant__ AttendParams<SEGS> p) {
+    using T = AttendTile<D>;
+    extern __shared__ uint8_t raw[];
+    __shared__ uint64_t bars[1 + 2 * T::kKStages + 2 * T::kVStages + 5];
+    __shared__ uint32_t tmem_at, skips[T::kFlags];
+    __shared__ int abort_flag;
+    volatile int* abort_word = &abort_flag;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t base = (sm::smem(raw) + 1023u) & ~1023u;
+    const uint32_t q_at = base, k_at = base + T::kTileBytes, v_at = k_at + T::kKStages * T::kTileBytes;
+    const uint32_t bar0 = sm::smem(bars);
+    const uint32_t q_full = bar0;
+    auto k_full = [&](int s) { return bar0 + 8u * (1 + s); };
+    auto k_empty = [&](int s) { return bar0 + 8u * (1 + T::kKStages + s); };
+    auto v_full = [&](int s) { return bar0 + 8u * (1 + 2 * T::kKStages + s); };
+    auto v_empty = [&](int s) { return bar0 + 8u * (1 + 2 * T::kKStages + T::kVStages + s); };
+    constexpr int kMore = 1 + 2 * T::kKStages + 2 * T::kVStages;
+    const uint32_t s_full = bar0 + 8u * kMore, s_free = s_full + 8u, p_ready = s_full + 16u, pv_done = s_full + 24u, drained = s_full + 32u;
+
+    // the item: (segment, block of queries -- the last ones, which see most, first --, KV head, share)
+    int si = 0;
+    {
+        int lo = 0, hi = p.segs - 1;
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (int(blockIdx.x) >= p.seg[mid].item0) lo = mid;
+            else hi = mid - 1;
+        }
+        si = lo;
+    }
+    const AttendSeg seg = p.seg[si];
+    const int item = int(blockIdx.x) - seg.item0;
+    const int share = item % seg.splits, g = item / seg.splits % p.nkv;
+    const int blocks = (seg.n + p.block_tokens - 1) / p.block_tokens;
+    const int tok0 = (blocks - 1 - item / (seg.splits * p.nkv)) * p.block_tokens;   // within the segment
+    const int toks = min(p.block_tokens, seg.n - tok0), rows = toks * p.group;
+    const bool causal = seg.pos0 != kNoCausal;
+    const int t0 = causal ? seg.pos0 + tok0 : 0, t1 = t0 + toks - 1;
+    const KeyRange range(seg, t0, t1, p.window, p.sinks);
+    const int first = int(int64_t(range.count) * share / seg.splits), n = int(int64_t(range.count) * (share + 1) / seg.splits) - first;
+    const int warps = (rows + 31) / 32;   // softmax warps with a row
+
+    if (threadIdx.x == 0) {
+        sm::bar_init(q_full, 1);
+        for (int s = 0; s < T::kKStages; ++s) { sm::bar_init(k_full(s), 1); sm::bar_init(k_empty(s), 1); }
+        for (int s = 0; s < T::kVStages; ++s) { sm::bar_init(v_full(s), 1); sm::bar_init(v_empty(s), 1); }
+        sm::bar_init(s_full, 1);
+        sm::bar_init(s_free, uint32_t(warps));
+        sm::bar_init(p_ready, uint32_t(warps));
+        sm::bar_init(pv_done, 1);
+        sm::bar_init(drained, 1);
+        abort_flag = 0;
+        sm::bar_fence_init();
+        sm::tma_prefetch_map(&map_q);
+        sm::tma_prefetch_map(&map_k);
+        sm::tma_prefetch_map(&map_v);
+    }
+    if (warp == 5) sm::tmem_alloc(sm::smem(&tmem_at), 256);
+    sm::tc_fence_before();
+    __syncthreads();
+    sm::tc_fence_after();
+    const uint32_t tmem = tmem_at;
+    sm::pdl_trigger();
+    sm::pdl_wait();
+
+    if (warp == 4) {
+        if (lane == 0 && n > 0) {
+            sm::bar_expect(q_full, uint32_t(p.block_tokens * p.group * D * 2));
+            for (int c = 0; c < T::kSubs; ++c)
+                sm::tma_load_3d(q_at + c * kBlockRows * T::kRowBytes, &map_q, q_full, c * T::kSub, g * p.group, seg.q0 + tok0);
+            bool ok = true;
+            int j = 0, jv = 0;   // tiles whose K, whose V copies are on their way
+            const int parts = p.table ? kKeys / p.box : 1;
+            const int32_t* table = p.table + int64_t(seg.cache) * p.max_blocks;
+            for (; j < n && ok; ++j) {
+                const int k0 = range.tile(first + j) * kKeys;
+                int at[16];
+                uint32_t skip = 0;   // bit: that part is not copied (nothing there is seen, or its block is not in the pool)
+                if (p.table) {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        at[i] = 0;
+                        if (i >= parts) continue;
+                        const int pos = k0 + i * p.box;
+                        const bool want = range.any(pos, p.box);
+                        const int b = want ? __ldg(table + pos / p.block) : 0;
+                        const bool good = unsigned(b) < unsigned(p.n_blocks);
+                        if (want && !good && p.status) *p.status = MK_ERR_BOUNDS;
+                        if (want && good) at[i] = b * p.block + pos % p.block;
+                        else skip |= 1u << i;
+                    }
+                }
+                skips[j % T::kFlags] = skip;
+                const uint32_t bytes = uint32_t(p.table ? (parts - __popc(skip)) * p.box : kKeys) * D * 2;
+                auto copy = [&](const CUtensorMap* map, uint32_t dst, uint32_t bar) {
+                    sm::bar_expect(bar, bytes);
+                    if (!p.table) {
+                        for (int c = 0; c < T::kSubs; ++c)
+                            sm::tma_load_4d(dst + c * kKeys * T::kRowBytes, map, bar, c * T::kSub, k0, g, seg.cache);
+                        return;
+                    }
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        if (i < parts && !(skip >> i & 1u))
+                            for (int c = 0; c < T::kSubs; ++c)
+                                sm::tma_load_4d(dst + (c * kKeys + i * p.box) * T::kRowBytes, map, bar, c * T::kSub, at[i], g, 0);
+                };
+                const int ks = j % T::kKStages, vs = j % T::kVStages;
+                if (j >= T::kKStages && !(ok = sm::bar_wait(k_empty(ks), uint32_t(j / T::kKStages - 1) & 1u, abort_word, p.status))) break;
+                copy(&map_k, k_at + ks * T::kTileBytes, k_full(ks));
+                if (j >= T::kVStages && !(ok = sm::bar_wait(v_empty(vs), uint32_t(j / T::kVStages - 1) & 1u, abort_word, p.status))) { ++j; break; }
+                copy(&map_v, v_at + vs * T::kTileBytes, v_full(vs));
+                jv = j + 1;
+            }
+            if (*abort_word) {   // the copies in flight land before the CTA gives its shared memory back
+                sm::bar_drain(q_full, 0);
+                for (int i = max(0, j - T::kKStages); i < j; ++i) sm::bar_drain(k_full(i % T::kKStages), uint32_t(i / T::kKStages) & 1u);
+                for (int i = max(0, jv - T::kVStages); i < jv; ++i) sm::bar_drain(v_full(i % T::kVStages), uint32_t(i / T::kVStages) & 1u);
+            }
+        }
+        __syncwarp();
+    } else if (warp == 5) {
+        if (lane == 0 && n > 0) {
+            constexpr uint32_t idesc_s = sm::mma_idesc(128, kKeys), idesc_o = sm::mma_idesc(128, D, true);
+            auto k_desc = [&](uint32_t tile, int step) {   // 16 elements of the head dimension from 16 * step
+                const uint32_t at = tile + step * 16 / T::kSub * (kKeys * T::kRowBytes) + step * 16 % T::kSub * 2;
+                return D == 32 ? sm::desc_k_sw64(at) : sm::desc_k_sw128(at);
+            };
+            auto scores = [&](int j) {
+                const int s = j % T::kKStages;
+                if (!sm::bar_wait(k_full(s), uint32_t(j / T::kKStages) & 1u, abort_word, p.status)) return false;
+                sm::tc_fence_after();
+#pragma unroll
+                for (int i = 0; i < D / 16; ++i)
+                    sm::mma_ss(tmem + T::kS, k_desc(q_at, i), k_desc(k_at + s * T::kTileBytes, i), idesc_s, i > 0);
+                sm::mma_commit(s_full);
+                sm::mma_commit(k_empty(s));
+                return true;
+            };
+            bool ok = sm::bar_wait(q_full, 0, abort_word, p.status) && scores(0);
+            for (int j = 0; j < n && ok; ++j) {
+                if (!T::kShareSP && j + 1 < n)   // the next scores as soon as these are in registers
+                    if (!(ok = sm::bar_wait(s_free, uint32_t(j) & 1u, abort_word, p.status) && scores(j + 1))) break;
+                const int s = j % T::kVStages;
+                if (!(ok = sm::bar_wait(p_ready, uint32_t(j) & 1u, abort_word, p.status) &&
+                           sm::bar_wait(v_full(s), uint32_t(j / T::kVStages) & 1u, abort_word, p.status)))
+                    break;
+                sm::tc_fence_after();
+#pragma unroll
+                for (int i = 0; i < kKeys / 16; ++i) {   // 16 keys: 8 columns of P, two groups of 8 rows of V
+                    const uint32_t at = v_at + s * T::kTileBytes + i * 16 * T::kRowBytes;
+                    sm::mma_ts(tmem + T::kO, tmem + T::kP + i * 8,
+                               D == 32 ? sm::desc_mn_sw64(at) : sm::desc_mn_sw128(at, kKeys * T::kRowBytes), idesc_o, j > 0 || i > 0);
+                }
+                sm::mma_commit(pv_done);
+                sm::mma_commit(v_empty(s));
+                if (T::kShareSP && j + 1 < n)   // the weights share the scores' columns: read first
+                    ok = sm::bar_wait(pv_done, uint32_t(j) & 1u, abort_word, p.status) && scores(j + 1);
+            }
+            if (*abort_word) { sm::mma_commit(drained); sm::bar_drain(drained, 0); }
+        }
+        __syncwarp();
+    } else if (warp < warps) {
+        const int row = threadIdx.x;
+        const bool live = row < rows;
+        const int tok = tok0 + row / p.group, head = g * p.group + row % p.group;
+        const int t = causal ? seg.pos0 + tok : seg.key1 - 1;
+        const int low = p.window ? max(t - p.window + 1, seg.key0) : seg.key0;
+        const int sinks = p.window ? p.sinks : 0;
+        const uint32_t lanes = uint32_t(warp * 32) << 16;
+        const float c = p.scale_log2;
+        float m = -INFINITY, l = 0.f;   // the reference (unscaled) and the weights' sum
+        bool ok = true;
+        for (int j = 0; j < n; ++j) {
+            const int k0 = range.tile(first + j) * kKeys;
+            if (!(ok = sm::bar_wait(s_full, uint32_t(j) & 1u, abort_word, p.status))) break;
+            sm::tc_fence_after();
+            uint32_t s[4][32];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) sm::tmem_ld32(tmem + T::kS + lanes + i * 32, s[i]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) sm::tmem_wait_ld(s[i]);
+            sm::tc_fence_before();
+            __syncwarp();
+            if (!T::kShareSP && lane == 0) sm::bar_arrive(s_free);
+            const uint32_t skip = p.table ? skips[j % T::kFlags] : 0u;
+            const bool seen = skip == 0 && k0 + kKeys - 1 <= (causal ? t0 : t) &&
+                              (k0 >= (p.window ? max(t1 - p.window + 1, seg.key0) : seg.key0) || k0 + kKeys <= sinks);
+            if (!seen) {
+                const int hi = t - k0, lo = low - k0, sk = sinks - k0;
+#pragma unroll
+                for (int i = 0; i < kKeys; ++i) {
+                    bool see = i <= hi && (i >= lo || i < sk);
+                    if (skip) see = see && !(skip >> (i / p.box) & 1u);
+                    if (!see) s[i / 32][i % 32] = 0xFF800000u;
+                }
+            }
+            float mx[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                mx[q] = __uint_as_float(s[q][0]);
+#pragma unroll
+                for (int i = 1; i < 32; ++i) mx[q] = fmaxf(mx[q], __uint_as_float(s[q][i]));
+            }
+            const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+            // the products that read the last weights and wrote O are done before either is touched
+            if (j > 0 && !(ok = sm::bar_wait(pv_done, uint32_t(j - 1) & 1u, abort_word, p.status))) break;
+            sm::tc_fence_after();
+            const bool rise = top > m && !((top - m) * c <= 8.f);
+            const float f = rise ? exp2_approx((m - top) * c) : 1.f;   // (0 where m is still -inf)
+            if (rise) m = top;
+            if (j > 0 && __any_sync(0xFFFFFFFFu, rise)) {
+                l *= f;
+#pragma unroll
+                for (int i = 0; i < D; i += 16) {
+                    uint32_t o[16];
+                    sm::tmem_ld16(tmem + T::kO + lanes + i, o);
+                    sm::tmem_wait_ld(o);
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                    sm::tmem_st16(tmem + T::kO + lanes + i, o);
+                }
+            }
+            const float b = m == -INFINITY ? 0.f : m * c;
+            float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                uint32_t w[32];
+#pragma unroll
+                for (int i = 0; i < 32; ++i) {
+                    const int e = h * 64 + 2 * i;
+                    const float x = exp2_approx(fmaf(__uint_as_float(s[e / 32][e % 32]), c, -b));
+                    const float y = exp2_approx(fmaf(__uint_as_float(s[e / 32][e % 32 + 1]), c, -b));
+                    sum[i & 1] += x;
+                    sum[2 + (i & 1)] += y;
+                    w[i] = pack_bf16(x, y);
+                }
+                sm::tmem_st32(tmem + T::kP + lanes + h * 32, w);
+            }
+            l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+            if (skip != 0 || !range.whole(k0, kKeys)) {
+                // rows of V that no query of the block sees may hold anything, and 0 x NaN is NaN: zero them
+                const int vs = j % T::kVStages;
+                if (!(ok = sm::bar_wait(v_full(vs), uint32_t(j / T::kVStages) & 1u, abort_word, p.status))) break;
+                for (int r = threadIdx.x; r < kKeys; r += warps * 32)
+                    if (!range.has(k0 + r) || (skip && (skip >> (r / p.box) & 1u)))
+                        for (int q = 0; q < T::kSubs; ++q)
+                            for (int i = 0; i < T::kRowBytes; i += 16)
+                                asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(
+                                    v_at + vs * T::kTileBytes + (q * kKeys + r) * T::kRowBytes + i), "r"(0) : "memory");
+                sm::fence_async_smem();
+            }
+            sm::tmem_wait_st();
+            sm::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) sm::bar_arrive(p_ready);
+        }
+        if (ok && n > 0) ok = sm::bar_wait(pv_done, uint32_t(n - 1) & 1u, abort_word, p.status);
+        if (ok) {
+            sm::tc_fence_after();
+            const bool whole = seg.splits == 1 && !p.prefix_seg;   // no other item adds to this row
+            const int64_t at = (int64_t(seg.part0) + int64_t(share) * seg.n + tok) * p.nq + head;
+            const float inv = l > 0.f ? 1.f / l : 0.f;
+            if (!whole && live) p.part_ml[at] = make_float2(m * c, l);
+#pragma unroll
+            for (int i = 0; i < D; i += 32) {
+                uint32_t o[32];
+                if (n > 0) {
+                    sm::tmem_ld32(tmem + T::kO + lanes + i, o);
+                    sm::tmem_wait_ld(o);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) o[e] = 0u;
+                }
+                if (!live) continue;
+                if (whole) {
+                    uint4* dst = reinterpret_cast<uint4*>(p.out + (seg.q0 + tok) * p.out_stride + head * D + i);
+#pragma unroll
+                    for (int e = 0; e < 32; e += 8) {
+                        float x[8];
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) x[k] = l > 0.f ? __uint_as_float(o[e + k]) * inv : 0.f;
+                        dst[e / 8] = make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
+                    }
+                } else {
+                    uint4* dst = reinterpret_cast<uint4*>(p.part_o + at * D + i);
+#pragma unroll
+                    for (int e = 0; e < 32; e += 4) dst[e / 4] = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+                }
+            }
+        }
+    }
+    sm::tc_fence_before();
+    __syncthreads();
+    sm::tc_fence_after();
+    if (warp == 5) sm::tmem_free(tmem, 256);
+}
+
+// Joins the parts of a row: with M = max m, out = sum 2^(m - M) o / sum 2^(m - M) l, in order of the
+// shares (the prefix's first).  One warp per (token, head).
+template <int D, int SEGS>
+__global__ void __launch_bounds__(128) attend_merge_kernel(const __grid_constant__ AttendParams<SEGS> p) {
+    sm::pdl_trigger();
+    sm::pdl_wait();
     const int lane = threadIdx.x & 31;
     const int64_t item = int64_t(blockIdx.x) * 4 + (threadIdx.x >> 5);
     if (item >= int64_t(p.tokens) * p.nq) return;
-    const int tok = int(item / p.nq), h = int(item % p.nq), g = h / p.group;
-    int b = 0;
-    while (tok >= p.seq[b].q0 + p.seq[b].n) ++b;
-    const int t = p.seq[b].len - p.seq[b].n + (tok - p.seq[b].q0);
-    const int e = p.d / 32;
-    float q[4], o[4] = {0.f, 0.f, 0.f, 0.f}, m = -INFINITY, l = 0.f;
-    const __nv_bfloat16* qr = p.q + tok * p.q_stride + int64_t(h) * p.d + lane * e;
-    for (int i = 0; i < 4; ++i) q[i] = i < e ? __bfloat162float(qr[i]) * p.scale : 0.f;
-    for (int pos = 0; pos <= t; ++pos) {
-        if (p.window && pos >= p.sinks) pos = max(pos, t - p.window + 1);
-        const int sb = pos < p.prefix ? 0 : b;
-        int64_t at;
-        if (p.table) {
-            const int blk = p.table[int64_t(sb) * p.max_blocks + pos / p.block];
-            if (unsigned(blk) >= unsigned(p.n_blocks)) {
-                if (p.status && lane == 0) *p.status = MK_ERR_BOUNDS;
-                continue;
-            }
-            at = g * p.head_stride + (int64_t(blk) * p.block + pos % p.block) * p.d;
-        } else {
-            at = sb * p.batch_stride + g * p.head_stride + int64_t(pos) * p.d;
+    const int tok = int(item / p.nq), head = int(item % p.nq);
+    int si;
+    {
+        int lo = p.prefix_seg, hi = p.segs - 1;   // the segment of this token
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (tok >= p.seg[mid].q0) lo = mid;
+            else hi = mid - 1;
         }
-        float s = 0.f;
-        for (int i = 0; i < e; ++i) s = fmaf(q[i], __bfloat162float(p.k[at + lane * e + i]), s);
-#pragma unroll
-        for (int x = 16; x; x >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, x);
-        const float mn = fmaxf(m, s), c = expf(m - mn), w = expf(s - mn);
-        l = l * c + w;
-        for (int i = 0; i < e; ++i) o[i] = o[i] * c + w * __bfloat162float(p.v[at + lane * e + i]);
-        m = mn;
+        si = lo;
     }
-    __nv_bfloat16* orow = p.out + tok * p.out_stride + int64_t(h) * p.d + lane * e;
-    for (int i = 0; i < e; ++i) orow[i] = __float2bfloat16_rn(l > 0.f ? o[i] / l : 0.f);
+    const AttendSeg& seg = p.seg[si];
+    const int np = p.prefix_seg ? p.seg[0].splits : 0, n = np + seg.splits;
+    if (n == 1) return;   // its item wrote it
+    auto at = [&](int s) {
+        const int64_t r = s < np ? int64_t(p.seg[0].part0) + int64_t(s) * p.seg[0].n + tok
+                                 : int64_t(seg.part0) + int64_t(s - np) * seg.n + tok - seg.q0;
+        return r * p.nq + head;
+    };
+    float M = -INFINITY;
+    for (int s = lane; s < n; s += 32) {
+        const float2 ml = p.part_ml[at(s)];
+        if (ml.y > 0.f) M = fmaxf(M, ml.x);
+    }
+#pragma unroll
+    for (int x = 16; x; x >>= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, x));
+    constexpr int E = D / 32;
+    float acc[E], total = 0.f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] = 0.f;
+    for (int s0 = 0; s0 < n; s0 += 32) {
+        float w = 0.f;
+        if (s0 + lane < n) {
+            const float2 ml = p.part_ml[at(s0 + lane)];
+            if (ml.y > 0.f) { w = exp2_approx(ml.x - M); total = fmaf(w, ml.y, total); }
+        }
+#pragma unroll 8
+        for (int s = 0; s < min(32, n - s0); ++s) {
+            const float ws = __shfl_sync(0xFFFFFFFFu, w, s);
+            const float* o = p.part_o + at(s0 + s) * D + lane * E;
+            float v[E];
+            if constexpr (E == 4) {
+                const float4 x = *reinterpret_cast<const float4*>(o);
+                v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
+            } else if constexpr (E == 2) {
+                const float2 x = *reinterpret_cast<const float2*>(o);
+                v[0] = x.x; v[1] = x.y;
+            } else {
+                v[0] = *o;
+            }
+#pragma unroll
+            for (int e = 0; e < E; ++e) acc[e] = ws > 0.f ? fmaf(ws, v[e], acc[e]) : acc[e];
+        }
+    }
+#pragma unroll
+    for (int x = 16; x; x >>= 1) total += __shfl_xor_sync(0xFFFFFFFFu, total, x);
+    const float inv = total > 0.f ? 1.f / total : 0.f;
+    __nv_bfloat16* dst = p.out + tok * p.out_stride + head * D + lane * E;
+    if constexpr (E == 1) *dst = __float2bfloat16_rn(acc[0] * inv);
+    else
+#pragma unroll
+        for (int e = 0; e < E; e += 2) *reinterpret_cast<uint32_t*>(dst + e) = pack_bf16(acc[e] * inv, acc[e + 1] * inv);
 }
 
 // Checks the arguments that the workspace's size depends on.
@@ -82,8 +485,8 @@ static mk_status attend_check_shape(const mk_attend_args* a) {
     if (a->batch < 1 || a->batch > MK_ATTEND_MAX_BATCH)
         return fail(MK_ERR_ARG, "attend: batch must be in [1, %d]", MK_ATTEND_MAX_BATCH);
     if (!a->q_lens || !a->kv_lens) return fail(MK_ERR_ARG, "attend: null lengths");
-    if (a->max_seq < 1 || a->layer < 0 || a->window < 0 || a->sinks < 0 || a->shared_prefix < 0)
-        return fail(MK_ERR_ARG, "attend: max_seq must be positive; layer, window, sinks and shared_prefix not negative");
+    if (a->max_seq < 1 || a->max_seq > (1 << 30) || a->layer < 0 || a->window < 0 || a->sinks < 0 || a->shared_prefix < 0)
+        return fail(MK_ERR_ARG, "attend: max_seq must be in [1, 2^30]; layer, window, sinks and shared_prefix not negative");
     if (a->shared_prefix && a->window) return fail(MK_ERR_ARG, "attend: a shared prefix needs window 0");
     if (!(a->scale >= 0.f) || std::isinf(a->scale)) return fail(MK_ERR_ARG, "attend: scale must be finite and not negative");
     int64_t tokens = 0;
@@ -132,41 +535,159 @@ static mk_status attend_check(const mk_attend_args* a) {
     return MK_OK;
 }
 
+// The segments, items and workspace of a call
+struct AttendPlan {
+    int64_t tokens = 0, items = 0, part_rows = 0;   // part_rows: rows of parts in the workspace
+    int segs = 0, prefix_seg = 0;
+    bool merge = false;
+    AttendSeg seg[MK_ATTEND_MAX_BATCH + 1];
+};
+static int64_t attend_tiles(const AttendSeg& s, int t0, int t1, int window, int sinks) {   // key tiles of a block (as KeyRange)
+    const int64_t end = s.pos0 == kNoCausal ? s.key1 : std::min(t1 + 1, s.key1);
+    int64_t low = window ? std::max<int64_t>(int64_t(t0) - window + 1, s.key0) : s.key0;
+    int64_t sink = window ? std::min<int64_t>(sinks, end) : 0;
+    if (sink >= low) { sink = 0; low = s.key0; }
+    const int64_t st = (sink + kKeys - 1) / kKeys;
+    return end > low ? st + std::max<int64_t>(0, (end + kKeys - 1) / kKeys - std::max(low / kKeys, st)) : 0;
+}
+static mk_status attend_plan(const mk_attend_args* a, int sms, AttendPlan& pl) {
+    const int group = a->n_q_heads / a->n_kv_heads, bt = kBlockRows / group;
+    for (int b = 0; b < a->batch; ++b) pl.tokens += a->q_lens[b];
+    if (a->shared_prefix && pl.tokens) {
+        pl.seg[pl.segs++] = {0, int32_t(pl.tokens), kNoCausal, 0, a->shared_prefix, 0, 1, 0, 0};
+        pl.prefix_seg = 1;
+    }
+    int64_t q0 = 0, work = 0;
+    for (int b = 0; b < a->batch; ++b) {
+        const int n = a->q_lens[b];
+        if (n) pl.seg[pl.segs++] = {int32_t(q0), n, a->kv_lens[b] - n, a->shared_prefix, a->kv_lens[b], b, 1, 0, 0};
+        q0 += n;
+    }
+    // key tiles in all (the longest block's for every block of a segment)
+    for (int i = 0; i < pl.segs; ++i) {
+        const AttendSeg& s = pl.seg[i];
+        const int last = (s.n - 1) / bt * bt;
+        const int64_t blocks = (s.n + bt - 1) / bt;
+        work += blocks * a->n_kv_heads * attend_tiles(s, s.pos0 + last, s.pos0 + s.n - 1, a->window, a->sinks);
+    }
+    // a share: what makes two CTAs on every SM, so far as there are tiles
+    const int64_t share = std::max<int64_t>(2, (work + 2 * sms - 1) / (2 * sms));
+    int64_t part = 0;
+    for (int i = 0; i < pl.segs; ++i) {
+        AttendSeg& s = pl.seg[i];
+        const int last = (s.n - 1) / bt * bt;
+        const int64_t blocks = (s.n + bt - 1) / bt;
+        const int64_t tiles = attend_tiles(s, s.pos0 + last, s.pos0 + s.n - 1, a->window, a->sinks);
+        s.splits = int32_t(std::min<int64_t>(std::max<int64_t>(1, (tiles + share - 1) / share), 256));
+        s.item0 = int32_t(pl.items);
+        pl.items += blocks * a->n_kv_heads * s.splits;
+        if (s.splits > 1 || pl.prefix_seg) {
+            pl.merge = true;
+            s.part0 = int32_t(part);
+            part += int64_t(s.splits) * s.n;
+        }
+        if (pl.items > INT_MAX || part > INT_MAX) return fail(MK_ERR_ARG, "attend: too many query tokens");
+    }
+    pl.part_rows = part * a->n_q_heads;
+    return MK_OK;
+}
+static size_t attend_bytes(const AttendPlan& pl, int d) {
+    return align256(size_t(pl.part_rows) * d * 4) + align256(size_t(pl.part_rows) * 8);
+}
+
+template <int D, int SEGS>
+static mk_status attend_launch(const mk_attend_args* a, const AttendCommon& common, const AttendPlan& pl, int device, cudaStream_t stream) {
+    using T = AttendTile<D>;
+    static std::atomic<uint64_t> set{0};
+    mk_status st = op_smem(reinterpret_cast<const void*>(&attend_kernel<D, SEGS>), T::kSmem, device, &set);
+    if (st != MK_OK) return st;
+    AttendParams<SEGS> p;
+    static_cast<AttendCommon&>(p) = common;
+    for (int i = 0; i < pl.segs; ++i) p.seg[i] = pl.seg[i];
+    const mk_kv& kv = *a->kv;
+    CUtensorMap mq, mk_, mv;
+    const int64_t qs = pl.tokens == 1 ? int64_t(p.nq) * D : a->q_stride;
+    const cuuint64_t qd[3] = {cuuint64_t(D), cuuint64_t(p.nq), cuuint64_t(pl.tokens)}, qst[2] = {cuuint64_t(D) * 2, cuuint64_t(qs) * 2};
+    const cuuint32_t qb[3] = {T::kSub, cuuint32_t(p.group), cuuint32_t(p.block_tokens)};
+    const int64_t positions = a->pages ? int64_t(a->pages->n_blocks) * a->pages->block_size : a->max_seq;
+    const int64_t seqs = a->pages ? 1 : a->batch, bs = seqs > 1 ? kv.batch_stride : kv.head_stride * p.nkv;
+    const cuuint64_t kd[4] = {cuuint64_t(D), cuuint64_t(positions), cuuint64_t(p.nkv), cuuint64_t(seqs)};
+    const cuuint64_t kst[3] = {cuuint64_t(D) * 2, cuuint64_t(kv.head_stride) * 2, cuuint64_t(bs) * 2};
+    const cuuint32_t kb[4] = {T::kSub, cuuint32_t(p.table ? p.box : kKeys), 1, 1};
+    const int64_t off = int64_t(a->layer) * kv.layer_stride;
+    if ((st = op_tensor_map(&mq, a->q, 3, qd, qst, qb)) != MK_OK) return st;
+    if ((st = op_tensor_map(&mk_, static_cast<const uint16_t*>(kv.k) + off, 4, kd, kst, kb)) != MK_OK) return st;
+    if ((st = op_tensor_map(&mv, static_cast<const uint16_t*>(kv.v) + off, 4, kd, kst, kb)) != MK_OK) return st;
+    cudaLaunchConfig_t cfg{};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    cfg.stream = stream;
+    cfg.gridDim = dim3(unsigned(pl.items));
+    cfg.blockDim = dim3(192);
+    cfg.dynamicSmemBytes = T::kSmem;
+    MK_CK(cudaLaunchKernelEx(&cfg, &attend_kernel<D, SEGS>, mq, mk_, mv, p));
+    if (pl.merge) {
+        cfg.gridDim = dim3(unsigned((pl.tokens * p.nq + 3) / 4));
+        cfg.blockDim = dim3(128);
+        cfg.dynamicSmemBytes = 0;
+        MK_CK(cudaLaunchKernelEx(&cfg, &attend_merge_kernel<D, SEGS>, p));
+    }
+    return MK_OK;
+}
+template <int D>
+static mk_status attend_launch_segs(const mk_attend_args* a, const AttendCommon& c, const AttendPlan& pl, int device, cudaStream_t stream) {
+    return pl.segs <= 16 ? attend_launch<D, 16>(a, c, pl, device, stream)
+                         : attend_launch<D, MK_ATTEND_MAX_BATCH + 1>(a, c, pl, device, stream);
+}
+
 }  // namespace mk
 
 using namespace mk;
 
 extern "C" size_t mk_attend_workspace(const mk_attend_args* a) {
+    int device = 0, sms = 0;
+    AttendPlan pl;
     if (attend_check_shape(a) != MK_OK) return 0;
-    return 0;
+    bool any = false;
+    for (int b = 0; b < a->batch; ++b) any = any || a->q_lens[b] > 0;
+    if (!any || op_device(&device, &sms) != MK_OK || attend_plan(a, sms, pl) != MK_OK) return 0;
+    return attend_bytes(pl, a->head_dim);
 }
 
 extern "C" mk_status mk_attend(const mk_attend_args* a, void* workspace, size_t workspace_bytes, void* stream) {
-    const mk_status st = attend_check(a);
+    mk_status st = attend_check(a);
     if (st != MK_OK) return st;
-    (void)workspace; (void)workspace_bytes;
-    AttendParams p{};
-    p.nq = a->n_q_heads; p.nkv = a->n_kv_heads; p.group = p.nq / p.nkv; p.d = a->head_dim; p.batch = a->batch;
-    for (int b = 0; b < a->batch; ++b) {
-        p.seq[b] = {p.tokens, a->q_lens[b], a->kv_lens[b], 0};
-        p.tokens += a->q_lens[b];
-    }
-    if (p.tokens == 0) return MK_OK;
-    p.q = static_cast<const __nv_bfloat16*>(a->q);
-    p.out = static_cast<__nv_bfloat16*>(a->out);
-    p.q_stride = a->q_stride; p.out_stride = a->out_stride;
-    p.k = static_cast<const __nv_bfloat16*>(a->kv->k) + a->layer * a->kv->layer_stride;
-    p.v = static_cast<const __nv_bfloat16*>(a->kv->v) + a->layer * a->kv->layer_stride;
-    p.batch_stride = a->kv->batch_stride; p.head_stride = a->kv->head_stride;
+    bool any = false;
+    for (int b = 0; b < a->batch; ++b) any = any || a->q_lens[b] > 0;
+    if (!any) return MK_OK;
+    int device = 0, sms = 0;
+    AttendPlan pl;
+    if ((st = op_device(&device, &sms)) != MK_OK || (st = attend_plan(a, sms, pl)) != MK_OK) return st;
+    const size_t need = attend_bytes(pl, a->head_dim);
+    if (need > 0 && (!workspace || !op_aligned(workspace, 256))) return fail(MK_ERR_ARG, "attend: workspace null or not 256-byte aligned");
+    if (need > workspace_bytes)
+        return fail(MK_ERR_CAPACITY, "attend: workspace of %zu bytes, %zu needed (mk_attend_workspace)", workspace_bytes, need);
+    AttendCommon p{};
+    p.nq = a->n_q_heads; p.nkv = a->n_kv_heads; p.group = p.nq / p.nkv; p.block_tokens = kBlockRows / p.group;
+    p.tokens = int32_t(pl.tokens); p.segs = pl.segs; p.prefix_seg = pl.prefix_seg;
+    p.window = std::min(a->window, 1 << 30); p.sinks = std::min(a->sinks, 1 << 30);   // (positions stay below 2^30)
+    p.scale_log2 = float((a->scale != 0.f ? double(a->scale) : 1.0 / std::sqrt(double(a->head_dim))) * 1.4426950408889634);
     if (a->pages) {
         p.table = a->pages->block_table; p.block = a->pages->block_size;
         p.max_blocks = a->pages->max_blocks; p.n_blocks = a->pages->n_blocks;
+        p.box = 8;
+        while (p.box < kKeys && p.block % (2 * p.box) == 0) p.box *= 2;
     }
-    p.window = a->window; p.sinks = a->sinks; p.prefix = a->shared_prefix;
-    p.scale = a->scale != 0.f ? a->scale : float(1.0 / std::sqrt(double(p.d)));
+    p.out = static_cast<__nv_bfloat16*>(a->out);
+    p.out_stride = a->out_stride;
+    p.part_o = static_cast<float*>(workspace);
+    p.part_ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) + align256(size_t(pl.part_rows) * a->head_dim * 4));
     p.status = a->status;
-    const int64_t warps = int64_t(p.tokens) * p.nq;
-    attend_simple_kernel<<<unsigned((warps + 3) / 4), 128, 0, static_cast<cudaStream_t>(stream)>>>(p);
-    MK_CK(cudaGetLastError());
-    return MK_OK;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (a->head_dim == 32) return attend_launch_segs<32>(a, p, pl, device, s);
+    if (a->head_dim == 64) return attend_launch_segs<64>(a, p, pl, device, s);
+    return attend_launch_segs<128>(a, p, pl, device, s);
 }

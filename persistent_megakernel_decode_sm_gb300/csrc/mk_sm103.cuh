@@ -43,7 +43,7 @@ __device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
 // waiting thread raises the CTA's abort word and the caller's status, every role leaves its loop,
 // and the CTA drains its copies and products in flight before it frees its tensor memory.
 constexpr uint64_t kWaitNs = 2000000000ull;
-__device__ __noinline__ bool bar_wait_slow(uint32_t bar, uint32_t parity, volatile int* abort_word, int32_t* status) {
+static __device__ __noinline__ bool bar_wait_slow(uint32_t bar, uint32_t parity, volatile int* abort_word, int32_t* status) {
     const uint64_t t0 = timer_ns();
     while (true) {
         for (int i = 0; i < 64; ++i)
@@ -126,6 +126,19 @@ __device__ __forceinline__ void tmem_wait_ld(uint32_t (&r)[16]) {
     asm volatile("tcgen05.wait::ld.sync.aligned;" : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]) :: "memory");
 }
 
+__device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(addr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+        : "memory");
+}
+
+__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&r)[16]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(addr),
+                 "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+                 : "memory");
+}
+
 // ---- matrix products (bf16 operands, fp32 accumulators) ----------------------------------------
 // Shared-memory operand: a tile of rows of 64 bf16 (128 bytes) in the 128-byte swizzle the TMA
 // writes, 8 rows (1024 bytes) apart from the next 8; the tile starts on a 1024-byte boundary.  A step
@@ -133,6 +146,21 @@ __device__ __forceinline__ void tmem_wait_ld(uint32_t (&r)[16]) {
 __device__ __forceinline__ uint64_t desc_k_sw128(uint32_t addr) {
     return uint64_t((addr & 0x3FFFFu) >> 4) | (uint64_t(1) << 16) | (uint64_t(1024 >> 4) << 32) | (uint64_t(1) << 46) |
            (uint64_t(2) << 61);
+}
+// The same for rows of 32 bf16 in the 64-byte swizzle (8 rows: 512 bytes).
+__device__ __forceinline__ uint64_t desc_k_sw64(uint32_t addr) {
+    return uint64_t((addr & 0x3FFFFu) >> 4) | (uint64_t(1) << 16) | (uint64_t(512 >> 4) << 32) | (uint64_t(1) << 46) |
+           (uint64_t(4) << 61);
+}
+// The transposed reading of such tiles (the contraction runs over the rows): 8 rows are one group
+// along the contraction; the next 64 columns start `next` bytes further.
+__device__ __forceinline__ uint64_t desc_mn_sw128(uint32_t addr, uint32_t next) {
+    return uint64_t((addr & 0x3FFFFu) >> 4) | (uint64_t(next >> 4) << 16) | (uint64_t(1024 >> 4) << 32) | (uint64_t(1) << 46) |
+           (uint64_t(2) << 61);
+}
+__device__ __forceinline__ uint64_t desc_mn_sw64(uint32_t addr) {
+    return uint64_t((addr & 0x3FFFFu) >> 4) | (uint64_t(1) << 16) | (uint64_t(512 >> 4) << 32) | (uint64_t(1) << 46) |
+           (uint64_t(4) << 61);
 }
 // Instruction descriptor: D fp32, A and B bf16, both K-major unless told otherwise, N columns, M rows
 __host__ __device__ constexpr uint32_t mma_idesc(int M, int N, bool b_mn_major = false) {
@@ -142,6 +170,12 @@ __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint3
     asm volatile(
         "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
         "l"(a), "l"(b), "r"(idesc), "r"(uint32_t(accumulate)) : "memory");
+}
+// A from tensor memory: lane = row, a 32-bit column = two neighbouring elements along the contraction
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool accumulate) {
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(uint32_t(accumulate)) : "memory");
 }
 __device__ __forceinline__ void mma_commit(uint32_t bar) {   // arrives on bar once every earlier product is done
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
