@@ -33,7 +33,7 @@ struct AttendCommon {
     int32_t window, sinks;
     float scale_log2;                       // scale / ln 2
     const int32_t* table;                   // paged: [batch][max_blocks]
-    int32_t block, max_blocks, n_blocks, box;   // box: positions one copy takes (a power of two that divides block)
+    int32_t block, max_blocks, n_blocks, box_log2;   // positions one copy takes: a power of two that divides block
     __nv_bfloat16* out;
     int64_t out_stride;
     float* part_o;                          // [row][d], then per row (m, l)
@@ -92,6 +92,28 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
 }
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+// Two fp32 operations in one instruction
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 r;
+    asm("{\n .reg .b64 a, b, c, d;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n mov.b64 c, {%6, %7};\n"
+        " fma.rn.f32x2 d, a, b, c;\n mov.b64 {%0, %1}, d;\n}\n"
+        : "=f"(r.x), "=f"(r.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return r;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    float2 r;
+    asm("{\n .reg .b64 a, b, d;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n add.rn.f32x2 d, a, b;\n mov.b64 {%0, %1}, d;\n}\n"
+        : "=f"(r.x), "=f"(r.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return r;
+}
+// The low n bits set (none for n <= 0, all for n >= 32)
+__device__ __forceinline__ uint32_t low_bits(int n) { return n >= 32 ? 0xFFFFFFFFu : n <= 0 ? 0u : (1u << n) - 1u; }
 
 // One pass over the key tiles: S = q K^T on the tensor cores into tensor memory, one thread per row turns its 128
 // scores into weights exp2(scale_log2 (s - m)) with a running reference m, writes them back as bf16, and
@@ -168,55 +190,49 @@ attend_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
     sm::pdl_wait();
 
     if (warp == 4) {
-        if (lane == 0 && n > 0) {
-            sm::bar_expect(q_full, uint32_t(p.block_tokens * p.group * D * 2));
-            for (int c = 0; c < T::kSubs; ++c)
-                sm::tma_load_3d(q_at + c * kBlockRows * T::kRowBytes, &map_q, q_full, c * T::kSub, g * p.group, seg.q0 + tok0);
-            bool ok = true;
-            int j = 0, jv = 0;   // tiles whose K, whose V copies are on their way
-            const int parts = p.table ? kKeys / p.box : 1;
+        if (n > 0) {
+            if (lane == 0) {
+                sm::bar_expect(q_full, uint32_t(p.block_tokens * p.group * D * 2));
+                for (int c = 0; c < T::kSubs; ++c)
+                    sm::tma_load_3d(q_at + c * kBlockRows * T::kRowBytes, &map_q, q_full, c * T::kSub, g * p.group, seg.q0 + tok0);
+            }
+            // a key tile is one copy, or one for each part of it that lies in one block: a lane's each
+            const int box = p.table ? 1 << p.box_log2 : kKeys, parts = kKeys / box;
             const int32_t* table = p.table + int64_t(seg.cache) * p.max_blocks;
-            for (; j < n && ok; ++j) {
-                const int k0 = range.tile(first + j) * kKeys;
-                int at[16];
-                uint32_t skip = 0;   // bit: that part is not copied (nothing there is seen, or its block is not in the pool)
-                if (p.table) {
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        at[i] = 0;
-                        if (i >= parts) continue;
-                        const int pos = k0 + i * p.box;
-                        const bool want = range.any(pos, p.box);
-                        const int b = want ? __ldg(table + pos / p.block) : 0;
-                        const bool good = unsigned(b) < unsigned(p.n_blocks);
-                        if (want && !good && p.status) *p.status = MK_ERR_BOUNDS;
-                        if (want && good) at[i] = b * p.block + pos % p.block;
-                        else skip |= 1u << i;
-                    }
+            const int cache = p.table ? 0 : seg.cache;
+            int j = 0, jv = 0;   // tiles whose K, whose V copies are on their way
+            for (; j < n; ++j) {
+                const int pos = range.tile(first + j) * kKeys + lane * box;
+                const bool want = lane < parts && range.any(pos, box);
+                int at = pos;
+                bool good = want;
+                if (p.table && want) {
+                    const int b = __ldg(table + pos / p.block);
+                    good = unsigned(b) < unsigned(p.n_blocks);
+                    if (!good && p.status) *p.status = MK_ERR_BOUNDS;
+                    at = b * p.block + pos % p.block;
                 }
-                skips[j % T::kFlags] = skip;
-                const uint32_t bytes = uint32_t(p.table ? (parts - __popc(skip)) * p.box : kKeys) * D * 2;
-                auto copy = [&](const CUtensorMap* map, uint32_t dst, uint32_t bar) {
-                    sm::bar_expect(bar, bytes);
-                    if (!p.table) {
-                        for (int c = 0; c < T::kSubs; ++c)
-                            sm::tma_load_4d(dst + c * kKeys * T::kRowBytes, map, bar, c * T::kSub, k0, g, seg.cache);
-                        return;
+                const uint32_t copied = __ballot_sync(0xFFFFFFFFu, good);
+                if (lane == 0) skips[j % T::kFlags] = ~copied & ((1u << parts) - 1u);
+                const uint32_t bytes = uint32_t(__popc(copied) * box * D * 2);
+                auto copy = [&](const CUtensorMap* map, uint32_t dst, uint32_t full, uint32_t empty, int stages) {
+                    int ok = 1;
+                    if (lane == 0) {
+                        if (j >= stages) ok = sm::bar_wait(empty, uint32_t(j / stages - 1) & 1u, abort_word, p.status);
+                        if (ok) sm::bar_expect(full, bytes);
                     }
-#pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        if (i < parts && !(skip >> i & 1u))
-                            for (int c = 0; c < T::kSubs; ++c)
-                                sm::tma_load_4d(dst + (c * kKeys + i * p.box) * T::kRowBytes, map, bar, c * T::kSub, at[i], g, 0);
+                    if (!__shfl_sync(0xFFFFFFFFu, ok, 0)) return false;
+                    if (good)
+                        for (int c = 0; c < T::kSubs; ++c)
+                            sm::tma_load_4d(dst + (c * kKeys + lane * box) * T::kRowBytes, map, full, c * T::kSub, at, g, cache);
+                    return true;
                 };
                 const int ks = j % T::kKStages, vs = j % T::kVStages;
-                if (j >= T::kKStages && !(ok = sm::bar_wait(k_empty(ks), uint32_t(j / T::kKStages - 1) & 1u, abort_word, p.status))) break;
-                copy(&map_k, k_at + ks * T::kTileBytes, k_full(ks));
-                if (j >= T::kVStages && !(ok = sm::bar_wait(v_empty(vs), uint32_t(j / T::kVStages - 1) & 1u, abort_word, p.status))) { ++j; break; }
-                copy(&map_v, v_at + vs * T::kTileBytes, v_full(vs));
+                if (!copy(&map_k, k_at + ks * T::kTileBytes, k_full(ks), k_empty(ks), T::kKStages)) break;
+                if (!copy(&map_v, v_at + vs * T::kTileBytes, v_full(vs), v_empty(vs), T::kVStages)) { ++j; break; }
                 jv = j + 1;
             }
-            if (*abort_word) {   // the copies in flight land before the CTA gives its shared memory back
+            if (lane == 0 && *abort_word) {   // the copies in flight land before the CTA gives its shared memory back
                 sm::bar_drain(q_full, 0);
                 for (int i = max(0, j - T::kKStages); i < j; ++i) sm::bar_drain(k_full(i % T::kKStages), uint32_t(i / T::kKStages) & 1u);
                 for (int i = max(0, jv - T::kVStages); i < jv; ++i) sm::bar_drain(v_full(i % T::kVStages), uint32_t(i / T::kVStages) & 1u);
@@ -287,24 +303,28 @@ attend_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
             sm::tc_fence_before();
             __syncwarp();
             if (!T::kShareSP && lane == 0) sm::bar_arrive(s_free);
-            const uint32_t skip = p.table ? skips[j % T::kFlags] : 0u;
+            const uint32_t skip = skips[j % T::kFlags];
             const bool seen = skip == 0 && k0 + kKeys - 1 <= (causal ? t0 : t) &&
                               (k0 >= (p.window ? max(t1 - p.window + 1, seg.key0) : seg.key0) || k0 + kKeys <= sinks);
             if (!seen) {
-                const int hi = t - k0, lo = low - k0, sk = sinks - k0;
+                const int hi = t - k0 + 1, lo = low - k0, sk = sinks - k0;
 #pragma unroll
-                for (int i = 0; i < kKeys; ++i) {
-                    bool see = i <= hi && (i >= lo || i < sk);
-                    if (skip) see = see && !(skip >> (i / p.box) & 1u);
-                    if (!see) s[i / 32][i % 32] = 0xFF800000u;
+                for (int q = 0; q < 4; ++q) {   // 32 keys: a bit for each that this row sees
+                    uint32_t see = low_bits(hi - 32 * q) & (~low_bits(lo - 32 * q) | low_bits(sk - 32 * q));
+                    if (skip)
+                        for (int i = 0; i < 4; ++i)
+                            if (skip >> ((32 * q + 8 * i) >> p.box_log2) & 1u) see &= ~(0xFFu << (8 * i));
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        if (!(see >> i & 1u)) s[q][i] = 0xFF800000u;
                 }
             }
             float mx[4];
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-                mx[q] = __uint_as_float(s[q][0]);
+                mx[q] = fmaxf(__uint_as_float(s[q][0]), __uint_as_float(s[q][1]));
 #pragma unroll
-                for (int i = 1; i < 32; ++i) mx[q] = fmaxf(mx[q], __uint_as_float(s[q][i]));
+                for (int i = 2; i < 32; i += 2) mx[q] = max3(mx[q], __uint_as_float(s[q][i]), __uint_as_float(s[q][i + 1]));
             }
             const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
             // the products that read the last weights and wrote O are done before either is touched
@@ -326,28 +346,27 @@ attend_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
                 }
             }
             const float b = m == -INFINITY ? 0.f : m * c;
-            float sum[4] = {0.f, 0.f, 0.f, 0.f};
+            float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                uint32_t w[32];
+            for (int q = 0; q < 4; ++q) {
+                uint32_t w[16];
 #pragma unroll
-                for (int i = 0; i < 32; ++i) {
-                    const int e = h * 64 + 2 * i;
-                    const float x = exp2_approx(fmaf(__uint_as_float(s[e / 32][e % 32]), c, -b));
-                    const float y = exp2_approx(fmaf(__uint_as_float(s[e / 32][e % 32 + 1]), c, -b));
-                    sum[i & 1] += x;
-                    sum[2 + (i & 1)] += y;
-                    w[i] = pack_bf16(x, y);
+                for (int i = 0; i < 16; ++i) {
+                    float2 x = make_float2(__uint_as_float(s[q][2 * i]), __uint_as_float(s[q][2 * i + 1]));
+                    x = fma2(x, make_float2(c, c), make_float2(-b, -b));
+                    x = make_float2(exp2_approx(x.x), exp2_approx(x.y));
+                    sum[i & 1] = add2(sum[i & 1], x);
+                    w[i] = pack_bf16(x.x, x.y);
                 }
-                sm::tmem_st32(tmem + T::kP + lanes + h * 32, w);
+                sm::tmem_st16(tmem + T::kP + lanes + q * 16, w);
             }
-            l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+            l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
             if (skip != 0 || !range.whole(k0, kKeys)) {
                 // rows of V that no query of the block sees may hold anything, and 0 x NaN is NaN: zero them
                 const int vs = j % T::kVStages;
                 if (!(ok = sm::bar_wait(v_full(vs), uint32_t(j / T::kVStages) & 1u, abort_word, p.status))) break;
                 for (int r = threadIdx.x; r < kKeys; r += warps * 32)
-                    if (!range.has(k0 + r) || (skip && (skip >> (r / p.box) & 1u)))
+                    if (!range.has(k0 + r) || (skip >> (r >> p.box_log2) & 1u))
                         for (int q = 0; q < T::kSubs; ++q)
                             for (int i = 0; i < T::kRowBytes; i += 16)
                                 asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(
@@ -613,7 +632,7 @@ static mk_status attend_launch(const mk_attend_args* a, const AttendCommon& comm
     const int64_t seqs = a->pages ? 1 : a->batch, bs = seqs > 1 ? kv.batch_stride : kv.head_stride * p.nkv;
     const cuuint64_t kd[4] = {cuuint64_t(D), cuuint64_t(positions), cuuint64_t(p.nkv), cuuint64_t(seqs)};
     const cuuint64_t kst[3] = {cuuint64_t(D) * 2, cuuint64_t(kv.head_stride) * 2, cuuint64_t(bs) * 2};
-    const cuuint32_t kb[4] = {T::kSub, cuuint32_t(p.table ? p.box : kKeys), 1, 1};
+    const cuuint32_t kb[4] = {T::kSub, cuuint32_t(p.table ? 1 << p.box_log2 : kKeys), 1, 1};
     const int64_t off = int64_t(a->layer) * kv.layer_stride;
     if ((st = op_tensor_map(&mq, a->q, 3, qd, qst, qb)) != MK_OK) return st;
     if ((st = op_tensor_map(&mk_, static_cast<const uint16_t*>(kv.k) + off, 4, kd, kst, kb)) != MK_OK) return st;
@@ -678,8 +697,8 @@ extern "C" mk_status mk_attend(const mk_attend_args* a, void* workspace, size_t 
     if (a->pages) {
         p.table = a->pages->block_table; p.block = a->pages->block_size;
         p.max_blocks = a->pages->max_blocks; p.n_blocks = a->pages->n_blocks;
-        p.box = 8;
-        while (p.box < kKeys && p.block % (2 * p.box) == 0) p.box *= 2;
+        p.box_log2 = 3;
+        while ((1 << p.box_log2) < kKeys && p.block % (2 << p.box_log2) == 0) ++p.box_log2;
     }
     p.out = static_cast<__nv_bfloat16*>(a->out);
     p.out_stride = a->out_stride;

@@ -57,8 +57,7 @@ static __device__ __noinline__ bool bar_wait_slow(uint32_t bar, uint32_t parity,
     }
 }
 __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile int* abort_word, int32_t* status) {
-    for (int i = 0; i < 8; ++i)
-        if (bar_try(bar, parity)) return true;
+    if (bar_try(bar, parity)) return true;
     return bar_wait_slow(bar, parity, abort_word, status);
 }
 __device__ __forceinline__ void bar_drain(uint32_t bar, uint32_t parity) {   // (after an abort: bounded, no report)
