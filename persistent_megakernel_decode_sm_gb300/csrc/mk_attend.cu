@@ -112,14 +112,19 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
         : "=f"(r.x), "=f"(r.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
     return r;
 }
+// The first 16 of 32 registers to 16 columns of tensor memory
+__device__ __forceinline__ void tmem_st16_head(uint32_t addr, const uint32_t (&r)[32]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(addr),
+                 "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+                 "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]) : "memory");
+}
 // The low n bits set (none for n <= 0, all for n >= 32)
 __device__ __forceinline__ uint32_t low_bits(int n) { return n >= 32 ? 0xFFFFFFFFu : n <= 0 ? 0u : (1u << n) - 1u; }
 
 // One pass over the key tiles: S = q K^T on the tensor cores into tensor memory, one thread per row turns its 128
-// scores into weights exp2(scale_log2 (s - m)) with a running reference m, writes them back as bf16, and
-// O += P V runs with P read from tensor memory.  m follows the row's maximum only when that rises by more
-// than 8 (in powers of two): until then weights stay below 2^8, and O need not be rescaled.  Two CTAs
-// share an SM, so one's products run while the other's threads are at their exponentials.
+// scores into weights exp2(scale_log2 (s - m)) with a reference m (below), writes them back as bf16, and
+// O += P V runs with P read from tensor memory.  Two CTAs share an SM, so one's products run while the
+// other's threads are at their exponentials.
 // Warps 0-3: softmax, a row per thread.  Warp 4: TMA producer.  Warp 5: tensor memory and MMA issue.
 template <int D, int SEGS>
 __global__ void __launch_bounds__(192, 2)
@@ -141,7 +146,7 @@ attend_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
     auto v_full = [&](int s) { return bar0 + 8u * (1 + 2 * T::kKStages + s); };
     auto v_empty = [&](int s) { return bar0 + 8u * (1 + 2 * T::kKStages + T::kVStages + s); };
     constexpr int kMore = 1 + 2 * T::kKStages + 2 * T::kVStages;
-    const uint32_t s_full = bar0 + 8u * kMore, s_free = s_full + 8u, p_ready = s_full + 16u, pv_done = s_full + 24u, drained = s_full + 32u;
+    const uint32_t s_full = bar0 + 8u * kMore, p_ready = s_full + 8u, pv_done = s_full + 16u, drained = s_full + 24u, s_free = s_full + 32u;
 
     // the item: (segment, block of queries -- the last ones, which see most, first --, KV head, share)
     int si = 0;
@@ -171,8 +176,8 @@ attend_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
         for (int s = 0; s < T::kKStages; ++s) { sm::bar_init(k_full(s), 1); sm::bar_init(k_empty(s), 1); }
         for (int s = 0; s < T::kVStages; ++s) { sm::bar_init(v_full(s), 1); sm::bar_init(v_empty(s), 1); }
         sm::bar_init(s_full, 1);
-        sm::bar_init(s_free, uint32_t(warps));
         sm::bar_init(p_ready, uint32_t(warps));
+        sm::bar_init(s_free, uint32_t(warps));
         sm::bar_init(pv_done, 1);
         sm::bar_init(drained, 1);
         abort_flag = 0;
@@ -240,44 +245,53 @@ attend_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
         }
         __syncwarp();
     } else if (warp == 5) {
-        if (lane == 0 && n > 0) {
+        if (n > 0) {
             constexpr uint32_t idesc_s = sm::mma_idesc(128, kKeys), idesc_o = sm::mma_idesc(128, D, true);
-            auto k_desc = [&](uint32_t tile, int step) {   // 16 elements of the head dimension from 16 * step
-                const uint32_t at = tile + step * 16 / T::kSub * (kKeys * T::kRowBytes) + step * 16 % T::kSub * 2;
-                return D == 32 ? sm::desc_k_sw64(at) : sm::desc_k_sw128(at);
-            };
+            const bool leader = sm::elect_one();
+            const uint64_t q_desc = D == 32 ? sm::desc_k_sw64(q_at) : sm::desc_k_sw128(q_at);
+            const uint64_t k_desc = D == 32 ? sm::desc_k_sw64(k_at) : sm::desc_k_sw128(k_at);
+            const uint64_t v_desc = D == 32 ? sm::desc_mn_sw64(v_at) : sm::desc_mn_sw128(v_at, kKeys * T::kRowBytes);
             auto scores = [&](int j) {
                 const int s = j % T::kKStages;
-                if (!sm::bar_wait(k_full(s), uint32_t(j / T::kKStages) & 1u, abort_word, p.status)) return false;
+                if (!sm::bar_wait_warp(k_full(s), uint32_t(j / T::kKStages) & 1u, abort_word, p.status)) return false;
                 sm::tc_fence_after();
+                const uint64_t k = k_desc + uint64_t(s * (T::kTileBytes >> 4));
+                if (leader) {
 #pragma unroll
-                for (int i = 0; i < D / 16; ++i)
-                    sm::mma_ss(tmem + T::kS, k_desc(q_at, i), k_desc(k_at + s * T::kTileBytes, i), idesc_s, i > 0);
-                sm::mma_commit(s_full);
-                sm::mma_commit(k_empty(s));
+                    for (int i = 0; i < D / 16; ++i) {   // 16 elements of the head dimension
+                        const int at = (i * 16 / T::kSub * (kKeys * T::kRowBytes) + i * 16 % T::kSub * 2) >> 4;
+                        sm::mma_ss(tmem + T::kS, q_desc + at, k + at, idesc_s, i > 0);
+                    }
+                    sm::mma_commit(s_full);
+                    sm::mma_commit(k_empty(s));
+                }
+                __syncwarp();
                 return true;
             };
-            bool ok = sm::bar_wait(q_full, 0, abort_word, p.status) && scores(0);
+            bool ok = sm::bar_wait_warp(q_full, 0, abort_word, p.status) && scores(0);
             for (int j = 0; j < n && ok; ++j) {
+                // a tile's weights are written: its scores are done with, the next may come (where the weights
+                // lie over them, once they are read); its product with V is what the next tile's need waits for last
                 if (!T::kShareSP && j + 1 < n)   // the next scores as soon as these are in registers
-                    if (!(ok = sm::bar_wait(s_free, uint32_t(j) & 1u, abort_word, p.status) && scores(j + 1))) break;
-                const int s = j % T::kVStages;
-                if (!(ok = sm::bar_wait(p_ready, uint32_t(j) & 1u, abort_word, p.status) &&
-                           sm::bar_wait(v_full(s), uint32_t(j / T::kVStages) & 1u, abort_word, p.status)))
-                    break;
+                    if (!(ok = sm::bar_wait_warp(s_free, uint32_t(j) & 1u, abort_word, p.status) && scores(j + 1))) break;
+                if (!(ok = sm::bar_wait_warp(p_ready, uint32_t(j) & 1u, abort_word, p.status))) break;
                 sm::tc_fence_after();
+                const int s = j % T::kVStages;
+                if (!(ok = sm::bar_wait_warp(v_full(s), uint32_t(j / T::kVStages) & 1u, abort_word, p.status))) break;
+                sm::tc_fence_after();
+                const uint64_t v = v_desc + uint64_t(s * (T::kTileBytes >> 4));
+                if (leader) {
 #pragma unroll
-                for (int i = 0; i < kKeys / 16; ++i) {   // 16 keys: 8 columns of P, two groups of 8 rows of V
-                    const uint32_t at = v_at + s * T::kTileBytes + i * 16 * T::kRowBytes;
-                    sm::mma_ts(tmem + T::kO, tmem + T::kP + i * 8,
-                               D == 32 ? sm::desc_mn_sw64(at) : sm::desc_mn_sw128(at, kKeys * T::kRowBytes), idesc_o, j > 0 || i > 0);
+                    for (int i = 0; i < kKeys / 16; ++i)   // 16 keys: 8 columns of P, two groups of 8 rows of V
+                        sm::mma_ts(tmem + T::kO, tmem + T::kP + i * 8, v + (i * 16 * T::kRowBytes >> 4), idesc_o, j > 0 || i > 0);
+                    sm::mma_commit(pv_done);
+                    sm::mma_commit(v_empty(s));
                 }
-                sm::mma_commit(pv_done);
-                sm::mma_commit(v_empty(s));
-                if (T::kShareSP && j + 1 < n)   // the weights share the scores' columns: read first
-                    ok = sm::bar_wait(pv_done, uint32_t(j) & 1u, abort_word, p.status) && scores(j + 1);
+                __syncwarp();
+                if (T::kShareSP && j + 1 < n)
+                    ok = sm::bar_wait_warp(pv_done, uint32_t(j) & 1u, abort_word, p.status) && scores(j + 1);
             }
-            if (*abort_word) { sm::mma_commit(drained); sm::bar_drain(drained, 0); }
+            if (*abort_word && leader) { sm::mma_commit(drained); sm::bar_drain(drained, 0); }
         }
         __syncwarp();
     } else if (warp < warps) {
@@ -289,53 +303,52 @@ attend_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
         const int sinks = p.window ? p.sinks : 0;
         const uint32_t lanes = uint32_t(warp * 32) << 16;
         const float c = p.scale_log2;
-        float m = -INFINITY, l = 0.f;   // the reference (unscaled) and the weights' sum
-        bool ok = true;
+        // The reference m of a row's weights exp2((s - m) c) need not be its maximum: the weights' and sums' formats
+        // have fp32's exponents, so any m will do that keeps a tile's sum within 2^-20 .. 2^20 (below, once
+        // some tile's is).  It starts at 0, which holds for scores of ordinary size, and no maximum is taken; a
+        // tile whose sum falls outside is read again, its maximum taken as the new reference.
+        float m = 0.f, l = 0.f;
+        bool set = false;   // some tile of this row counted
+        float high = 8.f / c, deep = -8.f / c;   // (d < 128) a maximum above, or a first one below: the new reference
+        bool ok = true;     // (a wait that ran out shows at the vote of its tile: until then the lanes stay together)
+        const int seen_end = causal ? t0 + 1 : seg.key1;   // keys that every row of the block sees: [seen_low, seen_end), the sinks
+        const int seen_low = p.window ? max(t1 - p.window + 1, seg.key0) : seg.key0;
         for (int j = 0; j < n; ++j) {
             const int k0 = range.tile(first + j) * kKeys;
-            if (!(ok = sm::bar_wait(s_full, uint32_t(j) & 1u, abort_word, p.status))) break;
+            ok = sm::bar_wait_sync(s_full, uint32_t(j) & 1u, abort_word, p.status) && ok;
             sm::tc_fence_after();
+            const uint32_t skip = p.table ? skips[j % T::kFlags] : 0u;
+            const bool seen = skip == 0 && k0 + kKeys <= seen_end && (k0 >= seen_low || k0 + kKeys <= sinks);
+            auto sees = [&](int at) {   // a bit for each of 32 keys from k0 + at: whether this row sees it
+                uint32_t see = low_bits(t - k0 - at + 1) & (~low_bits(low - k0 - at) | low_bits(sinks - k0 - at));
+                if (skip)
+                    for (int i = 0; i < 4; ++i)
+                        if (skip >> ((at + 8 * i) >> p.box_log2) & 1u) see &= ~(0xFFu << (8 * i));
+                return see;
+            };
             uint32_t s[4][32];
+            float total;
+            // (a pair of weights takes the place of a pair of scores)
+            auto weights = [&](bool store) {
+                const float b = m * c;
+                float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-            for (int i = 0; i < 4; ++i) sm::tmem_ld32(tmem + T::kS + lanes + i * 32, s[i]);
+                for (int q = 0; q < 4; ++q) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) sm::tmem_wait_ld(s[i]);
-            sm::tc_fence_before();
-            __syncwarp();
-            if (!T::kShareSP && lane == 0) sm::bar_arrive(s_free);
-            const uint32_t skip = skips[j % T::kFlags];
-            const bool seen = skip == 0 && k0 + kKeys - 1 <= (causal ? t0 : t) &&
-                              (k0 >= (p.window ? max(t1 - p.window + 1, seg.key0) : seg.key0) || k0 + kKeys <= sinks);
-            if (!seen) {
-                const int hi = t - k0 + 1, lo = low - k0, sk = sinks - k0;
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {   // 32 keys: a bit for each that this row sees
-                    uint32_t see = low_bits(hi - 32 * q) & (~low_bits(lo - 32 * q) | low_bits(sk - 32 * q));
-                    if (skip)
-                        for (int i = 0; i < 4; ++i)
-                            if (skip >> ((32 * q + 8 * i) >> p.box_log2) & 1u) see &= ~(0xFFu << (8 * i));
-#pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        if (!(see >> i & 1u)) s[q][i] = 0xFF800000u;
+                    for (int i = 0; i < 16; ++i) {
+                        float2 x = make_float2(__uint_as_float(s[q][2 * i]), __uint_as_float(s[q][2 * i + 1]));
+                        x = fma2(x, make_float2(c, c), make_float2(-b, -b));
+                        x = make_float2(exp2_approx(x.x), exp2_approx(x.y));
+                        sum[i & 1] = add2(sum[i & 1], x);
+                        s[q][i] = pack_bf16(x.x, x.y);
+                    }
+                    if (store) tmem_st16_head(tmem + T::kP + lanes + q * 16, s[q]);
                 }
-            }
-            float mx[4];
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                mx[q] = fmaxf(__uint_as_float(s[q][0]), __uint_as_float(s[q][1]));
-#pragma unroll
-                for (int i = 2; i < 32; i += 2) mx[q] = max3(mx[q], __uint_as_float(s[q][i]), __uint_as_float(s[q][i + 1]));
-            }
-            const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-            // the products that read the last weights and wrote O are done before either is touched
-            if (j > 0 && !(ok = sm::bar_wait(pv_done, uint32_t(j - 1) & 1u, abort_word, p.status))) break;
-            sm::tc_fence_after();
-            const bool rise = top > m && !((top - m) * c <= 8.f);
-            const float f = rise ? exp2_approx((m - top) * c) : 1.f;   // (0 where m is still -inf)
-            if (rise) m = top;
-            if (j > 0 && __any_sync(0xFFFFFFFFu, rise)) {
+                total = (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+            };
+            auto rescale = [&](float f) {
                 l *= f;
-#pragma unroll
+#pragma unroll 1
                 for (int i = 0; i < D; i += 16) {
                     uint32_t o[16];
                     sm::tmem_ld16(tmem + T::kO + lanes + i, o);
@@ -344,28 +357,90 @@ attend_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
                     for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
                     sm::tmem_st16(tmem + T::kO + lanes + i, o);
                 }
-            }
-            const float b = m == -INFINITY ? 0.f : m * c;
-            float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+            };
+            if constexpr (!T::kShareSP) {
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                uint32_t w[16];
+                for (int q = 0; q < 4; ++q) sm::tmem_ld32(tmem + T::kS + lanes + q * 32, s[q]);
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    float2 x = make_float2(__uint_as_float(s[q][2 * i]), __uint_as_float(s[q][2 * i + 1]));
-                    x = fma2(x, make_float2(c, c), make_float2(-b, -b));
-                    x = make_float2(exp2_approx(x.x), exp2_approx(x.y));
-                    sum[i & 1] = add2(sum[i & 1], x);
-                    w[i] = pack_bf16(x.x, x.y);
+                for (int q = 0; q < 4; ++q) sm::tmem_wait_ld(s[q]);
+                sm::tc_fence_before();   // the scores are in registers: the next may come
+                __syncwarp();
+                if (lane == 0) sm::bar_arrive(s_free);
+                if (!seen)
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const uint32_t see = sees(q * 32);
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            if (!(see >> i & 1u)) s[q][i] = 0xFF800000u;
+                    }
+                float mx[4];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    mx[q] = fmaxf(__uint_as_float(s[q][0]), __uint_as_float(s[q][1]));
+#pragma unroll
+                    for (int i = 2; i < 32; i += 2) mx[q] = max3(mx[q], __uint_as_float(s[q][i]), __uint_as_float(s[q][i + 1]));
                 }
-                sm::tmem_st16(tmem + T::kP + lanes + q * 16, w);
+                const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                // the products that read the last weights and wrote O are done before either is touched
+                if (j > 0) ok = sm::bar_wait_sync(pv_done, uint32_t(j - 1) & 1u, abort_word, p.status) && ok;
+                sm::tc_fence_after();
+                const bool rise = top > high || (top < deep && top > -INFINITY);
+                if (__any_sync(0xFFFFFFFFu, rise || !ok)) {
+                    if (!(ok = __all_sync(0xFFFFFFFFu, ok))) break;
+                    const float f = rise && deep == -INFINITY ? exp2_approx((m - top) * c) : 1.f;
+                    if (rise) { m = top; high = m + 8.f / c; }
+                    if (j > 0) rescale(f);
+                }
+                if (top > -INFINITY) deep = -INFINITY;
+                weights(true);
+            } else
+            for (int pass = 0;; ++pass) {
+#pragma unroll
+                for (int q = 0; q < 4; ++q) sm::tmem_ld32(tmem + T::kS + lanes + q * 32, s[q]);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) sm::tmem_wait_ld(s[q]);
+                if (!seen)
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const uint32_t see = sees(q * 32);
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            if (!(see >> i & 1u)) s[q][i] = 0xFF800000u;
+                    }
+                weights(false);
+                const bool off = !(total <= 1048576.f) || (!set && total < 9.5367431640625e-7f);
+                if (pass == 1 || !__any_sync(0xFFFFFFFFu, off || !ok)) break;
+                if (!(ok = __all_sync(0xFFFFFFFFu, ok))) break;
+                float top = -INFINITY;
+#pragma unroll 1
+                for (int q = 0; q < 4; ++q) {
+                    uint32_t v[32];
+                    sm::tmem_ld32(tmem + T::kS + lanes + q * 32, v);
+                    sm::tmem_wait_ld(v);
+                    const uint32_t see = seen ? 0xFFFFFFFFu : sees(q * 32);
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        if (see >> i & 1u) top = fmaxf(top, __uint_as_float(v[i]));
+                }
+                float f = 1.f;
+                if (off && top > -INFINITY && (!set || top > m)) {
+                    if (set) f = exp2_approx((m - top) * c);
+                    m = top;
+                }
+                if (j > 0) rescale(f);   // (the products before these scores are done)
             }
-            l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
-            if (skip != 0 || !range.whole(k0, kKeys)) {
+            if (!ok) break;
+            if (T::kShareSP)
+#pragma unroll
+                for (int q = 0; q < 4; ++q) tmem_st16_head(tmem + T::kP + lanes + q * 16, s[q]);
+            set = set || total > 0.f;
+            l += total;
+            if (!seen && (skip != 0 || !range.whole(k0, kKeys))) {
                 // rows of V that no query of the block sees may hold anything, and 0 x NaN is NaN: zero them
                 const int vs = j % T::kVStages;
-                if (!(ok = sm::bar_wait(v_full(vs), uint32_t(j / T::kVStages) & 1u, abort_word, p.status))) break;
-                for (int r = threadIdx.x; r < kKeys; r += warps * 32)
+                ok = sm::bar_wait_warp(v_full(vs), uint32_t(j / T::kVStages) & 1u, abort_word, p.status);
+                for (int r = threadIdx.x; ok && r < kKeys; r += warps * 32)
                     if (!range.has(k0 + r) || (skip >> (r >> p.box_log2) & 1u))
                         for (int q = 0; q < T::kSubs; ++q)
                             for (int i = 0; i < T::kRowBytes; i += 16)
@@ -378,7 +453,8 @@ attend_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
             __syncwarp();
             if (lane == 0) sm::bar_arrive(p_ready);
         }
-        if (ok && n > 0) ok = sm::bar_wait(pv_done, uint32_t(n - 1) & 1u, abort_word, p.status);
+        ok = __all_sync(0xFFFFFFFFu, ok);
+        if (ok && n > 0) ok = sm::bar_wait_warp(pv_done, uint32_t(n - 1) & 1u, abort_word, p.status);
         if (ok) {
             sm::tc_fence_after();
             const bool whole = seg.splits == 1 && !p.prefix_seg;   // no other item adds to this row

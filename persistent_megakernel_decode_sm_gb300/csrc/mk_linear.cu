@@ -237,7 +237,7 @@ linear_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
 #pragma unroll 1
             for (int k0 = kb0; k0 < kb1; k0 += piece, ++n) {
                 const int buf = n & 1;
-                if (!(ok = sm::bar_wait(acc_full(buf), uint32_t(n / 2) & 1u, abort_word, p.status))) break;
+                if (!(ok = sm::bar_wait_warp(acc_full(buf), uint32_t(n / 2) & 1u, abort_word, p.status))) break;
                 sm::tc_fence_after();
                 const uint32_t acc = tmem + buf * T::kBufCols + cols + lanes;
 #pragma unroll
@@ -450,7 +450,7 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
 #pragma unroll 1
             for (int k0 = kb0; k0 < kb1; k0 += piece, ++n) {
                 const int buf = n & 1;
-                if (!(ok = sm::bar_wait(acc_full(buf), uint32_t(n / 2) & 1u, abort_word, p.status))) break;
+                if (!(ok = sm::bar_wait_warp(acc_full(buf), uint32_t(n / 2) & 1u, abort_word, p.status))) break;
                 sm::tc_fence_after();
                 const uint32_t acc = tmem + buf * 256 + cols + lanes;
 #pragma unroll
@@ -465,6 +465,7 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
                 __syncwarp();
                 if (lane == 0) sm::bar_arrive_cluster(sm::cluster_addr(acc_empty(buf), leader));
             }
+            if (GATED) ok = sm::pair_sync(1 + cols / 128 * 2 + (quarter & 1), ok);   // (the warps that exchange leave together)
             if (!ok) break;
             if (p.split > 1) {   // partial sums to this CTA's stages (every product has read them): [column][row]
 #pragma unroll

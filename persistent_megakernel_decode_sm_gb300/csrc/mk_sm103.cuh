@@ -20,6 +20,14 @@ __device__ __forceinline__ uint64_t timer_ns() {
     return t;
 }
 
+// One lane of a converged warp.  The loops that issue copies and products run on the whole warp, with
+// only the issue itself under this: their addresses then stay warp-uniform.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xFFFFFFFF;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
+    return p != 0;
+}
+
 // ---- mbarriers -------------------------------------------------------------------------------
 __device__ __forceinline__ void bar_init(uint32_t bar, uint32_t count) {
     asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
@@ -59,6 +67,25 @@ static __device__ __noinline__ bool bar_wait_slow(uint32_t bar, uint32_t parity,
 __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile int* abort_word, int32_t* status) {
     if (bar_try(bar, parity)) return true;
     return bar_wait_slow(bar, parity, abort_word, status);
+}
+// The wait of a whole warp, which is converged after it (its lanes may see the barrier at different
+// tries, and what follows on tensor memory needs them together).  bar_wait_sync's answer can differ between
+// lanes after a wait that ran out, bar_wait_warp's cannot.
+__device__ __forceinline__ bool bar_wait_sync(uint32_t bar, uint32_t parity, volatile int* abort_word, int32_t* status) {
+    const bool ok = bar_wait(bar, parity, abort_word, status);
+    __syncwarp();
+    return ok;
+}
+__device__ __forceinline__ bool bar_wait_warp(uint32_t bar, uint32_t parity, volatile int* abort_word, int32_t* status) {
+    return __all_sync(0xFFFFFFFFu, bar_wait(bar, parity, abort_word, status));
+}
+// A barrier of two warps (id 1-15) that tells both whether every thread is ok, so that after a wait that ran
+// out they leave their loops together
+__device__ __forceinline__ bool pair_sync(int id, bool ok) {
+    uint32_t all;
+    asm volatile("{\n .reg .pred p, q;\n setp.ne.u32 q, %2, 0;\n bar.red.and.pred p, %1, 64, q;\n selp.u32 %0, 1, 0, p;\n}\n"
+                 : "=r"(all) : "r"(id), "r"(uint32_t(ok)) : "memory");
+    return all != 0;
 }
 __device__ __forceinline__ void bar_drain(uint32_t bar, uint32_t parity) {   // (after an abort: bounded, no report)
     const uint64_t t0 = timer_ns();
