@@ -471,6 +471,26 @@ typedef struct {
 size_t mk_attend_workspace(const mk_attend_args* a);
 mk_status mk_attend(const mk_attend_args* a, void* workspace, size_t workspace_bytes, void* stream);
 
+/* Fills the KV cache of a bound context from prompt tokens: the decoder's layers over all of them at
+ * once (RMSNorm, mk_linear for the projections, RoPE, mk_attend, SwiGLU), where the decode step takes one.
+ * The caller leaves each sequence's last prompt token to a decode step, which gives its logits and the next
+ * token; nothing of the last layer but its K and V is computed here.  A long prompt may be given in pieces.
+ *  tokens         HOST int32[sum n_tokens], in [0, vocab): the sequences' tokens back to back
+ *  n_tokens, pos  HOST int32[batch]: tokens of each sequence (0: none), and the position of its first;
+ *                 its cache holds the positions before; pos + n_tokens <= max_seq
+ *  shared_prefix  as in mk_attend: that many first positions are the same for every sequence, in the
+ *                 cache already (sequence 0's rows, or blocks every table names), pos[b] >= shared_prefix
+ *                 wherever n_tokens[b] > 0.  0: none
+ *  workspace      mk_prefill_workspace bytes of device memory, 256-byte aligned
+ * Activations between operators are bf16 (the residual stream, q k v before rotation and all sums fp32), so K and V
+ * agree with the decode step's to bf16 rounding of their inputs.  Enqueued on the bound stream, on the current device;
+ * device-side errors surface at the next mk_ctx_status or mk_decode_step.  Not capturable into a graph (it copies the
+ * host tokens).  Errors: MK_ERR_ARG (also: a paged cache with blocks that are not a multiple of 8 positions),
+ * MK_ERR_CAPACITY (workspace), MK_ERR_POISONED, MK_ERR_CUDA; on the device MK_ERR_BOUNDS, MK_ERR_TIMEOUT. */
+size_t mk_prefill_workspace(mk_ctx* c, const int32_t* n_tokens, const int32_t* pos, int32_t shared_prefix);
+mk_status mk_prefill(mk_ctx* c, const int32_t* tokens, const int32_t* n_tokens, const int32_t* pos, int32_t shared_prefix,
+                     void* workspace, size_t workspace_bytes);
+
 /* Number of SMs of the current CUDA device (the natural sm_count), or MK_ERR_CUDA. */
 mk_status mk_device_sm_count(int32_t* out);
 

@@ -8,6 +8,7 @@ Low level: the mk_* functions of the C ABI under the same names (``lib.mk_bind``
 High level:
     sched = Schedule(cfg, sm_count)               # mk_build_schedule
     dec = Decoder(sched, weights, kv)             # allocates counters/scratch with torch, mk_bind
+    dec.prefill([prompt[:-1]])                    # mk_prefill: the prompt into the KV cache
     nxt = dec.step(tokens, pos, logits)           # mk_decode_step (synchronous)
     dec.launch(tokens, pos, logits, next_dev)     # mk_launch_step (asynchronous)
 Prompt operators (asynchronous on torch's current stream of the tensors' device):
@@ -45,7 +46,8 @@ EXPORTS = ["mk_build_schedule", "mk_schedule_queues", "mk_schedule_counters", "m
            "mk_launch_step", "mk_ctx_status", "mk_device_sm_count", "mk_last_error", "mk_unbind", "mk_set_trace",
            "mk_decode_step_static", "mk_set_sync", "mk_decode_steps", "mk_bind_paged", "mk_schedule_attn_chunk",
            "mk_decode_persistent_start", "mk_decode_persistent_stop", "mk_decode_persistent_progress",
-           "mk_decode_persistent_wait", "mk_rebind_schedule", "mk_linear", "mk_attend", "mk_attend_workspace"]
+           "mk_decode_persistent_wait", "mk_rebind_schedule", "mk_linear", "mk_attend", "mk_attend_workspace",
+           "mk_prefill", "mk_prefill_workspace"]
 
 
 class MkError(RuntimeError):
@@ -158,6 +160,10 @@ lib.mk_attend_workspace.restype = ctypes.c_size_t
 lib.mk_attend_workspace.argtypes = [_P]
 lib.mk_attend.restype = ctypes.c_int
 lib.mk_attend.argtypes = [_P, _P, ctypes.c_size_t, _P]
+lib.mk_prefill_workspace.restype = ctypes.c_size_t
+lib.mk_prefill_workspace.argtypes = [_P, _I32P, _I32P, ctypes.c_int32]
+lib.mk_prefill.restype = ctypes.c_int
+lib.mk_prefill.argtypes = [_P, _I32P, _I32P, _I32P, ctypes.c_int32, _P, ctypes.c_size_t]
 lib.mk_unbind.restype = None
 lib.mk_unbind.argtypes = [_P]
 
@@ -329,6 +335,38 @@ class Decoder:
         out = (ctypes.c_int32 * (max(n_steps, 1) * B))()
         _check(lib.mk_decode_steps(self.handle, t, p, int(n_steps), _ptr(lg), _ptr(tokens_dev), out))
         return [list(out[i * B:(i + 1) * B]) for i in range(n_steps)]
+
+    def prefill(self, tokens: Sequence[Sequence[int]], pos: Optional[Sequence[int]] = None, shared_prefix: int = 0,
+                chunk: int = 4096, workspace=None):
+        """mk_prefill: fills the KV cache with the prompt tokens of each sequence (lists, one per sequence,
+        possibly empty) from position pos[b] on (default 0), in pieces of at most ``chunk`` tokens a
+        sequence, and waits for it.  Leave a prompt's last token to ``step``: it gives the logits.
+        shared_prefix: the first positions, the same for every sequence and already cached."""
+        import torch
+        B, dev = self.cfg.batch, self.counters.device
+        pos = list(pos) if pos is not None else [0] * B
+        if len(tokens) != B or len(pos) != B:
+            raise ValueError(f"tokens and pos must have an entry for each of {B} sequences")
+        if chunk < 1:
+            raise ValueError("chunk must be positive")
+        tokens = [array.array("i", t) for t in tokens]
+        at = [0] * B
+        with torch.cuda.device(dev):
+            while any(a < len(t) for a, t in zip(at, tokens)):
+                n = [min(chunk, len(t) - a) for a, t in zip(at, tokens)]
+                flat = array.array("i")
+                for a, k, t in zip(at, n, tokens):
+                    flat.extend(t[a:a + k])
+                c_t = (ctypes.c_int32 * len(flat)).from_buffer(flat)
+                c_n, c_p = (ctypes.c_int32 * B)(*n), (ctypes.c_int32 * B)(*[p + a for p, a in zip(pos, at)])
+                need = int(lib.mk_prefill_workspace(self.handle, c_n, c_p, int(shared_prefix)))
+                ws = workspace
+                if ws is None:   # (torch keeps it for this stream's later use: freed in stream order)
+                    with torch.cuda.stream(self.stream):
+                        ws = torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
+                _check(lib.mk_prefill(self.handle, c_t, c_n, c_p, int(shared_prefix), _ptr(ws), ws.numel() * ws.element_size()))
+                at = [a + k for a, k in zip(at, n)]
+            self.status()
 
     def rebind(self, sched: "Schedule"):
         """mk_rebind_schedule: continue on another schedule of the same model and SM count (new KV

@@ -7,6 +7,7 @@ Translation units compiled in parallel and linked into one shared library:
   csrc/mk_kernel_batch.cu  the batch > 1 instance of the same kernel source (tensor-core matvec tiles)
   csrc/mk_linear.cu  the linear map with a fused epilogue (prompt path)
   csrc/mk_attend.cu  attention of query tokens over the KV cache (prompt path)
+  csrc/mk_prefill.cu embedding, RMSNorm, RoPE and KV append of the prompt path
 """
 from __future__ import annotations
 
@@ -22,7 +23,8 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libmk.so")
 BUILD_DIR = os.path.join(HERE, "_build")
-SOURCES = ["mk_sched.cpp", "mk_api.cu", "mk_kernel.cu", "mk_kernel_batch.cu", "mk_linear.cu", "mk_attend.cu"]
+SOURCES = ["mk_sched.cpp", "mk_api.cu", "mk_kernel.cu", "mk_kernel_batch.cu", "mk_linear.cu", "mk_attend.cu",
+           "mk_prefill.cu"]
 HEADERS = ["mk_internal.h", "mk_ops.h", "mk_sm103.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 

@@ -21,7 +21,7 @@
 
 #include <atomic>
 
-#include "mk_internal.h"
+#include "mk_ops.h"
 
 namespace mk {
 const void* megakernel_fn(int cpl);
@@ -756,6 +756,142 @@ extern "C" mk_status mk_ctx_status(mk_ctx* c, int32_t* info) {
     if (c->run_active) return fail(MK_ERR_ARG, "a persistent launch is in flight (mk_decode_persistent_wait first)");
     if (c->poisoned && !info) return fail(MK_ERR_POISONED, "context poisoned by an earlier device error");
     return read_status(c, info);
+}
+
+// ---- prompts: the decoder's layers over many tokens at once, filling the KV cache ------------------
+struct PrefillLayout {   // workspace, each region 256-byte aligned
+    size_t tokens, x, xn, qkv, q, o, h, attend, total;
+};
+static PrefillLayout prefill_layout(const mk_model_cfg& c, int64_t n, size_t attend_bytes) {
+    const size_t T = size_t(n), H = c.hidden, qd = size_t(c.n_q_heads) * c.head_dim, kvd = size_t(c.n_kv_heads) * c.head_dim;
+    PrefillLayout l{};
+    size_t off = 0;
+    auto take = [&](size_t bytes) { const size_t r = off; off = align256(off + bytes); return r; };
+    l.tokens = take(T * 4);
+    l.x = take(T * H * 4);
+    l.xn = take(T * H * 2);
+    l.qkv = take(T * (qd + 2 * kvd) * 4);
+    l.q = take(T * qd * 2);
+    l.o = take(T * qd * 2);
+    l.h = take(T * size_t(c.ffn) * 2);
+    l.attend = take(attend_bytes);
+    l.total = off;
+    return l;
+}
+// The call's checked lengths and the attention arguments that hold for every layer
+struct PrefillCall {
+    int64_t tokens;
+    int32_t q_lens[kMaxBatch], kv_lens[kMaxBatch];
+    mk_kv kv;
+    mk_kv_pages pages;
+    mk_attend_args attend;
+    PrefillLayout lay;
+};
+static mk_status prefill_plan(mk_ctx* c, const int32_t* n_tokens, const int32_t* pos, int32_t shared_prefix, PrefillCall& r) {
+    if (!c || !n_tokens || !pos) return fail(MK_ERR_ARG, "null argument");
+    const Params& p = c->base;
+    r.tokens = 0;
+    for (int b = 0; b < c->cfg.batch; ++b) {
+        if (n_tokens[b] < 0 || pos[b] < 0 || int64_t(pos[b]) + n_tokens[b] > c->cfg.max_seq)
+            return fail(MK_ERR_ARG, "sequence %d: %d prompt tokens at position %d outside the KV capacity [0, %d)", b, n_tokens[b],
+                        pos[b], c->cfg.max_seq);
+        r.q_lens[b] = n_tokens[b];
+        r.kv_lens[b] = n_tokens[b] ? pos[b] + n_tokens[b] : 0;
+        r.tokens += n_tokens[b];
+    }
+    if (p.kv_table && p.attn_chunk % 8) return fail(MK_ERR_ARG, "prompts need a paged cache's blocks to be multiples of 8 positions");
+    r.kv = {p.kc, p.vc, p.kv_bstride, p.kv_lstride, p.kv_hstride};
+    r.pages = {p.kv_table, p.attn_chunk, p.kv_max_blocks, p.kv_n_blocks};
+    mk_attend_args& a = r.attend;
+    a = mk_attend_args{};
+    a.n_q_heads = p.nq; a.n_kv_heads = p.nkv; a.head_dim = p.d; a.batch = p.B;
+    a.q_lens = r.q_lens; a.kv_lens = r.kv_lens;
+    a.q_stride = a.out_stride = p.qd;
+    a.kv = &r.kv;
+    a.pages = p.kv_table ? &r.pages : nullptr;
+    a.max_seq = p.max_seq;
+    a.shared_prefix = shared_prefix;
+    a.status = p.err;
+    size_t ws = 0;
+    if (r.tokens) {
+        const mk_status st = mk_attend_plan(&a, &ws);
+        if (st != MK_OK) return st;
+    }
+    r.lay = prefill_layout(c->cfg, r.tokens, ws);
+    return MK_OK;
+}
+
+extern "C" size_t mk_prefill_workspace(mk_ctx* c, const int32_t* n_tokens, const int32_t* pos, int32_t shared_prefix) {
+    PrefillCall r;
+    return prefill_plan(c, n_tokens, pos, shared_prefix, r) == MK_OK && r.tokens ? r.lay.total : 0;
+}
+
+extern "C" mk_status mk_prefill(mk_ctx* c, const int32_t* tokens, const int32_t* n_tokens, const int32_t* pos,
+                                int32_t shared_prefix, void* workspace, size_t workspace_bytes) {
+    PrefillCall r;
+    mk_status st = prefill_plan(c, n_tokens, pos, shared_prefix, r);
+    if (st != MK_OK) return st;
+    if (c->run_active) return fail(MK_ERR_ARG, "a persistent launch is in flight (mk_decode_persistent_wait first)");
+    if (c->poisoned) return fail(MK_ERR_POISONED, "context poisoned by an earlier device error");
+    if (r.tokens == 0) return MK_OK;
+    if (!tokens || !workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u))
+        return fail(MK_ERR_ARG, "tokens null, or workspace null or not 256-byte aligned");
+    if (workspace_bytes < r.lay.total)
+        return fail(MK_ERR_CAPACITY, "prompt workspace of %zu bytes, %zu needed (mk_prefill_workspace)", workspace_bytes, r.lay.total);
+    for (int64_t i = 0; i < r.tokens; ++i)
+        if (tokens[i] < 0 || tokens[i] >= c->cfg.vocab) return fail(MK_ERR_ARG, "token %d out of range", tokens[i]);
+    int dev = -1;
+    CK(cudaGetDevice(&dev));
+    if (dev != c->device) return fail(MK_ERR_ARG, "the context is bound to device %d, device %d is current", c->device, dev);
+    cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
+    CK(cudaStreamIsCapturing(c->stream, &capture));
+    if (capture != cudaStreamCaptureStatusNone) return fail(MK_ERR_ARG, "a prompt's host tokens cannot be captured into a graph");
+    const Params& p = c->base;
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    int32_t* d_tokens = reinterpret_cast<int32_t*>(ws + r.lay.tokens);
+    float* x = reinterpret_cast<float*>(ws + r.lay.x);
+    float* qkv = reinterpret_cast<float*>(ws + r.lay.qkv);
+    void *xn = ws + r.lay.xn, *q = ws + r.lay.q, *o = ws + r.lay.o, *h = ws + r.lay.h;
+    const int32_t T = int32_t(r.tokens), H = p.H, F = p.F;
+    PrefillRows rows{};
+    rows.batch = p.B; rows.nq = p.nq; rows.nkv = p.nkv; rows.d = p.d;
+    for (int b = 0, at = 0; b < p.B; at += n_tokens[b], ++b) { rows.first[b] = at; rows.pos[b] = pos[b]; }
+    rows.rope = p.rope;
+    rows.batch_stride = p.kv_bstride; rows.head_stride = p.kv_hstride;
+    rows.table = p.kv_table; rows.block = p.attn_chunk; rows.max_blocks = p.kv_max_blocks; rows.n_blocks = p.kv_n_blocks;
+    rows.status = p.err;
+    r.attend.q = q;
+    r.attend.out = o;
+    // (pageable memory: the copy has read `tokens` when the call returns)
+    CK(cudaMemcpyAsync(d_tokens, tokens, size_t(T) * 4, cudaMemcpyHostToDevice, c->stream));
+    auto linear = [&](const void* in, int32_t k, const void* w, int32_t n, int32_t act, const void* residual, int32_t dtype, void* out) {
+        mk_linear_args a{};
+        a.rows = T; a.n = n; a.k = k; a.activation = act;
+        a.x = in; a.x_stride = k;
+        a.w = w;
+        a.residual = residual; a.residual_stride = n; a.residual_dtype = MK_F32;
+        a.out_dtype = dtype; a.out = out; a.out_stride = n;
+        a.status = p.err;
+        return mk_linear(&a, c->stream);
+    };
+    // a failure from here on leaves the cache rows of the call's tokens in an unknown state, nothing else
+    st = prefill_norm(x, d_tokens, c->w.embed, c->w.attn_norm[0], xn, T, H, p.rms_eps, c->stream);
+    for (int l = 0; l < p.L && st == MK_OK; ++l) {
+        st = linear(xn, H, c->w.wqkv[l], p.nqkv, MK_ACT_NONE, nullptr, MK_F32, qkv);
+        rows.k = reinterpret_cast<__nv_bfloat16*>(p.kc) + l * p.kv_lstride;
+        rows.v = reinterpret_cast<__nv_bfloat16*>(p.vc) + l * p.kv_lstride;
+        if (st == MK_OK) st = prefill_rope_append(qkv, q, rows, T, c->stream);
+        if (l == p.L - 1) break;   // the last layer's K and V are all that is needed of it
+        r.attend.layer = l;
+        if (st == MK_OK) st = mk_attend(&r.attend, ws + r.lay.attend, r.lay.total - r.lay.attend, c->stream);
+        if (st == MK_OK) st = linear(o, p.qd, c->w.wo[l], H, MK_ACT_NONE, x, MK_F32, x);
+        if (st == MK_OK) st = prefill_norm(x, nullptr, nullptr, c->w.mlp_norm[l], xn, T, H, p.rms_eps, c->stream);
+        if (st == MK_OK) st = linear(xn, H, c->w.wgate_up[l], F, MK_ACT_SWIGLU, nullptr, MK_BF16, h);
+        if (st == MK_OK) st = linear(h, F, c->w.wdown[l], H, MK_ACT_NONE, x, MK_F32, x);
+        if (st == MK_OK) st = prefill_norm(x, nullptr, nullptr, c->w.attn_norm[l + 1], xn, T, H, p.rms_eps, c->stream);
+    }
+    if (st == MK_OK) c->last_err = p.err;
+    return st;
 }
 
 extern "C" void mk_unbind(mk_ctx* c) {

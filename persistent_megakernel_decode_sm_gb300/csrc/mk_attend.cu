@@ -742,14 +742,23 @@ static mk_status attend_launch_segs(const mk_attend_args* a, const AttendCommon&
 
 using namespace mk;
 
-extern "C" size_t mk_attend_workspace(const mk_attend_args* a) {
-    int device = 0, sms = 0;
-    AttendPlan pl;
-    if (attend_check_shape(a) != MK_OK) return 0;
+mk_status mk::mk_attend_plan(const mk_attend_args* a, size_t* workspace_bytes) {
+    *workspace_bytes = 0;
+    mk_status st = attend_check_shape(a);
+    if (st != MK_OK) return st;
     bool any = false;
     for (int b = 0; b < a->batch; ++b) any = any || a->q_lens[b] > 0;
-    if (!any || op_device(&device, &sms) != MK_OK || attend_plan(a, sms, pl) != MK_OK) return 0;
-    return attend_bytes(pl, a->head_dim);
+    if (!any) return MK_OK;
+    int device = 0, sms = 0;
+    AttendPlan pl;
+    if ((st = op_device(&device, &sms)) != MK_OK || (st = attend_plan(a, sms, pl)) != MK_OK) return st;
+    *workspace_bytes = attend_bytes(pl, a->head_dim);
+    return MK_OK;
+}
+
+extern "C" size_t mk_attend_workspace(const mk_attend_args* a) {
+    size_t bytes = 0;
+    return mk_attend_plan(a, &bytes) == MK_OK ? bytes : 0;
 }
 
 extern "C" mk_status mk_attend(const mk_attend_args* a, void* workspace, size_t workspace_bytes, void* stream) {

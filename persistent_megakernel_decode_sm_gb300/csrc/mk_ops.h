@@ -2,6 +2,7 @@
 #pragma once
 
 #include <cuda.h>   // tensor-map types (the encoder itself is fetched through the runtime)
+#include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
 #include <atomic>
@@ -86,5 +87,24 @@ inline mk_status op_smem(const void* fn, int bytes, int device, std::atomic<uint
     done->fetch_or(uint64_t(1) << device);
     return MK_OK;
 }
+
+// The checks of mk_attend that need no pointers, and its workspace bytes
+mk_status mk_attend_plan(const mk_attend_args* a, size_t* workspace_bytes);
+
+// ---- the prompt path's small kernels (mk_prefill.cu) ----------------------------------------------
+struct PrefillRows {
+    int32_t batch, nq, nkv, d;
+    int32_t first[kMaxBatch], pos[kMaxBatch];   // per sequence: its first token of the call, that token's position
+    const float2* rope;                         // [max_seq][d / 2] (cos, sin)
+    __nv_bfloat16* k;                           // the layer's cache
+    __nv_bfloat16* v;
+    int64_t batch_stride, head_stride;
+    const int32_t* table;                       // paged: [batch][max_blocks]
+    int32_t block, max_blocks, n_blocks;
+    int32_t* status;
+};
+mk_status prefill_norm(float* x, const int32_t* tokens, const void* embed, const void* gain, void* y, int64_t rows, int H,
+                       float eps, cudaStream_t stream);
+mk_status prefill_rope_append(const float* qkv, void* q, const PrefillRows& rows, int64_t tokens, cudaStream_t stream);
 
 }  // namespace mk

@@ -1,0 +1,132 @@
+// The small kernels of the prompt path (mk_prefill): token embedding, RMSNorm, and the rotation of
+// q and k with the append of k and v to the cache.  Each reads and writes its rows once: bytes bound them.
+#include "mk_ops.h"
+#include "mk_sm103.cuh"
+
+namespace mk {
+
+constexpr int kNormThreads = 256;
+
+__device__ __forceinline__ float block_sum(float v) {   // the same in every thread
+    __shared__ float part[kNormThreads / 32];
+#pragma unroll
+    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
+    __syncthreads();
+    float s = 0.f;
+#pragma unroll
+    for (int w = 0; w < kNormThreads / 32; ++w) s += part[w];
+    return s;
+}
+
+// y = x / sqrt(mean(x^2) + eps) * gain, in fp32, rounded once to bf16; a block per token.  With tokens given
+// x is first taken from the embedding rows.  (H is a multiple of 8 and at most kMaxK: 8 vectors a thread.)
+__global__ void __launch_bounds__(kNormThreads) norm_kernel(float* x, const int32_t* tokens, const __nv_bfloat16* embed,
+                                                            const __nv_bfloat16* gain, __nv_bfloat16* y, int H, float eps) {
+    sm::pdl_trigger();
+    sm::pdl_wait();
+    const int64_t row = blockIdx.x;
+    float* xr = x + row * H;
+    constexpr int kVec = kMaxK / 8 / kNormThreads;
+    float v[kVec][8];
+    float ss = 0.f;
+#pragma unroll
+    for (int i = 0; i < kVec; ++i) {
+        const int c = (threadIdx.x + i * kNormThreads) * 8;
+        if (c >= H) break;
+        if (tokens) {
+            const uint4 u = *reinterpret_cast<const uint4*>(embed + int64_t(tokens[row]) * H + c);
+            const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                v[i][2 * k] = __uint_as_float(w[k] << 16);
+                v[i][2 * k + 1] = __uint_as_float(w[k] & 0xFFFF0000u);
+            }
+            *reinterpret_cast<float4*>(xr + c) = make_float4(v[i][0], v[i][1], v[i][2], v[i][3]);
+            *reinterpret_cast<float4*>(xr + c + 4) = make_float4(v[i][4], v[i][5], v[i][6], v[i][7]);
+        } else {
+            const float4 a = *reinterpret_cast<const float4*>(xr + c), b = *reinterpret_cast<const float4*>(xr + c + 4);
+            v[i][0] = a.x; v[i][1] = a.y; v[i][2] = a.z; v[i][3] = a.w;
+            v[i][4] = b.x; v[i][5] = b.y; v[i][6] = b.z; v[i][7] = b.w;
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) ss = fmaf(v[i][k], v[i][k], ss);
+    }
+    const float r = 1.f / sqrtf(block_sum(ss) / float(H) + eps);
+#pragma unroll
+    for (int i = 0; i < kVec; ++i) {
+        const int c = (threadIdx.x + i * kNormThreads) * 8;
+        if (c >= H) break;
+        const uint4 u = *reinterpret_cast<const uint4*>(gain + c);
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+        uint32_t out[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const float a = v[i][2 * k] * r * __uint_as_float(w[k] << 16);
+            const float b = v[i][2 * k + 1] * r * __uint_as_float(w[k] & 0xFFFF0000u);
+            asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(out[k]) : "f"(b), "f"(a));
+        }
+        *reinterpret_cast<uint4*>(y + row * H + c) = make_uint4(out[0], out[1], out[2], out[3]);
+    }
+}
+
+// Pairs (i, i + d/2) of q and k rotated by their position's angles (the bind's table), rounded once; q to its
+// own buffer, k and v to the cache row of their position.  A block per token.
+__global__ void __launch_bounds__(256) rope_append_kernel(const float* qkv, __nv_bfloat16* q, const __grid_constant__ PrefillRows p) {
+    sm::pdl_trigger();
+    sm::pdl_wait();
+    const int tok = blockIdx.x;
+    int b = 0;
+    while (b + 1 < p.batch && tok >= p.first[b + 1]) ++b;
+    const int pos = p.pos[b] + (tok - p.first[b]), half = p.d / 2;
+    const float2* cs = p.rope + int64_t(pos) * half;
+    const float* src = qkv + int64_t(tok) * (p.nq + 2 * p.nkv) * p.d;
+    int64_t base = int64_t(b) * p.batch_stride, slot = pos;
+    bool good = true;
+    if (p.table) {
+        const int blk = __ldg(p.table + int64_t(b) * p.max_blocks + pos / p.block);
+        good = unsigned(blk) < unsigned(p.n_blocks);
+        if (!good && threadIdx.x == 0) *p.status = MK_ERR_BOUNDS;   // (nothing is written there)
+        base = 0;
+        slot = int64_t(blk) * p.block + pos % p.block;
+    }
+    const int heads = p.nq + p.nkv;
+    for (int i = threadIdx.x; i < heads * half; i += blockDim.x) {
+        const int h = i / half, e = i % half;
+        const float a = src[h * p.d + e], c = src[h * p.d + e + half];
+        const float2 t = cs[e];
+        const __nv_bfloat16 r0 = __float2bfloat16_rn(a * t.x - c * t.y), r1 = __float2bfloat16_rn(a * t.y + c * t.x);
+        __nv_bfloat16* dst = h < p.nq ? q + (int64_t(tok) * p.nq + h) * p.d
+                                      : p.k + base + (h - p.nq) * p.head_stride + slot * p.d;
+        if (h < p.nq || good) { dst[e] = r0; dst[e + half] = r1; }
+    }
+    if (good)
+        for (int i = threadIdx.x; i < p.nkv * p.d; i += blockDim.x)
+            p.v[base + i / p.d * p.head_stride + slot * p.d + i % p.d] = __float2bfloat16_rn(src[heads * p.d + i]);
+}
+
+template <typename... Args, typename... Given>
+static mk_status prefill_launch(void (*fn)(Args...), int64_t blocks, cudaStream_t stream, Given... given) {
+    cudaLaunchConfig_t cfg{};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = dim3(unsigned(blocks));
+    cfg.blockDim = dim3(256);
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    MK_CK(cudaLaunchKernelEx(&cfg, fn, given...));
+    return MK_OK;
+}
+
+mk_status prefill_norm(float* x, const int32_t* tokens, const void* embed, const void* gain, void* y, int64_t rows, int H,
+                       float eps, cudaStream_t stream) {
+    return prefill_launch(&norm_kernel, rows, stream, x, tokens, static_cast<const __nv_bfloat16*>(embed),
+                          static_cast<const __nv_bfloat16*>(gain), static_cast<__nv_bfloat16*>(y), H, eps);
+}
+mk_status prefill_rope_append(const float* qkv, void* q, const PrefillRows& rows, int64_t tokens, cudaStream_t stream) {
+    return prefill_launch(&rope_append_kernel, tokens, stream, qkv, static_cast<__nv_bfloat16*>(q), rows);
+}
+
+}  // namespace mk
