@@ -166,44 +166,47 @@ linear_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
     };
 
     if (warp == 0) {
-        if (lane == 0) {
-            int it = 0;
-            bool ok = true;
-            for (int tile = first; tile < tiles && ok; tile += step) {
-                int n0, m0;
-                place(tile, n0, m0);
-                for (int kb = kb0; kb < kb1; ++kb, ++it) {
-                    const int s = it % T::kStages;
-                    if (it >= T::kStages && !(ok = sm::bar_wait(empty(s), uint32_t(it / T::kStages - 1) & 1u, abort_word, p.status))) break;
-                    const uint32_t at = stage0 + s * T::kStageBytes;
+        const bool issuer = sm::elect_one();
+        int it = 0, s = 0;
+        uint32_t phase = 1;   // (the first round finds every stage empty)
+        bool ok = true;
+        for (int tile = first; tile < tiles && ok; tile += step) {
+            int n0, m0;
+            place(tile, n0, m0);
+            for (int kb = kb0; kb < kb1; ++kb, ++it) {
+                if (!(ok = sm::bar_wait_warp(empty(s), phase, abort_word, p.status))) break;
+                const uint32_t at = stage0 + s * T::kStageBytes;
+                if (issuer) {
                     sm::bar_expect(full(s), T::kStageBytes);
                     sm::tma_load_2d(at, &map_w, full(s), kb * kLinK, n0);
                     if (GATED) sm::tma_load_2d(at + T::kABytes, &map_w, full(s), kb * kLinK, p.n + n0);
                     sm::tma_load_2d(at + T::kAccs * T::kABytes, &map_x, full(s), kb * kLinK, m0);
                 }
+                __syncwarp();
+                if (++s == T::kStages) { s = 0; phase ^= 1u; }
             }
-            if (*abort_word)   // the copies in flight land before the CTA gives its shared memory back
-                for (int i = max(0, it - T::kStages); i < it; ++i) sm::bar_drain(full(i % T::kStages), uint32_t(i / T::kStages) & 1u);
         }
+        if (*abort_word && issuer)   // the copies in flight land before the CTA gives its shared memory back
+            for (int i = max(0, it - T::kStages); i < it; ++i) sm::bar_drain(full(i % T::kStages), uint32_t(i / T::kStages) & 1u);
         __syncwarp();
     } else if (warp == 1) {
-        if (lane == 0) {
-            constexpr uint32_t idesc = sm::mma_idesc(128, BN);
-            int it = 0, n = 0;
-            bool ok = true;
-            for (int tile = first; tile < tiles && ok; tile += step)
-                for (int k0 = kb0; k0 < kb1 && ok; k0 += piece, ++n) {
-                    const int buf = n & 1;
-                    if (n >= 2 && !(ok = sm::bar_wait(acc_empty(buf), uint32_t(n / 2 - 1) & 1u, abort_word, p.status))) break;
+        constexpr uint32_t idesc = sm::mma_idesc(128, BN);
+        const bool leader = sm::elect_one();
+        const uint64_t a0 = sm::desc_k_sw128(stage0), b0 = sm::desc_k_sw128(stage0 + T::kAccs * T::kABytes);
+        int s = 0, n = 0;
+        uint32_t phase = 0;
+        bool ok = true;
+        for (int tile = first; tile < tiles && ok; tile += step)
+            for (int k0 = kb0; k0 < kb1 && ok; k0 += piece, ++n) {
+                const int buf = n & 1;
+                if (n >= 2 && !(ok = sm::bar_wait_warp(acc_empty(buf), uint32_t(n / 2 - 1) & 1u, abort_word, p.status))) break;
+                const uint32_t d = tmem + buf * T::kBufCols;
+                const int k1 = min(k0 + piece, kb1);
+                for (int kb = k0; kb < k1; ++kb) {
+                    if (!(ok = sm::bar_wait_warp(full(s), phase, abort_word, p.status))) break;
                     sm::tc_fence_after();
-                    const uint32_t d = tmem + buf * T::kBufCols;
-                    const int k1 = min(k0 + piece, kb1);
-                    for (int kb = k0; kb < k1; ++kb, ++it) {
-                        const int s = it % T::kStages;
-                        if (!(ok = sm::bar_wait(full(s), uint32_t(it / T::kStages) & 1u, abort_word, p.status))) break;
-                        sm::tc_fence_after();
-                        const uint32_t at = stage0 + s * T::kStageBytes;
-                        const uint64_t a = sm::desc_k_sw128(at), b = sm::desc_k_sw128(at + T::kAccs * T::kABytes);
+                    const uint64_t a = a0 + uint64_t(s * (T::kStageBytes >> 4)), b = b0 + uint64_t(s * (T::kStageBytes >> 4));
+                    if (leader) {
 #pragma unroll
                         for (int kk = 0; kk < kLinK / 16; ++kk) {   // (32 bytes along the row: 2 in the descriptor's units)
                             sm::mma_ss(d, a + 2 * kk, b + 2 * kk, idesc, kb > k0 || kk > 0);
@@ -211,10 +214,13 @@ linear_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
                         }
                         sm::mma_commit(empty(s));
                     }
-                    if (ok) sm::mma_commit(acc_full(buf));
+                    __syncwarp();
+                    if (++s == T::kStages) { s = 0; phase ^= 1u; }
                 }
-            if (*abort_word) { sm::mma_commit(drained); sm::bar_drain(drained, 0); }
-        }
+                if (ok && leader) sm::mma_commit(acc_full(buf));
+                __syncwarp();
+            }
+        if (*abort_word && leader) { sm::mma_commit(drained); sm::bar_drain(drained, 0); }
         __syncwarp();
     } else {
         const int quarter = warp & 3, row = quarter * 32 + lane, cols = (warp - 2) / 4 * T::kWidth;
@@ -374,57 +380,64 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
     };
 
     if (warp == 0) {
-        if (lane == 0) {
-            int it = 0;
-            bool ok = true;
-            for (int tile = first; tile < tiles && ok; tile += step) {
-                int n0, m0;
-                place(tile, n0, m0);
-                for (int kb = kb0; kb < kb1; ++kb, ++it) {
-                    const int s = it % T::kStages;
-                    if (it >= T::kStages && !(ok = sm::bar_wait(empty(s), uint32_t(it / T::kStages - 1) & 1u, abort_word, p.status))) break;
-                    const uint32_t at = stage0 + s * T::kStageBytes;
+        const bool issuer = sm::elect_one();
+        int it = 0, s = 0;
+        uint32_t phase = 1;   // (the first round finds every stage empty)
+        bool ok = true;
+        for (int tile = first; tile < tiles && ok; tile += step) {
+            int n0, m0;
+            place(tile, n0, m0);
+            for (int kb = kb0; kb < kb1; ++kb, ++it) {
+                if (!(ok = sm::bar_wait_warp(empty(s), phase, abort_word, p.status))) break;
+                const uint32_t at = stage0 + s * T::kStageBytes, bar = sm::cluster_addr(full(s), leader);
+                if (issuer) {
                     if (half == 0) sm::bar_expect(full(s), 2 * T::kStageBytes);   // both CTAs' copies
-                    const uint32_t bar = sm::cluster_addr(full(s), leader);
                     sm::tma_load_2d_pair(at, &map_w, bar, kb * kLinK, n0);
                     if (GATED) sm::tma_load_2d_pair(at + T::kHalfBytes / 2, &map_w, bar, kb * kLinK, p.n + n0);
                     sm::tma_load_2d_pair(at + T::kHalfBytes, &map_x, bar, kb * kLinK, m0 + half * 128);
                 }
+                __syncwarp();
+                if (++s == T::kStages) { s = 0; phase ^= 1u; }
             }
-            // the products' last arrivals on this CTA's barriers come before it leaves
-            for (int i = max(0, it - T::kStages); i < it && ok; ++i)
-                ok = sm::bar_wait(empty(i % T::kStages), uint32_t(i / T::kStages) & 1u, abort_word, p.status);
-            if (*abort_word) {   // the copies in flight land (microseconds) before the CTA leaves
-                const uint64_t t0 = sm::timer_ns();
-                while (sm::timer_ns() - t0 < 10000000ull) {}
-            }
+        }
+        // the products' last arrivals on this CTA's barriers come before it leaves
+        for (int i = max(0, it - T::kStages); i < it && ok; ++i)
+            ok = sm::bar_wait_warp(empty(i % T::kStages), uint32_t(i / T::kStages) & 1u, abort_word, p.status);
+        if (*abort_word) {   // the copies in flight land (microseconds) before the CTA leaves
+            const uint64_t t0 = sm::timer_ns();
+            while (sm::timer_ns() - t0 < 10000000ull) {}
         }
         __syncwarp();
     } else if (warp == 1) {
-        if (lane == 0 && half == 0) {
+        if (half == 0) {
             constexpr uint32_t idesc = sm::mma_idesc(256, 256);
             const uint16_t both = uint16_t(3u << leader);
-            int it = 0, n = 0;
+            const bool issuer = sm::elect_one();
+            const uint64_t a0 = sm::desc_k_sw128(stage0), b0 = sm::desc_k_sw128(stage0 + T::kHalfBytes);
+            int s = 0, n = 0;
+            uint32_t phase = 0;
             bool ok = true;
             for (int tile = first; tile < tiles && ok; tile += step)
                 for (int k0 = kb0; k0 < kb1 && ok; k0 += piece, ++n) {
                     const int buf = n & 1;
-                    if (n >= 2 && !(ok = sm::bar_wait(acc_empty(buf), uint32_t(n / 2 - 1) & 1u, abort_word, p.status))) break;
-                    sm::tc_fence_after();
+                    if (n >= 2 && !(ok = sm::bar_wait_warp(acc_empty(buf), uint32_t(n / 2 - 1) & 1u, abort_word, p.status))) break;
                     const uint32_t d = tmem + buf * 256;
                     const int k1 = min(k0 + piece, kb1);
-                    for (int kb = k0; kb < k1; ++kb, ++it) {
-                        const int s = it % T::kStages;
-                        if (!(ok = sm::bar_wait(full(s), uint32_t(it / T::kStages) & 1u, abort_word, p.status))) break;
+                    for (int kb = k0; kb < k1; ++kb) {
+                        if (!(ok = sm::bar_wait_warp(full(s), phase, abort_word, p.status))) break;
                         sm::tc_fence_after();
-                        const uint32_t at = stage0 + s * T::kStageBytes;
-                        const uint64_t a = sm::desc_k_sw128(at), b = sm::desc_k_sw128(at + T::kHalfBytes);
+                        const uint64_t a = a0 + uint64_t(s * (T::kStageBytes >> 4)), b = b0 + uint64_t(s * (T::kStageBytes >> 4));
+                        if (issuer) {
 #pragma unroll
-                        for (int kk = 0; kk < kLinK / 16; ++kk)
-                            sm::mma_ss_pair(d, a + 2 * kk, b + 2 * kk, idesc, kb > k0 || kk > 0);
-                        sm::mma_commit_pair(empty(s), both);
+                            for (int kk = 0; kk < kLinK / 16; ++kk)
+                                sm::mma_ss_pair(d, a + 2 * kk, b + 2 * kk, idesc, kb > k0 || kk > 0);
+                            sm::mma_commit_pair(empty(s), both);
+                        }
+                        __syncwarp();
+                        if (++s == T::kStages) { s = 0; phase ^= 1u; }
                     }
-                    if (ok) sm::mma_commit_pair(acc_full(buf), both);
+                    if (ok && issuer) sm::mma_commit_pair(acc_full(buf), both);
+                    __syncwarp();
                 }
             if (*abort_word) {   // products in flight end before the tensor memory is freed
                 const uint64_t t0 = sm::timer_ns();
