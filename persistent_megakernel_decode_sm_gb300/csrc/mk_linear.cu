@@ -563,95 +563,128 @@ struct LinearLaunch {
     }
 };
 
-// Over how many units of `unit` CTAs each (a cluster holds them) a tile's contraction is cut: the
-// count with the least time by rounds of the clusters that run at once, each round the blocks of one
-// unit at `cycles` plus a fixed part (set-up, epilogue), and the exchange of the partial sums
-// between units.  Clusters of 8 leave SMs out (15 run at once on 152 SMs, 36 of 4, 76 of 2): 16 tiles
-// over 8 CTAs each took two rounds, 46.7 us against 38.8 with 4 (512 x 2048 x 8192).
-static mk_status linear_split(const void* fn, LinearLaunch& cfg, std::atomic<int> (&resident)[8], int unit, int most, int64_t tiles,
-                              int blocks, int cycles, int least, int* split) {
-    int64_t best = INT64_MAX;
-    for (int s = 1; s <= most && unit * s <= 8; ++s) {
-        if (s > 1 && blocks < s * least) break;
+// How a call is cut: tiles, CTAs or pairs that share a tile's contraction, and what that costs
+struct LinearPlan {
+    int tiles_n, tiles_m, split;
+    int64_t clusters;   // of the grid
+    int64_t cost;       // estimated cycles
+};
+// Times by rounds of the clusters that run at once: a round's blocks of the contraction at `cycles` each, a fixed
+// part (set-up, the first copies' way, the epilogue) and, where the contraction is cut over `split` units of `unit`
+// CTAs, the exchange of partial sums (`join`).  Unsplit tiles go to a persistent grid whose fixed part shows once.
+// Clusters of 8 leave SMs out (15 run at once on 152 SMs, 36 of 4, 76 of 2): 16 tiles over 8 CTAs each took two
+// rounds, 46.7 us against 38.8 with 4 (512 x 2048 x 8192).
+static mk_status linear_split(const void* fn, LinearLaunch& cfg, std::atomic<int> (&resident)[8], int unit, int most, int blocks,
+                              int cycles, int fixed, int join, LinearPlan& pl) {
+    const int64_t tiles = int64_t(pl.tiles_n) * pl.tiles_m;
+    if (tiles > (1 << 28)) return fail(MK_ERR_ARG, "linear: %lld tiles", static_cast<long long>(tiles));
+    pl.cost = INT64_MAX;
+    for (int s = 1; s <= most && unit * s <= 8 && (s == 1 || blocks >= 2 * s); ++s) {
         int fit = resident[s - 1].load();
         if (!fit) {
             cfg.shape(unit * s, 1);
             MK_CK(cudaOccupancyMaxActiveClusters(&fit, fn, &cfg.c));
-            if (fit < 1) fit = s > 1 ? -1 : 0;
-            if (!fit) return fail(MK_ERR_RESOURCES, "linear: its CTAs cannot be resident");
-            resident[s - 1].store(fit);
+            if (fit < 1 && s == 1) return fail(MK_ERR_RESOURCES, "linear: its CTAs cannot be resident");
+            resident[s - 1].store(fit < 1 ? -1 : fit);
         }
-        if (fit < 0) break;
-        const int64_t rounds = (tiles + fit - 1) / fit;
-        const int64_t t = rounds * (int64_t((blocks + s - 1) / s) * cycles + 6000) + (s > 1 ? 1500 + 500 * s : 0);
-        if (t < best) { best = t; *split = s; }
+        if (fit < 1) break;
+        const int64_t rounds = (tiles + fit - 1) / fit, part = int64_t((blocks + s - 1) / s) * cycles;
+        const bool even = (s & (s - 1)) == 0;   // (else the shares of a tile's columns come out uneven)
+        const int64_t t = s == 1 ? rounds * part + fixed : rounds * (part + fixed + (even ? join : 2 * join));
+        if (t < pl.cost) { pl.cost = t; pl.split = s; pl.clusters = s > 1 || tiles < fit ? tiles : fit; }
     }
     return MK_OK;
 }
-
-template <int BN, bool GATED, bool F32>
-static mk_status linear_launch_one(const mk_linear_args* a, LinearParams& p, int device, int sms, cudaStream_t stream) {
-    using T = LinearTile<BN, GATED>;
-    constexpr int kLinCycles = BN * (GATED ? 4 : 2) < 384 ? 384 : BN * (GATED ? 4 : 2);   // a block: its bytes, or its products
-    static std::atomic<uint64_t> set{0};
-    static std::atomic<int> resident[64][8];
-    const void* fn = reinterpret_cast<const void*>(&linear_kernel<BN, GATED, F32>);
-    mk_status st = op_smem(fn, T::kSmem, device, &set);
-    if (st != MK_OK) return st;
-    CUtensorMap map_w, map_x;
-    const int64_t wr = int64_t(p.n) * T::kAccs, xs = p.rows == 1 ? p.k : a->x_stride;
-    const cuuint64_t wd[2] = {cuuint64_t(p.k), cuuint64_t(wr)}, ws[1] = {cuuint64_t(p.k) * 2};
+static mk_status linear_maps(const mk_linear_args* a, const LinearParams& p, int64_t w_rows, uint32_t w_box, uint32_t x_box,
+                             CUtensorMap* map_w, CUtensorMap* map_x) {
+    const int64_t xs = p.rows == 1 ? p.k : a->x_stride;
+    const cuuint64_t wd[2] = {cuuint64_t(p.k), cuuint64_t(w_rows)}, ws[1] = {cuuint64_t(p.k) * 2};
     const cuuint64_t xd[2] = {cuuint64_t(p.k), cuuint64_t(p.rows)}, xst[1] = {cuuint64_t(xs) * 2};
-    const cuuint32_t wb[2] = {kLinK, 128}, xb[2] = {kLinK, BN};
-    if ((st = op_tensor_map(&map_w, a->w, 2, wd, ws, wb)) != MK_OK) return st;
-    if ((st = op_tensor_map(&map_x, a->x, 2, xd, xst, xb)) != MK_OK) return st;
-    p.tiles_n = (p.n + 127) / 128;
-    p.tiles_m = (p.rows + BN - 1) / BN;
-    const int64_t tiles = int64_t(p.tiles_n) * p.tiles_m;
-    if (tiles > (1 << 30)) return fail(MK_ERR_ARG, "linear: %lld tiles", static_cast<long long>(tiles));
-    // fewer tiles than SMs: the contraction is cut over a cluster, two blocks of it each at least
-    const int blocks = (p.k + kLinK - 1) / kLinK;
-    LinearLaunch cfg(64 + 32 * T::kWarps, T::kSmem, stream);
-    p.split = 1;
-    if (tiles * 2 <= sms)
-        if ((st = linear_split(fn, cfg, resident[device], 1, 8, tiles, blocks, kLinCycles, 2, &p.split)) != MK_OK) return st;
-    cfg.shape(p.split, p.split > 1 ? tiles : (tiles < sms ? tiles : sms));
-    MK_CK(cudaLaunchKernelEx(&cfg.c, &linear_kernel<BN, GATED, F32>, map_w, map_x, p));
-    return MK_OK;
+    const cuuint32_t wb[2] = {kLinK, w_box}, xb[2] = {kLinK, x_box};
+    const mk_status st = op_tensor_map(map_w, a->w, 2, wd, ws, wb);
+    return st != MK_OK ? st : op_tensor_map(map_x, a->x, 2, xd, xst, xb);
 }
 
+// The two kernels behind one face: plan(), then launch() with its plan
+template <int BN, bool GATED, bool F32>
+struct LinearOne {
+    using T = LinearTile<BN, GATED>;
+    // cycles as fitted to 96 to 768 tokens by 688 or 2048 inputs by 1001 to 2048 outputs, splits 1 to 4 (1.87 GHz)
+    static constexpr int kCycles = GATED ? (BN < 128 ? 750 : 900) : BN <= 32 ? 355 : BN == 64 ? 374 : 450;
+    static constexpr int kFixed = BN < 128 ? 7800 : 8400, kJoin = BN == 128 ? 3400 : 500 + 32 * BN;
+    static mk_status plan(const LinearParams& p, int device, LinearPlan& pl) {
+        static std::atomic<uint64_t> set{0};
+        static std::atomic<int> resident[64][8];
+        const void* fn = reinterpret_cast<const void*>(&linear_kernel<BN, GATED, F32>);
+        const mk_status st = op_smem(fn, T::kSmem, device, &set);
+        if (st != MK_OK) return st;
+        pl.tiles_n = (p.n + 127) / 128;
+        pl.tiles_m = (p.rows + BN - 1) / BN;
+        LinearLaunch cfg(64 + 32 * T::kWarps, T::kSmem, nullptr);
+        return linear_split(fn, cfg, resident[device], 1, 8, (p.k + kLinK - 1) / kLinK, kCycles, kFixed, kJoin, pl);
+    }
+    static mk_status launch(const mk_linear_args* a, LinearParams& p, const LinearPlan& pl, cudaStream_t stream) {
+        CUtensorMap map_w, map_x;
+        const mk_status st = linear_maps(a, p, int64_t(p.n) * T::kAccs, 128, BN, &map_w, &map_x);
+        if (st != MK_OK) return st;
+        p.tiles_n = pl.tiles_n; p.tiles_m = pl.tiles_m; p.split = pl.split;
+        LinearLaunch cfg(64 + 32 * T::kWarps, T::kSmem, stream);
+        cfg.shape(pl.split, pl.clusters);
+        MK_CK(cudaLaunchKernelEx(&cfg.c, &linear_kernel<BN, GATED, F32>, map_w, map_x, p));
+        return MK_OK;
+    }
+};
 template <bool GATED, bool F32>
-static mk_status linear_launch_pair(const mk_linear_args* a, LinearParams& p, int device, cudaStream_t stream) {
+struct LinearPair {
     using T = PairTile<GATED>;
-    static std::atomic<uint64_t> set{0};
-    static std::atomic<int> resident[64][8];
-    const void* fn = reinterpret_cast<const void*>(&linear_pair_kernel<GATED, F32>);
-    mk_status st = op_smem(fn, T::kSmem, device, &set);
-    if (st != MK_OK) return st;
-    CUtensorMap map_w, map_x;
-    const int64_t wr = int64_t(p.n) * (GATED ? 2 : 1);
-    const cuuint64_t wd[2] = {cuuint64_t(p.k), cuuint64_t(wr)}, ws[1] = {cuuint64_t(p.k) * 2};
-    const cuuint64_t xd[2] = {cuuint64_t(p.k), cuuint64_t(p.rows)}, xst[1] = {cuuint64_t(a->x_stride) * 2};
-    const cuuint32_t wb[2] = {kLinK, T::kRows}, xb[2] = {kLinK, 128};
-    if ((st = op_tensor_map(&map_w, a->w, 2, wd, ws, wb)) != MK_OK) return st;
-    if ((st = op_tensor_map(&map_x, a->x, 2, xd, xst, xb)) != MK_OK) return st;
-    p.tiles_n = (p.n + 2 * T::kRows - 1) / (2 * T::kRows);
-    p.tiles_m = (p.rows + 255) / 256;
-    const int64_t tiles = int64_t(p.tiles_n) * p.tiles_m;
-    if (tiles > (1 << 28)) return fail(MK_ERR_ARG, "linear: %lld tiles", static_cast<long long>(tiles));
-    const int blocks = (p.k + kLinK - 1) / kLinK;
-    LinearLaunch cfg(320, T::kSmem, stream);
-    if ((st = linear_split(fn, cfg, resident[device], 2, 4, tiles, blocks, 512, 2, &p.split)) != MK_OK) return st;
-    const int fit = resident[device][p.split - 1].load();
-    cfg.shape(2 * p.split, p.split > 1 || tiles < fit ? tiles : fit);   // (a persistent grid of the pairs that run at once)
-    MK_CK(cudaLaunchKernelEx(&cfg.c, &linear_pair_kernel<GATED, F32>, map_w, map_x, p));
-    return MK_OK;
+    static mk_status plan(const LinearParams& p, int device, LinearPlan& pl) {
+        static std::atomic<uint64_t> set{0};
+        static std::atomic<int> resident[64][8];
+        const void* fn = reinterpret_cast<const void*>(&linear_pair_kernel<GATED, F32>);
+        const mk_status st = op_smem(fn, T::kSmem, device, &set);
+        if (st != MK_OK) return st;
+        pl.tiles_n = (p.n + 2 * T::kRows - 1) / (2 * T::kRows);
+        pl.tiles_m = (p.rows + 255) / 256;
+        LinearLaunch cfg(320, T::kSmem, nullptr);
+        return linear_split(fn, cfg, resident[device], 2, 4, (p.k + kLinK - 1) / kLinK, 515, GATED ? 20000 : 15000, 2500, pl);
+    }
+    static mk_status launch(const mk_linear_args* a, LinearParams& p, const LinearPlan& pl, cudaStream_t stream) {
+        CUtensorMap map_w, map_x;
+        const mk_status st = linear_maps(a, p, int64_t(p.n) * (GATED ? 2 : 1), T::kRows, 128, &map_w, &map_x);
+        if (st != MK_OK) return st;
+        p.tiles_n = pl.tiles_n; p.tiles_m = pl.tiles_m; p.split = pl.split;
+        LinearLaunch cfg(320, T::kSmem, stream);
+        cfg.shape(2 * pl.split, pl.clusters);
+        MK_CK(cudaLaunchKernelEx(&cfg.c, &linear_pair_kernel<GATED, F32>, map_w, map_x, p));
+        return MK_OK;
+    }
+};
+template <typename K>
+static mk_status linear_run(const mk_linear_args* a, LinearParams& p, int device, cudaStream_t stream) {
+    LinearPlan pl;
+    const mk_status st = K::plan(p, device, pl);
+    return st != MK_OK ? st : K::launch(a, p, pl, stream);
 }
-
-template <int BN, bool GATED>
-static mk_status linear_launch(const mk_linear_args* a, LinearParams& p, int device, int sms, cudaStream_t stream) {
-    return p.out_f32 ? linear_launch_one<BN, GATED, true>(a, p, device, sms, stream)
-                     : linear_launch_one<BN, GATED, false>(a, p, device, sms, stream);
+// The tile width (or the pairs) whose plan costs least: wide tiles read w fewer times and pairs make twice the products a
+// cycle, narrow tiles fill the device (2048 x 2048 weights, us: 96 tokens 7.2 with 64 columns over 4 CTAs each, 7.8
+// with 32 over 2, 8.4 with 128 over 4, 11.0 in pairs; 768 tokens 24.4 with 32, 13.3 with 128, 15.1 in pairs; 2048
+// tokens and more: pairs).
+template <bool GATED, bool F32>
+static mk_status linear_dispatch(const mk_linear_args* a, LinearParams& p, int device, cudaStream_t stream) {
+    LinearPlan best{}, pl{};
+    mk_status (*launch)(const mk_linear_args*, LinearParams&, const LinearPlan&, cudaStream_t) = nullptr;
+    mk_status st = MK_OK;
+    auto offer = [&](auto kernel, bool wanted) {
+        using K = decltype(kernel);
+        if (st != MK_OK || !wanted || (st = K::plan(p, device, pl)) != MK_OK) return;
+        if (!launch || pl.cost < best.cost) { best = pl; launch = &K::launch; }
+    };
+    offer(LinearOne<16, GATED, F32>{}, p.rows <= 64);
+    offer(LinearOne<32, GATED, F32>{}, p.rows > 16 && p.rows <= 768);
+    offer(LinearOne<64, GATED, F32>{}, p.rows > 32 && p.rows <= 1536);
+    offer(LinearOne<128, GATED, F32>{}, p.rows > 64);
+    offer(LinearPair<GATED, F32>{}, p.rows > 128);
+    return st != MK_OK ? st : launch(a, p, best, stream);
 }
 
 static mk_status linear_check(const mk_linear_args* a) {
@@ -707,16 +740,7 @@ extern "C" mk_status mk_linear(const mk_linear_args* a, void* stream) {
     const mk_status ds = op_device(&device, &sms);
     if (ds != MK_OK) return ds;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (a->activation == MK_ACT_SWIGLU) {
-        if (p.rows <= 16) return linear_launch<16, true>(a, p, device, sms, s);
-        if (p.rows <= 32) return linear_launch<32, true>(a, p, device, sms, s);
-        if (p.rows <= 64) return linear_launch<64, true>(a, p, device, sms, s);
-        if (p.rows <= 128) return linear_launch<128, true>(a, p, device, sms, s);
-        return p.out_f32 ? linear_launch_pair<true, true>(a, p, device, s) : linear_launch_pair<true, false>(a, p, device, s);
-    }
-    if (p.rows <= 16) return linear_launch<16, false>(a, p, device, sms, s);
-    if (p.rows <= 32) return linear_launch<32, false>(a, p, device, sms, s);
-    if (p.rows <= 64) return linear_launch<64, false>(a, p, device, sms, s);
-    if (p.rows <= 128) return linear_launch<128, false>(a, p, device, sms, s);
-    return p.out_f32 ? linear_launch_pair<false, true>(a, p, device, s) : linear_launch_pair<false, false>(a, p, device, s);
+    if (a->activation == MK_ACT_SWIGLU)
+        return p.out_f32 ? linear_dispatch<true, true>(a, p, device, s) : linear_dispatch<true, false>(a, p, device, s);
+    return p.out_f32 ? linear_dispatch<false, true>(a, p, device, s) : linear_dispatch<false, false>(a, p, device, s);
 }
