@@ -455,9 +455,8 @@ class Decoder:
 
 _LINEAR_ARGS = struct.Struct("@4iPqPPPq2iPqP")
 _ATTEND_ARGS = struct.Struct("@4iPPPqPqPP5ifP")
-_KV_ARGS, _PAGES_ARGS = struct.Struct("@PPqqq"), struct.Struct("@Piii")
 assert _LINEAR_ARGS.size == ctypes.sizeof(mk_linear_args) and _ATTEND_ARGS.size == ctypes.sizeof(mk_attend_args)
-assert _KV_ARGS.size == ctypes.sizeof(mk_kv)
+assert ctypes.sizeof(mk_kv) == 40 and ctypes.sizeof(mk_kv_pages) == 24   # five 64-bit words, three (packed below)
 
 
 def _operand(t, name, dtypes, device, dim):
@@ -473,10 +472,6 @@ def _operand(t, name, dtypes, device, dim):
     if strides[-1] != 1 and shape[-1] > 1:
         raise ValueError(f"{name}: its last dimension must be contiguous")
     return shape, strides
-
-
-def _address(data: bytes) -> int:
-    return ctypes.cast(data, _P).value
 
 
 def _status_ptr(status, device):
@@ -590,27 +585,25 @@ def attend(q, kv, q_lens: Sequence[int], kv_lens: Sequence[int], layer: int = 0,
     layers, nkv, positions = shape[-4:-1]
     if not 0 <= layer < layers:
         raise ValueError(f"layer {layer} of {layers}")
-    c_pages = None
     if pages is None:
         if shape[0] < batch:
             raise ValueError(f"the cache holds {shape[0]} sequences, q_lens name {batch}")
-        c_kv = _KV_ARGS.pack(k.data_ptr(), v.data_ptr(), ks[0], ks[1], ks[2])
+        cache = array.array("q", (k.data_ptr(), v.data_ptr(), ks[0], ks[1], ks[2]))
     else:
         table, block_size, n_blocks = pages
         tshape, ts = _operand(table, "the block table", (torch.int32,), dev, 2)
         if tshape[0] < batch or (ts[0] != tshape[1] and tshape[0] > 1):
             raise ValueError(f"the block table must be contiguous, with a row for each of {batch} sequences")
-        if positions < n_blocks * block_size:
-            raise ValueError(f"the pool holds {positions} positions a head, {n_blocks} blocks of {block_size} need more")
-        c_kv = _KV_ARGS.pack(k.data_ptr(), v.data_ptr(), 0, ks[0], ks[1])
-        c_pages = _PAGES_ARGS.pack(table.data_ptr(), block_size, tshape[1], n_blocks)
+        if block_size < 1 or n_blocks < 1 or positions < n_blocks * block_size:
+            raise ValueError(f"the pool holds {positions} positions a head, {n_blocks} blocks of {block_size} do not fit it")
+        cache = array.array("q", (k.data_ptr(), v.data_ptr(), 0, ks[0], ks[1],
+                                  table.data_ptr(), block_size | tshape[1] << 32, n_blocks))
         positions = tshape[1] * block_size
     lens = array.array("i", q_lens)
-    lens.extend(kv_lens)
-    at = lens.buffer_info()[0]
-    # (bytes objects keep their contents at a fixed address while they live)
+    lens.extend(array.array("i", kv_lens))
+    at, c_kv = lens.buffer_info()[0], cache.buffer_info()[0]
     a = _ATTEND_ARGS.pack(nq, nkv, d, batch, at, at + 4 * batch, q.data_ptr(), qs[0], out.data_ptr(), os[0],
-                          _address(c_kv), 0 if c_pages is None else _address(c_pages), layer, min(positions, 1 << 30),
+                          c_kv, c_kv + 40 if pages is not None else 0, layer, min(positions, 1 << 30),
                           window, sinks, shared_prefix, scale or 0.0, 0 if status is None else _status_ptr(status, dev))
     need = lib.mk_attend_workspace(a)
     ws, size = 0, 0

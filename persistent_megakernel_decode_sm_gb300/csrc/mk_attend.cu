@@ -22,6 +22,7 @@ struct AttendSeg {
     int32_t cache;         // the sequence whose cache rows (or table row) are read
     int32_t splits, item0; // shares of the key tiles; items of the segments before
     int32_t part0;         // first row group of its parts in the workspace (units of n_q_heads rows)
+    int32_t merge0;        // tokens with parts to join in the segments before (a sequence's, not the prefix's)
 };
 constexpr int32_t kNoCausal = INT_MIN;
 constexpr int kKeys = 128;     // key tile
@@ -30,6 +31,7 @@ constexpr int kBlockRows = 128;
 struct AttendCommon {
     int32_t nq, nkv, group, block_tokens;   // block_tokens: query tokens of a block, 128 / group
     int32_t tokens, segs, prefix_seg;       // prefix_seg: 1 where segment 0 is the shared prefix
+    int32_t merge_tokens;                   // tokens with parts to join
     int32_t window, sinks;
     float scale_log2;                       // scale / ln 2
     const int32_t* table;                   // paged: [batch][max_blocks]
@@ -79,6 +81,10 @@ struct AttendTile {
     // tensor memory: scores, output, softmax weights (two bf16 a column; at D = 128 over the scores' columns)
     static constexpr int kS = 0, kO = 128, kP = D == 128 ? 0 : 192;
     static constexpr bool kShareSP = D == 128;
+    // rows are divided by the sum of their weights as rounded, which cancels the rounding of a weight that
+    // outweighs the others -- but at D = 64, where that took 9% (97 us against 89; 4096 tokens, causal, 1B heads) and the
+    // reference is a maximum, so that such a weight is a power of two or near it
+    static constexpr bool kRoundedSum = D != 64;
     static constexpr int kFlags = 8;                            // ring of the copies' skip masks
 };
 
@@ -303,13 +309,14 @@ attend_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
         const int sinks = p.window ? p.sinks : 0;
         const uint32_t lanes = uint32_t(warp * 32) << 16;
         const float c = p.scale_log2;
-        // The reference m of a row's weights exp2((s - m) c) need not be its maximum: the weights' and sums' formats
-        // have fp32's exponents, so any m will do that keeps a tile's sum within 2^-20 .. 2^20 (below, once
-        // some tile's is).  It starts at 0, which holds for scores of ordinary size, and no maximum is taken; a
-        // tile whose sum falls outside is read again, its maximum taken as the new reference.
+        // The reference m of a row's weights exp2((s - m) c) need not be the maximum so far: the formats of weights and
+        // sums have fp32's exponents.  D < 128: it is the maximum of the first tile in which the row sees a key, and
+        // moves only to one more than 2^8 above it (O is rescaled then).  D = 128: it starts at 0, which holds for
+        // scores of ordinary size, and no maximum is taken; a tile whose sum of weights exceeds 2^20, or, while none
+        // counted, falls below 2^-20, is read again and its maximum becomes the reference.
         float m = 0.f, l = 0.f;
         bool set = false;   // some tile of this row counted
-        float high = 8.f / c, deep = -8.f / c;   // (d < 128) a maximum above, or a first one below: the new reference
+        float high = -INFINITY;   // (D < 128) a maximum above it is the new reference
         bool ok = true;     // (a wait that ran out shows at the vote of its tile: until then the lanes stay together)
         const int seen_end = causal ? t0 + 1 : seg.key1;   // keys that every row of the block sees: [seen_low, seen_end), the sinks
         const int seen_low = p.window ? max(t1 - p.window + 1, seg.key0) : seg.key0;
@@ -339,8 +346,10 @@ attend_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
                         float2 x = make_float2(__uint_as_float(s[q][2 * i]), __uint_as_float(s[q][2 * i + 1]));
                         x = fma2(x, make_float2(c, c), make_float2(-b, -b));
                         x = make_float2(exp2_approx(x.x), exp2_approx(x.y));
+                        const uint32_t w = pack_bf16(x.x, x.y);
+                        if (T::kRoundedSum) x = make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
                         sum[i & 1] = add2(sum[i & 1], x);
-                        s[q][i] = pack_bf16(x.x, x.y);
+                        s[q][i] = w;
                     }
                     if (store) tmem_st16_head(tmem + T::kP + lanes + q * 16, s[q]);
                 }
@@ -385,14 +394,13 @@ attend_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
                 // the products that read the last weights and wrote O are done before either is touched
                 if (j > 0) ok = sm::bar_wait_sync(pv_done, uint32_t(j - 1) & 1u, abort_word, p.status) && ok;
                 sm::tc_fence_after();
-                const bool rise = top > high || (top < deep && top > -INFINITY);
+                const bool rise = top > high;
                 if (__any_sync(0xFFFFFFFFu, rise || !ok)) {
                     if (!(ok = __all_sync(0xFFFFFFFFu, ok))) break;
-                    const float f = rise && deep == -INFINITY ? exp2_approx((m - top) * c) : 1.f;
+                    const float f = rise && set ? exp2_approx((m - top) * c) : 1.f;
                     if (rise) { m = top; high = m + 8.f / c; }
                     if (j > 0) rescale(f);
                 }
-                if (top > -INFINITY) deep = -INFINITY;
                 weights(true);
             } else
             for (int pass = 0;; ++pass) {
@@ -495,77 +503,94 @@ attend_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
     if (warp == 5) sm::tmem_free(tmem, 256);
 }
 
-// Joins the parts of a row: with M = max m, out = sum 2^(m - M) o / sum 2^(m - M) l, in order of the
-// shares (the prefix's first).  One warp per (token, head).
-template <int D, int SEGS>
+// Joins the parts of a row: with M = max m, out = sum 2^(m - M) o / sum 2^(m - M) l.  WARPS warps per row (token,
+// head): they load the rows' (m, l), then D / 4 threads a part's o, several parts at a time, and add their sums in a
+// fixed order.  A chain of memory latencies, so many parts take four warps, which halve it against one.
+template <int D, int SEGS, int WARPS>
 __global__ void __launch_bounds__(128) attend_merge_kernel(const __grid_constant__ AttendParams<SEGS> p) {
     sm::pdl_trigger();
     sm::pdl_wait();
-    const int lane = threadIdx.x & 31;
-    const int64_t item = int64_t(blockIdx.x) * 4 + (threadIdx.x >> 5);
-    if (item >= int64_t(p.tokens) * p.nq) return;
-    const int tok = int(item / p.nq), head = int(item % p.nq);
-    int si;
+    constexpr int kThreads = WARPS * 32, kLanes = D / 4, kGroups = kThreads / kLanes, kRows = 4 / WARPS;
+    constexpr int kMaxParts = 512;   // a sequence's and the prefix's shares, 256 each at most
+    __shared__ float weight[kRows][WARPS == 1 ? 64 : kMaxParts];
+    __shared__ float4 sums[kRows][kThreads];
+    __shared__ float red[kRows][2][WARPS];
+    const int r = threadIdx.x / kThreads, t = threadIdx.x % kThreads;
+    const int64_t item = int64_t(blockIdx.x) * kRows + r;
+    const bool live = item < int64_t(p.merge_tokens) * p.nq;
+    const int at_token = live ? int(item / p.nq) : 0, head = live ? int(item % p.nq) : 0;
+    int si = p.prefix_seg;
     {
-        int lo = p.prefix_seg, hi = p.segs - 1;   // the segment of this token
+        int lo = p.prefix_seg, hi = p.segs - 1;   // the segment of this token: the last that starts at or before it
         while (lo < hi) {
             const int mid = (lo + hi + 1) >> 1;
-            if (tok >= p.seg[mid].q0) lo = mid;
+            if (at_token >= p.seg[mid].merge0) lo = mid;
             else hi = mid - 1;
         }
         si = lo;
     }
     const AttendSeg& seg = p.seg[si];
-    const int np = p.prefix_seg ? p.seg[0].splits : 0, n = np + seg.splits;
-    if (n == 1) return;   // its item wrote it
+    const int local = at_token - seg.merge0, tok = seg.q0 + local;
+    const int np = p.prefix_seg ? p.seg[0].splits : 0, n = live ? np + seg.splits : 0;
     auto at = [&](int s) {
-        const int64_t r = s < np ? int64_t(p.seg[0].part0) + int64_t(s) * p.seg[0].n + tok
-                                 : int64_t(seg.part0) + int64_t(s - np) * seg.n + tok - seg.q0;
-        return r * p.nq + head;
+        const int64_t row = s < np ? int64_t(p.seg[0].part0) + int64_t(s) * p.seg[0].n + tok
+                                   : int64_t(seg.part0) + int64_t(s - np) * seg.n + local;
+        return row * p.nq + head;
     };
+    auto sync = [&]() { if (WARPS == 1) __syncwarp(); else __syncthreads(); };
     float M = -INFINITY;
-    for (int s = lane; s < n; s += 32) {
+    for (int s = t; s < n; s += kThreads) {
         const float2 ml = p.part_ml[at(s)];
         if (ml.y > 0.f) M = fmaxf(M, ml.x);
     }
 #pragma unroll
     for (int x = 16; x; x >>= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, x));
-    constexpr int E = D / 32;
-    float acc[E], total = 0.f;
+    if (WARPS > 1) {
+        if ((t & 31) == 0) red[r][0][t >> 5] = M;
+        sync();
 #pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] = 0.f;
-    for (int s0 = 0; s0 < n; s0 += 32) {
-        float w = 0.f;
-        if (s0 + lane < n) {
-            const float2 ml = p.part_ml[at(s0 + lane)];
-            if (ml.y > 0.f) { w = exp2_approx(ml.x - M); total = fmaf(w, ml.y, total); }
-        }
-#pragma unroll 8
-        for (int s = 0; s < min(32, n - s0); ++s) {
-            const float ws = __shfl_sync(0xFFFFFFFFu, w, s);
-            const float* o = p.part_o + at(s0 + s) * D + lane * E;
-            float v[E];
-            if constexpr (E == 4) {
-                const float4 x = *reinterpret_cast<const float4*>(o);
-                v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
-            } else if constexpr (E == 2) {
-                const float2 x = *reinterpret_cast<const float2*>(o);
-                v[0] = x.x; v[1] = x.y;
-            } else {
-                v[0] = *o;
-            }
-#pragma unroll
-            for (int e = 0; e < E; ++e) acc[e] = ws > 0.f ? fmaf(ws, v[e], acc[e]) : acc[e];
-        }
+        for (int w = 0; w < WARPS; ++w) M = fmaxf(M, red[r][0][w]);
+    }
+    float L = 0.f;
+    for (int s = t; s < n; s += kThreads) {
+        const float2 ml = p.part_ml[at(s)];
+        const float w = ml.y > 0.f ? exp2_approx(ml.x - M) : 0.f;   // (a part without a key: its o may hold anything)
+        weight[r][s] = w;
+        if (w > 0.f) L = fmaf(w, ml.y, L);
     }
 #pragma unroll
-    for (int x = 16; x; x >>= 1) total += __shfl_xor_sync(0xFFFFFFFFu, total, x);
-    const float inv = total > 0.f ? 1.f / total : 0.f;
-    __nv_bfloat16* dst = p.out + tok * p.out_stride + head * D + lane * E;
-    if constexpr (E == 1) *dst = __float2bfloat16_rn(acc[0] * inv);
-    else
+    for (int x = 16; x; x >>= 1) L += __shfl_xor_sync(0xFFFFFFFFu, L, x);
+    if (WARPS > 1 && (t & 31) == 0) red[r][1][t >> 5] = L;
+    sync();
+    if (WARPS > 1) {
+        L = 0.f;
 #pragma unroll
-        for (int e = 0; e < E; e += 2) *reinterpret_cast<uint32_t*>(dst + e) = pack_bf16(acc[e] * inv, acc[e + 1] * inv);
+        for (int w = 0; w < WARPS; ++w) L += red[r][1][w];
+    }
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    const int e = t % kLanes * 4;
+#pragma unroll 4
+    for (int s = t / kLanes; s < n; s += kGroups) {
+        const float w = weight[r][s];
+        const float4 o = *reinterpret_cast<const float4*>(p.part_o + at(s) * D + e);
+        if (w > 0.f) {
+            acc.x = fmaf(w, o.x, acc.x);
+            acc.y = fmaf(w, o.y, acc.y);
+            acc.z = fmaf(w, o.z, acc.z);
+            acc.w = fmaf(w, o.w, acc.w);
+        }
+    }
+    sums[r][t] = acc;
+    sync();
+    if (!live || t >= kLanes) return;
+#pragma unroll
+    for (int g = 1; g < kGroups; ++g) {
+        const float4 o = sums[r][g * kLanes + t];
+        acc.x += o.x; acc.y += o.y; acc.z += o.z; acc.w += o.w;
+    }
+    const float inv = L > 0.f ? 1.f / L : 0.f;
+    uint2* dst = reinterpret_cast<uint2*>(p.out + tok * p.out_stride + head * D + e);
+    *dst = make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
 }
 
 // Checks the arguments that the workspace's size depends on.
@@ -633,8 +658,8 @@ static mk_status attend_check(const mk_attend_args* a) {
 // The segments, items and workspace of a call
 struct AttendPlan {
     int64_t tokens = 0, items = 0, part_rows = 0;   // part_rows: rows of parts in the workspace
-    int segs = 0, prefix_seg = 0;
-    bool merge = false;
+    int64_t merge_tokens = 0;
+    int segs = 0, prefix_seg = 0, parts = 0;   // parts: of a row, at most
     AttendSeg seg[MK_ATTEND_MAX_BATCH + 1];
 };
 static int64_t attend_tiles(const AttendSeg& s, int t0, int t1, int window, int sinks) {   // key tiles of a block (as KeyRange)
@@ -647,39 +672,86 @@ static int64_t attend_tiles(const AttendSeg& s, int t0, int t1, int window, int 
 }
 static mk_status attend_plan(const mk_attend_args* a, int sms, AttendPlan& pl) {
     const int group = a->n_q_heads / a->n_kv_heads, bt = kBlockRows / group;
+    const uint32_t slots = 2 * uint32_t(sms);   // (two CTAs to an SM)
+    // of each segment: the key tiles of its last block of queries (the most) and of its middle one; blocks by heads
+    uint32_t tiles[MK_ATTEND_MAX_BATCH + 1] = {}, middle[MK_ATTEND_MAX_BATCH + 1] = {}, blocks[MK_ATTEND_MAX_BATCH + 1] = {};
     for (int b = 0; b < a->batch; ++b) pl.tokens += a->q_lens[b];
+    auto add = [&](const AttendSeg& s) {
+        auto seen = [&](int t) {
+            const bool causal = s.pos0 != kNoCausal;
+            return uint32_t(attend_tiles(s, causal ? s.pos0 + t : 0, causal ? s.pos0 + std::min(t + bt, s.n) - 1 : 0, a->window, a->sinks));
+        };
+        const int n = (s.n + bt - 1) / bt;
+        const uint32_t k = seen((n - 1) * bt);
+        int at = pl.segs++;   // longest first, behind the prefix: what starts last is short
+        for (; at > pl.prefix_seg && tiles[at - 1] < k; --at) {
+            pl.seg[at] = pl.seg[at - 1];
+            tiles[at] = tiles[at - 1];
+            middle[at] = middle[at - 1];
+            blocks[at] = blocks[at - 1];
+        }
+        pl.seg[at] = s;
+        tiles[at] = k;
+        middle[at] = seen(n / 2 * bt < s.n ? n / 2 * bt : 0);
+        blocks[at] = uint32_t(n) * uint32_t(a->n_kv_heads);   // (2^24 tokens by 4096 heads at most, 4096 / 8 of them: fits)
+    };
     if (a->shared_prefix && pl.tokens) {
-        pl.seg[pl.segs++] = {0, int32_t(pl.tokens), kNoCausal, 0, a->shared_prefix, 0, 1, 0, 0};
+        add({0, int32_t(pl.tokens), kNoCausal, 0, a->shared_prefix, 0, 1, 0, 0, 0});
         pl.prefix_seg = 1;
     }
     int64_t q0 = 0, work = 0;
+    uint32_t longest = 1;
     for (int b = 0; b < a->batch; ++b) {
         const int n = a->q_lens[b];
-        if (n) pl.seg[pl.segs++] = {int32_t(q0), n, a->kv_lens[b] - n, a->shared_prefix, a->kv_lens[b], b, 1, 0, 0};
+        if (n) add({int32_t(q0), n, a->kv_lens[b] - n, a->shared_prefix, a->kv_lens[b], b, 1, 0, 0, 0});
         q0 += n;
     }
-    // key tiles in all (the longest block's for every block of a segment)
     for (int i = 0; i < pl.segs; ++i) {
-        const AttendSeg& s = pl.seg[i];
-        const int last = (s.n - 1) / bt * bt;
-        const int64_t blocks = (s.n + bt - 1) / bt;
-        work += blocks * a->n_kv_heads * attend_tiles(s, s.pos0 + last, s.pos0 + s.n - 1, a->window, a->sinks);
+        work += int64_t(blocks[i]) * middle[i];
+        longest = std::max(longest, tiles[i]);
     }
-    // a share: what makes two CTAs on every SM, so far as there are tiles
-    const int64_t share = std::max<int64_t>(2, (work + 2 * sms - 1) / (2 * sms));
+    // A share of the key tiles: the one with the least time, in tiles, by this estimate: an item costs its tiles and
+    // kItem more; long items of one length run in whole rounds of `slots`, the others (a causal prompt's blocks, of every
+    // length) fill what these leave; joining costs kMerge.  (Eight single tokens with windows of 4096: shares of
+    // 8 tiles made 320 items for 304 places and so two rounds, 43 us against 32 with shares of 9.)
+    constexpr uint32_t kItem = 2, kMerge = 3;
+    auto splits = [](uint32_t t, uint32_t share) { return std::min(std::max(1u, (t + share - 1) / share), 256u); };
+    auto cost = [&](uint32_t share) {
+        uint32_t top = 0, each[MK_ATTEND_MAX_BATCH + 1];
+        int64_t all = 0, many = 0;
+        bool merge = pl.prefix_seg != 0;
+        for (int i = 0; i < pl.segs; ++i) {
+            const uint32_t n = splits(tiles[i], share);
+            each[i] = (tiles[i] + n - 1) / n + kItem;
+            top = std::max(top, each[i]);
+            all += int64_t(blocks[i]) * (middle[i] + n * kItem);
+            merge = merge || n > 1;
+        }
+        for (int i = 0; i < pl.segs; ++i)
+            if (2 * each[i] > top && 4 * middle[i] > 3 * tiles[i]) many += int64_t(blocks[i]) * splits(tiles[i], share);
+        return std::max({(many + slots - 1) / slots * top, (all + slots - 1) / slots, int64_t(top)}) + (merge ? kMerge : 0);
+    };
+    uint32_t share = longest;
+    if (work < int64_t(slots) * longest * 4) {   // (else the blocks alone fill the device for rounds)
+        int64_t best = cost(longest);
+        for (uint32_t k : {1u, 2u, 4u})
+            for (uint32_t s = std::max<uint32_t>(2, uint32_t(work / (slots * k))), end = 2 * s; s <= end && s < longest; s += std::max(1u, s / 4)) {
+                const int64_t c = cost(s);
+                if (c < best) { best = c; share = s; }
+            }
+    }
     int64_t part = 0;
     for (int i = 0; i < pl.segs; ++i) {
         AttendSeg& s = pl.seg[i];
-        const int last = (s.n - 1) / bt * bt;
-        const int64_t blocks = (s.n + bt - 1) / bt;
-        const int64_t tiles = attend_tiles(s, s.pos0 + last, s.pos0 + s.n - 1, a->window, a->sinks);
-        s.splits = int32_t(std::min<int64_t>(std::max<int64_t>(1, (tiles + share - 1) / share), 256));
+        s.splits = int32_t(splits(tiles[i], share));
         s.item0 = int32_t(pl.items);
-        pl.items += blocks * a->n_kv_heads * s.splits;
+        s.merge0 = int32_t(pl.merge_tokens);
+        pl.items += blocks[i] * s.splits;
         if (s.splits > 1 || pl.prefix_seg) {
-            pl.merge = true;
             s.part0 = int32_t(part);
             part += int64_t(s.splits) * s.n;
+            if (i >= pl.prefix_seg) pl.merge_tokens += s.n;
+            pl.parts = std::max(pl.parts, s.splits + (pl.prefix_seg ? pl.seg[0].splits : 0));
         }
         if (pl.items > INT_MAX || part > INT_MAX) return fail(MK_ERR_ARG, "attend: too many query tokens");
     }
@@ -724,11 +796,14 @@ static mk_status attend_launch(const mk_attend_args* a, const AttendCommon& comm
     cfg.blockDim = dim3(192);
     cfg.dynamicSmemBytes = T::kSmem;
     MK_CK(cudaLaunchKernelEx(&cfg, &attend_kernel<D, SEGS>, mq, mk_, mv, p));
-    if (pl.merge) {
-        cfg.gridDim = dim3(unsigned((pl.tokens * p.nq + 3) / 4));
+    if (pl.merge_tokens) {
+        const int64_t rows = pl.merge_tokens * p.nq;
+        const bool wide = pl.parts > 8;
+        if ((wide ? rows : (rows + 3) / 4) > INT_MAX) return fail(MK_ERR_ARG, "attend: too many query tokens");
+        cfg.gridDim = dim3(unsigned(wide ? rows : (rows + 3) / 4));
         cfg.blockDim = dim3(128);
         cfg.dynamicSmemBytes = 0;
-        MK_CK(cudaLaunchKernelEx(&cfg, &attend_merge_kernel<D, SEGS>, p));
+        MK_CK(wide ? cudaLaunchKernelEx(&cfg, &attend_merge_kernel<D, SEGS, 4>, p) : cudaLaunchKernelEx(&cfg, &attend_merge_kernel<D, SEGS, 1>, p));
     }
     return MK_OK;
 }
@@ -776,7 +851,7 @@ extern "C" mk_status mk_attend(const mk_attend_args* a, void* workspace, size_t 
         return fail(MK_ERR_CAPACITY, "attend: workspace of %zu bytes, %zu needed (mk_attend_workspace)", workspace_bytes, need);
     AttendCommon p{};
     p.nq = a->n_q_heads; p.nkv = a->n_kv_heads; p.group = p.nq / p.nkv; p.block_tokens = kBlockRows / p.group;
-    p.tokens = int32_t(pl.tokens); p.segs = pl.segs; p.prefix_seg = pl.prefix_seg;
+    p.tokens = int32_t(pl.tokens); p.segs = pl.segs; p.prefix_seg = pl.prefix_seg; p.merge_tokens = int32_t(pl.merge_tokens);
     p.window = std::min(a->window, 1 << 30); p.sinks = std::min(a->sinks, 1 << 30);   // (positions stay below 2^30)
     p.scale_log2 = float((a->scale != 0.f ? double(a->scale) : 1.0 / std::sqrt(double(a->head_dim))) * 1.4426950408889634);
     if (a->pages) {
