@@ -605,14 +605,19 @@ def attend(q, kv, q_lens: Sequence[int], kv_lens: Sequence[int], layer: int = 0,
     a = _ATTEND_ARGS.pack(nq, nkv, d, batch, at, at + 4 * batch, q.data_ptr(), qs[0], out.data_ptr(), os[0],
                           c_kv, c_kv + 40 if pages is not None else 0, layer, min(positions, 1 << 30),
                           window, sinks, shared_prefix, scale or 0.0, 0 if status is None else _status_ptr(status, dev))
-    need = lib.mk_attend_workspace(a)
-    ws, size = 0, 0
     if workspace is not None:
         if not workspace.is_cuda or workspace.get_device() != dev or not workspace.is_contiguous():
             raise ValueError("workspace must be contiguous, on q's device")
-        ws, size = workspace.data_ptr(), workspace.numel() * workspace.element_size()
-    elif need:
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-        ws, size = workspace.data_ptr(), need
-    _launch(dev, lib.mk_attend, a, ws, size)
+        _launch(dev, lib.mk_attend, a, workspace.data_ptr(), workspace.numel() * workspace.element_size())
+        return out
+    need = lib.mk_attend_workspace(a)
+    if not need:
+        _launch(dev, lib.mk_attend, a, 0, 0)
+        return out
+    # from torch's allocator, for this stream: given back at once, it is reused behind the call in stream order
+    ws = torch._C._cuda_cudaCachingAllocator_raw_alloc(need, torch._C._cuda_getCurrentRawStream(dev))
+    try:
+        _launch(dev, lib.mk_attend, a, ws, need)
+    finally:
+        torch._C._cuda_cudaCachingAllocator_raw_delete(ws)
     return out

@@ -131,6 +131,12 @@ __device__ __forceinline__ uint32_t low_bits(int n) { return n >= 32 ? 0xFFFFFFF
 // scores into weights exp2(scale_log2 (s - m)) with a reference m (below), writes them back as bf16, and
 // O += P V runs with P read from tensor memory.  Two CTAs share an SM, so one's products run while the
 // other's threads are at their exponentials.
+// What bounds it with many rows is the chain of one warp's ~650 instructions per tile, two such warps to a scheduler
+// (4096 causal tokens of 32 / 8 heads by 64: 84 us, 820 TFLOP/s, tensor pipe 37% and special functions 37% busy; 128 wide:
+// 930 TFLOP/s, tensor pipe 48%).  Measured against: two threads per row at 80 or 96 registers 107 us; tiles of 64 keys
+// with three or four CTAs 107 and 161; registers moved between warps (setmaxnreg) 98; the exponentials taken out
+// left the time as it was, the products taken out 10% of it (24% at width 128).  With few rows the cache's bytes
+// bound it (8 tokens with windows of 4096, 8 heads by 128: 32 us, 4.3 TB/s).
 // Warps 0-3: softmax, a row per thread.  Warp 4: TMA producer.  Warp 5: tensor memory and MMA issue.
 template <int D, int SEGS>
 __global__ void __launch_bounds__(192, 2)
@@ -316,7 +322,7 @@ attend_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
         // counted, falls below 2^-20, is read again and its maximum becomes the reference.
         float m = 0.f, l = 0.f;
         bool set = false;   // some tile of this row counted
-        float high = -INFINITY;   // (D < 128) a maximum above it is the new reference
+        float high = live ? -INFINITY : INFINITY;   // (D < 128) a maximum above it is the new reference
         bool ok = true;     // (a wait that ran out shows at the vote of its tile: until then the lanes stay together)
         const int seen_end = causal ? t0 + 1 : seg.key1;   // keys that every row of the block sees: [seen_low, seen_end), the sinks
         const int seen_low = p.window ? max(t1 - p.window + 1, seg.key0) : seg.key0;
@@ -335,8 +341,9 @@ attend_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
             };
             uint32_t s[4][32];
             float total;
-            // (a pair of weights takes the place of a pair of scores)
-            auto weights = [&](bool store) {
+            // the tile's weights, their sum, and (store) the weights to tensor memory from halfway on, where `middle` has
+            // waited for the place (a pair of weights takes the place of a pair of scores in registers)
+            auto weights = [&](bool store, auto&& middle) {
                 const float b = m * c;
                 float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
@@ -351,7 +358,9 @@ attend_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
                         sum[i & 1] = add2(sum[i & 1], x);
                         s[q][i] = w;
                     }
-                    if (store) tmem_st16_head(tmem + T::kP + lanes + q * 16, s[q]);
+                    if (q == 1) middle();
+                    if (store && q >= 1) tmem_st16_head(tmem + T::kP + lanes + q * 16, s[q]);
+                    if (store && q == 1) tmem_st16_head(tmem + T::kP + lanes, s[0]);
                 }
                 total = (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
             };
@@ -391,17 +400,22 @@ attend_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
                     for (int i = 2; i < 32; i += 2) mx[q] = max3(mx[q], __uint_as_float(s[q][i]), __uint_as_float(s[q][i + 1]));
                 }
                 const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-                // the products that read the last weights and wrote O are done before either is touched
-                if (j > 0) ok = sm::bar_wait_sync(pv_done, uint32_t(j - 1) & 1u, abort_word, p.status) && ok;
-                sm::tc_fence_after();
                 const bool rise = top > high;
                 if (__any_sync(0xFFFFFFFFu, rise || !ok)) {
+                    // the products that wrote O are done before it is touched
+                    if (j > 0) ok = sm::bar_wait_sync(pv_done, uint32_t(j - 1) & 1u, abort_word, p.status) && ok;
+                    sm::tc_fence_after();
                     if (!(ok = __all_sync(0xFFFFFFFFu, ok))) break;
                     const float f = rise && set ? exp2_approx((m - top) * c) : 1.f;
                     if (rise) { m = top; high = m + 8.f / c; }
                     if (j > 0) rescale(f);
                 }
-                weights(true);
+                // (halfway through them the products that read the last weights are mostly done: waiting for them before
+                // the maximum or behind all weights took 3% and 5% more)
+                weights(true, [&] {
+                    if (j > 0) ok = sm::bar_wait_warp(pv_done, uint32_t(j - 1) & 1u, abort_word, p.status);
+                    sm::tc_fence_after();
+                });
             } else
             for (int pass = 0;; ++pass) {
 #pragma unroll
@@ -416,8 +430,8 @@ attend_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
                         for (int i = 0; i < 32; ++i)
                             if (!(see >> i & 1u)) s[q][i] = 0xFF800000u;
                     }
-                weights(false);
-                const bool off = !(total <= 1048576.f) || (!set && total < 9.5367431640625e-7f);
+                weights(false, [] {});
+                const bool off = live && (!(total <= 1048576.f) || (!set && total < 9.5367431640625e-7f));
                 if (pass == 1 || !__any_sync(0xFFFFFFFFu, off || !ok)) break;
                 if (!(ok = __all_sync(0xFFFFFFFFu, ok))) break;
                 float top = -INFINITY;
@@ -642,7 +656,8 @@ static mk_status attend_check(const mk_attend_args* a) {
             return fail(MK_ERR_ARG, "attend: blocks of a multiple of 8 positions, a table that covers max_seq");
         if (kv.head_stride < int64_t(pg.n_blocks) * pg.block_size * d)
             return fail(MK_ERR_ARG, "attend: KV strides must cover the pool per head");
-    } else if (kv.head_stride < a->max_seq * d || (a->batch > 1 && kv.batch_stride < kv.head_stride * a->n_kv_heads)) {
+    } else if (kv.head_stride < a->max_seq * d || (a->batch > 1 && kv.batch_stride < kv.head_stride * a->n_kv_heads) ||
+               (a->layer > 0 && kv.layer_stride < kv.head_stride * a->n_kv_heads)) {
         return fail(MK_ERR_ARG, "attend: KV strides must cover [max_seq, head_dim] per head");
     }
     if (tokens == 0) return MK_OK;
@@ -650,8 +665,11 @@ static mk_status attend_check(const mk_attend_args* a) {
         return fail(MK_ERR_ARG, "attend: q and out must be 16-byte aligned");
     if (tokens > 1 && (a->q_stride < ql || a->out_stride < ql || a->q_stride % 8 || a->out_stride % 8))
         return fail(MK_ERR_ARG, "attend: q and out strides must be multiples of 8 and cover the heads");
-    if (spans_overlap({a->out, tokens, ql * 2, a->out_stride * 2}, {a->q, tokens, ql * 2, a->q_stride * 2}))
-        return fail(MK_ERR_ARG, "attend: out overlaps q");
+    const RowSpan out{a->out, tokens, ql * 2, a->out_stride * 2};
+    if (spans_overlap(out, {a->q, tokens, ql * 2, a->q_stride * 2})) return fail(MK_ERR_ARG, "attend: out overlaps q");
+    const int64_t cached = a->layer * kv.layer_stride + (a->pages ? 0 : (a->batch - 1) * kv.batch_stride) + a->n_kv_heads * kv.head_stride;
+    if (spans_overlap(out, {kv.k, 1, cached * 2, 0}) || spans_overlap(out, {kv.v, 1, cached * 2, 0}))
+        return fail(MK_ERR_ARG, "attend: out overlaps the cache");
     return MK_OK;
 }
 

@@ -173,17 +173,28 @@ def test_strides_layers_and_scale():
     assert torch.equal(got, check(q.contiguous(), kv, [10, 50], [400, 123], layer=2, scale=0.3))
 
 
-def test_sharp_and_flat_softmax():
-    # scores far apart (one weight near 1, the maximum rising along the row) and all alike
-    d = 64
+@pytest.mark.parametrize("d", [32, 64, 128])
+@pytest.mark.parametrize("q_len", [1, 64])
+def test_sharp_and_flat_softmax(d, q_len):
+    # scores far apart (one weight near 1), all alike, far above and below zero, and a maximum that rises along
+    # the row by much more than the formats hold, within a tile and from tile to tile
     kv = cache(1, 1, d, 600)
-    q = randn((64, 4, d), 5, 12.0)
-    check(q, kv, [64], [600])
-    ramp = torch.arange(600, device="cuda") / 20.0
-    kv.k[0, 0, 0] = (ramp[:, None] * torch.ones(d, device="cuda")).to(BF)
-    check(torch.ones((64, 4, d), device="cuda", dtype=BF), kv, [64], [600])
-    check(-torch.ones((64, 4, d), device="cuda", dtype=BF), kv, [64], [600])
-    check(torch.zeros((64, 4, d), device="cuda", dtype=BF), kv, [64], [600])
+    check(randn((q_len, 4, d), 5, 12.0), kv, [q_len], [600])
+    one = torch.ones((q_len, 4, d), device="cuda", dtype=BF)
+    for ramp in (torch.arange(600, device="cuda") / 20.0, torch.arange(600, device="cuda") // 128 * 8.0,
+                 torch.arange(600, device="cuda") // 128 * -8.0, torch.full((600,), 30.0, device="cuda")):
+        kv.k[0, 0, 0] = (ramp[:, None] * torch.ones(d, device="cuda")).to(BF)
+        for q in (one, -one, 0 * one):
+            check(q, kv, [q_len], [600])
+            check(q, kv, [q_len], [600], window=300, sinks=2)
+
+
+def test_one_weight_that_outweighs_the_rest_is_exact():
+    # rows that see one key, or one that matters, return its value as it is
+    for d in (32, 64, 128):
+        kv = cache(1, 1, d, 300)
+        got = mk.attend(randn((7, 4, d), 5), kv, [7], [300], window=1)
+        assert torch.equal(got, kv.v[0, 0, 0, 293:300, None].expand(7, 4, d))
 
 
 def test_far_positions():

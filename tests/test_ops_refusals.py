@@ -56,6 +56,8 @@ def attend_args(q_lens=(1, 2), kv_lens=(5, 9), kv=None, pages=None, **over):
     dict(shared_prefix=3, window=8), dict(scale=float("nan")), dict(scale=float("inf")), dict(q=None), dict(out=None),
     dict(q=A + 8), dict(out=2 * A + 4), dict(q_stride=120), dict(q_stride=132), dict(out_stride=64), dict(status=A + 1),
     dict(out=A), dict(out=A + 64),                                                           # out overlaps q
+    dict(out=5 * A + 64), dict(out=6 * A), dict(layer=1, out=5 * A + 2 * 4096),                # and the cache
+    dict(layer=1, kv=mk.mk_kv(5 * A, 6 * A, 4096, 2048, 2048)),                              # layers overlap
     dict(kv=mk.mk_kv(None, A, 4096, 4096, 2048)), dict(kv=mk.mk_kv(5 * A + 8, 6 * A, 4096, 4096, 2048)),
     dict(kv=mk.mk_kv(5 * A, 6 * A, 4096, 4096, 2040)),                                       # heads do not cover max_seq
     dict(kv=mk.mk_kv(5 * A, 6 * A, 4088, 4096, 2048)),                                       # sequences overlap
