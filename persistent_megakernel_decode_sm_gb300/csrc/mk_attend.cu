@@ -180,7 +180,11 @@ attend_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
     const bool causal = seg.pos0 != kNoCausal;
     const int t0 = causal ? seg.pos0 + tok0 : 0, t1 = t0 + toks - 1;
     const KeyRange range(seg, t0, t1, p.window, p.sinks);
-    const int first = int(int64_t(range.count) * share / seg.splits), n = int(int64_t(range.count) * (share + 1) / seg.splits) - first;
+    int first = 0, n = range.count;
+    if (seg.splits > 1) {   // (at most 2^23 tiles by 256 shares: 32 bits hold the products)
+        first = int(uint32_t(range.count) * uint32_t(share) / uint32_t(seg.splits));
+        n = int(uint32_t(range.count) * uint32_t(share + 1) / uint32_t(seg.splits)) - first;
+    }
     const int warps = (rows + 31) / 32;   // softmax warps with a row
 
     if (threadIdx.x == 0) {
@@ -263,11 +267,12 @@ attend_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
             const uint64_t q_desc = D == 32 ? sm::desc_k_sw64(q_at) : sm::desc_k_sw128(q_at);
             const uint64_t k_desc = D == 32 ? sm::desc_k_sw64(k_at) : sm::desc_k_sw128(k_at);
             const uint64_t v_desc = D == 32 ? sm::desc_mn_sw64(v_at) : sm::desc_mn_sw128(v_at, kKeys * T::kRowBytes);
+            auto k_there = [&](int j) { return sm::bar_wait_warp(k_full(j % T::kKStages), uint32_t(j / T::kKStages) & 1u, abort_word, p.status); };
+            auto v_there = [&](int j) { return sm::bar_wait_warp(v_full(j % T::kVStages), uint32_t(j / T::kVStages) & 1u, abort_word, p.status); };
             auto scores = [&](int j) {
                 const int s = j % T::kKStages;
-                if (!sm::bar_wait_warp(k_full(s), uint32_t(j / T::kKStages) & 1u, abort_word, p.status)) return false;
-                sm::tc_fence_after();
                 const uint64_t k = k_desc + uint64_t(s * (T::kTileBytes >> 4));
+                sm::tc_fence_after();
                 if (leader) {
 #pragma unroll
                     for (int i = 0; i < D / 16; ++i) {   // 16 elements of the head dimension
@@ -278,19 +283,21 @@ attend_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
                     sm::mma_commit(k_empty(s));
                 }
                 __syncwarp();
-                return true;
             };
-            bool ok = sm::bar_wait_warp(q_full, 0, abort_word, p.status) && scores(0);
+            // (the copies are waited for ahead of the barriers that the softmax is behind: a wait that is over still costs
+            // 100 cycles, and there it would be in the tile's chain)
+            bool ok = sm::bar_wait_warp(q_full, 0, abort_word, p.status) && k_there(0);
+            if (ok) scores(0);
             for (int j = 0; j < n && ok; ++j) {
-                // a tile's weights are written: its scores are done with, the next may come (where the weights
-                // lie over them, once they are read); its product with V is what the next tile's need waits for last
-                if (!T::kShareSP && j + 1 < n)   // the next scores as soon as these are in registers
-                    if (!(ok = sm::bar_wait_warp(s_free, uint32_t(j) & 1u, abort_word, p.status) && scores(j + 1))) break;
-                if (!(ok = sm::bar_wait_warp(p_ready, uint32_t(j) & 1u, abort_word, p.status))) break;
+                if (!T::kShareSP && j + 1 < n) {   // the next scores as soon as these are in registers
+                    if (!(ok = k_there(j + 1) && sm::bar_wait_warp(s_free, uint32_t(j) & 1u, abort_word, p.status))) break;
+                    scores(j + 1);
+                }
+                if (!(ok = v_there(j) && (!T::kShareSP || j + 1 >= n || k_there(j + 1)) &&
+                           sm::bar_wait_warp(p_ready, uint32_t(j) & 1u, abort_word, p.status)))
+                    break;
                 sm::tc_fence_after();
                 const int s = j % T::kVStages;
-                if (!(ok = sm::bar_wait_warp(v_full(s), uint32_t(j / T::kVStages) & 1u, abort_word, p.status))) break;
-                sm::tc_fence_after();
                 const uint64_t v = v_desc + uint64_t(s * (T::kTileBytes >> 4));
                 if (leader) {
 #pragma unroll
@@ -300,8 +307,10 @@ attend_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
                     sm::mma_commit(v_empty(s));
                 }
                 __syncwarp();
-                if (T::kShareSP && j + 1 < n)
-                    ok = sm::bar_wait_warp(pv_done, uint32_t(j) & 1u, abort_word, p.status) && scores(j + 1);
+                if (T::kShareSP && j + 1 < n) {   // the weights share the scores' columns: read first
+                    if (!(ok = sm::bar_wait_warp(pv_done, uint32_t(j) & 1u, abort_word, p.status))) break;
+                    scores(j + 1);
+                }
             }
             if (*abort_word && leader) { sm::mma_commit(drained); sm::bar_drain(drained, 0); }
         }
