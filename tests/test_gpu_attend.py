@@ -251,6 +251,51 @@ def test_captured_and_replayed():
         assert torch.equal(o, mk.attend(q, kv, [1, 4], lens, pages=pages))
 
 
+def test_captured_without_a_workspace_of_its_own():
+    # the workspace of each captured call is the graph's: eager calls in between take other memory
+    kv = cache(2, 2, 64, 3000)
+    q = randn((2, 8, 64), 5)
+    want = [mk.attend(q, kv, [1, 1], lens) for lens in ([3000, 2500], [1200, 3000])]
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        got = [mk.attend(q, kv, [1, 1], lens) for lens in ([3000, 2500], [1200, 3000])]
+    for _ in range(3):
+        other = mk.attend(randn((2, 8, 64), 6), kv, [1, 1], [3000, 3000])
+        g.replay()
+        other = mk.attend(randn((2, 8, 64), 7), kv, [1, 1], [2000, 3000])
+    torch.cuda.synchronize()
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]) and torch.isfinite(other).all()
+
+
+def test_workspace_is_checked():
+    kv, q = cache(1, 1, 64, 4000), randn((1, 4, 64), 5)
+    for ws, status in ((torch.empty(256, dtype=torch.uint8, device="cuda"), mk.MK_ERR_CAPACITY),
+                       (torch.empty(1 << 22, dtype=torch.uint8, device="cuda")[16:], mk.MK_ERR_ARG)):
+        with pytest.raises(mk.MkError) as e:
+            mk.attend(q, kv, [1], [4000], workspace=ws)
+        assert e.value.status == status
+    with pytest.raises(ValueError):
+        mk.attend(q, kv, [1], [4000], workspace=torch.empty(1 << 22, dtype=torch.uint8))
+
+
+def test_a_single_kv_head_taken_out_of_a_cache():
+    kv = cache(2, 4, 64, 200)
+    one = KVCache(kv.k[:, :, 1:2], kv.v[:, :, 1:2])
+    odd = KVCache(*(x.as_strided(x.shape, (x.stride(0), x.stride(1), 0, 64, 1), x.storage_offset()) for x in (one.k, one.v)))
+    q = randn((9, 4, 64), 5)
+    a = check(q, one, [4, 5], [200, 90])
+    assert torch.equal(mk.attend(q, odd, [4, 5], [200, 90]), a)
+
+
+def test_many_short_sequences_and_many_tokens():
+    q_lens = [1 + b % 3 for b in range(256)]
+    kv_lens = [n + 7 * b % 90 for b, n in enumerate(q_lens)]
+    check(randn((sum(q_lens), 4, 32), 5), cache(256, 2, 32, 100), q_lens, kv_lens)
+    check(randn((sum(q_lens), 4, 32), 5), cache(256, 2, 32, 200), q_lens, [90 + k for k in kv_lens], shared_prefix=90)
+    check(randn((20000, 1, 32), 5), cache(1, 1, 32, 20000), [20000], [20000], window=40, sinks=1)
+
+
 def test_refuses_tensors_it_cannot_take():
     kv, (pk, pages) = cache(2, 2, 64, 100), pool(2, 2, 64, 100, 16)
     q = randn((3, 8, 64), 5)

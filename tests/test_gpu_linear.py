@@ -99,6 +99,41 @@ def test_residual_in_place(rows, dtype):
     assert torch.equal(mk.linear(x, w, residual=r, out=r), want)
 
 
+def test_outputs_past_2_to_the_31():
+    # 2.2e9 outputs: offsets need 64 bits; a few rows and columns of every corner are checked
+    rows, n, k = 40000, 55000, 16
+    x, w = randn((rows, k), 1), randn((n, k), 2, k ** -0.5)
+    got = mk.linear(x, w)
+    for r in (slice(0, 3), slice(39040, 39060), slice(rows - 3, rows)):
+        want, bound = reference(x[r], w, None, None, None, BF)
+        assert ((got[r].double() - want).abs() <= bound).all()
+
+
+def test_captured_before_any_other_call():
+    # a process whose first calls are captured: kernels are loaded and set up during the capture
+    import os
+    import subprocess
+    import sys
+    code = """
+import torch, persistent_megakernel_decode_sm_gb300 as mk
+from workload import KVCache
+x, w = torch.randn(300, 64, device="cuda").bfloat16(), torch.randn(96, 64, device="cuda").bfloat16()
+kv = KVCache(*(torch.randn(1, 1, 1, 900, 64, device="cuda").bfloat16() for _ in range(2)))
+q = torch.randn(1, 4, 64, device="cuda").bfloat16()
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    y, o = mk.linear(x, w), mk.attend(q, kv, [1], [900])
+g.replay()
+torch.cuda.synchronize()
+assert torch.equal(y, mk.linear(x, w)) and torch.equal(o, mk.attend(q, kv, [1], [900]))
+print("fine")
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "fine" in r.stdout, r.stderr[-2000:]
+
+
 def test_no_rows():
     assert mk.linear(randn((0, 64), 1), randn((10, 64), 2)).shape == (0, 10)
 
