@@ -391,7 +391,7 @@ typedef enum {
 
 /* out[r][j] = act(sum_i x[r][i] w[j][i] + bias[j]) + residual[r][j]
  *  rows, n, k     tokens, output features, input features; rows may be 0 (nothing is done); k a
- *                 multiple of 8; n any
+ *                 multiple of 8; rows and n at most 2^30
  *  x              bf16, row r at x + r * x_stride elements (x_stride a multiple of 8, >= k)
  *  w              bf16 row-major [n, k] ([2 n, k] for MK_ACT_SWIGLU)
  *  bias           bf16 [n] ([2 n] for MK_ACT_SWIGLU), or NULL
@@ -477,7 +477,8 @@ mk_status mk_attend(const mk_attend_args* a, void* workspace, size_t workspace_b
  * token; nothing of the last layer but its K and V is computed here.  A long prompt may be given in pieces.
  *  tokens         HOST int32[sum n_tokens], in [0, vocab): the sequences' tokens back to back
  *  n_tokens, pos  HOST int32[batch]: tokens of each sequence (0: none), and the position of its first;
- *                 its cache holds the positions before; pos + n_tokens <= max_seq
+ *                 its cache holds the positions before; pos + n_tokens <= max_seq (the schedule's KV windows
+ *                 bound decode steps only)
  *  shared_prefix  as in mk_attend: that many first positions are the same for every sequence, in the
  *                 cache already (sequence 0's rows, or blocks every table names), pos[b] >= shared_prefix
  *                 wherever n_tokens[b] > 0.  0: none

@@ -451,7 +451,8 @@ class Decoder:
 
 # ---- prompt operators ------------------------------------------------------------------------
 # A call's host time counts beside kernels of a few microseconds, so the argument structs are packed
-# in one go (native alignment, the layouts of mk_linear_args and mk_attend_args).
+# in one go (native alignment, the layouts of mk_linear_args and mk_attend_args).  They record no
+# gradients, whatever their operands' requires_grad: the framework runs models, it does not train them.
 
 _LINEAR_ARGS = struct.Struct("@4iPqPPPq2iPqP")
 _ATTEND_ARGS = struct.Struct("@4iPPPqPqPP5ifP")
@@ -465,7 +466,7 @@ def _operand(t, name, dtypes, device, dim):
     shape, strides = t.shape, t.stride()
     if t.dtype not in dtypes:
         raise ValueError(f"{name} must be one of {dtypes}, not {t.dtype}")
-    if not t.is_cuda or t.get_device() != device:
+    if t.get_device() != device or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor on the first operand's device, not on {t.device}")
     if len(shape) != dim:
         raise ValueError(f"{name} must have {dim} dimensions, not {len(shape)}")
@@ -521,10 +522,9 @@ def linear(x, weight, bias=None, activation: Optional[str] = None, residual=None
             raise ValueError("swiglu takes an even number of weight rows: gate rows, then up rows")
         n //= 2
     if out is None:
-        out = torch.empty((rows, n), dtype=out_dtype or bf, device=x.device)
-        if out.dtype is not bf and out.dtype is not f32:
+        if out_dtype is not None and out_dtype is not bf and out_dtype is not f32:
             raise ValueError(f"out_dtype must be torch.bfloat16 or torch.float32, not {out_dtype}")
-        os = n
+        out, os = torch.empty((rows, n), dtype=out_dtype or bf, device=x.device), n
     else:
         if out_dtype is not None and out.dtype != out_dtype:
             raise ValueError(f"out is {out.dtype}, out_dtype {out_dtype}")
@@ -579,9 +579,9 @@ def attend(q, kv, q_lens: Sequence[int], kv_lens: Sequence[int], layer: int = 0,
     k, v = kv.k, kv.v
     dims = 5 if pages is None else 4
     shape, ks = _operand(k, "kv.k", (bf,), dev, dims)
-    vshape, vs = _operand(v, "kv.v", (bf,), dev, dims)
-    if shape != vshape or ks != vs or shape[-1] != d or (ks[-2] != d and shape[-2] > 1):
-        raise ValueError("kv.k and kv.v must be alike, with contiguous [positions, head_dim] rows of q's head_dim")
+    if (v.shape != shape or v.stride() != ks or v.dtype is not bf or v.get_device() != dev or shape[-1] != d or
+            (ks[-2] != d and shape[-2] > 1)):
+        raise ValueError("kv.k and kv.v must be alike (shape, strides, type, device), with contiguous [positions, head_dim] rows of q's head_dim")
     layers, nkv, positions = shape[-4:-1]
     head_stride = ks[-3] if nkv > 1 else max(ks[-3], positions * d)   # (a single head's stride says nothing)
     if not 0 <= layer < layers:
@@ -600,8 +600,7 @@ def attend(q, kv, q_lens: Sequence[int], kv_lens: Sequence[int], layer: int = 0,
         cache = array.array("q", (k.data_ptr(), v.data_ptr(), 0, ks[0], head_stride,
                                   table.data_ptr(), block_size | tshape[1] << 32, n_blocks))
         positions = tshape[1] * block_size
-    lens = array.array("i", q_lens)
-    lens.extend(array.array("i", kv_lens))
+    lens = array.array("i", [*q_lens, *kv_lens])
     at, c_kv = lens.buffer_info()[0], cache.buffer_info()[0]
     a = _ATTEND_ARGS.pack(nq, nkv, d, batch, at, at + 4 * batch, q.data_ptr(), qs[0], out.data_ptr(), os[0],
                           c_kv, c_kv + 40 if pages is not None else 0, layer, min(positions, 1 << 30),
@@ -610,15 +609,26 @@ def attend(q, kv, q_lens: Sequence[int], kv_lens: Sequence[int], layer: int = 0,
         if not workspace.is_cuda or workspace.get_device() != dev or not workspace.is_contiguous():
             raise ValueError("workspace must be contiguous, on q's device")
         _launch(dev, lib.mk_attend, a, workspace.data_ptr(), workspace.numel() * workspace.element_size())
-        return out
-    need = lib.mk_attend_workspace(a)
-    if not need:
-        _launch(dev, lib.mk_attend, a, 0, 0)
-        return out
-    # from torch's allocator, for this stream: given back at once, it is reused behind the call in stream order
-    ws = torch._C._cuda_cudaCachingAllocator_raw_alloc(need, torch._C._cuda_getCurrentRawStream(dev))
-    try:
-        _launch(dev, lib.mk_attend, a, ws, need)
-    finally:
-        torch._C._cuda_cudaCachingAllocator_raw_delete(ws)
+    elif torch._C._cuda_getDevice() == dev:
+        _attend_allocating(dev, a)
+    else:
+        with torch.cuda.device(dev):   # (the workspace's size depends on the device)
+            _attend_allocating(dev, a)
     return out
+
+
+def _attend_allocating(device: int, a: bytes):
+    """mk_attend on the current device, with a workspace from torch's allocator: taken for torch's
+    current stream and given back at once, it is reused behind the call in stream order."""
+    import torch
+    stream, need = torch._C._cuda_getCurrentRawStream(device), lib.mk_attend_workspace(a)
+    if not need:
+        st = lib.mk_attend(a, 0, 0, stream)
+    else:
+        ws = torch._C._cuda_cudaCachingAllocator_raw_alloc(need, stream)
+        try:
+            st = lib.mk_attend(a, ws, need, stream)
+        finally:
+            torch._C._cuda_cudaCachingAllocator_raw_delete(ws)
+    if st:
+        _check(st)

@@ -719,7 +719,7 @@ static mk_status attend_plan(const mk_attend_args* a, int sms, AttendPlan& pl) {
         }
         pl.seg[at] = s;
         tiles[at] = k;
-        middle[at] = seen(n / 2 * bt < s.n ? n / 2 * bt : 0);
+        middle[at] = std::max(seen(n / 2 * bt < s.n ? n / 2 * bt : 0), (k + 1) / 2);   // (0 with more tokens than positions)
         blocks[at] = uint32_t(n) * uint32_t(a->n_kv_heads);   // (2^24 tokens by 4096 heads at most, 4096 / 8 of them: fits)
     };
     if (a->shared_prefix && pl.tokens) {
@@ -773,7 +773,7 @@ static mk_status attend_plan(const mk_attend_args* a, int sms, AttendPlan& pl) {
         s.splits = int32_t(splits(tiles[i], share));
         s.item0 = int32_t(pl.items);
         s.merge0 = int32_t(pl.merge_tokens);
-        pl.items += blocks[i] * s.splits;
+        pl.items += int64_t(blocks[i]) * s.splits;
         if (s.splits > 1 || pl.prefix_seg) {
             s.part0 = int32_t(part);
             part += int64_t(s.splits) * s.n;

@@ -689,15 +689,14 @@ static mk_status linear_dispatch(const mk_linear_args* a, LinearParams& p, int d
 
 static mk_status linear_check(const mk_linear_args* a) {
     if (!a) return fail(MK_ERR_ARG, "null argument");
-    if (a->rows < 0 || a->n < 1 || a->k < 8 || a->k % 8)
-        return fail(MK_ERR_ARG, "linear: rows %d, n %d, k %d (rows >= 0, n >= 1, k a multiple of 8)", a->rows, a->n, a->k);
+    if (a->rows < 0 || a->rows > (1 << 30) || a->n < 1 || a->n > (1 << 30) || a->k < 8 || a->k % 8)
+        return fail(MK_ERR_ARG, "linear: rows %d, n %d, k %d (rows in [0, 2^30], n in [1, 2^30], k a multiple of 8)", a->rows, a->n, a->k);
     if (a->activation < MK_ACT_NONE || a->activation > MK_ACT_SWIGLU)
         return fail(MK_ERR_ARG, "linear: unknown activation %d", a->activation);
     if ((a->out_dtype != MK_BF16 && a->out_dtype != MK_F32) ||
         (a->residual && a->residual_dtype != MK_BF16 && a->residual_dtype != MK_F32))
         return fail(MK_ERR_ARG, "linear: unknown data type");
     const bool gated = a->activation == MK_ACT_SWIGLU;
-    if (gated && a->n > (1 << 30)) return fail(MK_ERR_ARG, "linear: n %d too large", a->n);
     if (a->rows == 0) return MK_OK;
     const int64_t os = a->out_dtype == MK_F32 ? 4 : 2, rs = a->residual_dtype == MK_F32 ? 4 : 2;
     if (!a->x || !a->w || !a->out) return fail(MK_ERR_ARG, "linear: null pointer");

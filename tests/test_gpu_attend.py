@@ -279,6 +279,16 @@ def test_workspace_is_checked():
         mk.attend(q, kv, [1], [4000], workspace=torch.empty(1 << 22, dtype=torch.uint8))
 
 
+def test_more_queries_than_positions_need_little_workspace():
+    # most of the tokens see nothing: the shares must not multiply their parts (one part here is 41 MB a 20000 tokens)
+    kv, q = cache(1, 1, 128, 5000), randn((20000, 4, 128), 5)
+    parts = 20000 * 4 * (128 * 4 + 8)
+    ws = torch.empty(4 * parts, dtype=torch.uint8, device="cuda")
+    got = mk.attend(q, kv, [20000], [5000], workspace=ws)
+    assert (got[:15000] == 0).all()
+    check(q, kv, [20000], [5000])
+
+
 def test_a_single_kv_head_taken_out_of_a_cache():
     kv = cache(2, 4, 64, 200)
     one = KVCache(kv.k[:, :, 1:2], kv.v[:, :, 1:2])

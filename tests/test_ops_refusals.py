@@ -17,7 +17,7 @@ def linear_args(**over):
 
 
 @pytest.mark.parametrize("over", [
-    dict(rows=-1), dict(n=0), dict(k=0), dict(k=60), dict(activation=4), dict(activation=-1), dict(out_dtype=2),
+    dict(rows=-1), dict(rows=(1 << 30) + 1), dict(n=(1 << 30) + 1, out_stride=1 << 31), dict(n=0), dict(k=0), dict(k=60), dict(activation=4), dict(activation=-1), dict(out_dtype=2),
     dict(residual=4 * A, residual_stride=24, residual_dtype=5), dict(x=None), dict(w=None), dict(out=None),
     dict(x=A + 2), dict(w=2 * A + 8), dict(out=3 * A + 1), dict(out_dtype=mk.F32, out=3 * A + 2), dict(bias=A + 1),
     dict(residual=4 * A + 2, residual_stride=24, residual_dtype=mk.F32), dict(status=A + 2),
