@@ -25,8 +25,8 @@ struct AttendSeg {
     int32_t merge0;        // tokens with parts to join in the segments before (a sequence's, not the prefix's)
 };
 constexpr int32_t kNoCausal = INT_MIN;
-constexpr int kKeys = 128;     // key tile
 constexpr int kBlockRows = 128;
+constexpr int attend_keys(int d) { return d == 128 ? 64 : 128; }   // keys of a tile
 
 struct AttendCommon {
     int32_t nq, nkv, group, block_tokens;   // block_tokens: query tokens of a block, 128 / group
@@ -36,6 +36,11 @@ struct AttendCommon {
     float scale_log2;                       // scale / ln 2
     const int32_t* table;                   // paged: [batch][max_blocks]
     int32_t block, max_blocks, n_blocks, box_log2;   // positions one copy takes: a power of two that divides block
+    // pos / block as pos * block_inv >> block_shift, exact for pos < 2^30: with 2^(L-1) < block <= 2^L and
+    // block_inv = ceil(2^(30 + L) / block), block_inv * block - 2^(30 + L) < block <= 2^L, so the quotient is off by
+    // less than pos 2^L / (2^(30 + L) block) < 1 / block
+    uint32_t block_inv;
+    int32_t block_shift;
     __nv_bfloat16* out;
     int64_t out_stride;
     float* part_o;                          // [row][d], then per row (m, l)
@@ -49,6 +54,7 @@ struct AttendParams : AttendCommon {
 
 // The key tiles a block of queries at positions [t0, t1] of a segment sees, in two ranges of positions:
 // [0, sink_end) and [low, end)
+template <int kKeys>
 struct KeyRange {
     int sink_end, low, end;
     int sink_tiles, first, count;   // tiles of the sinks, first tile of the window, tiles in all
@@ -75,17 +81,22 @@ struct AttendTile {
     static constexpr int kSub = D < 64 ? D : 64;                // elements of a swizzled row
     static constexpr int kSubs = D / kSub;
     static constexpr int kRowBytes = kSub * 2;
-    static constexpr int kTileBytes = kKeys * D * 2;            // 128 rows of q, K or V
-    static constexpr int kKStages = D == 128 ? 1 : 3, kVStages = D == 128 ? 1 : 2;
-    static constexpr int kSmem = kTileBytes * (1 + kKStages + kVStages) + 1024;
-    // tensor memory: scores, output, softmax weights (two bf16 a column; at D = 128 over the scores' columns)
-    static constexpr int kS = 0, kO = 128, kP = D == 128 ? 0 : 192;
+    static constexpr int kKeys = attend_keys(D);
+    static constexpr int kQBytes = kBlockRows * D * 2, kTileBytes = kKeys * D * 2;   // the queries; a tile of K or V
+    static constexpr int kKStages = 3, kVStages = 2;
+    static constexpr int kBars = 1 + 2 * kKStages + 2 * kVStages + 8, kFlags = 8;   // kFlags: ring of the copies' skip masks
+    static constexpr int kTiles = kQBytes + kTileBytes * (kKStages + kVStages);
+    static constexpr int kSmem = kTiles + kBars * 8 + kFlags * 4 + 8;   // (two CTAs to an SM: 114 KB each at most)
+    static_assert(kSmem + 1024 <= 228 * 512);
+    // tensor memory: scores, output, softmax weights (two bf16 a column).  At D = 128, where the output takes half of the
+    // CTA's columns, there are two places for a tile's scores in turn, and its weights go over them.
     static constexpr bool kShareSP = D == 128;
+    static constexpr int kPlaces = kShareSP ? 2 : 1;
+    static constexpr int kS = 0, kO = 128, kP = kShareSP ? 0 : 192;
     // rows are divided by the sum of their weights as rounded, which cancels the rounding of a weight that
     // outweighs the others -- but at D = 64, where that took 9% (97 us against 89; 4096 tokens, causal, 1B heads) and the
     // reference is a maximum, so that such a weight is a power of two or near it
     static constexpr bool kRoundedSum = D != 64;
-    static constexpr int kFlags = 8;                            // ring of the copies' skip masks
 };
 
 __device__ __forceinline__ float exp2_approx(float x) {
@@ -131,26 +142,35 @@ __device__ __forceinline__ uint32_t low_bits(int n) { return n >= 32 ? 0xFFFFFFF
 // scores into weights exp2(scale_log2 (s - m)) with a reference m (below), writes them back as bf16, and
 // O += P V runs with P read from tensor memory.  Two CTAs share an SM, so one's products run while the
 // other's threads are at their exponentials.
-// What bounds it with many rows is the chain of one warp's ~650 instructions per tile, two such warps to a scheduler
-// (4096 causal tokens of 32 / 8 heads by 64: 84 us, 820 TFLOP/s, tensor pipe 37% and special functions 37% busy; 128 wide:
-// 930 TFLOP/s, tensor pipe 48%).  Measured against: two threads per row at 80 or 96 registers 107 us; tiles of 64 keys
-// with three or four CTAs 107 and 161; registers moved between warps (setmaxnreg) 98; the exponentials taken out
-// left the time as it was, the products taken out 10% of it (24% at width 128).  With few rows the cache's bytes
-// bound it (8 tokens with windows of 4096, 8 heads by 128: 32 us, 4.3 TB/s).
+// What bounds it with many rows at widths up to 64 is the chain of one warp's instructions per tile, two such warps to a
+// scheduler (4096 causal tokens of 32 / 8 heads by 64: 80 us, 855 TFLOP/s; tensor pipe 35% and special functions 38%
+// busy).  Measured against: two threads per row at 80 or 96 registers 107 us; tiles of 64 keys with three or four CTAs 107
+// and 161; registers moved between warps (setmaxnreg) 98; the exponentials taken out left the time as it was.
+// At width 128 a tile has 64 keys, so that two tiles' scores have a place and the products of one run beside the weights
+// of the other: 1170 TFLOP/s for 4096 causal tokens (1097 with 128 keys and one place), 1410 for 16384, although a product
+// of 128 x 64 scores takes 48 cycles where half of a 128 x 128 one takes 32 (its operands' way out of shared memory).
+// Reading a row's scores while the tensor cores write others takes 400 cycles, alone 92.
+// With few rows the cache's bytes bound it (8 tokens with windows of 4096, 8 heads by 128: 28 us, 4.8 TB/s; 32.6 with
+// tiles of 128 keys and one place each for K and V).
 // Warps 0-3: softmax, a row per thread.  Warp 4: TMA producer.  Warp 5: tensor memory and MMA issue.
 template <int D, int SEGS>
 __global__ void __launch_bounds__(192, 2)
 attend_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
               const __grid_constant__ CUtensorMap map_v, const __grid_constant__ AttendParams<SEGS> p) {
     using T = AttendTile<D>;
-    extern __shared__ uint8_t raw[];
-    __shared__ uint64_t bars[1 + 2 * T::kKStages + 2 * T::kVStages + 5];
-    __shared__ uint32_t tmem_at, skips[T::kFlags];
-    __shared__ int abort_flag;
-    volatile int* abort_word = &abort_flag;
+    constexpr int kKeys = T::kKeys;
+    extern __shared__ __align__(1024) uint8_t raw[];   // tiles, barriers, skip masks, tensor memory's place, abort word
+    uint64_t* bars = reinterpret_cast<uint64_t*>(raw + T::kTiles);
+    uint32_t* skips = reinterpret_cast<uint32_t*>(bars + T::kBars);
+    uint32_t& tmem_at = skips[T::kFlags];
+    volatile int* abort_word = reinterpret_cast<volatile int*>(skips + T::kFlags + 1);
+    if (sm::smem(raw) & 1023u) {   // (the swizzled tiles need it; there is no static shared memory to displace them)
+        if (threadIdx.x == 0 && p.status) *p.status = MK_ERR_RESOURCES;
+        return;
+    }
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const uint32_t base = (sm::smem(raw) + 1023u) & ~1023u;
-    const uint32_t q_at = base, k_at = base + T::kTileBytes, v_at = k_at + T::kKStages * T::kTileBytes;
+    const uint32_t base = sm::smem(raw);
+    const uint32_t q_at = base, k_at = base + T::kQBytes, v_at = k_at + T::kKStages * T::kTileBytes;
     const uint32_t bar0 = sm::smem(bars);
     const uint32_t q_full = bar0;
     auto k_full = [&](int s) { return bar0 + 8u * (1 + s); };
@@ -158,7 +178,11 @@ attend_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
     auto v_full = [&](int s) { return bar0 + 8u * (1 + 2 * T::kKStages + s); };
     auto v_empty = [&](int s) { return bar0 + 8u * (1 + 2 * T::kKStages + T::kVStages + s); };
     constexpr int kMore = 1 + 2 * T::kKStages + 2 * T::kVStages;
-    const uint32_t s_full = bar0 + 8u * kMore, p_ready = s_full + 8u, pv_done = s_full + 16u, drained = s_full + 24u, s_free = s_full + 32u;
+    auto s_full = [&](int j) { return bar0 + 8u * (kMore + j % T::kPlaces); };          // (of tile j's place)
+    auto p_ready = [&](int j) { return bar0 + 8u * (kMore + 2 + j % T::kPlaces); };
+    auto turn = [&](int j) { return uint32_t(j / T::kPlaces) & 1u; };
+    auto pv_done = [&](int j) { return bar0 + 8u * (kMore + 4 + j % T::kPlaces); };
+    const uint32_t drained = bar0 + 8u * (kMore + 6), s_free = drained + 8u;
 
     // the item: (segment, block of queries -- the last ones, which see most, first --, KV head, share)
     int si = 0;
@@ -179,9 +203,9 @@ attend_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
     const int toks = min(p.block_tokens, seg.n - tok0), rows = toks * p.group;
     const bool causal = seg.pos0 != kNoCausal;
     const int t0 = causal ? seg.pos0 + tok0 : 0, t1 = t0 + toks - 1;
-    const KeyRange range(seg, t0, t1, p.window, p.sinks);
+    const KeyRange<kKeys> range(seg, t0, t1, p.window, p.sinks);
     int first = 0, n = range.count;
-    if (seg.splits > 1) {   // (at most 2^23 tiles by 256 shares: 32 bits hold the products)
+    if (seg.splits > 1) {   // (at most 2^24 tiles by 255 shares: 32 bits hold the products)
         first = int(uint32_t(range.count) * uint32_t(share) / uint32_t(seg.splits));
         n = int(uint32_t(range.count) * uint32_t(share + 1) / uint32_t(seg.splits)) - first;
     }
@@ -191,12 +215,14 @@ attend_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
         sm::bar_init(q_full, 1);
         for (int s = 0; s < T::kKStages; ++s) { sm::bar_init(k_full(s), 1); sm::bar_init(k_empty(s), 1); }
         for (int s = 0; s < T::kVStages; ++s) { sm::bar_init(v_full(s), 1); sm::bar_init(v_empty(s), 1); }
-        sm::bar_init(s_full, 1);
-        sm::bar_init(p_ready, uint32_t(warps));
+        for (int i = 0; i < T::kPlaces; ++i) {
+            sm::bar_init(s_full(i), 1);
+            sm::bar_init(p_ready(i), uint32_t(warps));
+            sm::bar_init(pv_done(i), 1);
+        }
         sm::bar_init(s_free, uint32_t(warps));
-        sm::bar_init(pv_done, 1);
         sm::bar_init(drained, 1);
-        abort_flag = 0;
+        *abort_word = 0;
         sm::bar_fence_init();
         sm::tma_prefetch_map(&map_q);
         sm::tma_prefetch_map(&map_k);
@@ -221,41 +247,66 @@ attend_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
             const int box = p.table ? 1 << p.box_log2 : kKeys, parts = kKeys / box;
             const int32_t* table = p.table + int64_t(seg.cache) * p.max_blocks;
             const int cache = p.table ? 0 : seg.cache;
-            int j = 0, jv = 0;   // tiles whose K, whose V copies are on their way
-            for (; j < n; ++j) {
-                const int pos = range.tile(first + j) * kKeys + lane * box;
-                const bool want = lane < parts && range.any(pos, box);
-                int at = pos;
-                bool good = want;
-                if (p.table && want) {
-                    const int b = __ldg(table + pos / p.block);
-                    good = unsigned(b) < unsigned(p.n_blocks);
-                    if (!good && p.status) *p.status = MK_ERR_BOUNDS;
-                    at = b * p.block + pos % p.block;
+            // The K of a tile goes ahead of the V of the tile before it, in the order of their use.
+            int jk = 0, jv = 0;   // tiles whose K, whose V copies are on their way
+            int at = 0, v_pos = 0;          // the lane's part of the tile in the cache; of the tile before
+            bool good = false, v_good = false;
+            uint32_t bytes = 0, v_bytes = 0;
+            auto copy = [&](const CUtensorMap* map, uint32_t dst, uint32_t full, uint32_t empty, int i, int stages) {
+                int ok = 1;
+                if (lane == 0) {
+                    if (i >= stages) ok = sm::bar_wait(empty, uint32_t(i / stages - 1) & 1u, abort_word, p.status);
+                    if (ok) sm::bar_expect(full, bytes);
                 }
-                const uint32_t copied = __ballot_sync(0xFFFFFFFFu, good);
-                if (lane == 0) skips[j % T::kFlags] = ~copied & ((1u << parts) - 1u);
-                const uint32_t bytes = uint32_t(__popc(copied) * box * D * 2);
-                auto copy = [&](const CUtensorMap* map, uint32_t dst, uint32_t full, uint32_t empty, int stages) {
-                    int ok = 1;
-                    if (lane == 0) {
-                        if (j >= stages) ok = sm::bar_wait(empty, uint32_t(j / stages - 1) & 1u, abort_word, p.status);
-                        if (ok) sm::bar_expect(full, bytes);
+                if (!__shfl_sync(0xFFFFFFFFu, ok, 0)) return false;
+                if (good)
+                    for (int c = 0; c < T::kSubs; ++c)
+                        sm::tma_load_4d(dst + (c * kKeys + lane * box) * T::kRowBytes, map, full, c * T::kSub, at, g, cache);
+                return true;
+            };
+            int pos = 0, blk = 0, entry = 0;   // of the next tile, its table entry read a tile ahead
+            bool want = false;
+            auto look = [&](int j) {
+                pos = range.tile(first + j) * kKeys + lane * box;
+                want = lane < parts && range.any(pos, box);
+                if (p.table && want) {
+                    blk = int(uint64_t(uint32_t(pos)) * p.block_inv >> p.block_shift);   // pos / p.block
+                    entry = __ldg(table + blk);
+                }
+            };
+            look(0);
+            for (int j = 0; j <= n; ++j) {
+                v_pos = at; v_good = good; v_bytes = bytes;
+                if (j < n) {
+                    at = pos;
+                    good = want;
+                    if (p.table && want) {
+                        good = unsigned(entry) < unsigned(p.n_blocks);
+                        if (!good && p.status) *p.status = MK_ERR_BOUNDS;
+                        at = entry * p.block + (pos - blk * p.block);
                     }
-                    if (!__shfl_sync(0xFFFFFFFFu, ok, 0)) return false;
-                    if (good)
-                        for (int c = 0; c < T::kSubs; ++c)
-                            sm::tma_load_4d(dst + (c * kKeys + lane * box) * T::kRowBytes, map, full, c * T::kSub, at, g, cache);
-                    return true;
-                };
-                const int ks = j % T::kKStages, vs = j % T::kVStages;
-                if (!copy(&map_k, k_at + ks * T::kTileBytes, k_full(ks), k_empty(ks), T::kKStages)) break;
-                if (!copy(&map_v, v_at + vs * T::kTileBytes, v_full(vs), v_empty(vs), T::kVStages)) { ++j; break; }
-                jv = j + 1;
+                    const uint32_t copied = __ballot_sync(0xFFFFFFFFu, good);
+                    if (lane == 0) skips[j % T::kFlags] = ~copied & ((1u << parts) - 1u);
+                    bytes = uint32_t(__popc(copied) * box * D * 2);
+                    const int ks = j % T::kKStages;
+                    if (!copy(&map_k, k_at + ks * T::kTileBytes, k_full(ks), k_empty(ks), j, T::kKStages)) break;
+                    jk = j + 1;
+                    if (j + 1 < n) look(j + 1);   // (on its way while the V copy waits for its place)
+                }
+                if (j > 0) {
+                    const int vs = (j - 1) % T::kVStages;
+                    const int k_pos = at;
+                    const bool k_good = good;
+                    const uint32_t k_bytes = bytes;
+                    at = v_pos; good = v_good; bytes = v_bytes;
+                    if (!copy(&map_v, v_at + vs * T::kTileBytes, v_full(vs), v_empty(vs), j - 1, T::kVStages)) break;
+                    jv = j;
+                    at = k_pos; good = k_good; bytes = k_bytes;
+                }
             }
             if (lane == 0 && *abort_word) {   // the copies in flight land before the CTA gives its shared memory back
                 sm::bar_drain(q_full, 0);
-                for (int i = max(0, j - T::kKStages); i < j; ++i) sm::bar_drain(k_full(i % T::kKStages), uint32_t(i / T::kKStages) & 1u);
+                for (int i = max(0, jk - T::kKStages); i < jk; ++i) sm::bar_drain(k_full(i % T::kKStages), uint32_t(i / T::kKStages) & 1u);
                 for (int i = max(0, jv - T::kVStages); i < jv; ++i) sm::bar_drain(v_full(i % T::kVStages), uint32_t(i / T::kVStages) & 1u);
             }
         }
@@ -276,10 +327,11 @@ attend_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
                 if (leader) {
 #pragma unroll
                     for (int i = 0; i < D / 16; ++i) {   // 16 elements of the head dimension
-                        const int at = (i * 16 / T::kSub * (kKeys * T::kRowBytes) + i * 16 % T::kSub * 2) >> 4;
-                        sm::mma_ss(tmem + T::kS, q_desc + at, k + at, idesc_s, i > 0);
+                        const int sub = i * 16 / T::kSub, at = i * 16 % T::kSub * 2;
+                        sm::mma_ss(tmem + T::kS + j % T::kPlaces * kKeys, q_desc + ((sub * kBlockRows * T::kRowBytes + at) >> 4),
+                                   k + ((sub * kKeys * T::kRowBytes + at) >> 4), idesc_s, i > 0);
                     }
-                    sm::mma_commit(s_full);
+                    sm::mma_commit(s_full(j));
                     sm::mma_commit(k_empty(s));
                 }
                 __syncwarp();
@@ -288,28 +340,27 @@ attend_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
             // 100 cycles, and there it would be in the tile's chain)
             bool ok = sm::bar_wait_warp(q_full, 0, abort_word, p.status) && k_there(0);
             if (ok) scores(0);
+            if (T::kShareSP && ok && n > 1 && (ok = k_there(1))) scores(1);
             for (int j = 0; j < n && ok; ++j) {
                 if (!T::kShareSP && j + 1 < n) {   // the next scores as soon as these are in registers
                     if (!(ok = k_there(j + 1) && sm::bar_wait_warp(s_free, uint32_t(j) & 1u, abort_word, p.status))) break;
                     scores(j + 1);
                 }
-                if (!(ok = v_there(j) && (!T::kShareSP || j + 1 >= n || k_there(j + 1)) &&
-                           sm::bar_wait_warp(p_ready, uint32_t(j) & 1u, abort_word, p.status)))
-                    break;
+                if (!(ok = v_there(j) && sm::bar_wait_warp(p_ready(j), turn(j), abort_word, p.status))) break;
                 sm::tc_fence_after();
                 const int s = j % T::kVStages;
                 const uint64_t v = v_desc + uint64_t(s * (T::kTileBytes >> 4));
                 if (leader) {
 #pragma unroll
                     for (int i = 0; i < kKeys / 16; ++i)   // 16 keys: 8 columns of P, two groups of 8 rows of V
-                        sm::mma_ts(tmem + T::kO, tmem + T::kP + i * 8, v + (i * 16 * T::kRowBytes >> 4), idesc_o, j > 0 || i > 0);
-                    sm::mma_commit(pv_done);
+                        sm::mma_ts(tmem + T::kO, tmem + T::kP + j % T::kPlaces * kKeys + i * 8, v + (i * 16 * T::kRowBytes >> 4), idesc_o, j > 0 || i > 0);
+                    sm::mma_commit(pv_done(j));
                     sm::mma_commit(v_empty(s));
                 }
                 __syncwarp();
-                if (T::kShareSP && j + 1 < n) {   // the weights share the scores' columns: read first
-                    if (!(ok = sm::bar_wait_warp(pv_done, uint32_t(j) & 1u, abort_word, p.status))) break;
-                    scores(j + 1);
+                if (T::kShareSP && j + 2 < n) {   // the next scores of this place, once its weights are read
+                    if (!(ok = k_there(j + 2) && sm::bar_wait_warp(pv_done(j), turn(j), abort_word, p.status))) break;
+                    scores(j + 2);
                 }
             }
             if (*abort_word && leader) { sm::mma_commit(drained); sm::bar_drain(drained, 0); }
@@ -335,10 +386,18 @@ attend_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
         bool ok = true;     // (a wait that ran out shows at the vote of its tile: until then the lanes stay together)
         const int seen_end = causal ? t0 + 1 : seg.key1;   // keys that every row of the block sees: [seen_low, seen_end), the sinks
         const int seen_low = p.window ? max(t1 - p.window + 1, seg.key0) : seg.key0;
+        constexpr int kQ = kKeys / 32;
+        uint32_t s[kQ][32];   // scores, then in the low half of each 32 registers their weights
+        auto place = [&](int j) { return tmem + lanes + j % T::kPlaces * kKeys; };   // of the scores, at D = 128 of the weights too
+        auto load = [&](int j) {
+            ok = sm::bar_wait_sync(s_full(j), turn(j), abort_word, p.status) && ok;
+            sm::tc_fence_after();
+#pragma unroll
+            for (int q = 0; q < kQ; ++q) sm::tmem_ld32(place(j) + q * 32, s[q]);
+        };
         for (int j = 0; j < n; ++j) {
             const int k0 = range.tile(first + j) * kKeys;
-            ok = sm::bar_wait_sync(s_full, uint32_t(j) & 1u, abort_word, p.status) && ok;
-            sm::tc_fence_after();
+            load(j);
             const uint32_t skip = p.table ? skips[j % T::kFlags] : 0u;
             const bool seen = skip == 0 && k0 + kKeys <= seen_end && (k0 >= seen_low || k0 + kKeys <= sinks);
             auto sees = [&](int at) {   // a bit for each of 32 keys from k0 + at: whether this row sees it
@@ -348,7 +407,6 @@ attend_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
                         if (skip >> ((at + 8 * i) >> p.box_log2) & 1u) see &= ~(0xFFu << (8 * i));
                 return see;
             };
-            uint32_t s[4][32];
             float total;
             // the tile's weights, their sum, and (store) the weights to tensor memory from halfway on, where `middle` has
             // waited for the place (a pair of weights takes the place of a pair of scores in registers)
@@ -356,7 +414,7 @@ attend_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
                 const float b = m * c;
                 float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
+                for (int q = 0; q < kQ; ++q) {
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
                         float2 x = make_float2(__uint_as_float(s[q][2 * i]), __uint_as_float(s[q][2 * i + 1]));
@@ -387,53 +445,54 @@ attend_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
             };
             if constexpr (!T::kShareSP) {
 #pragma unroll
-                for (int q = 0; q < 4; ++q) sm::tmem_ld32(tmem + T::kS + lanes + q * 32, s[q]);
-#pragma unroll
-                for (int q = 0; q < 4; ++q) sm::tmem_wait_ld(s[q]);
+                for (int q = 0; q < kQ; ++q) sm::tmem_wait_ld(s[q]);
                 sm::tc_fence_before();   // the scores are in registers: the next may come
                 __syncwarp();
                 if (lane == 0) sm::bar_arrive(s_free);
                 if (!seen)
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
+                    for (int q = 0; q < kQ; ++q) {
                         const uint32_t see = sees(q * 32);
 #pragma unroll
                         for (int i = 0; i < 32; ++i)
                             if (!(see >> i & 1u)) s[q][i] = 0xFF800000u;
                     }
-                float mx[4];
+                float mx[8];
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    mx[q] = fmaxf(__uint_as_float(s[q][0]), __uint_as_float(s[q][1]));
+                for (int q = 0; q < 8; ++q) {
+                    const uint32_t* x = &s[q / 2][q % 2 * 16];
+                    mx[q] = fmaxf(__uint_as_float(x[0]), __uint_as_float(x[1]));
 #pragma unroll
-                    for (int i = 2; i < 32; i += 2) mx[q] = max3(mx[q], __uint_as_float(s[q][i]), __uint_as_float(s[q][i + 1]));
+                    for (int i = 2; i < 16; i += 2) mx[q] = max3(mx[q], __uint_as_float(x[i]), __uint_as_float(x[i + 1]));
                 }
-                const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                const float top = max3(max3(mx[0], mx[1], mx[2]), max3(mx[3], mx[4], mx[5]), fmaxf(mx[6], mx[7]));
                 const bool rise = top > high;
                 if (__any_sync(0xFFFFFFFFu, rise || !ok)) {
                     // the products that wrote O are done before it is touched
-                    if (j > 0) ok = sm::bar_wait_sync(pv_done, uint32_t(j - 1) & 1u, abort_word, p.status) && ok;
+                    if (j > 0) ok = sm::bar_wait_sync(pv_done(j - 1), turn(j - 1), abort_word, p.status) && ok;
                     sm::tc_fence_after();
                     if (!(ok = __all_sync(0xFFFFFFFFu, ok))) break;
                     const float f = rise && set ? exp2_approx((m - top) * c) : 1.f;
                     if (rise) { m = top; high = m + 8.f / c; }
                     if (j > 0) rescale(f);
                 }
+                const bool was_done = j == 0 || sm::bar_test(pv_done(j - 1), turn(j - 1));   // (asked ahead of its use)
                 // (halfway through them the products that read the last weights are mostly done: waiting for them before
                 // the maximum or behind all weights took 3% and 5% more)
                 weights(true, [&] {
-                    if (j > 0) ok = sm::bar_wait_warp(pv_done, uint32_t(j - 1) & 1u, abort_word, p.status);
+                    if (!__all_sync(0xFFFFFFFFu, was_done)) ok = sm::bar_wait_warp(pv_done(j - 1), turn(j - 1), abort_word, p.status);
                     sm::tc_fence_after();
                 });
             } else
             for (int pass = 0;; ++pass) {
+                if (pass == 1)
 #pragma unroll
-                for (int q = 0; q < 4; ++q) sm::tmem_ld32(tmem + T::kS + lanes + q * 32, s[q]);
+                    for (int q = 0; q < kQ; ++q) sm::tmem_ld32(place(j) + q * 32, s[q]);
 #pragma unroll
-                for (int q = 0; q < 4; ++q) sm::tmem_wait_ld(s[q]);
+                for (int q = 0; q < kQ; ++q) sm::tmem_wait_ld(s[q]);
                 if (!seen)
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
+                    for (int q = 0; q < kQ; ++q) {
                         const uint32_t see = sees(q * 32);
 #pragma unroll
                         for (int i = 0; i < 32; ++i)
@@ -445,9 +504,9 @@ attend_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
                 if (!(ok = __all_sync(0xFFFFFFFFu, ok))) break;
                 float top = -INFINITY;
 #pragma unroll 1
-                for (int q = 0; q < 4; ++q) {
+                for (int q = 0; q < kQ; ++q) {
                     uint32_t v[32];
-                    sm::tmem_ld32(tmem + T::kS + lanes + q * 32, v);
+                    sm::tmem_ld32(place(j) + q * 32, v);
                     sm::tmem_wait_ld(v);
                     const uint32_t see = seen ? 0xFFFFFFFFu : sees(q * 32);
 #pragma unroll
@@ -459,12 +518,17 @@ attend_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
                     if (set) f = exp2_approx((m - top) * c);
                     m = top;
                 }
-                if (j > 0) rescale(f);   // (the products before these scores are done)
+                if (j > 0) {   // the products that wrote O are done before it is touched
+                    ok = sm::bar_wait_sync(pv_done(j - 1), turn(j - 1), abort_word, p.status);
+                    if (!(ok = __all_sync(0xFFFFFFFFu, ok))) break;
+                    sm::tc_fence_after();
+                    rescale(f);
+                }
             }
             if (!ok) break;
             if (T::kShareSP)
 #pragma unroll
-                for (int q = 0; q < 4; ++q) tmem_st16_head(tmem + T::kP + lanes + q * 16, s[q]);
+                for (int q = 0; q < kQ; ++q) tmem_st16_head(place(j) + q * 16, s[q]);
             set = set || total > 0.f;
             l += total;
             if (!seen && (skip != 0 || !range.whole(k0, kKeys))) {
@@ -482,10 +546,10 @@ attend_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
             sm::tmem_wait_st();
             sm::tc_fence_before();
             __syncwarp();
-            if (lane == 0) sm::bar_arrive(p_ready);
+            if (lane == 0) sm::bar_arrive(p_ready(j));
         }
         ok = __all_sync(0xFFFFFFFFu, ok);
-        if (ok && n > 0) ok = sm::bar_wait_warp(pv_done, uint32_t(n - 1) & 1u, abort_word, p.status);
+        if (ok && n > 0) ok = sm::bar_wait_warp(pv_done(n - 1), turn(n - 1), abort_word, p.status);
         if (ok) {
             sm::tc_fence_after();
             const bool whole = seg.splits == 1 && !p.prefix_seg;   // no other item adds to this row
@@ -534,7 +598,7 @@ __global__ void __launch_bounds__(128) attend_merge_kernel(const __grid_constant
     sm::pdl_trigger();
     sm::pdl_wait();
     constexpr int kThreads = WARPS * 32, kLanes = D / 4, kGroups = kThreads / kLanes, kRows = 4 / WARPS;
-    constexpr int kMaxParts = 512;   // a sequence's and the prefix's shares, 256 each at most
+    constexpr int kMaxParts = 512;   // a sequence's and the prefix's shares, 255 each at most
     __shared__ float weight[kRows][WARPS == 1 ? 64 : kMaxParts];
     __shared__ float4 sums[kRows][kThreads];
     __shared__ float red[kRows][2][WARPS];
@@ -689,7 +753,7 @@ struct AttendPlan {
     int segs = 0, prefix_seg = 0, parts = 0;   // parts: of a row, at most
     AttendSeg seg[MK_ATTEND_MAX_BATCH + 1];
 };
-static int64_t attend_tiles(const AttendSeg& s, int t0, int t1, int window, int sinks) {   // key tiles of a block (as KeyRange)
+static int64_t attend_tiles(const AttendSeg& s, int t0, int t1, int window, int sinks, int kKeys) {   // key tiles of a block (as KeyRange)
     const int64_t end = s.pos0 == kNoCausal ? s.key1 : std::min(t1 + 1, s.key1);
     int64_t low = window ? std::max<int64_t>(int64_t(t0) - window + 1, s.key0) : s.key0;
     int64_t sink = window ? std::min<int64_t>(sinks, end) : 0;
@@ -698,7 +762,7 @@ static int64_t attend_tiles(const AttendSeg& s, int t0, int t1, int window, int 
     return end > low ? st + std::max<int64_t>(0, (end + kKeys - 1) / kKeys - std::max(low / kKeys, st)) : 0;
 }
 static mk_status attend_plan(const mk_attend_args* a, int sms, AttendPlan& pl) {
-    const int group = a->n_q_heads / a->n_kv_heads, bt = kBlockRows / group;
+    const int group = a->n_q_heads / a->n_kv_heads, bt = kBlockRows / group, keys = attend_keys(a->head_dim);
     const uint32_t slots = 2 * uint32_t(sms);   // (two CTAs to an SM)
     // of each segment: the key tiles of its last block of queries (the most) and of its middle one; blocks by heads
     uint32_t tiles[MK_ATTEND_MAX_BATCH + 1] = {}, middle[MK_ATTEND_MAX_BATCH + 1] = {}, blocks[MK_ATTEND_MAX_BATCH + 1] = {};
@@ -706,7 +770,7 @@ static mk_status attend_plan(const mk_attend_args* a, int sms, AttendPlan& pl) {
     auto add = [&](const AttendSeg& s) {
         auto seen = [&](int t) {
             const bool causal = s.pos0 != kNoCausal;
-            return uint32_t(attend_tiles(s, causal ? s.pos0 + t : 0, causal ? s.pos0 + std::min(t + bt, s.n) - 1 : 0, a->window, a->sinks));
+            return uint32_t(attend_tiles(s, causal ? s.pos0 + t : 0, causal ? s.pos0 + std::min(t + bt, s.n) - 1 : 0, a->window, a->sinks, keys));
         };
         const int n = (s.n + bt - 1) / bt;
         const uint32_t k = seen((n - 1) * bt);
@@ -741,8 +805,8 @@ static mk_status attend_plan(const mk_attend_args* a, int sms, AttendPlan& pl) {
     // kItem more; long items of one length run in whole rounds of `slots`, the others (a causal prompt's blocks, of every
     // length) fill what these leave; joining costs kMerge.  (Eight single tokens with windows of 4096: shares of
     // 8 tiles made 320 items for 304 places and so two rounds, 43 us against 32 with shares of 9.)
-    constexpr uint32_t kItem = 2, kMerge = 3;
-    auto splits = [](uint32_t t, uint32_t share) { return std::min(std::max(1u, (t + share - 1) / share), 256u); };
+    const uint32_t kItem = 256 / keys, kMerge = 384 / keys;
+    auto splits = [](uint32_t t, uint32_t share) { return std::min(std::max(1u, (t + share - 1) / share), 255u); };
     auto cost = [&](uint32_t share) {
         uint32_t top = 0, each[MK_ATTEND_MAX_BATCH + 1];
         int64_t all = 0, many = 0;
@@ -807,7 +871,7 @@ static mk_status attend_launch(const mk_attend_args* a, const AttendCommon& comm
     const int64_t seqs = a->pages ? 1 : a->batch, bs = seqs > 1 ? kv.batch_stride : kv.head_stride * p.nkv;
     const cuuint64_t kd[4] = {cuuint64_t(D), cuuint64_t(positions), cuuint64_t(p.nkv), cuuint64_t(seqs)};
     const cuuint64_t kst[3] = {cuuint64_t(D) * 2, cuuint64_t(kv.head_stride) * 2, cuuint64_t(bs) * 2};
-    const cuuint32_t kb[4] = {T::kSub, cuuint32_t(p.table ? 1 << p.box_log2 : kKeys), 1, 1};
+    const cuuint32_t kb[4] = {T::kSub, cuuint32_t(p.table ? 1 << p.box_log2 : T::kKeys), 1, 1};
     const int64_t off = int64_t(a->layer) * kv.layer_stride;
     if ((st = op_tensor_map(&mq, a->q, 3, qd, qst, qb)) != MK_OK) return st;
     if ((st = op_tensor_map(&mk_, static_cast<const uint16_t*>(kv.k) + off, 4, kd, kst, kb)) != MK_OK) return st;
@@ -884,8 +948,11 @@ extern "C" mk_status mk_attend(const mk_attend_args* a, void* workspace, size_t 
     if (a->pages) {
         p.table = a->pages->block_table; p.block = a->pages->block_size;
         p.max_blocks = a->pages->max_blocks; p.n_blocks = a->pages->n_blocks;
+        p.block_shift = 30;
+        while ((int64_t(1) << (p.block_shift - 30)) < p.block) ++p.block_shift;
+        p.block_inv = uint32_t(((uint64_t(1) << p.block_shift) + uint32_t(p.block) - 1) / uint32_t(p.block));
         p.box_log2 = 3;
-        while ((1 << p.box_log2) < kKeys && p.block % (2 << p.box_log2) == 0) ++p.box_log2;
+        while ((1 << p.box_log2) < attend_keys(a->head_dim) && p.block % (2 << p.box_log2) == 0) ++p.box_log2;
     }
     p.out = static_cast<__nv_bfloat16*>(a->out);
     p.out_stride = a->out_stride;

@@ -46,6 +46,13 @@ __device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
         : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
     return ok != 0;
 }
+__device__ __forceinline__ bool bar_test(uint32_t bar, uint32_t parity) {   // (never suspends the thread)
+    uint32_t ok;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
+    return ok != 0;
+}
 
 // A wait that ran out (2 s: far beyond any kernel here) ends the kernel instead of hanging it: the
 // waiting thread raises the CTA's abort word and the caller's status, every role leaves its loop,
