@@ -2,7 +2,10 @@
 
 A kernel takes scores in fp32 (d products of bf16 values, error at most d 2^-23 of their absolute
 sum), rounds its softmax weights to bf16 (half a step, 2^-8 relative) and its output to bf16 (2^-8
-relative); exponentials, running sums and a merge of parts add less than 2^-16 together."""
+relative); exponentials, running sums and a merge of parts add less than 2^-16 together.  At head
+dims other than 64 the rows are divided by the sum of the rounded weights: with weights p_i (1 + e_i),
+|e_i| <= 2^-8, and e their mean under p, the output is off by sum p_i |e_i - e| |v_i| / (1 + e), where
+|e_i - e| <= 2 2^-8 (two keys, one of them with a small v, come near it): twice the bound of exact sums."""
 import math
 
 import torch
@@ -24,6 +27,7 @@ def attend_reference(q, kv, q_lens, kv_lens, layer=0, window=0, sinks=0, shared_
     out = torch.zeros((tokens, nq, d), dtype=torch.float64, device=q.device)
     bound = torch.zeros_like(out)
     row = 0
+    weights = 2.0 ** -8 if d == 64 else 2.0 ** -7 + 2.0 ** -15   # (the last term: 1 / (1 + e))
     for b, (n, length) in enumerate(zip(q_lens, kv_lens)):
         if n == 0:
             continue
@@ -51,6 +55,6 @@ def attend_reference(q, kv, q_lens, kv_lens, layer=0, window=0, sinks=0, shared_
             o = p @ vv
             ds = (qq.abs() @ kk.abs().T * scale * d * 2.0 ** -23).masked_fill(~see, 0.0).amax(1, keepdim=True) if length else 0.0
             out[row:row + n, h] = o
-            bound[row:row + n, h] = 2.0 ** -8 * o.abs() + (2.0 ** -8 + 2 * ds + 2.0 ** -16) * (p @ vv.abs()) + 1e-37
+            bound[row:row + n, h] = 2.0 ** -8 * o.abs() + (weights + 2 * ds + 2.0 ** -16) * (p @ vv.abs()) + 1e-37
         row += n
     return out, bound

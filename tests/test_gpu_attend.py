@@ -66,6 +66,42 @@ def test_windows(window, sinks, q_len, kv_len):
     check(randn((q_len, 8, 64), 5, 1.5), cache(1, 2, 64, 704), [q_len], [kv_len], window=window, sinks=sinks)
 
 
+@pytest.mark.parametrize("window,sinks", [(1, 1), (5, 3), (63, 0), (64, 64), (65, 10), (130, 64), (300, 150), (1000, 4), (40, 1000)])
+@pytest.mark.parametrize("q_len,kv_len", [(1, 700), (40, 700), (333, 333)])
+@pytest.mark.parametrize("d", [32, 128])
+def test_windows_at_other_widths(d, window, sinks, q_len, kv_len):
+    check(randn((q_len, 4, d), 5, 1.5), cache(1, 1, d, 704), [q_len], [kv_len], window=window, sinks=sinks)
+
+
+@pytest.mark.parametrize("q_len,kv_len", [(1, 63), (1, 64), (1, 65), (63, 63), (64, 64), (65, 65), (128, 192), (200, 321), (17, 64 * 31 + 1)])
+@pytest.mark.parametrize("group", [1, 4, 7])
+def test_lengths_about_a_tile_of_64(group, q_len, kv_len):
+    check(randn((q_len, group, 128), 5, 1.5), cache(1, 1, 128, kv_len), [q_len], [kv_len])
+
+
+def test_masked_places_and_rising_maxima_at_width_128():
+    kv = cache(2, 2, 128, 384)
+    q_lens, kv_lens = [60, 200], [200, 333]
+    q = randn((260, 4, 128), 5)
+    for window, sinks in ((0, 0), (90, 5)):
+        want = mk.attend(q, kv, q_lens, kv_lens, window=window, sinks=sinks)
+        bad = KVCache(kv.k.clone(), kv.v.clone())
+        for c, fill in ((bad.k, float("nan")), (bad.v, float("inf"))):
+            for b, n in enumerate(kv_lens):
+                c[b, :, :, n:] = fill
+                if window:
+                    c[b, :, :, sinks:n - q_lens[b] - window + 1] = fill
+        assert torch.equal(mk.attend(q, bad, q_lens, kv_lens, window=window, sinks=sinks), want)
+    # a maximum that rises and falls from one tile of 64 keys to the next, and alternates between them
+    kv, one = cache(1, 1, 128, 900), torch.ones((64, 4, 128), device="cuda", dtype=BF)
+    at = torch.arange(900, device="cuda")
+    for ramp in (at // 64 * 4.0, at // 64 * -4.0, at // 64 % 2 * 12.0, at // 64 % 3 * -9.0, (at == 700) * 30.0):
+        kv.k[0, 0, 0] = (ramp[:, None] * torch.ones(128, device="cuda")).to(BF)
+        for q in (one, -one):
+            check(q, kv, [64], [900])
+            check(q, kv, [64], [900], window=500, sinks=70)
+
+
 @pytest.mark.parametrize("window,sinks", [(0, 0), (70, 3)])
 def test_ragged_batch(window, sinks):
     q_lens, kv_lens = [1, 0, 37, 200, 1, 3, 0, 129], [1, 17, 300, 200, 513, 3, 0, 400]
