@@ -71,7 +71,8 @@ __global__ void __launch_bounds__(kNormThreads) norm_kernel(float* x, const int3
 }
 
 // Pairs (i, i + d/2) of q and k rotated by their position's angles (the bind's table), rounded once; q to its
-// own buffer, k and v to the cache row of their position.  A block per token.
+// own buffer, k and v to the cache row of their position.  A block per token, four pairs or four values of v a thread
+// (d is 32, 64 or 128: shifts; rows and cache are 16-byte aligned).
 __global__ void __launch_bounds__(256) rope_append_kernel(const float* qkv, __nv_bfloat16* q, const __grid_constant__ PrefillRows p) {
     sm::pdl_trigger();
     sm::pdl_wait();
@@ -90,19 +91,39 @@ __global__ void __launch_bounds__(256) rope_append_kernel(const float* qkv, __nv
         base = 0;
         slot = int64_t(blk) * p.block + pos % p.block;
     }
-    const int heads = p.nq + p.nkv;
-    for (int i = threadIdx.x; i < heads * half; i += blockDim.x) {
-        const int h = i / half, e = i % half;
-        const float a = src[h * p.d + e], c = src[h * p.d + e + half];
-        const float2 t = cs[e];
-        const __nv_bfloat16 r0 = __float2bfloat16_rn(a * t.x - c * t.y), r1 = __float2bfloat16_rn(a * t.y + c * t.x);
+    const int heads = p.nq + p.nkv, quads = half / 4, log2_quads = __ffs(quads) - 1;
+    auto pack4 = [](const float (&x)[4]) {
+        uint2 r;
+        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r.x) : "f"(x[1]), "f"(x[0]));
+        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r.y) : "f"(x[3]), "f"(x[2]));
+        return r;
+    };
+    for (int i = threadIdx.x; i < heads << log2_quads; i += blockDim.x) {
+        const int h = i >> log2_quads, e = (i & (quads - 1)) * 4;
+        const float4 a4 = *reinterpret_cast<const float4*>(src + h * p.d + e), c4 = *reinterpret_cast<const float4*>(src + h * p.d + e + half);
+        const float4 t01 = *reinterpret_cast<const float4*>(cs + e), t23 = *reinterpret_cast<const float4*>(cs + e + 2);
+        const float a[4] = {a4.x, a4.y, a4.z, a4.w}, c[4] = {c4.x, c4.y, c4.z, c4.w};
+        const float co[4] = {t01.x, t01.z, t23.x, t23.z}, si[4] = {t01.y, t01.w, t23.y, t23.w};
+        float r0[4], r1[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            r0[k] = a[k] * co[k] - c[k] * si[k];
+            r1[k] = a[k] * si[k] + c[k] * co[k];
+        }
         __nv_bfloat16* dst = h < p.nq ? q + (int64_t(tok) * p.nq + h) * p.d
                                       : p.k + base + (h - p.nq) * p.head_stride + slot * p.d;
-        if (h < p.nq || good) { dst[e] = r0; dst[e + half] = r1; }
+        if (h < p.nq || good) {
+            *reinterpret_cast<uint2*>(dst + e) = pack4(r0);
+            *reinterpret_cast<uint2*>(dst + e + half) = pack4(r1);
+        }
     }
     if (good)
-        for (int i = threadIdx.x; i < p.nkv * p.d; i += blockDim.x)
-            p.v[base + i / p.d * p.head_stride + slot * p.d + i % p.d] = __float2bfloat16_rn(src[heads * p.d + i]);
+        for (int i = threadIdx.x; i < p.nkv << (log2_quads + 1); i += blockDim.x) {
+            const int h = i >> (log2_quads + 1), e = (i & (2 * quads - 1)) * 4;
+            const float4 v = *reinterpret_cast<const float4*>(src + (heads + h) * p.d + e);
+            const float x[4] = {v.x, v.y, v.z, v.w};
+            *reinterpret_cast<uint2*>(p.v + base + h * p.head_stride + slot * p.d + e) = pack4(x);
+        }
 }
 
 template <typename... Args, typename... Given>
