@@ -143,7 +143,7 @@ __device__ __forceinline__ uint32_t low_bits(int n) { return n >= 32 ? 0xFFFFFFF
 // O += P V runs with P read from tensor memory.  Two CTAs share an SM, so one's products run while the
 // other's threads are at their exponentials.
 // What bounds it with many rows at widths up to 64 is the chain of one warp's instructions per tile, two such warps to a
-// scheduler (4096 causal tokens of 32 / 8 heads by 64: 80 us, 855 TFLOP/s; tensor pipe 35% and special functions 38%
+// scheduler (4096 causal tokens of 32 / 8 heads by 64: 80 us, 855 TFLOP/s; tensor pipe 39% and special functions 39%
 // busy).  Measured against: two threads per row at 80 or 96 registers 107 us; tiles of 64 keys with three or four CTAs 107
 // and 161; registers moved between warps (setmaxnreg) 98; the exponentials taken out left the time as it was.
 // At width 128 a tile has 64 keys, so that two tiles' scores have a place and the products of one run beside the weights
