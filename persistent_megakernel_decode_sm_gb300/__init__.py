@@ -31,6 +31,7 @@ LIB_PATH = os.path.join(_HERE, "libmk.so")
 if not os.path.exists(LIB_PATH):
     raise ImportError(f"{LIB_PATH} is missing: build it first (python -c 'import __graft_entry__ as g; g.build()')")
 lib = ctypes.CDLL(LIB_PATH)
+from . import _mk_call   # noqa: E402  (built with the library; a missing one raises here)
 
 MK_OK, MK_ERR_ARG, MK_ERR_CAPACITY, MK_ERR_RESOURCES, MK_ERR_CUDA, MK_ERR_TIMEOUT, MK_ERR_OPCODE, \
     MK_ERR_BOUNDS, MK_ERR_POISONED = range(9)
@@ -450,8 +451,10 @@ class Decoder:
 
 
 # ---- prompt operators ------------------------------------------------------------------------
-# A call's host time counts beside kernels of a few microseconds, so the argument structs are packed
-# in one go (native alignment, the layouts of mk_linear_args and mk_attend_args).  They record no
+# A call's host time counts beside kernels of a few microseconds, so the common call is checked and made in C
+# (csrc/mk_python.c).  What that does not take comes here: the same checks, which say what is wrong, and calls
+# for another device than the current one.  Argument structs are packed in one go (native alignment, the layouts
+# of mk_linear_args and mk_attend_args).  They record no
 # gradients, whatever their operands' requires_grad: the framework runs models, it does not train them.
 
 _LINEAR_ARGS = struct.Struct("@4iPqPPPq2iPqP")
@@ -473,6 +476,20 @@ def _operand(t, name, dtypes, device, dim):
     if strides[-1] != 1 and shape[-1] > 1:
         raise ValueError(f"{name}: its last dimension must be contiguous")
     return shape, strides
+
+
+_fast = None   # _mk_call, once it has torch's objects
+
+
+def _setup():
+    global _fast
+    import torch
+    c = torch._C
+    _mk_call.setup(*(ctypes.cast(f, _P).value for f in (lib.mk_linear, lib.mk_attend, lib.mk_attend_workspace)), torch.bfloat16,
+                   torch.float32, torch.int32, torch.empty, c._cuda_getCurrentRawStream, c._cuda_getDevice,
+                   c._cuda_cudaCachingAllocator_raw_alloc, c._cuda_cudaCachingAllocator_raw_delete)
+    _fast = _mk_call
+    return _fast
 
 
 def _status_ptr(status, device):
@@ -505,6 +522,9 @@ def linear(x, weight, bias=None, activation: Optional[str] = None, residual=None
     bias bf16 [n] ([2 n]), residual bf16 or fp32 [rows, n] (or an expanded row).  activation: None,
     "silu", "gelu" (the erf form) or "swiglu".  out: a bf16 or fp32 [rows, n] tensor, which may be
     the residual itself; by default one of out_dtype (bf16) is allocated.  Returns out."""
+    y = (_fast or _setup()).linear(x, weight, bias, activation, residual, out, out_dtype, status)
+    if y is not None:
+        return y
     import torch
     bf, f32 = torch.bfloat16, torch.float32
     dev = x.get_device()
@@ -557,6 +577,10 @@ def attend(q, kv, q_lens: Sequence[int], kv_lens: Sequence[int], layer: int = 0,
     window those with p > t - window or p < sinks.  shared_prefix: the first positions, the same
     for every sequence, read once through sequence 0.  out: bf16, shaped like q (allocated by
     default); workspace: at least attend_workspace bytes (allocated by default).  Returns out."""
+    o = (_fast or _setup()).attend(q, kv.k, kv.v, q_lens, kv_lens, layer, window, sinks, shared_prefix, scale, pages, out, workspace,
+                                   status)
+    if o is not None:
+        return o
     import torch
     bf = torch.bfloat16
     dev = q.get_device()
@@ -566,7 +590,7 @@ def attend(q, kv, q_lens: Sequence[int], kv_lens: Sequence[int], layer: int = 0,
         raise ValueError("q_lens and kv_lens must have the same length")
     if sum(q_lens) > tokens:
         raise ValueError(f"q holds {tokens} tokens, q_lens add up to {sum(q_lens)}")
-    if scale is not None and not scale > 0:
+    if scale is not None and not scale > 1e-45:   # (what rounds to zero in fp32 would stand for the default)
         raise ValueError("scale must be positive")
     if out is None:
         out, os = torch.empty((tokens, nq, d), dtype=bf, device=q.device), (nq * d, d)

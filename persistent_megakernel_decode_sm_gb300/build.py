@@ -8,12 +8,15 @@ Translation units compiled in parallel and linked into one shared library:
   csrc/mk_linear.cu  the linear map with a fused epilogue (prompt path)
   csrc/mk_attend.cu  attention of query tokens over the KV cache (prompt path)
   csrc/mk_prefill.cu embedding, RMSNorm, RoPE and KV append of the prompt path
+and beside it, with the host's C compiler, the Python module _mk_call.so:
+  csrc/mk_python.c   argument handling of linear() and attend()
 """
 from __future__ import annotations
 
 import os
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 from typing import List
 
@@ -22,6 +25,7 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libmk.so")
+CALL_SOURCE, CALL = os.path.join(CSRC, "mk_python.c"), os.path.join(HERE, "_mk_call.so")
 BUILD_DIR = os.path.join(HERE, "_build")
 SOURCES = ["mk_sched.cpp", "mk_api.cu", "mk_kernel.cu", "mk_kernel_batch.cu", "mk_linear.cu", "mk_attend.cu",
            "mk_prefill.cu"]
@@ -38,14 +42,14 @@ def _nvcc() -> str:
 
 def _inputs() -> List[str]:
     files = [os.path.join(CSRC, s) for s in SOURCES]
-    files += [os.path.join(CSRC, h) for h in HEADERS] + [os.path.join(INCLUDE, "mk.h"), __file__]
+    files += [os.path.join(CSRC, h) for h in HEADERS] + [os.path.join(INCLUDE, "mk.h"), CALL_SOURCE, __file__]
     return files
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(CALL):
         return False
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(CALL))
     return all(os.path.getmtime(f) <= t for f in _inputs())
 
 
@@ -71,8 +75,18 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
             sys.stderr.write(r.stdout + r.stderr)
         return obj
 
-    with ThreadPoolExecutor(len(SOURCES)) as ex:
+    def compile_call() -> None:
+        tmp = CALL + f".{os.getpid()}.tmp"
+        r = subprocess.run([os.environ.get("CC", "gcc"), "-O2", "-Wall", "-shared", "-fPIC", f"-I{sysconfig.get_paths()['include']}",
+                            f"-I{INCLUDE}", CALL_SOURCE, "-o", tmp], capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"C compiler failed on mk_python.c:\n{r.stdout}\n{r.stderr}")
+        os.replace(tmp, CALL)
+
+    with ThreadPoolExecutor(len(SOURCES) + 1) as ex:
+        call = ex.submit(compile_call)
         objs = list(ex.map(compile_one, SOURCES))
+        call.result()
     tmp = LIB + f".{os.getpid()}.tmp"
     link = [nvcc, *ARCH, "-shared", "-cudart", "shared", *objs, "-o", tmp]
     r = subprocess.run(link, capture_output=True, text=True)

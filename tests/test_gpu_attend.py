@@ -342,6 +342,65 @@ def test_many_short_sequences_and_many_tokens():
     check(randn((20000, 1, 32), 5), cache(1, 1, 32, 20000), [20000], [20000], window=40, sinks=1)
 
 
+class _Python:
+    """In the place of the C call module: leaves every call to Python."""
+
+    @staticmethod
+    def linear(*args):
+        return None
+
+    attend = linear
+
+
+def test_c_and_python_calls_agree_and_keep_nothing(monkeypatch):
+    import sys
+    kv, q = cache(3, 2, 64, 500), randn((9, 4, 64), 5)
+    pool = KVCache(kv.k[:, 0].permute(1, 0, 2, 3).reshape(1, 2, 1500, 64).contiguous(),
+                   kv.v[:, 0].permute(1, 0, 2, 3).reshape(1, 2, 1500, 64).contiguous())
+    table = torch.arange(15, device="cuda", dtype=torch.int32).reshape(3, 5)
+    out, status = torch.empty_like(q), torch.zeros(1, device="cuda", dtype=torch.int32)
+    ws = torch.empty(1 << 22, device="cuda", dtype=torch.uint8)
+    calls = [(kv, [1, 3, 5], [500, 200, 60], {}), (kv, (1, 3, 5), (500, 200, 60), dict(window=40, sinks=3, scale=0.3, status=status)),
+             (kv, [2, 0, 1], [500, 0, 300], dict(out=out, workspace=ws)), (kv, [1, 1, 1], [400, 300, 450], dict(shared_prefix=128)),
+             (pool, [1, 3, 5], [480, 200, 60], dict(pages=(table, 96, 15)))]
+    bad = [(kv, [1, 3, 5], [500, 200], {}), (kv, [1, 3, 5], [500, 200, 501], {}), (kv, [9, 9, 9], [500, 200, 60], {}),
+           (kv, [1, 3, 5], [500, 200, 60], dict(layer=1)), (kv, [1, 3, 5], [500, 200, 60], dict(scale=-1.0)),
+           (kv, [1, 3, 5], [500, 200, 60], dict(scale=1e-60)), (kv, [1, 3, 5], [500, 200, 60], dict(workspace=ws.cpu())),
+           (kv, [1, 3, 5], [500, 200, 60], dict(out=q)), (kv, [1, 3, 5], [500, 200, 60], dict(status=status.float())),
+           (pool, [1, 3, 5], [480, 200, 60], dict(pages=(table, 96, 16))), (kv, [], [], {})]
+
+    def run(c):
+        try:
+            return mk.attend(q, c[0], c[1], c[2], **c[3]).clone()
+        except (ValueError, mk.MkError) as e:
+            return str(e)
+
+    taken = [run(c) for c in calls]
+    refused = [run(c) for c in bad]
+    assert all(isinstance(t, torch.Tensor) for t in taken) and all(isinstance(r, str) for r in refused)
+    with monkeypatch.context() as m:
+        m.setattr(mk, "_fast", _Python)
+        for c, t in zip(calls, taken):
+            n = sum(c[1])
+            assert torch.equal(run(c)[:n], t[:n])
+        assert [run(c) for c in bad] == refused
+    del taken
+    torch.cuda.synchronize()
+    held = torch.cuda.memory_allocated(), [sys.getrefcount(o) for o in (q, out, ws, table, status, kv.k, torch.bfloat16)]
+    for _ in range(100):
+        for c in calls + bad:
+            run(c)
+    assert (torch.cuda.memory_allocated(), [sys.getrefcount(o) for o in (q, out, ws, table, status, kv.k, torch.bfloat16)]) == held
+
+
+def test_lengths_may_be_any_sequence_of_ints():
+    import numpy as np
+    kv, q = cache(2, 1, 64, 300), randn((5, 4, 64), 5)
+    want = mk.attend(q, kv, [2, 3], [300, 40])
+    assert torch.equal(mk.attend(q, kv, np.array([2, 3]), np.array([300, 40])), want)
+    assert torch.equal(mk.attend(q, kv, range(2, 4), (300, 40)), want)
+
+
 def test_refuses_tensors_it_cannot_take():
     kv, (pk, pages) = cache(2, 2, 64, 100), pool(2, 2, 64, 100, 16)
     q = randn((3, 8, 64), 5)

@@ -134,6 +134,41 @@ print("fine")
     assert r.returncode == 0 and "fine" in r.stdout, r.stderr[-2000:]
 
 
+def test_c_and_python_calls_agree_and_keep_nothing(monkeypatch):
+    import sys
+    x, w, b = randn((5, 64), 1), randn((32, 64), 2), randn((32,), 3)
+    r, out = randn((5, 32), 4), torch.empty((5, 32), device="cuda", dtype=torch.float32)
+    calls = [(x, w, {}), (x, w, dict(bias=b, activation="gelu")), (x, w, dict(residual=r, out_dtype=torch.float32)),
+             (x, w, dict(residual=r.float(), out=out)), (x, w, dict(bias=b, activation="swiglu", residual=r[:, :16])),
+             (x[:0], w, {}), (x[1:2], w, dict(activation="silu", residual=r[:1].expand(1, 32)))]
+    bad = [(x, w[:, :56], {}), (x.float(), w, {}), (x, w, dict(bias=b[:31])), (x, w, dict(activation="relu")), (x, w, dict(out=out[:4])),
+           (x, w, dict(out=out, out_dtype=torch.bfloat16)), (x, w, dict(out_dtype=torch.float16)), (x, w[:31], dict(activation="swiglu")),
+           (x, w, dict(residual=r[:4])), (x[0], w, {}), (x[:, 1:57], w[:, :56].contiguous(), {}), (x.T, w, {})]
+
+    class Python:
+        linear = staticmethod(lambda *a: None)
+
+    def run(c):
+        try:
+            return mk.linear(c[0], c[1], **c[2]).clone()
+        except (ValueError, mk.MkError) as e:
+            return str(e)
+
+    taken, refused = [run(c) for c in calls], [run(c) for c in bad]
+    assert all(isinstance(t, torch.Tensor) for t in taken) and all(isinstance(t, str) for t in refused)
+    with monkeypatch.context() as m:
+        m.setattr(mk, "_fast", Python)
+        assert all(torch.equal(run(c), t) and run(c).dtype == t.dtype for c, t in zip(calls, taken))
+        assert [run(c) for c in bad] == refused
+    del taken
+    torch.cuda.synchronize()
+    held = torch.cuda.memory_allocated(), [sys.getrefcount(o) for o in (x, w, b, r, out, torch.bfloat16, torch.float32)]
+    for _ in range(100):
+        for c in calls + bad:
+            run(c)
+    assert (torch.cuda.memory_allocated(), [sys.getrefcount(o) for o in (x, w, b, r, out, torch.bfloat16, torch.float32)]) == held
+
+
 def test_no_rows():
     assert mk.linear(randn((0, 64), 1), randn((10, 64), 2)).shape == (0, 10)
 

@@ -79,3 +79,35 @@ def test_attend_refuses_null_and_takes_no_tokens():
     a = attend_args(q_lens=(0, 0), q=None, out=None)
     assert mk.lib.mk_attend_workspace(ctypes.byref(a)) == 0
     assert mk.lib.mk_attend(ctypes.byref(a), None, 0, None) == mk.MK_OK
+
+
+def test_operands_off_the_gpu_are_named():
+    torch = pytest.importorskip("torch")
+    x = torch.ones(2, 16, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="x must be a CUDA tensor"):
+        mk.linear(x, x)
+    kv = type("KV", (), dict(k=torch.ones(1, 1, 1, 8, 32, dtype=torch.bfloat16), v=torch.ones(1, 1, 1, 8, 32, dtype=torch.bfloat16)))
+    with pytest.raises(ValueError, match="q must be a CUDA tensor"):
+        mk.attend(torch.ones(1, 1, 32, dtype=torch.bfloat16), kv, [1], [8])
+    with pytest.raises(AttributeError):
+        mk.linear(None, x)
+
+
+def test_call_module_hands_over_what_it_does_not_take():
+    # nothing is kept or raised by a call that it leaves to Python
+    import sys
+    torch = pytest.importorskip("torch")
+    fast = mk._fast or mk._setup()
+    x = torch.ones(2, 16, dtype=torch.bfloat16)
+    linear = ((), (x,), (x, x, None, None, None, None, None, None), (1, 2, 3, 4, 5, 6, 7, 8), (x, x, x, "tanh", x, x, 5, x))
+    attend = ((), (x,) * 14, (x, x, x, [1], [2], 0, 0, 0, 0, None, None, None, None, None), (None,) * 14)
+
+    def counts():
+        return sys.getrefcount(x), sys.getrefcount(torch.bfloat16)
+
+    before = counts()
+    results = {id(f(*args)) for _ in range(50) for f, calls in ((fast.linear, linear), (fast.attend, attend)) for args in calls}
+    after = counts()
+    assert results == {id(None)} and after == before
+    with pytest.raises(TypeError):
+        fast.setup(1)
