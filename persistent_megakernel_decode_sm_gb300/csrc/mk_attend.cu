@@ -625,6 +625,13 @@ __global__ void __launch_bounds__(128) attend_merge_kernel(const __grid_constant
         return row * p.nq + head;
     };
     auto sync = [&]() { if (WARPS == 1) __syncwarp(); else __syncthreads(); };
+    const int e = t % kLanes * 4;
+    auto part = [&](int s) { return *reinterpret_cast<const float4*>(p.part_o + at(s) * D + e); };
+    constexpr int kAhead = 4;   // parts of o on their way while the weights are made
+    float4 ahead[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i)
+        if (t / kLanes + i * kGroups < n) ahead[i] = part(t / kLanes + i * kGroups);
     float M = -INFINITY;
     for (int s = t; s < n; s += kThreads) {
         const float2 ml = p.part_ml[at(s)];
@@ -655,18 +662,20 @@ __global__ void __launch_bounds__(128) attend_merge_kernel(const __grid_constant
         for (int w = 0; w < WARPS; ++w) L += red[r][1][w];
     }
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    const int e = t % kLanes * 4;
-#pragma unroll 4
-    for (int s = t / kLanes; s < n; s += kGroups) {
+    auto join = [&](int s, const float4& o) {
         const float w = weight[r][s];
-        const float4 o = *reinterpret_cast<const float4*>(p.part_o + at(s) * D + e);
         if (w > 0.f) {
             acc.x = fmaf(w, o.x, acc.x);
             acc.y = fmaf(w, o.y, acc.y);
             acc.z = fmaf(w, o.z, acc.z);
             acc.w = fmaf(w, o.w, acc.w);
         }
-    }
+    };
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i)
+        if (t / kLanes + i * kGroups < n) join(t / kLanes + i * kGroups, ahead[i]);
+#pragma unroll 4
+    for (int s = t / kLanes + kAhead * kGroups; s < n; s += kGroups) join(s, part(s));
     sums[r][t] = acc;
     sync();
     if (!live || t >= kLanes) return;
