@@ -632,8 +632,9 @@ __global__ void __launch_bounds__(128) attend_merge_kernel(const __grid_constant
 #pragma unroll
     for (int i = 0; i < kAhead; ++i)
         if (t / kLanes + i * kGroups < n) ahead[i] = part(t / kLanes + i * kGroups);
-    float M = -INFINITY;
-    for (int s = t; s < n; s += kThreads) {
+    const float2 own = t < n ? p.part_ml[at(t)] : make_float2(0.f, 0.f);
+    float M = own.y > 0.f ? own.x : -INFINITY;
+    for (int s = t + kThreads; s < n; s += kThreads) {
         const float2 ml = p.part_ml[at(s)];
         if (ml.y > 0.f) M = fmaxf(M, ml.x);
     }
@@ -647,7 +648,7 @@ __global__ void __launch_bounds__(128) attend_merge_kernel(const __grid_constant
     }
     float L = 0.f;
     for (int s = t; s < n; s += kThreads) {
-        const float2 ml = p.part_ml[at(s)];
+        const float2 ml = s == t ? own : p.part_ml[at(s)];
         const float w = ml.y > 0.f ? exp2_approx(ml.x - M) : 0.f;   // (a part without a key: its o may hold anything)
         weight[r][s] = w;
         if (w > 0.f) L = fmaf(w, ml.y, L);
