@@ -596,7 +596,6 @@ attend_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
 template <int D, int SEGS, int WARPS>
 __global__ void __launch_bounds__(128) attend_merge_kernel(const __grid_constant__ AttendParams<SEGS> p) {
     sm::pdl_trigger();
-    sm::pdl_wait();
     constexpr int kThreads = WARPS * 32, kLanes = D / 4, kGroups = kThreads / kLanes, kRows = 4 / WARPS;
     constexpr int kMaxParts = 512;   // a sequence's and the prefix's shares, 255 each at most
     __shared__ float weight[kRows][WARPS == 1 ? 64 : kMaxParts];
@@ -627,6 +626,7 @@ __global__ void __launch_bounds__(128) attend_merge_kernel(const __grid_constant
     auto sync = [&]() { if (WARPS == 1) __syncwarp(); else __syncthreads(); };
     const int e = t % kLanes * 4;
     auto part = [&](int s) { return *reinterpret_cast<const float4*>(p.part_o + at(s) * D + e); };
+    sm::pdl_wait();
     constexpr int kAhead = 4;   // parts of o on their way while the weights are made
     float4 ahead[kAhead];
 #pragma unroll
