@@ -425,7 +425,8 @@ mk_status mk_linear(const mk_linear_args* a, void* stream);
  * every one with window 0, else those with p > t - window or p < sinks.  Query head h reads KV head
  * h / (n_q_heads / n_kv_heads).
  *   out[token][h] = sum_p softmax_p(scale q[token][h] . K[p]) V[p]
- * A token without a visible position (t < 0: more query tokens than positions) gets zeros.
+ * A token without a visible position (t < 0: more query tokens than positions) gets zeros; a row with a NaN
+ * or +infinity among its scores, or with -infinity alone, is NaN as the formula is.
  *  q, out         bf16; sequences back to back, token r's heads at q + r * q_stride elements
  *                 ([n_q_heads, head_dim], q_stride a multiple of 8, 16-byte aligned); out
  *                 likewise.  out does not overlap q or the cache.  Tokens past the last sequence

@@ -4,6 +4,7 @@
 #include "mk_sm103.cuh"
 
 #include <algorithm>
+#include <cfloat>
 #include <climits>
 #include <cmath>
 
@@ -25,6 +26,9 @@ struct AttendSeg {
     int32_t merge0;        // tokens with parts to join in the segments before (a sequence's, not the prefix's)
 };
 constexpr int32_t kNoCausal = INT_MIN;
+// m of a part that sees no key, and of one whose scores are all -infinity (both have l = 0): a row of such
+// parts alone is zeros, or 0 / 0 with one of the second kind
+constexpr float kNoKeys = -INFINITY, kNoWeight = -FLT_MAX;
 constexpr int kBlockRows = 128;
 constexpr int attend_keys(int d) { return d == 128 ? 64 : 128; }   // keys of a tile
 
@@ -382,6 +386,7 @@ attend_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
         // counted, falls below 2^-20, is read again and its maximum becomes the reference.
         float m = 0.f, l = 0.f;
         bool set = false;   // some tile of this row counted
+        bool keys = false;  // the row sees a key of this share (its scores may all be -infinity)
         float high = live ? -INFINITY : INFINITY;   // (D < 128) a maximum above it is the new reference
         bool ok = true;     // (a wait that ran out shows at the vote of its tile: until then the lanes stay together)
         const int seen_end = causal ? t0 + 1 : seg.key1;   // keys that every row of the block sees: [seen_low, seen_end), the sinks
@@ -400,6 +405,7 @@ attend_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
             load(j);
             const uint32_t skip = p.table ? skips[j % T::kFlags] : 0u;
             const bool seen = skip == 0 && k0 + kKeys <= seen_end && (k0 >= seen_low || k0 + kKeys <= sinks);
+            keys = keys || seen;
             auto sees = [&](int at) {   // a bit for each of 32 keys from k0 + at: whether this row sees it
                 uint32_t see = low_bits(t - k0 - at + 1) & (~low_bits(low - k0 - at) | low_bits(sinks - k0 - at));
                 if (skip)
@@ -453,6 +459,7 @@ attend_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
 #pragma unroll
                     for (int q = 0; q < kQ; ++q) {
                         const uint32_t see = sees(q * 32);
+                        keys = keys || see != 0;
 #pragma unroll
                         for (int i = 0; i < 32; ++i)
                             if (!(see >> i & 1u)) s[q][i] = 0xFF800000u;
@@ -494,6 +501,7 @@ attend_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
 #pragma unroll
                     for (int q = 0; q < kQ; ++q) {
                         const uint32_t see = sees(q * 32);
+                        keys = keys || see != 0;
 #pragma unroll
                         for (int i = 0; i < 32; ++i)
                             if (!(see >> i & 1u)) s[q][i] = 0xFF800000u;
@@ -554,8 +562,9 @@ attend_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
             sm::tc_fence_after();
             const bool whole = seg.splits == 1 && !p.prefix_seg;   // no other item adds to this row
             const int64_t at = (int64_t(seg.part0) + int64_t(share) * seg.n + tok) * p.nq + head;
-            const float inv = l > 0.f ? 1.f / l : 0.f;
-            if (!whole && live) p.part_ml[at] = make_float2(m * c, l);
+            // a row without a key is zeros; one whose scores hold a NaN, or are all -infinity, is 0 / 0 as the formula has it
+            const float inv = 1.f / l;
+            if (!whole && live) p.part_ml[at] = make_float2(!keys ? kNoKeys : l == 0.f ? kNoWeight : m * c, l);
 #pragma unroll
             for (int i = 0; i < D; i += 32) {
                 uint32_t o[32];
@@ -573,7 +582,7 @@ attend_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
                     for (int e = 0; e < 32; e += 8) {
                         float x[8];
 #pragma unroll
-                        for (int k = 0; k < 8; ++k) x[k] = l > 0.f ? __uint_as_float(o[e + k]) * inv : 0.f;
+                        for (int k = 0; k < 8; ++k) x[k] = keys ? __uint_as_float(o[e + k]) * inv : 0.f;
                         dst[e / 8] = make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
                     }
                 } else {
@@ -590,7 +599,8 @@ attend_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
     if (warp == 5) sm::tmem_free(tmem, 256);
 }
 
-// Joins the parts of a row: with M = max m, out = sum 2^(m - M) o / sum 2^(m - M) l.  WARPS warps per row (token,
+// Joins the parts of a row: with M = max m, out = sum 2^(m - M) o / sum 2^(m - M) l; parts with l = 0 add nothing.
+// l is NaN where a score of the part is, and so is out then.  WARPS warps per row (token,
 // head): they load the rows' (m, l), then D / 4 threads a part's o, several parts at a time, and add their sums in a
 // fixed order.  A chain of memory latencies: many parts take four warps, which halve it against one, and the first parts' o is
 // on its way while the weights are made (one token over 8192 positions, both kernels: 8.8 us, 10.1 with o behind them).
@@ -633,12 +643,9 @@ __global__ void __launch_bounds__(128) attend_merge_kernel(const __grid_constant
 #pragma unroll
     for (int i = 0; i < kAhead; ++i)
         if (t / kLanes + i * kGroups < n) ahead[i] = part(t / kLanes + i * kGroups);
-    const float2 own = t < n ? p.part_ml[at(t)] : make_float2(0.f, 0.f);
-    float M = own.y > 0.f ? own.x : -INFINITY;
-    for (int s = t + kThreads; s < n; s += kThreads) {
-        const float2 ml = p.part_ml[at(s)];
-        if (ml.y > 0.f) M = fmaxf(M, ml.x);
-    }
+    const float2 own = t < n ? p.part_ml[at(t)] : make_float2(kNoKeys, 0.f);
+    float M = own.x;
+    for (int s = t + kThreads; s < n; s += kThreads) M = fmaxf(M, p.part_ml[at(s)].x);
 #pragma unroll
     for (int x = 16; x; x >>= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, x));
     if (WARPS > 1) {
@@ -650,9 +657,9 @@ __global__ void __launch_bounds__(128) attend_merge_kernel(const __grid_constant
     float L = 0.f;
     for (int s = t; s < n; s += kThreads) {
         const float2 ml = s == t ? own : p.part_ml[at(s)];
-        const float w = ml.y > 0.f ? exp2_approx(ml.x - M) : 0.f;   // (a part without a key: its o may hold anything)
+        const float w = ml.y != 0.f ? exp2_approx(ml.x - M) : 0.f;   // (a part without a key: its o may hold anything)
         weight[r][s] = w;
-        if (w > 0.f) L = fmaf(w, ml.y, L);
+        if (ml.y != 0.f) L = fmaf(w, ml.y, L);   // (NaN also where w is 0)
     }
 #pragma unroll
     for (int x = 16; x; x >>= 1) L += __shfl_xor_sync(0xFFFFFFFFu, L, x);
@@ -666,7 +673,7 @@ __global__ void __launch_bounds__(128) attend_merge_kernel(const __grid_constant
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     auto join = [&](int s, const float4& o) {
         const float w = weight[r][s];
-        if (w > 0.f) {
+        if (w != 0.f) {
             acc.x = fmaf(w, o.x, acc.x);
             acc.y = fmaf(w, o.y, acc.y);
             acc.z = fmaf(w, o.z, acc.z);
@@ -686,7 +693,7 @@ __global__ void __launch_bounds__(128) attend_merge_kernel(const __grid_constant
         const float4 o = sums[r][g * kLanes + t];
         acc.x += o.x; acc.y += o.y; acc.z += o.z; acc.w += o.w;
     }
-    const float inv = L > 0.f ? 1.f / L : 0.f;
+    const float inv = M > kNoKeys ? 1.f / L : 0.f;
     uint2* dst = reinterpret_cast<uint2*>(p.out + tok * p.out_stride + head * D + e);
     *dst = make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
 }
