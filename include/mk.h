@@ -476,7 +476,8 @@ mk_status mk_attend(const mk_attend_args* a, void* workspace, size_t workspace_b
  * once (RMSNorm, mk_linear for the projections, RoPE, mk_attend, SwiGLU), where the decode step takes one.
  * The caller leaves each sequence's last prompt token to a decode step, which gives its logits and the next
  * token; nothing of the last layer but its K and V is computed here.  A long prompt may be given in pieces.
- *  tokens         HOST int32[sum n_tokens], in [0, vocab): the sequences' tokens back to back
+ *  tokens         HOST int32[sum n_tokens], in [0, vocab): the sequences' tokens back to back (as the other host
+ *                 arrays read before the call returns, page-locked or not)
  *  n_tokens, pos  HOST int32[batch]: tokens of each sequence (0: none), and the position of its first;
  *                 its cache holds the positions before; pos + n_tokens <= max_seq (the schedule's KV windows
  *                 bound decode steps only)

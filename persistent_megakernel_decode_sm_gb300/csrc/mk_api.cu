@@ -862,8 +862,6 @@ extern "C" mk_status mk_prefill(mk_ctx* c, const int32_t* tokens, const int32_t*
     rows.status = p.err;
     r.attend.q = q;
     r.attend.out = o;
-    // (pageable memory: the copy has read `tokens` when the call returns)
-    CK(cudaMemcpyAsync(d_tokens, tokens, size_t(T) * 4, cudaMemcpyHostToDevice, c->stream));
     auto linear = [&](const void* in, int32_t k, const void* w, int32_t n, int32_t act, const void* residual, int32_t dtype, void* out) {
         mk_linear_args a{};
         a.rows = T; a.n = n; a.k = k; a.activation = act;
@@ -875,7 +873,8 @@ extern "C" mk_status mk_prefill(mk_ctx* c, const int32_t* tokens, const int32_t*
         return mk_linear(&a, c->stream);
     };
     // a failure from here on leaves the cache rows of the call's tokens in an unknown state, nothing else
-    st = prefill_norm(x, d_tokens, c->w.embed, c->w.attn_norm[0], xn, T, H, p.rms_eps, c->stream);
+    st = prefill_tokens(tokens, T, d_tokens, c->stream);
+    if (st == MK_OK) st = prefill_norm(x, d_tokens, c->w.embed, c->w.attn_norm[0], xn, T, H, p.rms_eps, c->stream);
     for (int l = 0; l < p.L && st == MK_OK; ++l) {
         st = linear(xn, H, c->w.wqkv[l], p.nqkv, MK_ACT_NONE, nullptr, MK_F32, qkv);
         rows.k = reinterpret_cast<__nv_bfloat16*>(p.kc) + l * p.kv_lstride;

@@ -103,6 +103,7 @@ struct PrefillRows {
     int32_t block, max_blocks, n_blocks;
     int32_t* status;
 };
+mk_status prefill_tokens(const int32_t* tokens, int64_t n, int32_t* out, cudaStream_t stream);   // (HOST tokens, read before it returns)
 mk_status prefill_norm(float* x, const int32_t* tokens, const void* embed, const void* gain, void* y, int64_t rows, int H,
                        float eps, cudaStream_t stream);
 mk_status prefill_rope_append(const float* qkv, void* q, const PrefillRows& rows, int64_t tokens, cudaStream_t stream);

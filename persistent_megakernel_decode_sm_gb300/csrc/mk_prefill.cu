@@ -1,9 +1,27 @@
-// The small kernels of the prompt path (mk_prefill): token embedding, RMSNorm, and the rotation of
-// q and k with the append of k and v to the cache.  Each reads and writes its rows once: bytes bound them.
+// The small kernels of the prompt path (mk_prefill): host tokens to the device, token embedding, RMSNorm, and
+// the rotation of q and k with the append of k and v to the cache.  Each reads and writes its rows once: bytes bound them.
+#include <algorithm>
+#include <cstring>
+
 #include "mk_ops.h"
 #include "mk_sm103.cuh"
 
 namespace mk {
+
+// A piece of the call's host tokens, read by the launch itself, whatever memory the caller keeps them in (a copy
+// from page-locked memory would read them after the call has returned).  4 KB a launch: the size that every launch
+// may have; 5 of them for 4096 tokens.
+struct TokenPiece {
+    int32_t n;
+    int32_t token[1000];
+};
+constexpr int kTokenPiece = int(sizeof(TokenPiece::token) / sizeof(int32_t));
+__global__ void __launch_bounds__(256) tokens_kernel(int32_t* out, const __grid_constant__ TokenPiece p) {
+    sm::pdl_trigger();
+    sm::pdl_wait();
+    const int i = blockIdx.x * blockDim.x + threadIdx.x;
+    if (i < p.n) out[i] = p.token[i];
+}
 
 constexpr int kNormThreads = 256;
 
@@ -141,6 +159,16 @@ static mk_status prefill_launch(void (*fn)(Args...), int64_t blocks, cudaStream_
     return MK_OK;
 }
 
+mk_status prefill_tokens(const int32_t* tokens, int64_t n, int32_t* out, cudaStream_t stream) {
+    for (int64_t at = 0; at < n; at += kTokenPiece) {
+        TokenPiece p{};
+        p.n = int32_t(std::min<int64_t>(kTokenPiece, n - at));
+        std::memcpy(p.token, tokens + at, size_t(p.n) * sizeof(int32_t));
+        const mk_status st = prefill_launch(&tokens_kernel, (p.n + 255) / 256, stream, out + at, p);
+        if (st != MK_OK) return st;
+    }
+    return MK_OK;
+}
 mk_status prefill_norm(float* x, const int32_t* tokens, const void* embed, const void* gain, void* y, int64_t rows, int H,
                        float eps, cudaStream_t stream) {
     return prefill_launch(&norm_kernel, rows, stream, x, tokens, static_cast<const __nv_bfloat16*>(embed),
