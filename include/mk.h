@@ -364,7 +364,7 @@ mk_status mk_decode_persistent_wait(mk_ctx* c, int32_t* steps_done, int32_t* tok
 
 /* Asynchronous form: enqueues one step on the bound stream and returns.  next_tokens_dev is a
  * DEVICE int32[batch] buffer or NULL.  Device-side errors surface at the next mk_ctx_status or
- * mk_decode_step. */
+ * synchronous step. */
 mk_status mk_launch_step(mk_ctx* c, const int32_t* tokens, const int32_t* pos, float* logits,
                          int32_t* next_tokens_dev);
 
@@ -487,8 +487,9 @@ mk_status mk_attend(const mk_attend_args* a, void* workspace, size_t workspace_b
  *  workspace      mk_prefill_workspace bytes of device memory, 256-byte aligned
  * Activations between operators are bf16 (the residual stream, q k v before rotation and all sums fp32), so K and V
  * agree with the decode step's to bf16 rounding of their inputs.  Enqueued on the bound stream, on the current device;
- * device-side errors surface at the next mk_ctx_status or mk_decode_step.  Not capturable into a graph (it copies the
- * host tokens).  Errors: MK_ERR_ARG (also: a paged cache with blocks that are not a multiple of 8 positions),
+ * device-side errors surface at the next mk_ctx_status or synchronous step (mk_decode_step_static included).  Not
+ * capturable into a graph (its tokens are the host's).  Errors: MK_ERR_ARG (also: a paged cache with blocks that are not
+ * a multiple of 8 positions),
  * MK_ERR_CAPACITY (workspace), MK_ERR_POISONED, MK_ERR_CUDA; on the device MK_ERR_BOUNDS, MK_ERR_TIMEOUT. */
 size_t mk_prefill_workspace(mk_ctx* c, const int32_t* n_tokens, const int32_t* pos, int32_t shared_prefix);
 mk_status mk_prefill(mk_ctx* c, const int32_t* tokens, const int32_t* n_tokens, const int32_t* pos, int32_t shared_prefix,

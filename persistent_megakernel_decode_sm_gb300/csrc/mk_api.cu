@@ -42,13 +42,14 @@ struct mk_ctx {
     int32_t* d_queues;
     uint32_t* d_totals;
     LayerPtrs* d_layers;
-    int32_t* h_result;   // pinned: err[16] then tokens[8]
+    int32_t* h_result;   // pinned: err[16] then tokens[8]; from word 32 the bound scratch's err[8]
     uint32_t epoch;
     bool poisoned;
     // a step ran on the static scratch: the bound scratch's activation words did not advance with
     // the epoch (the 3-bit SwiGLU tag repeats every 7 steps), so it is cleared before its next use
     bool bound_stale;
     const int32_t* last_err;   // error word of the last launched step (bound or static scratch)
+    bool bound_unread;         // work enqueued on the bound scratch since its error word was last read
     uint8_t* d_tmaps;          // batch > 1: the weights' TMA tensor maps
     uint32_t* d_step_bar;      // grid-wide step word: each CTA adds 1 per step it retires
     volatile int32_t* h_ctl;   // mapped pinned words: [0] stop request (host), [1] steps done (device)
@@ -560,6 +561,7 @@ static mk_status launch_params(mk_ctx* c, Params& p) {
         return fail(MK_ERR_RESOURCES, "cooperative launch of %d CTAs does not fit the device", c->grid);
     if (e != cudaSuccess) return cuda_fail(e, "cudaLaunchCooperativeKernel");
     c->last_err = p.err;
+    c->bound_unread = c->bound_unread || p.err == c->base.err;
     c->epoch += 1;
     return MK_OK;
 }
@@ -611,22 +613,29 @@ extern "C" mk_status mk_launch_step(mk_ctx* c, const int32_t* tokens, const int3
 }
 
 // Reads back the error word (and output tokens) of the context's last step -- from the scratch
-// that step used -- and poisons the context on a device error.
+// that step used, behind it the bound scratch's where a prompt or a step ran on it unread -- and poisons
+// the context on a device error.
 static mk_status read_status(mk_ctx* c, int32_t* info) {
+    constexpr int kBound = 32;   // (words; h_result has 64)
+    const bool both = c->bound_unread && c->last_err != c->base.err;
     cudaError_t e = cudaMemcpyAsync(c->h_result, c->last_err, 96, cudaMemcpyDeviceToHost, c->stream);
+    if (e == cudaSuccess && both)
+        e = cudaMemcpyAsync(c->h_result + kBound, c->base.err, 32, cudaMemcpyDeviceToHost, c->stream);
     if (e == cudaSuccess) e = cudaStreamSynchronize(c->stream);
     if (e != cudaSuccess) {
         c->poisoned = true;
         return cuda_fail(e, "step readback");
     }
+    c->bound_unread = false;
+    const int32_t* r = both && c->h_result[kBound] ? c->h_result + kBound : c->h_result;   // (the earlier error)
     if (info)
-        for (int i = 0; i < 8; ++i) info[i] = c->h_result[i];
-    const int code = c->h_result[0];
+        for (int i = 0; i < 8; ++i) info[i] = r[i];
+    const int code = r[0];
     if (code != 0) {
         c->poisoned = true;
+        c->bound_unread = r != c->h_result;   // (a later mk_ctx_status finds it again)
         return fail(mk_status(code), "device error %d (CTA %d, queue slot %d, counter %d, seen %d, wanted %d, role %d)",
-                    code, c->h_result[1], c->h_result[2], c->h_result[3], c->h_result[4], c->h_result[5],
-                    c->h_result[6]);
+                    code, r[1], r[2], r[3], r[4], r[5], r[6]);
     }
     return MK_OK;
 }
@@ -873,6 +882,8 @@ extern "C" mk_status mk_prefill(mk_ctx* c, const int32_t* tokens, const int32_t*
         return mk_linear(&a, c->stream);
     };
     // a failure from here on leaves the cache rows of the call's tokens in an unknown state, nothing else
+    c->last_err = p.err;
+    c->bound_unread = true;
     st = prefill_tokens(tokens, T, d_tokens, c->stream);
     if (st == MK_OK) st = prefill_norm(x, d_tokens, c->w.embed, c->w.attn_norm[0], xn, T, H, p.rms_eps, c->stream);
     for (int l = 0; l < p.L && st == MK_OK; ++l) {
@@ -889,7 +900,6 @@ extern "C" mk_status mk_prefill(mk_ctx* c, const int32_t* tokens, const int32_t*
         if (st == MK_OK) st = linear(h, F, c->w.wdown[l], H, MK_ACT_NONE, x, MK_F32, x);
         if (st == MK_OK) st = prefill_norm(x, nullptr, nullptr, c->w.attn_norm[l + 1], xn, T, H, p.rms_eps, c->stream);
     }
-    if (st == MK_OK) c->last_err = p.err;
     return st;
 }
 
