@@ -385,7 +385,7 @@ typedef enum { MK_BF16 = 0, MK_F32 = 1 } mk_dtype;
 typedef enum {
     MK_ACT_NONE = 0,
     MK_ACT_SILU = 1,     /* y / (1 + exp(-y))                                                 */
-    MK_ACT_GELU = 2,     /* y (1 + erf(y / sqrt 2)) / 2                                       */
+    MK_ACT_GELU = 2,     /* y (1 + erf(y / sqrt 2)) / 2 (to fp32's precision at either end)   */
     MK_ACT_SWIGLU = 3    /* silu(gate) * up: w has 2 n rows, the n gate rows then the n up rows */
 } mk_activation;
 

@@ -18,14 +18,33 @@ struct LinearParams {
     int32_t* status;
 };
 
+// y Phi(y) by the lower tail Q(a) = Phi(-a), a = |y|: y Q for y < 0, y (1 - Q) else, so nothing cancels (1 + erf does,
+// below -1; erfcf takes 1.2 us more for 333 x 1001 outputs than this and erff).  Q = exp(-a^2 / 2) t P(t) with
+// t = 1 / (1 + 0.34 a): exp(a^2 / 2) Q(a) falls like 1 / a, so P is smooth over all of it.  P is the least-squares fit of
+// degree 8 over a in [0, 14], its points reweighted towards equal errors: off by 3e-8 of the value, 4e-7 evaluated in fp32.
+__device__ __forceinline__ float linear_gelu(float y) {
+    const float a = fabsf(y);
+    float t, e;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(t) : "f"(fmaf(a, 0.34f, 1.f)));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(a * a * -0.72134752f));   // (log2(e) / 2)
+    float q = -0.0261204801f;
+    q = fmaf(q, t, 0.139499515f);
+    q = fmaf(q, t, -0.273132801f);
+    q = fmaf(q, t, 0.202182725f);
+    q = fmaf(q, t, -0.0447184853f);
+    q = fmaf(q, t, 0.115359172f);
+    q = fmaf(q, t, 0.115197659f);
+    q = fmaf(q, t, 0.136112198f);
+    q = fmaf(q, t, 0.135620505f);
+    q = q * t * e;
+    return y * (y < 0.f ? q : 1.f - q);
+}
 // y and the up factor of one output, bias included, to the value before the residual, in fp32
 __device__ __forceinline__ float linear_act(int act, float y, float up) {
-    switch (act) {
-        case MK_ACT_SILU: return y / (1.f + expf(-y));
-        case MK_ACT_GELU: return 0.5f * y * (1.f + erff(y * 0.70710678118654752f));
-        case MK_ACT_SWIGLU: return y / (1.f + expf(-y)) * up;
-        default: return y;
-    }
+    if (act == MK_ACT_NONE) return y;
+    if (act == MK_ACT_GELU) return linear_gelu(y);
+    const float s = y / (1.f + expf(-y));
+    return act == MK_ACT_SWIGLU ? s * up : s;
 }
 // The residuals of the tokens r, r + 1, .. of feature j, of which `left` exist (zeros where not wanted)
 template <int N>
