@@ -433,7 +433,8 @@ mk_status mk_linear(const mk_linear_args* a, void* stream);
  *                 are not touched.
  *  q_lens,        HOST int32[batch], each >= 0; kv_lens[b] <= max_seq
  *  kv_lens
- *  kv, layer      the cache and the layer to read; positions a token does not see are never used,
+ *  kv, layer      the cache and the layer to read (a stride counts where there is a second sequence, layer or
+ *                 head for it to reach); positions a token does not see are never used,
  *                 whatever they hold, apart from this: a position that one token of a block of 128 / (n_q_heads
  *                 / n_kv_heads) neighbouring tokens sees must hold finite values
  *  max_seq        positions per (sequence, head) of a contiguous cache, or the most positions a

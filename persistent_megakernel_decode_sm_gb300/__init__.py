@@ -607,13 +607,12 @@ def attend(q, kv, q_lens: Sequence[int], kv_lens: Sequence[int], layer: int = 0,
             (ks[-2] != d and shape[-2] > 1)):
         raise ValueError("kv.k and kv.v must be alike (shape, strides, type, device), with contiguous [positions, head_dim] rows of q's head_dim")
     layers, nkv, positions = shape[-4:-1]
-    head_stride = ks[-3] if nkv > 1 else max(ks[-3], positions * d)   # (a single head's stride says nothing)
     if not 0 <= layer < layers:
         raise ValueError(f"layer {layer} of {layers}")
     if pages is None:
         if shape[0] < batch:
             raise ValueError(f"the cache holds {shape[0]} sequences, q_lens name {batch}")
-        cache = array.array("q", (k.data_ptr(), v.data_ptr(), ks[0], ks[1], head_stride))
+        cache = array.array("q", (k.data_ptr(), v.data_ptr(), ks[0], ks[1], ks[2]))
     else:
         table, block_size, n_blocks = pages
         tshape, ts = _operand(table, "the block table", (torch.int32,), dev, 2)
@@ -621,7 +620,7 @@ def attend(q, kv, q_lens: Sequence[int], kv_lens: Sequence[int], layer: int = 0,
             raise ValueError(f"the block table must be contiguous, with a row for each of {batch} sequences")
         if block_size < 1 or n_blocks < 1 or positions < n_blocks * block_size:
             raise ValueError(f"the pool holds {positions} positions a head, {n_blocks} blocks of {block_size} do not fit it")
-        cache = array.array("q", (k.data_ptr(), v.data_ptr(), 0, ks[0], head_stride,
+        cache = array.array("q", (k.data_ptr(), v.data_ptr(), 0, ks[0], ks[1],
                                   table.data_ptr(), block_size | tshape[1] << 32, n_blocks))
         positions = tshape[1] * block_size
     lens = array.array("i", [*q_lens, *kv_lens])

@@ -728,6 +728,14 @@ static mk_status attend_check_shape(const mk_attend_args* a) {
     return MK_OK;
 }
 
+// Positions of a head in the cache, and the elements from one head to the next
+static int64_t attend_positions(const mk_attend_args* a) {
+    return a->pages ? int64_t(a->pages->n_blocks) * a->pages->block_size : a->max_seq;
+}
+static int64_t attend_head_stride(const mk_attend_args* a) {
+    return a->n_kv_heads > 1 ? a->kv->head_stride : attend_positions(a) * a->head_dim;
+}
+
 static mk_status attend_check(const mk_attend_args* a) {
     const mk_status st = attend_check_shape(a);
     if (st != MK_OK) return st;
@@ -737,7 +745,10 @@ static mk_status attend_check(const mk_attend_args* a) {
     if (!op_aligned(a->kv->k, 16) || !op_aligned(a->kv->v, 16)) return fail(MK_ERR_ARG, "attend: KV pointers must be 16-byte aligned");
     const int64_t d = a->head_dim, ql = int64_t(a->n_q_heads) * d;
     const mk_kv& kv = *a->kv;
-    if (kv.head_stride % 8 || kv.layer_stride % 8 || kv.batch_stride % 8 || kv.layer_stride < 0)
+    // (a stride counts where there is a second head, sequence or layer to reach)
+    const bool batched = !a->pages && a->batch > 1;
+    if ((a->n_kv_heads > 1 && kv.head_stride % 8) || (a->layer > 0 && (kv.layer_stride % 8 || kv.layer_stride < 0)) ||
+        (batched && kv.batch_stride % 8))
         return fail(MK_ERR_ARG, "attend: KV strides must be multiples of 8 elements");
     if (a->pages) {
         const mk_kv_pages& pg = *a->pages;
@@ -745,12 +756,10 @@ static mk_status attend_check(const mk_attend_args* a) {
         if (pg.block_size < 8 || pg.block_size % 8 || pg.n_blocks < 1 || pg.max_blocks < 1 ||
             int64_t(pg.n_blocks) * pg.block_size > INT_MAX || int64_t(pg.max_blocks) * pg.block_size < a->max_seq)
             return fail(MK_ERR_ARG, "attend: blocks of a multiple of 8 positions, a table that covers max_seq");
-        if (kv.head_stride < int64_t(pg.n_blocks) * pg.block_size * d)
-            return fail(MK_ERR_ARG, "attend: KV strides must cover the pool per head");
-    } else if (kv.head_stride < a->max_seq * d || (a->batch > 1 && kv.batch_stride < kv.head_stride * a->n_kv_heads) ||
-               (a->layer > 0 && kv.layer_stride < kv.head_stride * a->n_kv_heads)) {
-        return fail(MK_ERR_ARG, "attend: KV strides must cover [max_seq, head_dim] per head");
     }
+    const int64_t rows = attend_positions(a) * d, heads = attend_head_stride(a) * (a->n_kv_heads - 1) + rows;   // elements of a head, of a layer
+    if (attend_head_stride(a) < rows || (batched && kv.batch_stride < heads) || (!a->pages && a->layer > 0 && kv.layer_stride < heads))
+        return fail(MK_ERR_ARG, "attend: KV strides must cover a head's positions, its sequence's and its layer's heads");
     if (tokens == 0) return MK_OK;
     if (!a->q || !a->out || !op_aligned(a->q, 16) || !op_aligned(a->out, 16) || !op_aligned(a->status, 4))
         return fail(MK_ERR_ARG, "attend: q and out must be 16-byte aligned");
@@ -758,7 +767,7 @@ static mk_status attend_check(const mk_attend_args* a) {
         return fail(MK_ERR_ARG, "attend: q and out strides must be multiples of 8 and cover the heads");
     const RowSpan out{a->out, tokens, ql * 2, a->out_stride * 2};
     if (spans_overlap(out, {a->q, tokens, ql * 2, a->q_stride * 2})) return fail(MK_ERR_ARG, "attend: out overlaps q");
-    const int64_t cached = a->layer * kv.layer_stride + (a->pages ? 0 : (a->batch - 1) * kv.batch_stride) + a->n_kv_heads * kv.head_stride;
+    const int64_t cached = (a->layer > 0 ? a->layer * kv.layer_stride : 0) + (batched ? (a->batch - 1) * kv.batch_stride : 0) + heads;
     if (spans_overlap(out, {kv.k, 1, cached * 2, 0}) || spans_overlap(out, {kv.v, 1, cached * 2, 0}))
         return fail(MK_ERR_ARG, "attend: out overlaps the cache");
     return MK_OK;
@@ -885,10 +894,9 @@ static mk_status attend_launch(const mk_attend_args* a, const AttendCommon& comm
     const int64_t qs = pl.tokens == 1 ? int64_t(p.nq) * D : a->q_stride;
     const cuuint64_t qd[3] = {cuuint64_t(D), cuuint64_t(p.nq), cuuint64_t(pl.tokens)}, qst[2] = {cuuint64_t(D) * 2, cuuint64_t(qs) * 2};
     const cuuint32_t qb[3] = {T::kSub, cuuint32_t(p.group), cuuint32_t(p.block_tokens)};
-    const int64_t positions = a->pages ? int64_t(a->pages->n_blocks) * a->pages->block_size : a->max_seq;
-    const int64_t seqs = a->pages ? 1 : a->batch, bs = seqs > 1 ? kv.batch_stride : kv.head_stride * p.nkv;
-    const cuuint64_t kd[4] = {cuuint64_t(D), cuuint64_t(positions), cuuint64_t(p.nkv), cuuint64_t(seqs)};
-    const cuuint64_t kst[3] = {cuuint64_t(D) * 2, cuuint64_t(kv.head_stride) * 2, cuuint64_t(bs) * 2};
+    const int64_t seqs = a->pages ? 1 : a->batch, hs = attend_head_stride(a), bs = seqs > 1 ? kv.batch_stride : hs;
+    const cuuint64_t kd[4] = {cuuint64_t(D), cuuint64_t(attend_positions(a)), cuuint64_t(p.nkv), cuuint64_t(seqs)};
+    const cuuint64_t kst[3] = {cuuint64_t(D) * 2, cuuint64_t(hs) * 2, cuuint64_t(bs) * 2};
     const cuuint32_t kb[4] = {T::kSub, cuuint32_t(p.table ? 1 << p.box_log2 : T::kKeys), 1, 1};
     const int64_t off = int64_t(a->layer) * kv.layer_stride;
     if ((st = op_tensor_map(&mq, a->q, 3, qd, qst, qb)) != MK_OK) return st;

@@ -218,7 +218,7 @@ static PyObject* call_attend(PyObject* self, PyObject* const* arg, Py_ssize_t n_
     kv.k = (void*)vk.ptr;
     kv.v = (void*)vv.ptr;
     kv.layer_stride = stride[0];
-    kv.head_stride = shape[1] > 1 || stride[1] > positions * d ? stride[1] : positions * d;   /* (one head's says nothing) */
+    kv.head_stride = stride[1];
     if (pages == Py_None) {
         if (vk.shape[0] < batch) return leave(NULL);
         kv.batch_stride = vk.stride[0];
