@@ -19,6 +19,7 @@ from __future__ import annotations
 
 import array
 import ctypes
+import importlib.util
 import os
 import struct
 from typing import List, Optional, Sequence
@@ -31,7 +32,8 @@ LIB_PATH = os.path.join(_HERE, "libmk.so")
 if not os.path.exists(LIB_PATH):
     raise ImportError(f"{LIB_PATH} is missing: build it first (python -c 'import __graft_entry__ as g; g.build()')")
 lib = ctypes.CDLL(LIB_PATH)
-from . import _mk_call   # noqa: E402  (built with the library; a missing one raises here)
+# Built where Python's headers are: without it linear() and attend() make their calls from Python.
+_mk_call = importlib.import_module("._mk_call", __name__) if importlib.util.find_spec(__name__ + "._mk_call") else None
 
 MK_OK, MK_ERR_ARG, MK_ERR_CAPACITY, MK_ERR_RESOURCES, MK_ERR_CUDA, MK_ERR_TIMEOUT, MK_ERR_OPCODE, \
     MK_ERR_BOUNDS, MK_ERR_POISONED = range(9)
@@ -478,11 +480,22 @@ def _operand(t, name, dtypes, device, dim):
     return shape, strides
 
 
+class _NoCallModule:   # (leaves every call to Python)
+    @staticmethod
+    def linear(*args):
+        return None
+
+    attend = linear
+
+
 _fast = None   # _mk_call, once it has torch's objects
 
 
 def _setup():
     global _fast
+    if _mk_call is None:
+        _fast = _NoCallModule
+        return _fast
     import torch
     c = torch._C
     _mk_call.setup(*(ctypes.cast(f, _P).value for f in (lib.mk_linear, lib.mk_attend, lib.mk_attend_workspace)), torch.bfloat16,

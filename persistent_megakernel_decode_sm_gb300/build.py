@@ -8,8 +8,9 @@ Translation units compiled in parallel and linked into one shared library:
   csrc/mk_linear.cu  the linear map with a fused epilogue (prompt path)
   csrc/mk_attend.cu  attention of query tokens over the KV cache (prompt path)
   csrc/mk_prefill.cu embedding, RMSNorm, RoPE and KV append of the prompt path
-and beside it, with the host's C compiler, the Python module _mk_call.so:
+and beside it, with the host's C compiler, the Python module _mk_call, named for the interpreter it is built for:
   csrc/mk_python.c   argument handling of linear() and attend()
+Where Python's headers are missing the module is left out, and that is done in Python.
 """
 from __future__ import annotations
 
@@ -18,14 +19,14 @@ import subprocess
 import sys
 import sysconfig
 from concurrent.futures import ThreadPoolExecutor
-from typing import List
+from typing import List, Optional
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libmk.so")
-CALL_SOURCE, CALL = os.path.join(CSRC, "mk_python.c"), os.path.join(HERE, "_mk_call.so")
+CALL_SOURCE, CALL = os.path.join(CSRC, "mk_python.c"), os.path.join(HERE, "_mk_call" + (sysconfig.get_config_var("EXT_SUFFIX") or ".so"))
 BUILD_DIR = os.path.join(HERE, "_build")
 SOURCES = ["mk_sched.cpp", "mk_api.cu", "mk_kernel.cu", "mk_kernel_batch.cu", "mk_linear.cu", "mk_attend.cu",
            "mk_prefill.cu"]
@@ -46,10 +47,16 @@ def _inputs() -> List[str]:
     return files
 
 
+def _python_headers() -> Optional[str]:
+    path = sysconfig.get_paths()["include"]
+    return path if os.path.exists(os.path.join(path, "Python.h")) else None
+
+
 def up_to_date() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(CALL):
+    built = [LIB, CALL] if _python_headers() else [LIB]
+    if not all(os.path.exists(f) for f in built):
         return False
-    t = min(os.path.getmtime(LIB), os.path.getmtime(CALL))
+    t = min(os.path.getmtime(f) for f in built)
     return all(os.path.getmtime(f) <= t for f in _inputs())
 
 
@@ -76,8 +83,15 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
         return obj
 
     def compile_call() -> None:
+        old = os.path.join(HERE, "_mk_call.so")   # (a module without a tag would load in any interpreter)
+        if old != CALL and os.path.exists(old):
+            os.remove(old)
+        headers = _python_headers()
+        if not headers:
+            sys.stderr.write("Python.h not found: linear() and attend() take their arguments in Python\n")
+            return
         tmp = CALL + f".{os.getpid()}.tmp"
-        r = subprocess.run([os.environ.get("CC", "gcc"), "-O2", "-Wall", "-shared", "-fPIC", f"-I{sysconfig.get_paths()['include']}",
+        r = subprocess.run([os.environ.get("CC", "gcc"), "-O2", "-Wall", "-shared", "-fPIC", f"-I{headers}",
                             f"-I{INCLUDE}", CALL_SOURCE, "-o", tmp], capture_output=True, text=True)
         if r.returncode != 0:
             raise RuntimeError(f"C compiler failed on mk_python.c:\n{r.stdout}\n{r.stderr}")
