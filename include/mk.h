@@ -380,7 +380,8 @@ mk_status mk_ctx_status(mk_ctx* c, int32_t* info);
  * allocate nothing and synchronise nothing, so they can be captured into a CUDA graph; what they
  * take from host memory (argument structs, lengths) is read before the call returns.  `status`
  * (where an argument struct has it) is an optional DEVICE int32 that receives an mk_status when the
- * device meets an error (it is left alone otherwise; the caller zeroes it first). */
+ * device meets an error (it is left alone otherwise; the caller zeroes it first); without it such an
+ * error leaves no trace.  A wait inside these kernels runs out after 2 s, whatever mk_set_timeout says. */
 typedef enum { MK_BF16 = 0, MK_F32 = 1 } mk_dtype;
 typedef enum {
     MK_ACT_NONE = 0,

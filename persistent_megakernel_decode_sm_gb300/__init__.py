@@ -456,8 +456,8 @@ class Decoder:
 # A call's host time counts beside kernels of a few microseconds, so the common call is checked and made in C
 # (csrc/mk_python.c).  What that does not take comes here: the same checks, which say what is wrong, and calls
 # for another device than the current one.  Argument structs are packed in one go (native alignment, the layouts
-# of mk_linear_args and mk_attend_args).  They record no
-# gradients, whatever their operands' requires_grad: the framework runs models, it does not train them.
+# of mk_linear_args and mk_attend_args).  They record no gradients, whatever their operands' requires_grad: the
+# framework runs models, it does not train them.
 
 _LINEAR_ARGS = struct.Struct("@4iPqPPPq2iPqP")
 _ATTEND_ARGS = struct.Struct("@4iPPPqPqPP5ifP")
@@ -534,7 +534,11 @@ def linear(x, weight, bias=None, activation: Optional[str] = None, residual=None
     contiguous -- [2 n, k] with activation "swiglu": n gate rows, then n up rows, silu(gate) * up --
     bias bf16 [n] ([2 n]), residual bf16 or fp32 [rows, n] (or an expanded row).  activation: None,
     "silu", "gelu" (the erf form) or "swiglu".  out: a bf16 or fp32 [rows, n] tensor, which may be
-    the residual itself; by default one of out_dtype (bf16) is allocated.  Returns out."""
+    the residual itself; by default one of out_dtype (bf16) is allocated.  Returns out.
+
+    status: a CUDA int32 tensor of one element, zeroed by the caller, that receives an mk_status when the
+    device meets an error (MK_ERR_TIMEOUT: out is not valid).  Without it such an error leaves no trace.
+    No gradients are recorded."""
     y = (_fast or _setup()).linear(x, weight, bias, activation, residual, out, out_dtype, status)
     if y is not None:
         return y
@@ -589,7 +593,12 @@ def attend(q, kv, q_lens: Sequence[int], kv_lens: Sequence[int], layer: int = 0,
     pages = (block_table, block_size, n_blocks).  A token at position t sees positions p <= t; with a
     window those with p > t - window or p < sinks.  shared_prefix: the first positions, the same
     for every sequence, read once through sequence 0.  out: bf16, shaped like q (allocated by
-    default); workspace: at least attend_workspace bytes (allocated by default).  Returns out."""
+    default; rows behind the last sequence's are not written); workspace: at least mk_attend_workspace
+    bytes (allocated by default).  Returns out.
+
+    status: a CUDA int32 tensor of one element, zeroed by the caller, that receives an mk_status when the
+    device meets an error: MK_ERR_BOUNDS (a table entry outside the pool; its positions count as not visible) or
+    MK_ERR_TIMEOUT (out is not valid).  Without it such an error leaves no trace.  No gradients are recorded."""
     o = (_fast or _setup()).attend(q, kv.k, kv.v, q_lens, kv_lens, layer, window, sinks, shared_prefix, scale, pages, out, workspace,
                                    status)
     if o is not None:

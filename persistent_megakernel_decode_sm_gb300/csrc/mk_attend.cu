@@ -34,7 +34,7 @@ constexpr int attend_keys(int d) { return d == 128 ? 64 : 128; }   // keys of a 
 
 struct AttendCommon {
     int32_t nq, nkv, group, block_tokens;   // block_tokens: query tokens of a block, 128 / group
-    int32_t tokens, segs, prefix_seg;       // prefix_seg: 1 where segment 0 is the shared prefix
+    int32_t segs, prefix_seg;               // prefix_seg: 1 where segment 0 is the shared prefix
     int32_t merge_tokens;                   // tokens with parts to join
     int32_t window, sinks;
     float scale_log2;                       // scale / ln 2
@@ -98,8 +98,9 @@ struct AttendTile {
     static constexpr int kPlaces = kShareSP ? 2 : 1;
     static constexpr int kS = 0, kO = 128, kP = kShareSP ? 0 : 192;
     // rows are divided by the sum of their weights as rounded, which cancels the rounding of a weight that
-    // outweighs the others -- but at D = 64, where that took 9% (97 us against 89; 4096 tokens, causal, 1B heads) and the
-    // reference is a maximum, so that such a weight is a power of two or near it
+    // outweighs the others -- but at D = 64, where that took 9% (97 us against 89; 4096 tokens, causal, 1B heads).  There
+    // such a weight is 1 where its key is the maximum of the reference's tile; in a later tile it can be anything up to
+    // 2^8, and its rounding, half a bf16 step at most, stays in the row beside the output's own.
     static constexpr bool kRoundedSum = D != 64;
 };
 
@@ -968,7 +969,7 @@ extern "C" mk_status mk_attend(const mk_attend_args* a, void* workspace, size_t 
         return fail(MK_ERR_CAPACITY, "attend: workspace of %zu bytes, %zu needed (mk_attend_workspace)", workspace_bytes, need);
     AttendCommon p{};
     p.nq = a->n_q_heads; p.nkv = a->n_kv_heads; p.group = p.nq / p.nkv; p.block_tokens = kBlockRows / p.group;
-    p.tokens = int32_t(pl.tokens); p.segs = pl.segs; p.prefix_seg = pl.prefix_seg; p.merge_tokens = int32_t(pl.merge_tokens);
+    p.segs = pl.segs; p.prefix_seg = pl.prefix_seg; p.merge_tokens = int32_t(pl.merge_tokens);
     p.window = std::min(a->window, 1 << 30); p.sinks = std::min(a->sinks, 1 << 30);   // (positions stay below 2^30)
     p.scale_log2 = float((a->scale != 0.f ? double(a->scale) : 1.0 / std::sqrt(double(a->head_dim))) * 1.4426950408889634);
     if (a->pages) {
