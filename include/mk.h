@@ -418,6 +418,10 @@ typedef struct {
     int32_t* status;
 } mk_linear_args;
 mk_status mk_linear(const mk_linear_args* a, void* stream);
+/* How mk_linear cuts this call on the current device: plan[6] receives the CTAs that make a tile together (1, or 2: a
+ * pair), features and tokens of a tile, such units that share a tile's contraction, tiles, and tiles made at a time.  No
+ * operand is read and nothing is launched.  Errors: MK_ERR_ARG (as mk_linear; no rows), MK_ERR_CUDA. */
+mk_status mk_linear_plan(const mk_linear_args* a, int32_t* plan);
 
 /* Attention of query tokens over a KV cache of mk_kv / mk_kv_pages (the caches mk_bind and
  * mk_bind_paged take), one layer of it.  Sequence b has q_lens[b] query tokens, the last ones of

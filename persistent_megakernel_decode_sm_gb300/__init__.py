@@ -49,8 +49,8 @@ EXPORTS = ["mk_build_schedule", "mk_schedule_queues", "mk_schedule_counters", "m
            "mk_launch_step", "mk_ctx_status", "mk_device_sm_count", "mk_last_error", "mk_unbind", "mk_set_trace",
            "mk_decode_step_static", "mk_set_sync", "mk_decode_steps", "mk_bind_paged", "mk_schedule_attn_chunk",
            "mk_decode_persistent_start", "mk_decode_persistent_stop", "mk_decode_persistent_progress",
-           "mk_decode_persistent_wait", "mk_rebind_schedule", "mk_linear", "mk_attend", "mk_attend_workspace",
-           "mk_prefill", "mk_prefill_workspace"]
+           "mk_decode_persistent_wait", "mk_rebind_schedule", "mk_linear", "mk_linear_plan", "mk_attend",
+           "mk_attend_workspace", "mk_prefill", "mk_prefill_workspace"]
 
 
 class MkError(RuntimeError):
@@ -159,6 +159,8 @@ lib.mk_set_sync.restype = ctypes.c_int
 lib.mk_set_sync.argtypes = [_P, ctypes.c_int32]
 lib.mk_linear.restype = ctypes.c_int
 lib.mk_linear.argtypes = [_P, _P]   # (a packed mk_linear_args)
+lib.mk_linear_plan.restype = ctypes.c_int
+lib.mk_linear_plan.argtypes = [_P, _I32P]
 lib.mk_attend_workspace.restype = ctypes.c_size_t
 lib.mk_attend_workspace.argtypes = [_P]
 lib.mk_attend.restype = ctypes.c_int

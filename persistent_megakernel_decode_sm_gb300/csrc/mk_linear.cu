@@ -628,6 +628,7 @@ static mk_status linear_maps(const mk_linear_args* a, const LinearParams& p, int
 template <int BN, bool GATED, bool F32>
 struct LinearOne {
     using T = LinearTile<BN, GATED>;
+    static constexpr int kTokens = BN, kFeatures = 128, kUnit = 1;
     // cycles as fitted to 96 to 768 tokens by 688 or 2048 inputs by 1001 to 2048 outputs, splits 1 to 4 (1.87 GHz)
     static constexpr int kCycles = GATED ? (BN < 128 ? 750 : 900) : BN <= 32 ? 355 : BN == 64 ? 374 : 450;
     static constexpr int kFixed = BN < 128 ? 7800 : 8400, kJoin = BN == 128 ? 3400 : 500 + 32 * BN;
@@ -656,6 +657,7 @@ struct LinearOne {
 template <bool GATED, bool F32>
 struct LinearPair {
     using T = PairTile<GATED>;
+    static constexpr int kTokens = 256, kFeatures = 2 * T::kRows, kUnit = 2;
     static mk_status plan(const LinearParams& p, int device, LinearPlan& pl) {
         static std::atomic<uint64_t> set{0};
         static std::atomic<int> resident[64][8];
@@ -678,32 +680,31 @@ struct LinearPair {
         return MK_OK;
     }
 };
-template <typename K>
-static mk_status linear_run(const mk_linear_args* a, LinearParams& p, int device, cudaStream_t stream) {
-    LinearPlan pl;
-    const mk_status st = K::plan(p, device, pl);
-    return st != MK_OK ? st : K::launch(a, p, pl, stream);
-}
 // The tile width (or the pairs) whose plan costs least: wide tiles read w fewer times and pairs make twice the products a
 // cycle, narrow tiles fill the device (2048 x 2048 weights, us: 96 tokens 7.2 with 64 columns over 4 CTAs each, 7.8
 // with 32 over 2, 8.4 with 128 over 4, 11.0 in pairs; 768 tokens 24.4 with 32, 13.3 with 128, 15.1 in pairs; 2048
 // tokens and more: pairs).
+struct LinearChoice {
+    LinearPlan plan;
+    int tokens, features, unit;   // of a tile; CTAs of a unit (2: a pair)
+    mk_status (*launch)(const mk_linear_args*, LinearParams&, const LinearPlan&, cudaStream_t);
+};
 template <bool GATED, bool F32>
-static mk_status linear_dispatch(const mk_linear_args* a, LinearParams& p, int device, cudaStream_t stream) {
-    LinearPlan best{}, pl{};
-    mk_status (*launch)(const mk_linear_args*, LinearParams&, const LinearPlan&, cudaStream_t) = nullptr;
+static mk_status linear_choose(const LinearParams& p, int device, LinearChoice& best) {
+    LinearPlan pl{};
+    best = LinearChoice{};
     mk_status st = MK_OK;
     auto offer = [&](auto kernel, bool wanted) {
         using K = decltype(kernel);
         if (st != MK_OK || !wanted || (st = K::plan(p, device, pl)) != MK_OK) return;
-        if (!launch || pl.cost < best.cost) { best = pl; launch = &K::launch; }
+        if (!best.launch || pl.cost < best.plan.cost) best = {pl, K::kTokens, K::kFeatures, K::kUnit, &K::launch};
     };
     offer(LinearOne<16, GATED, F32>{}, p.rows <= 64);
     offer(LinearOne<32, GATED, F32>{}, p.rows > 16 && p.rows <= 768);
     offer(LinearOne<64, GATED, F32>{}, p.rows > 32 && p.rows <= 1536);
     offer(LinearOne<128, GATED, F32>{}, p.rows > 64);
     offer(LinearPair<GATED, F32>{}, p.rows > 128);
-    return st != MK_OK ? st : launch(a, p, best, stream);
+    return st;
 }
 
 static mk_status linear_check(const mk_linear_args* a) {
@@ -741,10 +742,8 @@ static mk_status linear_check(const mk_linear_args* a) {
 
 using namespace mk;
 
-extern "C" mk_status mk_linear(const mk_linear_args* a, void* stream) {
-    const mk_status st = linear_check(a);
-    if (st != MK_OK || a->rows == 0) return st;
-    LinearParams p{};
+// The parameters of a checked call, and its plan on the current device
+static mk_status linear_plan(const mk_linear_args* a, LinearParams& p, LinearChoice& choice) {
     p.rows = a->rows; p.n = a->n; p.k = a->k; p.act = a->activation;
     p.bias = static_cast<const __nv_bfloat16*>(a->bias);
     p.residual = a->residual;
@@ -755,10 +754,31 @@ extern "C" mk_status mk_linear(const mk_linear_args* a, void* stream) {
     p.out_stride = a->out_stride;
     p.status = a->status;
     int device = 0, sms = 0;
-    const mk_status ds = op_device(&device, &sms);
-    if (ds != MK_OK) return ds;
-    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const mk_status st = op_device(&device, &sms);
+    if (st != MK_OK) return st;
     if (a->activation == MK_ACT_SWIGLU)
-        return p.out_f32 ? linear_dispatch<true, true>(a, p, device, s) : linear_dispatch<true, false>(a, p, device, s);
-    return p.out_f32 ? linear_dispatch<false, true>(a, p, device, s) : linear_dispatch<false, false>(a, p, device, s);
+        return p.out_f32 ? linear_choose<true, true>(p, device, choice) : linear_choose<true, false>(p, device, choice);
+    return p.out_f32 ? linear_choose<false, true>(p, device, choice) : linear_choose<false, false>(p, device, choice);
+}
+
+extern "C" mk_status mk_linear(const mk_linear_args* a, void* stream) {
+    mk_status st = linear_check(a);
+    if (st != MK_OK || a->rows == 0) return st;
+    LinearParams p{};
+    LinearChoice c;
+    if ((st = linear_plan(a, p, c)) != MK_OK) return st;
+    return c.launch(a, p, c.plan, static_cast<cudaStream_t>(stream));
+}
+
+extern "C" mk_status mk_linear_plan(const mk_linear_args* a, int32_t* plan) {
+    if (!plan) return fail(MK_ERR_ARG, "null argument");
+    mk_status st = linear_check(a);
+    if (st != MK_OK) return st;
+    if (a->rows == 0) return fail(MK_ERR_ARG, "linear: no rows, no plan");
+    LinearParams p{};
+    LinearChoice c;
+    if ((st = linear_plan(a, p, c)) != MK_OK) return st;
+    const int32_t out[6] = {c.unit, c.features, c.tokens, c.plan.split, c.plan.tiles_n * c.plan.tiles_m, int32_t(c.plan.clusters)};
+    for (int i = 0; i < 6; ++i) plan[i] = out[i];
+    return MK_OK;
 }
