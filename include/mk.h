@@ -478,6 +478,127 @@ typedef struct {
 size_t mk_attend_workspace(const mk_attend_args* a);
 mk_status mk_attend(const mk_attend_args* a, void* workspace, size_t workspace_bytes, void* stream);
 
+/* mk_linear with low-rank adapters of many requests beside the shared weights:
+ *   out[r] = act(x[r] w^T + bias + scale[a] (x[r] down[a]^T) up[a]^T) + residual[r],  a = index[r]
+ *  n_adapters, rank  adapters (1 to 65536), and their rank: a multiple of 8, at most 256 (a smaller one is
+ *                    padded with zeros)
+ *  down              bf16 [n_adapters, rank, k]
+ *  up                bf16 [n_adapters, n, rank] ([n_adapters, 2 n, rank] for MK_ACT_SWIGLU: gate rows, then up rows)
+ *  scale             DEVICE fp32 [n_adapters], or NULL: 1
+ *  index             DEVICE int32 [rows]: each token's adapter; negative: none.  An entry of n_adapters or more is not
+ *                    followed: it counts as none and status receives MK_ERR_BOUNDS
+ * down and up are 16-byte aligned, scale and index 4-byte aligned; out overlaps none of them.  What holds for mk_linear
+ * holds here; sums are fp32, scale[a] x down[a]^T enters the second product in two bf16 parts (16 bits; three parts, 24 bits, for an
+ * fp32 output).  An adapter that some token of a block of 256 tokens names (counted from the first row) must hold finite values for
+ * the other tokens of the block to be right; adapters that no token names are not read.
+ * workspace: mk_linear_adapted_workspace bytes of device memory, 256-byte aligned, which depend on the current device; calls that
+ * may overlap need workspaces of their own.  Errors: MK_ERR_ARG, MK_ERR_CAPACITY (the workspace is too small), MK_ERR_CUDA;
+ * status: MK_ERR_BOUNDS, MK_ERR_TIMEOUT. */
+#define MK_ADAPTERS_MAX_RANK 256
+typedef struct {
+    int32_t n_adapters, rank;
+    const void* down;
+    const void* up;
+    const float* scale;
+    const int32_t* index;
+} mk_adapters;
+/* Workspace bytes of mk_linear_adapted for these arguments (0 where they are not valid, or with no rows; nothing is read
+ * through pointers). */
+size_t mk_linear_adapted_workspace(const mk_linear_args* a, const mk_adapters* ad);
+mk_status mk_linear_adapted(const mk_linear_args* a, const mk_adapters* ad, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Takes projected tokens to attention's operands: norms of every q and k head, rotation by the tokens' positions, q to its
+ * own buffer, k and v to the KV cache.  For head h of token t (heads in order q, k, v: x = row t, elements h d ..):
+ *   y = x / sqrt(mean(x^2) + eps) * gain                     q and k, where their gain is given
+ *   (y_i, y_j) -> (y_i c - y_j s, y_i s + y_j c)             q and k: pair p = 0 .. rotary / 2 - 1 of elements i, j,
+ *                                                            c, s = cos, sin of positions[axis(p)][t] * freqs[p]
+ * all in fp32 (angles exactly reduced, whatever the position), rounded once to bf16.  Elements behind `rotary` and v pass
+ * as they are (rounded).
+ *  tokens         may be 0 (nothing is done); at most 2^30
+ *  head_dim       a multiple of 16, at most 256; n_q_heads + 2 n_kv_heads at most 4096
+ *  qkv            of qkv_dtype, token t at qkv + t * qkv_stride elements; 16-byte aligned, qkv_stride a multiple of 8
+ *                 (4 for fp32)
+ *  q_gain, k_gain bf16 [head_dim], 16-byte aligned, or NULL: that kind is not normed.  eps: finite, >= 0
+ *  rotary         rotated elements of a head: a multiple of 16 (0: none), at most head_dim
+ *  neighbours     0: pair p is elements p and p + rotary / 2; 1: elements 2 p and 2 p + 1
+ *  freqs          HOST double [rotary / 2], finite: radians per position (read before the call returns, as sections)
+ *  n_axes,        position axes (1 to 4) and the pairs of each, in order: HOST int32 sections[n_axes], adding up to
+ *  sections       rotary / 2.  NULL: one axis
+ *  positions      DEVICE int32, position of token t on axis a at positions + a * position_stride + t
+ *  slots          DEVICE int32 [tokens]: where the cache takes the token's k and v: slot b * max_seq + p is position p of
+ *                 sequence b; in a paged cache max_seq is n_blocks * block_size, and slot block * block_size + offset (what
+ *                 mk_assign_pages gives).  Negative: this token's k and v are not stored (its q is).  A slot of
+ *                 sequences * max_seq or more is not followed, and status receives MK_ERR_BOUNDS.  Two tokens of one slot
+ *                 leave either's values there, or parts of both
+ *  kv, layer      the cache as in mk_attend, of `sequences` sequences (1: a pool, or a single one)
+ *  q              bf16, token t's heads at q + t * q_stride elements (a multiple of 8; 16-byte aligned).  It may be the
+ *                 q part of a bf16 qkv itself (the same pointer and stride); else it overlaps no input and not the cache
+ * Errors: MK_ERR_ARG, MK_ERR_CUDA; status: MK_ERR_BOUNDS. */
+typedef struct {
+    int32_t tokens, n_q_heads, n_kv_heads, head_dim;
+    const void* qkv;
+    int64_t qkv_stride;
+    int32_t qkv_dtype, rotary;
+    const void* q_gain;
+    const void* k_gain;
+    float eps;
+    int32_t neighbours, n_axes;
+    const int32_t* sections;
+    const double* freqs;
+    const int32_t* positions;
+    int64_t position_stride;
+    const int32_t* slots;
+    const mk_kv* kv;
+    int32_t layer, max_seq, sequences;
+    void* q;
+    int64_t q_stride;
+    int32_t* status;
+} mk_rope_args;
+mk_status mk_rope_append(const mk_rope_args* a, void* stream);
+
+/* Blocks of a paged cache for requests that grow, shrink or end, and where the new positions go, all on the device.  Request b
+ * holds positions [0, lens[b]) and shall hold [0, new_lens[b]).  With P = shared_prefix / block_size whole blocks that every
+ * request shares (its table row names them; they are neither taken nor given back) it holds max(P, ceil(len / block_size))
+ * blocks.  One call, for all requests in order:
+ *  - blocks that requests no longer need go to the back of the ring of free blocks (in order of request and table column; their
+ *    table entries stay),
+ *  - blocks they need more are taken from its front (from the returned ones too, behind those that were free before) into
+ *    the next columns of their table rows,
+ *  - the positions [lens[b], new_lens[b]) of request b become tokens first[b] .. first[b + 1] - 1 of the step: slots (table
+ *    block * block_size + offset), positions and sequences (b) of each.
+ *  batch          1 to MK_PAGES_MAX_BATCH
+ *  ring, n_blocks DEVICE int32[n_blocks]: the ring of free block ids; n_blocks * block_size <= 2^31 - 1
+ *  ends           DEVICE int32[3]: the ring's front, the number of free blocks (at ring[(front + i) % n_blocks]), and a word that
+ *                 is 0 between calls
+ *  ends_out       DEVICE int32[3], receives the ends after the call; may be ends itself.  Where it is another buffer, the call can be
+ *                 made again from the same state
+ *  table          DEVICE int32[batch][max_blocks]
+ *  lens, new_lens DEVICE int32[batch]
+ *  max_tokens     entries of slots, positions and sequences (each DEVICE int32[max_tokens], positions, sequences and first may be
+ *                 NULL); those behind the last token get -1, 0, -1
+ *  first          DEVICE int32[batch + 1]
+ * Where one request cannot be served nothing changes for any: slots and sequences are all -1, positions and first 0, ends_out
+ * is ends, and status receives MK_ERR_BOUNDS (a length below 0 or above max_blocks * block_size, ends that cannot be) or
+ * MK_ERR_CAPACITY (too few free blocks, more tokens than max_tokens).  A block id outside [0, n_blocks) in the table or the ring is
+ * passed on as it is; a token that needs it gets slot -1, and status receives MK_ERR_BOUNDS.  Nothing is allocated; every pointer is
+ * 4-byte aligned, no buffer overlaps another.  Errors: MK_ERR_ARG, MK_ERR_CUDA. */
+#define MK_PAGES_MAX_BATCH 1024
+typedef struct {
+    int32_t batch, block_size, max_blocks, n_blocks, shared_prefix, max_tokens;
+    int32_t* ring;
+    const int32_t* ends;
+    int32_t* ends_out;
+    int32_t* table;
+    const int32_t* lens;
+    const int32_t* new_lens;
+    int32_t* slots;
+    int32_t* positions;
+    int32_t* sequences;
+    int32_t* first;
+    int32_t* status;
+} mk_pages_args;
+mk_status mk_assign_pages(const mk_pages_args* a, void* stream);
+
 /* Fills the KV cache of a bound context from prompt tokens: the decoder's layers over all of them at
  * once (RMSNorm, mk_linear for the projections, RoPE, mk_attend, SwiGLU), where the decode step takes one.
  * The caller leaves each sequence's last prompt token to a decode step, which gives its logits and the next

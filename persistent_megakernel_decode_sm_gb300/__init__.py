@@ -14,6 +14,9 @@ High level:
 Prompt operators (asynchronous on torch's current stream of the tensors' device):
     y = linear(x, w, bias, activation, residual)  # mk_linear
     o = attend(q, kv, q_lens, kv_lens, window=..) # mk_attend
+    y = adapted_linear(x, w, adapters, index)     # mk_linear_adapted
+    q = rope_append(qkv, kv, positions, slots, freqs)                             # mk_rope_append
+    slots, positions, sequences, first = assign_pages(ring, ends, table, lens, new_lens, block_size, max_tokens)   # mk_assign_pages
 """
 from __future__ import annotations
 
@@ -43,6 +46,8 @@ SYNC_TAGS, SYNC_COUNTERS = 0, 1   # mk_sync_mode
 BF16, F32 = 0, 1                  # mk_dtype
 ACTIVATIONS = {None: 0, "silu": 1, "gelu": 2, "swiglu": 3}   # mk_activation
 ATTEND_MAX_BATCH = 256            # MK_ATTEND_MAX_BATCH
+ADAPTERS_MAX_RANK = 256           # MK_ADAPTERS_MAX_RANK
+PAGES_MAX_BATCH = 1024            # MK_PAGES_MAX_BATCH
 
 EXPORTS = ["mk_build_schedule", "mk_schedule_queues", "mk_schedule_counters", "mk_schedule_patch",
            "mk_scratch_bytes", "mk_schedule_free", "mk_bind", "mk_set_timeout", "mk_decode_step",
@@ -50,7 +55,8 @@ EXPORTS = ["mk_build_schedule", "mk_schedule_queues", "mk_schedule_counters", "m
            "mk_decode_step_static", "mk_set_sync", "mk_decode_steps", "mk_bind_paged", "mk_schedule_attn_chunk",
            "mk_decode_persistent_start", "mk_decode_persistent_stop", "mk_decode_persistent_progress",
            "mk_decode_persistent_wait", "mk_rebind_schedule", "mk_linear", "mk_linear_plan", "mk_attend",
-           "mk_attend_workspace", "mk_prefill", "mk_prefill_workspace"]
+           "mk_attend_workspace", "mk_prefill", "mk_prefill_workspace", "mk_linear_adapted", "mk_linear_adapted_workspace",
+           "mk_rope_append", "mk_assign_pages"]
 
 
 class MkError(RuntimeError):
@@ -105,6 +111,25 @@ class mk_attend_args(ctypes.Structure):
                 ("out_stride", ctypes.c_int64), ("kv", ctypes.POINTER(mk_kv)), ("pages", ctypes.POINTER(mk_kv_pages))] + \
                [(n, ctypes.c_int32) for n in ("layer", "max_seq", "window", "sinks", "shared_prefix")] + \
                [("scale", ctypes.c_float), ("status", _P)]
+
+
+class mk_adapters(ctypes.Structure):
+    _fields_ = [("n_adapters", ctypes.c_int32), ("rank", ctypes.c_int32), ("down", _P), ("up", _P), ("scale", _P), ("index", _P)]
+
+
+class mk_rope_args(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("tokens", "n_q_heads", "n_kv_heads", "head_dim")] + \
+               [("qkv", _P), ("qkv_stride", ctypes.c_int64), ("qkv_dtype", ctypes.c_int32), ("rotary", ctypes.c_int32),
+                ("q_gain", _P), ("k_gain", _P), ("eps", ctypes.c_float), ("neighbours", ctypes.c_int32), ("n_axes", ctypes.c_int32),
+                ("sections", _I32P), ("freqs", ctypes.POINTER(ctypes.c_double)), ("positions", _P),
+                ("position_stride", ctypes.c_int64), ("slots", _P), ("kv", ctypes.POINTER(mk_kv)), ("layer", ctypes.c_int32),
+                ("max_seq", ctypes.c_int32), ("sequences", ctypes.c_int32), ("q", _P), ("q_stride", ctypes.c_int64), ("status", _P)]
+
+
+class mk_pages_args(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("batch", "block_size", "max_blocks", "n_blocks", "shared_prefix", "max_tokens")] + \
+               [(n, _P) for n in ("ring", "ends", "ends_out", "table", "lens", "new_lens", "slots", "positions", "sequences",
+                                  "first", "status")]
 
 
 lib.mk_build_schedule.restype = ctypes.c_int
@@ -169,6 +194,14 @@ lib.mk_prefill_workspace.restype = ctypes.c_size_t
 lib.mk_prefill_workspace.argtypes = [_P, _I32P, _I32P, ctypes.c_int32]
 lib.mk_prefill.restype = ctypes.c_int
 lib.mk_prefill.argtypes = [_P, _I32P, _I32P, _I32P, ctypes.c_int32, _P, ctypes.c_size_t]
+lib.mk_linear_adapted_workspace.restype = ctypes.c_size_t
+lib.mk_linear_adapted_workspace.argtypes = [_P, _P]   # (a packed mk_linear_args, a packed mk_adapters)
+lib.mk_linear_adapted.restype = ctypes.c_int
+lib.mk_linear_adapted.argtypes = [_P, _P, _P, ctypes.c_size_t, _P]
+lib.mk_rope_append.restype = ctypes.c_int
+lib.mk_rope_append.argtypes = [_P, _P]
+lib.mk_assign_pages.restype = ctypes.c_int
+lib.mk_assign_pages.argtypes = [_P, _P]
 lib.mk_unbind.restype = None
 lib.mk_unbind.argtypes = [_P]
 
@@ -463,6 +496,11 @@ class Decoder:
 
 _LINEAR_ARGS = struct.Struct("@4iPqPPPq2iPqP")
 _ATTEND_ARGS = struct.Struct("@4iPPPqPqPP5ifP")
+_ADAPTERS = struct.Struct("@2i4P")
+_ROPE_ARGS = struct.Struct("@4iPq2iPPf2iPPPqPP3iPqP")
+_PAGES_ARGS = struct.Struct("@6i11P")
+assert _ADAPTERS.size == ctypes.sizeof(mk_adapters) and _ROPE_ARGS.size == ctypes.sizeof(mk_rope_args)
+assert _PAGES_ARGS.size == ctypes.sizeof(mk_pages_args)
 assert _LINEAR_ARGS.size == ctypes.sizeof(mk_linear_args) and _ATTEND_ARGS.size == ctypes.sizeof(mk_attend_args)
 assert ctypes.sizeof(mk_kv) == 40 and ctypes.sizeof(mk_kv_pages) == 24   # five 64-bit words, three (packed below)
 
@@ -544,6 +582,13 @@ def linear(x, weight, bias=None, activation: Optional[str] = None, residual=None
     y = (_fast or _setup()).linear(x, weight, bias, activation, residual, out, out_dtype, status)
     if y is not None:
         return y
+    dev, out, args = _linear_args(x, weight, bias, activation, residual, out, out_dtype, status)
+    _launch(dev, lib.mk_linear, args)
+    return out
+
+
+def _linear_args(x, weight, bias, activation, residual, out, out_dtype, status):
+    """(device, out, packed mk_linear_args) of a linear map's operands, which are checked."""
     import torch
     bf, f32 = torch.bfloat16, torch.float32
     dev = x.get_device()
@@ -577,11 +622,9 @@ def linear(x, weight, bias=None, activation: Optional[str] = None, residual=None
         if shape[0] != rows or shape[1] != n:
             raise ValueError(f"residual must be [{rows}, {n}], not {tuple(shape)}")
         rp, rs, rt = residual.data_ptr(), rs[0], F32 if residual.dtype is f32 else BF16
-    _launch(dev, lib.mk_linear,
-            _LINEAR_ARGS.pack(rows, n, k, act, x.data_ptr(), xs[0], weight.data_ptr(), 0 if bias is None else bias.data_ptr(),
-                              rp, rs, rt, F32 if out.dtype is f32 else BF16, out.data_ptr(), os,
-                              0 if status is None else _status_ptr(status, dev)))
-    return out
+    return dev, out, _LINEAR_ARGS.pack(
+        rows, n, k, act, x.data_ptr(), xs[0], weight.data_ptr(), 0 if bias is None else bias.data_ptr(), rp, rs, rt,
+        F32 if out.dtype is f32 else BF16, out.data_ptr(), os, 0 if status is None else _status_ptr(status, dev))
 
 
 def attend(q, kv, q_lens: Sequence[int], kv_lens: Sequence[int], layer: int = 0, window: int = 0, sinks: int = 0,
@@ -652,30 +695,177 @@ def attend(q, kv, q_lens: Sequence[int], kv_lens: Sequence[int], layer: int = 0,
     a = _ATTEND_ARGS.pack(nq, nkv, d, batch, at, at + 4 * batch, q.data_ptr(), qs[0], out.data_ptr(), os[0],
                           c_kv, c_kv + 40 if pages is not None else 0, layer, min(positions, 1 << 30),
                           window, sinks, shared_prefix, scale or 0.0, 0 if status is None else _status_ptr(status, dev))
-    if workspace is not None:
-        if not workspace.is_cuda or workspace.get_device() != dev or not workspace.is_contiguous():
-            raise ValueError("workspace must be contiguous, on q's device")
-        _launch(dev, lib.mk_attend, a, workspace.data_ptr(), workspace.numel() * workspace.element_size())
-    elif torch._C._cuda_getDevice() == dev:
-        _attend_allocating(dev, a)
-    else:
-        with torch.cuda.device(dev):   # (the workspace's size depends on the device)
-            _attend_allocating(dev, a)
+    _with_workspace(dev, workspace, lib.mk_attend, lib.mk_attend_workspace, a)
     return out
 
 
-def _attend_allocating(device: int, a: bytes):
-    """mk_attend on the current device, with a workspace from torch's allocator: taken for torch's
-    current stream and given back at once, it is reused behind the call in stream order."""
+def _with_workspace(device: int, workspace, call, size, *args):
+    """call(*args, workspace, bytes, stream) with `device` current, on the caller's workspace or one of torch's."""
     import torch
-    stream, need = torch._C._cuda_getCurrentRawStream(device), lib.mk_attend_workspace(a)
+    if workspace is not None:
+        if not workspace.is_cuda or workspace.get_device() != device or not workspace.is_contiguous():
+            raise ValueError("workspace must be contiguous, on the operands' device")
+        _launch(device, call, *args, workspace.data_ptr(), workspace.numel() * workspace.element_size())
+    elif torch._C._cuda_getDevice() == device:
+        _allocating(device, call, size, *args)
+    else:
+        with torch.cuda.device(device):   # (the workspace's size depends on the device)
+            _allocating(device, call, size, *args)
+
+
+def _allocating(device: int, call, size, *args):
+    """call(*args, workspace, bytes, stream) on the current device, with a workspace of size(*args) bytes from torch's
+    allocator: taken for torch's current stream and given back at once, it is reused behind the call in stream order."""
+    import torch
+    stream, need = torch._C._cuda_getCurrentRawStream(device), size(*args)
     if not need:
-        st = lib.mk_attend(a, 0, 0, stream)
+        st = call(*args, 0, 0, stream)
     else:
         ws = torch._C._cuda_cudaCachingAllocator_raw_alloc(need, stream)
         try:
-            st = lib.mk_attend(a, ws, need, stream)
+            st = call(*args, ws, need, stream)
         finally:
             torch._C._cuda_cudaCachingAllocator_raw_delete(ws)
     if st:
         _check(st)
+
+
+# ---- around the paged cache of a serving step ---------------------------------------------------
+
+
+def adapted_linear(x, weight, adapters, index, bias=None, activation: Optional[str] = None, residual=None, out=None, out_dtype=None,
+                   workspace=None, status=None):
+    """mk_linear_adapted: act(x @ weight.T + bias + scale[a] * (x @ down[a].T) @ up[a].T) + residual, a the token's adapter,
+    in fp32, rounded once to the output's type.
+
+    adapters: (down, up) or (down, up, scale) -- down bf16 [n_adapters, rank, k], up bf16 [n_adapters, n, rank] ([n_adapters,
+    2 n, rank] with "swiglu": gate rows, then up rows), both contiguous, scale fp32 [n_adapters] or None (1).  index: int32
+    [rows], each token's adapter, negative for none.  The other operands are linear()'s.  workspace: at least
+    mk_linear_adapted_workspace bytes (allocated by default).  Returns out.
+
+    status: as in linear(), and MK_ERR_BOUNDS for an index of n_adapters or more, which counts as none.  No gradients are
+    recorded."""
+    import torch
+    bf = torch.bfloat16
+    down, up, scale = adapters if len(adapters) == 3 else (*adapters, None)
+    dev, out, args = _linear_args(x, weight, bias, activation, residual, out, out_dtype, status)
+    (count, rank, k), ds = _operand(down, "down", (bf,), dev, 3)
+    ushape, us = _operand(up, "up", (bf,), dev, 3)
+    wide = weight.shape[0]
+    if k != x.shape[1] or not down.is_contiguous():
+        raise ValueError(f"down {tuple(down.shape)} must be contiguous, with rows of {x.shape[1]}")
+    if tuple(ushape) != (count, wide, rank) or not up.is_contiguous():
+        raise ValueError(f"up {tuple(ushape)} must be contiguous, [{count}, {wide}, {rank}]")
+    if scale is not None and (_operand(scale, "scale", (torch.float32,), dev, 1)[0][0] != count or not scale.is_contiguous()):
+        raise ValueError(f"scale must have {count} elements")
+    if _operand(index, "index", (torch.int32,), dev, 1)[0][0] != x.shape[0] or not index.is_contiguous():
+        raise ValueError(f"index must have {x.shape[0]} contiguous elements")
+    ad = _ADAPTERS.pack(count, rank, down.data_ptr(), up.data_ptr(), 0 if scale is None else scale.data_ptr(), index.data_ptr())
+    _with_workspace(dev, workspace, lib.mk_linear_adapted, lib.mk_linear_adapted_workspace, args, ad)
+    return out
+
+
+def rope_append(qkv, kv, positions, slots, freqs, layer: int = 0, sections: Optional[Sequence[int]] = None, neighbours: bool = False,
+                q_gain=None, k_gain=None, eps: float = 1e-5, out=None, status=None):
+    """mk_rope_append: norms of every q and k head (where their gain is given), rotation of q and k by the tokens' positions,
+    q to its own buffer, k and v to the cache.
+
+    qkv [tokens, (n_q_heads + 2 n_kv_heads) head_dim] bf16 or fp32: q, k, v heads in order (rows may be strided by 16 bytes);
+    n_kv_heads and head_dim are the cache's.  kv: the cache as attend() takes it -- kv.k / kv.v [batch, layers, kv heads,
+    max_seq, head_dim], or the pool [layers, kv heads, n_blocks * block_size, head_dim].  slots int32 [tokens]: b * max_seq + p
+    in the first, block * block_size + offset in the second (assign_pages()); negative: not stored.
+    freqs: float64 on the CPU, radians per position of each pair (theta ** (-2 p / rotary)); 2 len(freqs) elements of a head
+    are rotated, pair p is elements p and p + len(freqs), or 2 p and 2 p + 1 with neighbours.  positions int32 [tokens], or
+    [axes, tokens] with sections: the pairs of each axis in order, adding up to len(freqs).
+    q_gain, k_gain bf16 [head_dim].  out: bf16 [tokens, n_q_heads, head_dim] (allocated by default; it may be the q part of a
+    bf16 qkv).  Returns out.
+
+    status: a CUDA int32 tensor of one element, zeroed by the caller, that receives MK_ERR_BOUNDS for a slot behind the
+    cache (not stored).  No gradients are recorded."""
+    import torch
+    bf, f32 = torch.bfloat16, torch.float32
+    dev = qkv.get_device()
+    (tokens, width), xs = _operand(qkv, "qkv", (bf, f32), dev, 2)
+    k, v = kv.k, kv.v
+    dims = k.dim()
+    if dims not in (4, 5):
+        raise ValueError(f"kv.k must have 5 dimensions, or 4 (a pool), not {dims}")
+    shape, ks = _operand(k, "kv.k", (bf,), dev, dims)
+    if v.shape != shape or v.stride() != ks or v.dtype is not bf or v.get_device() != dev or (ks[-2] != shape[-1] and shape[-2] > 1):
+        raise ValueError("kv.k and kv.v must be alike (shape, strides, type, device), with contiguous [positions, head_dim] rows")
+    layers, nkv, positions_of, d = shape[-4:]
+    if not 0 <= layer < layers:
+        raise ValueError(f"layer {layer} of {layers}")
+    nq = width // d - 2 * nkv if d else 0
+    if nq < 1 or (nq + 2 * nkv) * d != width:
+        raise ValueError(f"qkv rows of {width} are not q heads and 2 x {nkv} kv heads of {d}")
+    if freqs.dtype is not torch.float64 or freqs.is_cuda or freqs.dim() != 1 or not freqs.is_contiguous():
+        raise ValueError("freqs must be a contiguous float64 tensor on the CPU")
+    axes = 1 if sections is None else len(sections)
+    pshape, ps = _operand(positions, "positions", (torch.int32,), dev, 1 if sections is None else 2)
+    if pshape[-1] != tokens or (sections is not None and pshape[0] != axes):
+        raise ValueError(f"positions must be [{tokens}]" if sections is None else f"positions must be [{axes}, {tokens}]")
+    if _operand(slots, "slots", (torch.int32,), dev, 1)[0][0] != tokens:
+        raise ValueError(f"slots must have {tokens} elements")
+    for name, gain in (("q_gain", q_gain), ("k_gain", k_gain)):
+        if gain is not None and _operand(gain, name, (bf,), dev, 1)[0][0] != d:
+            raise ValueError(f"{name} must have {d} elements")
+    if out is None:
+        out, os = torch.empty((tokens, nq, d), dtype=bf, device=qkv.device), nq * d
+    else:
+        oshape, os = _operand(out, "out", (bf,), dev, 3)
+        if tuple(oshape) != (tokens, nq, d) or (os[1] != d and nq > 1):
+            raise ValueError(f"out must be [{tokens}, {nq}, {d}] with contiguous heads of a token")
+        os = os[0]
+    c_kv = mk_kv(k.data_ptr(), v.data_ptr(), ks[0] if dims == 5 else 0, ks[-4], ks[-3])
+    c_sections = None if sections is None else (ctypes.c_int32 * axes)(*sections)
+    args = _ROPE_ARGS.pack(tokens, nq, nkv, d, qkv.data_ptr(), xs[0], F32 if qkv.dtype is f32 else BF16, 2 * freqs.numel(),
+                           0 if q_gain is None else q_gain.data_ptr(), 0 if k_gain is None else k_gain.data_ptr(), eps, bool(neighbours),
+                           axes, 0 if sections is None else ctypes.addressof(c_sections), freqs.data_ptr(), positions.data_ptr(),
+                           ps[0] if sections is not None else 0, slots.data_ptr(), ctypes.addressof(c_kv), layer, positions_of,
+                           shape[0] if dims == 5 else 1, out.data_ptr(), os, 0 if status is None else _status_ptr(status, dev))
+    _launch(dev, lib.mk_rope_append, args)
+    return out
+
+
+def assign_pages(ring, ends, table, lens, new_lens, block_size: int, max_tokens: int, shared_prefix: int = 0, ends_out=None, out=None,
+                 status=None):
+    """mk_assign_pages: blocks of a paged cache for requests that grow, shrink or end, and the slots of the step's tokens,
+    worked out on the device.
+
+    ring int32 [n_blocks] and ends int32 [3] (front, free blocks, 0): the free block ids, as a ring.  table int32 [batch,
+    max_blocks].  lens, new_lens int32 [batch]: positions held and wanted; 0 ends a request.  Blocks no longer needed go to
+    the back of the ring, new ones come from its front into table.  ends_out: receives the ends after the call (default: ends
+    itself).  shared_prefix: positions whose whole blocks every row shares and no request owns.
+    Returns (slots, positions, sequences, first): int32 [max_tokens] each (-1, 0, -1 behind the last token) and [batch + 1],
+    or the four tensors of out.
+
+    status: a CUDA int32 tensor of one element, zeroed by the caller: MK_ERR_CAPACITY (too few free blocks, more tokens than
+    max_tokens) or MK_ERR_BOUNDS (lengths or ends that cannot be) where nothing was assigned and every slot is -1; MK_ERR_BOUNDS
+    also for a block id outside the ring's n_blocks."""
+    import torch
+    dev, i32 = ring.get_device(), (torch.int32,)
+    operands = dict(ring=(ring, 1), ends=(ends, 1), table=(table, 2), lens=(lens, 1), new_lens=(new_lens, 1))
+    if ends_out is None:
+        ends_out = ends
+    else:
+        operands["ends_out"] = (ends_out, 1)
+    for name, (t, dim) in operands.items():
+        _operand(t, name, i32, dev, dim)
+    (batch, columns), n_blocks = table.shape, ring.shape[0]
+    if not table.is_contiguous() or lens.shape[0] != batch or new_lens.shape[0] != batch:
+        raise ValueError("table must be contiguous, with a row for each of lens and new_lens")
+    if ends.shape[0] != 3 or ends_out.shape[0] != 3:
+        raise ValueError("ends and ends_out must have 3 elements")
+    if out is None:
+        out = tuple(torch.empty(n, dtype=torch.int32, device=ring.device) for n in (max_tokens, max_tokens, max_tokens, batch + 1))
+    else:
+        out = tuple(out)
+        for name, t, n in zip(("slots", "positions", "sequences", "first"), out, (max_tokens, max_tokens, max_tokens, batch + 1), strict=True):
+            if _operand(t, name, i32, dev, 1)[0][0] != n:
+                raise ValueError(f"{name} must have {n} elements")
+    _launch(dev, lib.mk_assign_pages,
+            _PAGES_ARGS.pack(batch, block_size, columns, n_blocks, shared_prefix, max_tokens, ring.data_ptr(), ends.data_ptr(),
+                             ends_out.data_ptr(), table.data_ptr(), lens.data_ptr(), new_lens.data_ptr(), *(t.data_ptr() for t in out),
+                             0 if status is None else _status_ptr(status, dev)))
+    return out

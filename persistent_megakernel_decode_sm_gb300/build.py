@@ -8,6 +8,9 @@ Translation units compiled in parallel and linked into one shared library:
   csrc/mk_linear.cu  the linear map with a fused epilogue (prompt path)
   csrc/mk_attend.cu  attention of query tokens over the KV cache (prompt path)
   csrc/mk_prefill.cu embedding, RMSNorm, RoPE and KV append of the prompt path
+  csrc/mk_adapt.cu   the linear map with low-rank adapters (its kernels are mk_linear.cu's, in csrc/mk_linear.cuh)
+  csrc/mk_rope.cu    norms of q and k, rotation, append to the cache
+  csrc/mk_pages.cu   block tables and slot maps of a paged cache
 and beside it, with the host's C compiler, the Python module _mk_call, named for the interpreter it is built for:
   csrc/mk_python.c   argument handling of linear() and attend()
 Where Python's headers are missing the module is left out, and that is done in Python.
@@ -29,8 +32,8 @@ LIB = os.path.join(HERE, "libmk.so")
 CALL_SOURCE, CALL = os.path.join(CSRC, "mk_python.c"), os.path.join(HERE, "_mk_call" + (sysconfig.get_config_var("EXT_SUFFIX") or ".so"))
 BUILD_DIR = os.path.join(HERE, "_build")
 SOURCES = ["mk_sched.cpp", "mk_api.cu", "mk_kernel.cu", "mk_kernel_batch.cu", "mk_linear.cu", "mk_attend.cu",
-           "mk_prefill.cu"]
-HEADERS = ["mk_internal.h", "mk_ops.h", "mk_sm103.cuh"]
+           "mk_prefill.cu", "mk_adapt.cu", "mk_rope.cu", "mk_pages.cu"]
+HEADERS = ["mk_internal.h", "mk_ops.h", "mk_sm103.cuh", "mk_linear.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -73,7 +76,7 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
         cmd = [nvcc, *common, *ARCH, "-lineinfo", "-c", os.path.join(CSRC, src), "-o", obj]
         if src.endswith(".cpp"):
             cmd = [nvcc, *common, "-x", "c++", "-c", os.path.join(CSRC, src), "-o", obj]
-        if ptxas_info and src in ("mk_kernel.cu", "mk_linear.cu", "mk_attend.cu"):
+        if ptxas_info and src in ("mk_kernel.cu", "mk_linear.cu", "mk_attend.cu", "mk_adapt.cu", "mk_rope.cu", "mk_pages.cu"):
             cmd.insert(1, "-Xptxas=-v")
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:

@@ -1,0 +1,328 @@
+// The linear map with low-rank adapters of many requests (mk_linear_adapted): the low-rank rows t = scale x down^T of every
+// token with its own adapter, then the linear map with the adapters' part as a longer contraction (mk_linear.cuh).
+#include <algorithm>
+
+#include "mk_linear.cuh"
+
+namespace mk {
+
+constexpr int kLowThreads = 256, kLowWarps = kLowThreads / 32;
+constexpr int kLowRank = 32;        // columns of the rank at a time: 4 products of 8
+constexpr int kLowTile = 256;       // most tokens of a tile of the linear map
+
+struct LowParams {
+    int rows, k, rank, n_adapters;
+    int tile, subs;                 // tokens of a tile of the linear map, blocks of kTokens tokens in it
+    int slots, items, f32;          // as LinearExtra; whether the output is fp32: three terms
+    const __nv_bfloat16* x;
+    int64_t x_stride;
+    const __nv_bfloat16* down;
+    const float* scale;
+    const int32_t* index;
+    int32_t* count;
+    int32_t* list;
+    __nv_bfloat16* terms;
+    int64_t terms_stride;
+    int32_t* status;
+};
+
+__device__ __forceinline__ void low_mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// A cluster works on `16 MT` neighbouring tokens of one tile of the linear map, for the tile's adapters y, y + gridDim.y, ..: those of
+// its tokens that name the adapter get their low-rank row, the others zeros.  x and down are read from global memory straight
+// into the operands of m16n8k16 products (a thread's 16 bytes of a row are the elements 2 i, 2 i + 1 of two products: the
+// contraction may take its elements in any order as long as both operands do), only rows that count.  The contraction is
+// shared out over the warps and the CTAs of the cluster in blocks of 32; the sums meet in shared memory, in a fixed order.
+// These products need no more than the reading of x and down does (they are 1/8 to 1/100 of the linear map's), so they stay on
+// mma.sync, with registers for operands and no staging.
+template <int MT>
+__global__ void __launch_bounds__(kLowThreads) low_rank_kernel(const __grid_constant__ LowParams p) {
+    constexpr int kTokens = 16 * MT;
+    __shared__ int name[kLowTile], list[kLowTile], warp_heads[kLowWarps];
+    __shared__ float part[kLowWarps][16][kLowRank], sums[kTokens][kLowRank];
+    // every kernel before this one is done when the next one may start: it reads x beside this one
+    sm::pdl_wait();
+    sm::pdl_trigger();
+    const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+    const int split = int(gridDim.z), rank_z = int(blockIdx.z);
+    const int m = int(blockIdx.x) / p.subs, sub = int(blockIdx.x) % p.subs, m0 = m * p.tile, tokens = min(p.tile, p.rows - m0);
+    // the tile's adapters in the order in which its tokens name them
+    int mine = -1;
+    if (t < tokens) {
+        mine = p.index[m0 + t];
+        if (mine >= p.n_adapters) {
+            if (p.status) *p.status = MK_ERR_BOUNDS;
+            mine = -1;
+        }
+    }
+    name[t] = mine;
+    __syncthreads();
+    bool head = mine >= 0 && (t == 0 || name[t - 1] != mine);
+    for (int i = 0; head && i + 1 < t; ++i) head = name[i] != mine;
+    const uint32_t heads = __ballot_sync(0xFFFFFFFFu, head);
+    if (lane == 0) warp_heads[warp] = __popc(heads);
+    __syncthreads();
+    int before = __popc(heads & ((1u << lane) - 1)), count = 0;
+#pragma unroll
+    for (int w = 0; w < kLowWarps; ++w) {
+        if (w < warp) before += warp_heads[w];
+        count += warp_heads[w];
+    }
+    if (head) list[before] = mine;
+    __syncthreads();
+    if (sub == 0 && blockIdx.y == 0 && rank_z == 0) {
+        if (t == 0) p.count[m] = count;
+        if (t < count) p.list[int64_t(m) * p.slots + t] = list[t];
+    }
+
+    const int row0 = sub * kTokens;                     // in the tile
+    if (row0 >= tokens) return;                         // (all CTAs of the cluster)
+    const int g = lane >> 2, q = lane & 3;              // a product's row, and its quarter of 32 elements
+    const int width = p.items * 16, blocks = (p.k + 31) / 32, item_cols = p.f32 ? 64 : 32;
+    for (int slot = int(blockIdx.y); slot < count; slot += int(gridDim.y)) {
+        const int adapter = list[slot];
+        bool any = false, use[MT][2];
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                use[i][h] = name[row0 + 16 * i + 8 * h + g] == adapter;   // (names behind the last token are -1)
+                any = any || use[i][h];
+            }
+        any = __any_sync(0xFFFFFFFFu, any);             // (every warp looks at every token)
+        const __nv_bfloat16* down = p.down + int64_t(adapter) * p.rank * p.k;
+        for (int c0 = 0; c0 < width; c0 += kLowRank) {
+            if (any) {
+                float acc[MT][4][4];
+#pragma unroll
+                for (int i = 0; i < MT; ++i)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+#pragma unroll
+                        for (int v = 0; v < 4; ++v) acc[i][j][v] = 0.f;
+#pragma unroll 2
+                for (int b = rank_z * kLowWarps + warp; b < blocks; b += split * kLowWarps) {
+                    const int at = b * 32 + q * 8;
+                    const bool in = at < p.k;
+                    uint4 xs[MT][2], ds[4];
+                    const uint4 zero = make_uint4(0, 0, 0, 0);
+#pragma unroll
+                    for (int i = 0; i < MT; ++i)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h)
+                            xs[i][h] = in && use[i][h] ? __ldg(reinterpret_cast<const uint4*>(p.x + int64_t(m0 + row0 + 16 * i + 8 * h + g) * p.x_stride + at)) : zero;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        ds[j] = in && c0 + 8 * j + g < p.rank ? __ldg(reinterpret_cast<const uint4*>(down + int64_t(c0 + 8 * j + g) * p.k + at)) : zero;
+#pragma unroll
+                    for (int i = 0; i < MT; ++i)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            low_mma(acc[i][j], xs[i][0].x, xs[i][1].x, xs[i][0].y, xs[i][1].y, ds[j].x, ds[j].y);
+                            low_mma(acc[i][j], xs[i][0].z, xs[i][1].z, xs[i][0].w, xs[i][1].w, ds[j].z, ds[j].w);
+                        }
+                }
+#pragma unroll
+                for (int i = 0; i < MT; ++i) {
+                    __syncthreads();
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h)
+                            *reinterpret_cast<float2*>(&part[warp][g + 8 * h][8 * j + 2 * q]) = make_float2(acc[i][j][2 * h], acc[i][j][2 * h + 1]);
+                    __syncthreads();
+                    for (int e = t; e < 16 * kLowRank; e += kLowThreads) {
+                        float s = 0.f;
+#pragma unroll
+                        for (int w = 0; w < kLowWarps; ++w) s += part[w][e / kLowRank][e % kLowRank];
+                        sums[16 * i + e / kLowRank][e % kLowRank] = s;
+                    }
+                }
+                __syncwarp();
+                if (split > 1) sm::cluster_sync();
+                else __syncthreads();
+            }
+            // the cluster's CTAs share out the pairs of columns; a token's row is complete over them
+            const float scale = p.scale ? p.scale[adapter] : 1.f;
+            for (int e = rank_z * kLowThreads + t; e < kTokens * kLowRank / 2; e += split * kLowThreads) {
+                const int r = e / (kLowRank / 2), c = e % (kLowRank / 2) * 2, col = c0 + c;
+                if (row0 + r >= tokens || col >= width) continue;
+                float v[2] = {0.f, 0.f};
+                if (any && name[row0 + r] == adapter) {
+                    const uint32_t src = sm::smem(&sums[r][c]);
+                    for (int z = 0; z < split; ++z) {
+                        const uint32_t peer = sm::cluster_addr(src, uint32_t(z));
+                        v[0] += sm::cluster_ld(peer);
+                        v[1] += sm::cluster_ld(peer + 4);
+                    }
+                    v[0] *= scale;
+                    v[1] *= scale;
+                }
+                __nv_bfloat16* dst = p.terms + int64_t(m0 + row0 + r) * p.terms_stride + int64_t(slot * p.items + col / 16) * item_cols + col % 16;
+                for (int term = 0; term < (p.f32 ? 3 : 2); ++term, dst += 16) {
+                    const __nv_bfloat16 h0 = __float2bfloat16_rn(v[0]), h1 = __float2bfloat16_rn(v[1]);
+                    __nv_bfloat162 pair;
+                    pair.x = h0;
+                    pair.y = h1;
+                    *reinterpret_cast<__nv_bfloat162*>(dst) = pair;
+                    // (an infinity, or a value that rounds to one, leaves no rest)
+                    v[0] = isinf(__bfloat162float(h0)) ? 0.f : v[0] - __bfloat162float(h0);
+                    v[1] = isinf(__bfloat162float(h1)) ? 0.f : v[1] - __bfloat162float(h1);
+                }
+            }
+            __syncwarp();
+            if (any && split > 1) sm::cluster_sync();   // (the sums are read before they are written again)
+        }
+    }
+}
+
+// A call is made in pieces of rows whose terms fit this; each at least a tile
+constexpr int64_t kAdaptTermsBytes = 256ll << 20;
+
+struct AdaptPlan {
+    LinearChoice<true> choice;
+    int slots, items, tiles;        // of a piece
+    int64_t rows, cols;             // tokens of a piece, columns of the terms
+    size_t terms, list, bytes;      // offsets of the terms and lists behind the counts; all
+};
+
+static mk_status adapt_check(const mk_linear_args* a, const mk_adapters* ad, bool pointers) {
+    if (!a || !ad) return fail(MK_ERR_ARG, "null argument");
+    if (ad->n_adapters < 1 || ad->n_adapters > 65536) return fail(MK_ERR_ARG, "linear_adapted: %d adapters (1 to 65536)", ad->n_adapters);
+    if (ad->rank < 8 || ad->rank > MK_ADAPTERS_MAX_RANK || ad->rank % 8)
+        return fail(MK_ERR_ARG, "linear_adapted: rank %d (a multiple of 8, at most %d)", ad->rank, MK_ADAPTERS_MAX_RANK);
+    if (!pointers) return MK_OK;
+    if (!ad->down || !ad->up || !ad->index) return fail(MK_ERR_ARG, "linear_adapted: null pointer");
+    if (!op_aligned(ad->down, 16) || !op_aligned(ad->up, 16) || !op_aligned(ad->scale, 4) || !op_aligned(ad->index, 4))
+        return fail(MK_ERR_ARG, "linear_adapted: down and up must be 16-byte aligned, scale and index 4-byte aligned");
+    const int64_t os = a->out_dtype == MK_F32 ? 4 : 2, f = a->activation == MK_ACT_SWIGLU ? 2 : 1;
+    const RowSpan out{a->out, a->rows, a->n * os, a->out_stride * os};
+    const int64_t per = int64_t(ad->n_adapters) * ad->rank * 2;
+    if (spans_overlap(out, {ad->down, 1, per * a->k, 0}) || spans_overlap(out, {ad->up, 1, per * f * a->n, 0}) ||
+        spans_overlap(out, {ad->scale, 1, int64_t(ad->n_adapters) * 4, 0}) || spans_overlap(out, {ad->index, 1, int64_t(a->rows) * 4, 0}))
+        return fail(MK_ERR_ARG, "linear_adapted: out overlaps an input");
+    return MK_OK;
+}
+
+static mk_status adapt_plan(const mk_linear_args* a, const mk_adapters* ad, AdaptPlan& pl) {
+    LinearParams p{};
+    const bool f32 = a->out_dtype == MK_F32;
+    pl.items = (ad->rank + 15) / 16;
+    // blocks of the adapters' part, for the estimate: few tokens name an adapter each, of many neighbours share theirs
+    const int named = std::min({a->rows <= 64 ? a->rows : 4, ad->n_adapters, 64});
+    const int extra = f32 ? named * pl.items : (named * pl.items + 1) / 2;
+    const mk_status st = linear_plan(a, extra, p, pl.choice);
+    if (st != MK_OK) return st;
+    const int tile = pl.choice.tokens;
+    pl.slots = std::min({tile, ad->n_adapters, a->rows});
+    const int64_t items = int64_t(pl.slots) * pl.items;
+    pl.cols = (f32 ? items : (items + 1) / 2) * 64;
+    const int64_t all = (int64_t(a->rows) + tile - 1) / tile;
+    pl.tiles = int(std::min(all, std::max<int64_t>(1, kAdaptTermsBytes / (pl.cols * 2 * tile))));
+    pl.rows = std::min<int64_t>(a->rows, int64_t(pl.tiles) * tile);
+    pl.list = align256(size_t(pl.tiles) * 4);
+    pl.terms = pl.list + align256(size_t(pl.tiles) * size_t(pl.slots) * 4);
+    pl.bytes = pl.terms + align256(size_t(pl.rows) * size_t(pl.cols) * 2);
+    return MK_OK;
+}
+
+template <int MT>
+static mk_status low_launch(LowParams& p, int sms, cudaStream_t stream) {
+    constexpr int kTokens = 16 * MT;
+    p.subs = (p.tile + kTokens - 1) / kTokens;
+    const int64_t subs = int64_t((p.rows + p.tile - 1) / p.tile) * p.subs;
+    // adapters of a tile side by side where there are few tokens, then the contraction over clusters of 2, 4 or 8 while two CTAs
+    // an SM are not reached and each warp keeps a block of 32
+    const int lanes = p.rows <= 512 ? std::min({p.slots, 16}) : std::min(p.slots, 2);
+    int split = 1;
+    while (split < 8 && subs * lanes * split * 2 <= 2 * sms && 2 * split * kLowWarps * 32 <= p.k) split *= 2;
+    cudaLaunchConfig_t cfg{};
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = unsigned(split);
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    cfg.stream = stream;
+    cfg.gridDim = dim3(unsigned(subs), unsigned(lanes), unsigned(split));
+    cfg.blockDim = dim3(kLowThreads);
+    MK_CK(cudaLaunchKernelEx(&cfg, &low_rank_kernel<MT>, p));
+    return MK_OK;
+}
+
+}  // namespace mk
+
+using namespace mk;
+
+extern "C" size_t mk_linear_adapted_workspace(const mk_linear_args* a, const mk_adapters* ad) {
+    AdaptPlan pl{};
+    if (linear_check(a) != MK_OK || adapt_check(a, ad, false) != MK_OK || a->rows == 0 || adapt_plan(a, ad, pl) != MK_OK) return 0;
+    return pl.bytes;
+}
+
+extern "C" mk_status mk_linear_adapted(const mk_linear_args* a, const mk_adapters* ad, void* workspace, size_t workspace_bytes,
+                                       void* stream) {
+    mk_status st = linear_check(a);
+    if (st != MK_OK || (st = adapt_check(a, ad, a && a->rows > 0)) != MK_OK || a->rows == 0) return st;
+    AdaptPlan pl{};
+    int device = 0, sms = 0;
+    if ((st = op_device(&device, &sms)) != MK_OK || (st = adapt_plan(a, ad, pl)) != MK_OK) return st;
+    if (!workspace || !op_aligned(workspace, 256)) return fail(MK_ERR_ARG, "linear_adapted: workspace null or not 256-byte aligned");
+    if (workspace_bytes < pl.bytes)
+        return fail(MK_ERR_CAPACITY, "linear_adapted: workspace of %zu bytes, %zu needed (mk_linear_adapted_workspace)", workspace_bytes, pl.bytes);
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const bool f32 = a->out_dtype == MK_F32;
+    for (int64_t r0 = 0; r0 < a->rows; r0 += pl.rows) {
+        mk_linear_args c = *a;   // this piece's rows
+        c.rows = int32_t(std::min<int64_t>(pl.rows, a->rows - r0));
+        c.x = static_cast<const uint16_t*>(a->x) + r0 * a->x_stride;
+        c.out = static_cast<uint8_t*>(a->out) + r0 * a->out_stride * (f32 ? 4 : 2);
+        if (a->residual) c.residual = static_cast<const uint8_t*>(a->residual) + r0 * a->residual_stride * (a->residual_dtype == MK_F32 ? 4 : 2);
+        LowParams low{};
+        low.rows = c.rows; low.k = c.k; low.rank = ad->rank; low.n_adapters = ad->n_adapters;
+        low.tile = pl.choice.tokens; low.slots = pl.slots; low.items = pl.items; low.f32 = f32;
+        low.x = static_cast<const __nv_bfloat16*>(c.x);
+        low.x_stride = c.rows == 1 ? c.k : c.x_stride;
+        low.down = static_cast<const __nv_bfloat16*>(ad->down);
+        low.scale = ad->scale;
+        low.index = ad->index + r0;
+        low.count = reinterpret_cast<int32_t*>(ws);
+        low.list = reinterpret_cast<int32_t*>(ws + pl.list);
+        low.terms = reinterpret_cast<__nv_bfloat16*>(ws + pl.terms);
+        low.terms_stride = pl.cols;
+        low.status = a->status;
+        if ((st = c.rows > 512 ? low_launch<4>(low, sms, s) : low_launch<1>(low, sms, s)) != MK_OK) return st;
+        LinearExtra<true> e{};
+        e.count = low.count;
+        e.list = low.list;
+        e.slots = pl.slots;
+        e.items = pl.items;
+        const int64_t w_rows = int64_t(c.n) * (c.activation == MK_ACT_SWIGLU ? 2 : 1);
+        const cuuint64_t ud[3] = {cuuint64_t(ad->rank), cuuint64_t(w_rows), cuuint64_t(ad->n_adapters)};
+        const cuuint64_t us[2] = {cuuint64_t(ad->rank) * 2, cuuint64_t(w_rows) * cuuint64_t(ad->rank) * 2};
+        const cuuint32_t ub[3] = {16, cuuint32_t(pl.choice.unit == 2 ? pl.choice.features / 2 : 128), 1};
+        if ((st = op_tensor_map(&e.up, ad->up, 3, ud, us, ub)) != MK_OK) return st;
+        const cuuint64_t td[2] = {cuuint64_t(pl.cols), cuuint64_t(c.rows)}, ts[1] = {cuuint64_t(pl.cols) * 2};
+        const cuuint32_t tb[2] = {64, cuuint32_t(pl.choice.unit == 2 ? 128 : pl.choice.tokens)};
+        if ((st = op_tensor_map(&e.terms, low.terms, 2, td, ts, tb)) != MK_OK) return st;
+        // (the piece's own tiles: pieces are whole tiles but for the last)
+        LinearParams p{};
+        LinearPlan plan = pl.choice.plan;
+        p.rows = c.rows; p.n = c.n; p.k = c.k; p.act = c.activation;
+        p.bias = static_cast<const __nv_bfloat16*>(c.bias);
+        p.residual = c.residual; p.residual_stride = c.residual_stride; p.residual_f32 = c.residual_dtype == MK_F32;
+        p.out_f32 = f32; p.out = c.out; p.out_stride = c.out_stride; p.status = c.status;
+        plan.tiles_m = (c.rows + pl.choice.tokens - 1) / pl.choice.tokens;
+        const int64_t tiles = int64_t(plan.tiles_n) * plan.tiles_m;
+        plan.clusters = plan.split > 1 ? tiles : std::min(tiles, plan.clusters);
+        if ((st = pl.choice.launch(&c, p, e, plan, s)) != MK_OK) return st;
+    }
+    return MK_OK;
+}

@@ -41,7 +41,7 @@ inline bool spans_overlap(const RowSpan& a, const RowSpan& b) {
 }
 
 // bf16 tensor map: `rank` extents, the byte strides of all but the innermost, the box; 128-byte
-// swizzle (64 bytes for boxes of 64-byte rows); what lies outside the extents reads as zeros
+// swizzle (64 or 32 bytes for boxes of such rows); what lies outside the extents reads as zeros
 inline mk_status op_tensor_map(CUtensorMap* out, const void* base, int rank, const cuuint64_t* dim, const cuuint64_t* stride,
                                const cuuint32_t* box) {
     typedef CUresult (*Encode)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
@@ -60,7 +60,9 @@ inline mk_status op_tensor_map(CUtensorMap* out, const void* base, int rank, con
     }
     const cuuint32_t es[5] = {1, 1, 1, 1, 1};
     const CUresult r = enc(out, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, cuuint32_t(rank), const_cast<void*>(base), dim, stride, box, es,
-                           CU_TENSOR_MAP_INTERLEAVE_NONE, box[0] == 32 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+                           CU_TENSOR_MAP_INTERLEAVE_NONE, box[0] == 16   ? CU_TENSOR_MAP_SWIZZLE_32B
+                           : box[0] == 32 ? CU_TENSOR_MAP_SWIZZLE_64B
+                                          : CU_TENSOR_MAP_SWIZZLE_128B,
                            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? MK_OK : fail(MK_ERR_CUDA, "cuTensorMapEncodeTiled: error %d", int(r));
 }
