@@ -7,6 +7,7 @@ t = scale x . down has (k / 16 + 20) 2^-22 of its own absolute sum (up to 16 par
 the second product in two bf16 parts, each off by at most 2^-9 of what is left (2^-18 together), or three (2^-27, below fp32's
 own 2^-24); the second product adds 3 steps per 16 columns of the rank to the contraction.  Activations and output as
 for mk_linear."""
+import gc
 import math
 
 import pytest
@@ -20,6 +21,13 @@ if not torch.cuda.is_available():
 import persistent_megakernel_decode_sm_gb300 as mk  # noqa: E402
 
 BF, F32 = torch.bfloat16, torch.float32
+
+
+@pytest.fixture(scope="module", autouse=True)
+def nothing_left_behind():
+    """Tracebacks of refused calls hold tensors in cycles: they go before the next module's tests look at the memory."""
+    yield
+    gc.collect()
 
 
 def randn(shape, seed, std=1.0, dtype=BF):

@@ -1,5 +1,6 @@
 """mk_assign_pages against a plain restatement that walks the requests one by one: every output is a whole number and has to be
 equal."""
+import gc
 import random
 
 import pytest
@@ -11,6 +12,13 @@ if not torch.cuda.is_available():
     pytest.skip("needs a CUDA GPU", allow_module_level=True)
 
 import persistent_megakernel_decode_sm_gb300 as mk  # noqa: E402
+
+
+@pytest.fixture(scope="module", autouse=True)
+def nothing_left_behind():
+    """Tracebacks of refused calls hold tensors in cycles: they go before the next module's tests look at the memory."""
+    yield
+    gc.collect()
 
 
 class Pool:

@@ -4,6 +4,8 @@ both layouts, padded batches.
 Tolerance per element: x, gains, cosines and sines enter in fp32 (an angle's error is at most 2^-23, the arithmetic of the norm
 and of the rotation about 12 roundings of 2^-24), so values are off by at most 2^-19 of the larger of the pair before the
 output's own rounding (half a step of bf16, 2^-8 of the value)."""
+import gc
+
 import pytest
 import torch
 
@@ -16,6 +18,13 @@ import persistent_megakernel_decode_sm_gb300 as mk  # noqa: E402
 from workload import KVCache  # noqa: E402
 
 BF, F32 = torch.bfloat16, torch.float32
+
+
+@pytest.fixture(scope="module", autouse=True)
+def nothing_left_behind():
+    """Tracebacks of refused calls hold tensors in cycles: they go before the next module's tests look at the memory."""
+    yield
+    gc.collect()
 
 
 def randn(shape, seed, std=1.0, dtype=BF):
