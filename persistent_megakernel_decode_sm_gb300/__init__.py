@@ -525,7 +525,7 @@ class _NoCallModule:   # (leaves every call to Python)
     def linear(*args):
         return None
 
-    attend = linear
+    attend = adapted_linear = rope_append = assign_pages = linear
 
 
 _fast = None   # _mk_call, once it has torch's objects
@@ -538,8 +538,9 @@ def _setup():
         return _fast
     import torch
     c = torch._C
-    _mk_call.setup(*(ctypes.cast(f, _P).value for f in (lib.mk_linear, lib.mk_attend, lib.mk_attend_workspace)), torch.bfloat16,
-                   torch.float32, torch.int32, torch.empty, c._cuda_getCurrentRawStream, c._cuda_getDevice,
+    _mk_call.setup(*(ctypes.cast(f, _P).value for f in (lib.mk_linear, lib.mk_attend, lib.mk_attend_workspace, lib.mk_linear_adapted,
+                                                        lib.mk_linear_adapted_workspace, lib.mk_rope_append, lib.mk_assign_pages)),
+                   torch.bfloat16, torch.float32, torch.float64, torch.int32, torch.empty, c._cuda_getCurrentRawStream, c._cuda_getDevice,
                    c._cuda_cudaCachingAllocator_raw_alloc, c._cuda_cudaCachingAllocator_raw_delete)
     _fast = _mk_call
     return _fast
@@ -745,9 +746,12 @@ def adapted_linear(x, weight, adapters, index, bias=None, activation: Optional[s
 
     status: as in linear(), and MK_ERR_BOUNDS for an index of n_adapters or more, which counts as none.  No gradients are
     recorded."""
+    down, up, scale = adapters if len(adapters) == 3 else (*adapters, None)
+    y = (_fast or _setup()).adapted_linear(x, weight, bias, activation, residual, out, out_dtype, status, down, up, scale, index, workspace)
+    if y is not None:
+        return y
     import torch
     bf = torch.bfloat16
-    down, up, scale = adapters if len(adapters) == 3 else (*adapters, None)
     dev, out, args = _linear_args(x, weight, bias, activation, residual, out, out_dtype, status)
     (count, rank, k), ds = _operand(down, "down", (bf,), dev, 3)
     ushape, us = _operand(up, "up", (bf,), dev, 3)
@@ -782,6 +786,10 @@ def rope_append(qkv, kv, positions, slots, freqs, layer: int = 0, sections: Opti
 
     status: a CUDA int32 tensor of one element, zeroed by the caller, that receives MK_ERR_BOUNDS for a slot behind the
     cache (not stored).  No gradients are recorded."""
+    q = (_fast or _setup()).rope_append(qkv, kv.k, kv.v, positions, slots, freqs, layer, sections, neighbours, q_gain, k_gain, eps, out,
+                                        status)
+    if q is not None:
+        return q
     import torch
     bf, f32 = torch.bfloat16, torch.float32
     dev = qkv.get_device()
@@ -843,13 +851,17 @@ def assign_pages(ring, ends, table, lens, new_lens, block_size: int, max_tokens:
     status: a CUDA int32 tensor of one element, zeroed by the caller: MK_ERR_CAPACITY (too few free blocks, more tokens than
     max_tokens) or MK_ERR_BOUNDS (lengths or ends that cannot be) where nothing was assigned and every slot is -1; MK_ERR_BOUNDS
     also for a block id outside the ring's n_blocks."""
-    import torch
-    dev, i32 = ring.get_device(), (torch.int32,)
-    operands = dict(ring=(ring, 1), ends=(ends, 1), table=(table, 2), lens=(lens, 1), new_lens=(new_lens, 1))
     if ends_out is None:
         ends_out = ends
-    else:
-        operands["ends_out"] = (ends_out, 1)
+    if out is not None:
+        out = tuple(out)
+    taken = (_fast or _setup()).assign_pages(ring, ends, ends_out, table, lens, new_lens, block_size, max_tokens, shared_prefix, out,
+                                             status)
+    if taken is not None:
+        return taken
+    import torch
+    dev, i32 = ring.get_device(), (torch.int32,)
+    operands = dict(ring=(ring, 1), ends=(ends, 1), ends_out=(ends_out, 1), table=(table, 2), lens=(lens, 1), new_lens=(new_lens, 1))
     for name, (t, dim) in operands.items():
         _operand(t, name, i32, dev, dim)
     (batch, columns), n_blocks = table.shape, ring.shape[0]
@@ -860,7 +872,6 @@ def assign_pages(ring, ends, table, lens, new_lens, block_size: int, max_tokens:
     if out is None:
         out = tuple(torch.empty(n, dtype=torch.int32, device=ring.device) for n in (max_tokens, max_tokens, max_tokens, batch + 1))
     else:
-        out = tuple(out)
         for name, t, n in zip(("slots", "positions", "sequences", "first"), out, (max_tokens, max_tokens, max_tokens, batch + 1), strict=True):
             if _operand(t, name, i32, dev, 1)[0][0] != n:
                 raise ValueError(f"{name} must have {n} elements")
