@@ -1,5 +1,6 @@
 // Norms of q and k, rotation by the tokens' positions, q to its buffer, k and v to the cache (mk_rope_append).
 #include <algorithm>
+#include <atomic>
 #include <climits>
 #include <cmath>
 
@@ -10,12 +11,12 @@ namespace mk {
 
 constexpr int kRopePairs = 128;     // of the widest head
 constexpr int kRopeThreads = 128;
+constexpr int kRopeCtas = 4;        // of an SM
 
 struct RopeParams {
-    int tokens, nq, nkv, heads;     // heads: nq + 2 nkv
+    int tokens, nq, nkv;
     int units, turned;              // 16 elements each: of a head, of its rotated part
-    int rounds, per;                // of a token: rounds of the heads that a warp takes at a time; rounds of one warp
-    int parts;                      // warps of a token
+    int rounds_q, rounds_k, rounds; // of a token: rounds of heads that a warp takes at a time, for q, k and in all
     const void* qkv;
     int64_t qkv_stride;
     const __nv_bfloat16* q_gain;
@@ -36,145 +37,239 @@ struct RopeParams {
 };
 
 // cos and sin of position * rate: the product wraps at whole turns, so the angle is reduced exactly for every 32-bit
-// position (an angle in fp32 radians would be off by 2^-24 of itself); 31 bits of it become an fp32 in [-1, 1) half turns.
+// position (an angle in fp32 radians would be off by 2^-24 of itself); 32 bits of it become radians in [-pi, pi), where the
+// special-function unit's sine and cosine are off by at most 2^-20.9: their precise forms cost 50 instructions a pair, a quarter of a token's,
+// and an output keeps 2^-9 of its value.
 __device__ __forceinline__ float2 rope_angle(int position, uint64_t rate) {
     const uint64_t turns = uint64_t(int64_t(position)) * rate;
-    float2 cs;
-    sincospif(float(int32_t(turns >> 32)) * 0x1p-31f, &cs.y, &cs.x);
-    return cs;
+    const float angle = float(int32_t(turns >> 32)) * 1.46291807926715968e-9f;   // pi / 2^31
+    return make_float2(__cosf(angle), __sinf(angle));
 }
-
-// 8 elements at `at` in fp32
-template <bool F32>
-__device__ __forceinline__ void rope_load(const void* row, int at, uint4 (&raw)[F32 ? 2 : 1]) {
-    if constexpr (F32) {
-        const uint4* p = reinterpret_cast<const uint4*>(static_cast<const float*>(row) + at);
-        raw[0] = __ldcs(p);
-        raw[1] = __ldcs(p + 1);
-    } else {
-        raw[0] = __ldcs(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(row) + at));
-    }
-}
-__device__ __forceinline__ void rope_widen(const uint4& u, float* x) {
+__device__ __forceinline__ void rope_widen(const uint4& u, float2* x) {   // 8 bf16
     const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        x[2 * k] = __uint_as_float(w[k] << 16);
-        x[2 * k + 1] = __uint_as_float(w[k] & 0xFFFF0000u);
-    }
+    for (int k = 0; k < 4; ++k) x[k] = make_float2(__uint_as_float(w[k] << 16), __uint_as_float(w[k] & 0xFFFF0000u));
 }
-template <bool F32>
-__device__ __forceinline__ void rope_values(const uint4 (&raw)[F32 ? 2 : 1], float* x) {
-    if constexpr (F32) {
-        *reinterpret_cast<uint4*>(x) = raw[0];
-        *reinterpret_cast<uint4*>(x + 4) = raw[1];
-    } else {
-        rope_widen(raw[0], x);
-    }
-}
-__device__ __forceinline__ uint4 rope_pack(const float* x) {
+__device__ __forceinline__ uint4 rope_pack(const float2* x) {
     uint32_t w[4];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[k]) : "f"(x[2 * k + 1]), "f"(x[2 * k]));
+    for (int k = 0; k < 4; ++k) asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[k]) : "f"(x[k].y), "f"(x[k].x));
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// A warp takes `per` rounds of a token's heads; a round is 32 / GROUP heads of GROUP lanes, a lane holds 16 elements (two
-// 16-byte pieces of bf16): the pairs 8 u .. 8 u + 7, whose elements lie rotary / 2 apart or side by side, or 16 elements that
-// only pass.  A head's sum of squares is a shuffle over its lanes; a token's cosines and sines are worked out once by the warp.
+// A round is 32 / GROUP heads of one kind (q, k or v) of GROUP lanes each; a lane holds 16 elements, two pieces of 8: pairs of
+// elements between the pieces (rotary / 2 apart) or within them, or elements that only pass.  A head's sum of squares is a shuffle
+// over its lanes; a token's cosines and sines are worked out once by the warp, and a kind's gains are multiplied into them once.
+//
+// The rounds of all tokens in order are shared out evenly over the warps.  A warp's heads come as bulk copies of up to kRounds
+// rounds into places of its own, kDepth of them in flight, through the next tokens: what is in flight takes neither registers nor
+// instructions.
+// What bounds it: 16384 tokens of 48 heads of 128, bf16, normed, three axes 69 us (5.8 TB/s, 86% of a copy's rate), 4096 of fp32 26.5
+// (5.7 TB/s; 2 us of it the launch and the first copies' way): the chain sums - shuffles - root - products of a round, with 16
+// warps an SM (a lane's 32 factors take 112 registers; 20 warps with 96 take as long) and issue slots half used.  Loads
+// straight into registers took 88 and 29.7; 16-byte copies by every lane (cp.async) 72 and 42; whole tokens to the warps in turn 74 and 28.9
+// (their last round fills the device unevenly); copies of 4 KB, three in flight, 72 and 26.8; two rounds side by side 73.
+template <bool F32>
+struct RopeTile {
+    static constexpr int kPlace = 2048, kRounds = kPlace / (F32 ? 2048 : 1024), kDepth = 4;   // (a round is at most 512 elements)
+    static constexpr int kSmem = kRopeThreads / 32 * kDepth * kPlace;
+};
 template <int GROUP, bool F32, bool NEIGHBOURS>
-__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constant__ RopeParams p) {
-    __shared__ float4 angles[kRopeThreads / 32][kRopePairs / 2];
+__global__ void __launch_bounds__(kRopeThreads, kRopeCtas) rope_kernel(const __grid_constant__ RopeParams p) {
+    using T = RopeTile<F32>;
+    constexpr int kHeads = 32 / GROUP, kSize = F32 ? 4 : 2;
+    extern __shared__ __align__(16) uint8_t places[];
+    __shared__ __align__(16) float angles[kRopeThreads / 32][2][kRopePairs];   // cosines, sines
+    __shared__ uint64_t bars[kRopeThreads / 32][T::kDepth];
+    __shared__ int abort_flag;
+    volatile int* abort_word = &abort_flag;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const uint32_t place0 = sm::smem(places) + uint32_t(warp * T::kDepth * T::kPlace), bar0 = sm::smem(bars[warp]);
+    if (threadIdx.x == 0) abort_flag = 0;
+    if (lane == 0) {
+        for (int i = 0; i < T::kDepth; ++i) sm::bar_init(bar0 + 8u * i, 1);
+        sm::bar_fence_init();
+    }
+    __syncthreads();
     sm::pdl_trigger();
     sm::pdl_wait();
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t job = int64_t(blockIdx.x) * (kRopeThreads / 32) + warp;
-    const int t = int(job / p.parts), r0 = int(job % p.parts) * p.per, r1 = min(r0 + p.per, p.rounds);
-    if (t >= p.tokens) return;
-    float2* mine = reinterpret_cast<float2*>(angles[warp]);
-    for (int i = lane; i < 8 * p.turned; i += 32) mine[i] = rope_angle(p.positions[p.axis[i] * p.position_stride + t], p.turn[i]);
-    const int slot = p.slots[t];
-    const bool stored = slot >= 0 && slot < p.limit;
-    if (slot >= p.limit && p.status) *p.status = MK_ERR_BOUNDS;
-    const int sequence = stored ? slot / p.max_seq : 0;
     const int d = 16 * p.units;
-    const int64_t cache = int64_t(sequence) * p.batch_stride + (int64_t(slot) - int64_t(sequence) * p.max_seq) * d;
-    __syncwarp();
+    const int64_t all = int64_t(p.tokens) * p.rounds, warps = int64_t(gridDim.x) * (kRopeThreads / 32),
+                  self = int64_t(blockIdx.x) * (kRopeThreads / 32) + warp, begin = all * self / warps;
+    const int count = int(all * (self + 1) / warps - begin);   // this warp's rounds, from a token and a round of it
+    const int t0 = int(begin / p.rounds), round0 = int(begin - int64_t(t0) * p.rounds);
+    const int round_k = p.rounds_q, round_v = p.rounds_q + p.rounds_k;
+
+    // the next copy: rounds [r, r + n) of the token of `row`, whose heads lie one behind the other whatever their kinds
+    auto head_of = [&](int r) {   // the first head of a round (of the one behind the last: all)
+        return r <= round_k ? min(r * kHeads, p.nq) : r <= round_v ? p.nq + min((r - round_k) * kHeads, p.nkv) : p.nq + p.nkv + min((r - round_v) * kHeads, p.nkv);
+    };
+    int next_left = count, next_r = round0, next_at = 0;
+    const char* row = static_cast<const char*>(p.qkv) + int64_t(t0) * p.qkv_stride * kSize;
+    auto fetch = [&] {
+        if (next_left <= 0) return;
+        const int n = min(min(p.rounds - next_r, T::kRounds), next_left);
+        if (lane == 0) {
+            const int from = head_of(next_r);
+            const uint32_t bytes = uint32_t((head_of(next_r + n) - from) * d * kSize), bar = bar0 + 8u * next_at;
+            sm::bar_expect(bar, bytes);
+            sm::bulk_load(place0 + uint32_t(next_at * T::kPlace), row + int64_t(from) * d * kSize, bytes, bar);
+        }
+        next_left -= n;
+        next_r += n;
+        if (next_r == p.rounds) {
+            next_r = 0;
+            row += p.qkv_stride * kSize;
+        }
+        next_at = next_at + 1 == T::kDepth ? 0 : next_at + 1;
+    };
+#pragma unroll 1
+    for (int i = 0; i < T::kDepth; ++i) fetch();
 
     const int u = lane % GROUP, sub = lane / GROUP;
-    const bool live = u < p.units, turns = u < p.turned;
-    const int lo = turns && !NEIGHBOURS ? 8 * u : 16 * u, hi = turns && !NEIGHBOURS ? 8 * (p.turned + u) : 16 * u + 8;
-    float cs[16];   // the lane's 8 pairs: cosine, sine
-    if (turns)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) *reinterpret_cast<float4*>(cs + 4 * i) = angles[warp][4 * u + i];
-    const int64_t row = int64_t(t) * p.qkv_stride;
-    const void* src = F32 ? static_cast<const void*>(static_cast<const float*>(p.qkv) + row)
-                          : static_cast<const void*>(static_cast<const __nv_bfloat16*>(p.qkv) + row);
-    constexpr int kAhead = F32 ? 2 : 4;   // rounds whose loads are in flight together
-    for (int r = r0; r < r1; r += kAhead) {
-        uint4 raw[kAhead][2][F32 ? 2 : 1];
-#pragma unroll
-        for (int i = 0; i < kAhead; ++i) {
-            const int h = (r + i) * (32 / GROUP) + sub;
-            if (r + i < r1 && h < p.heads && live) {
-                rope_load<F32>(src, h * d + lo, raw[i][0]);
-                rope_load<F32>(src, h * d + hi, raw[i][1]);
+    const bool live = u < p.units;
+    // where the lane's pieces start in a head: of q and k, and of v (neighbouring lanes' pieces lie side by side)
+    const int from = u < p.turned ? 0 : p.turned, lo_qk = 16 * from + 8 * (u - from),
+              hi_qk = lo_qk + 8 * (u < p.turned ? p.turned : p.units - p.turned);
+    int at = 0, have = 0, chunk_head = 0;   // rounds left of the copy being read, its first head
+    uint32_t phase = 0;
+    bool ok = true;
+#pragma unroll 1
+    for (int t = t0, left = count, first = round0; left > 0 && ok; ++t, first = 0) {
+        const int last = min(first + left, p.rounds);
+        left -= last - first;
+        __syncwarp();
+        if (first < round_v)
+            for (int i = lane; i < 8 * p.turned; i += 32) {
+                const float2 cs = rope_angle(p.positions[p.axis[i] * p.position_stride + t], p.turn[i]);
+                angles[warp][0][i] = cs.x;
+                angles[warp][1][i] = cs.y;
             }
-        }
+        const int slot = p.slots[t];
+        const bool stored = slot >= 0 && slot < p.limit;
+        if (slot >= p.limit && p.status) *p.status = MK_ERR_BOUNDS;
+        const int sequence = stored ? slot / p.max_seq : 0;
+        const int64_t cache = int64_t(sequence) * p.batch_stride + (int64_t(slot) - int64_t(sequence) * p.max_seq) * d;
+        __syncwarp();
+        int r = first;
+#pragma unroll 1
+        for (int kind = 0; kind < 3 && ok; ++kind) {
+            const int heads = kind == 0 ? p.nq : p.nkv, r0 = kind == 0 ? 0 : kind == 1 ? round_k : round_v,
+                      r1 = min(last, kind == 0 ? round_k : kind == 1 ? round_v : p.rounds);
+            if (r >= r1) continue;
+            const bool turn = u < p.turned && kind < 2;
+            const int lo = kind < 2 ? lo_qk : 8 * u, hi = kind < 2 ? hi_qk : 8 * (p.units + u);
+            __nv_bfloat16* const out = kind == 0 ? p.q + int64_t(t) * p.q_stride : (kind == 1 ? p.k : p.v) + cache;
+            const int64_t out_stride = kind == 0 ? d : p.head_stride;
+            const bool writes = live && (kind == 0 || stored);
+            const __nv_bfloat16* gain = kind == 0 ? p.q_gain : kind == 1 ? p.k_gain : nullptr;
+            // an element's own factor, and that of the other one of its pair: (a, b) -> (a g c - b h s, b h c + a g s)
+            float2 own[8], across[8];
 #pragma unroll
-        for (int i = 0; i < kAhead; ++i) {
-            if (r + i >= r1) break;
-            const int h = (r + i) * (32 / GROUP) + sub;
-            const bool here = h < p.heads && live;
-            float x[16];
-#pragma unroll
-            for (int k = 0; k < 16; ++k) x[k] = 0.f;
-            if (here) {
-                rope_values<F32>(raw[i][0], x);
-                rope_values<F32>(raw[i][1], x + 8);
+            for (int k = 0; k < 8; ++k) own[k] = make_float2(1.f, 1.f);
+            if (gain && live) {
+                rope_widen(__ldg(reinterpret_cast<const uint4*>(gain + lo)), own);
+                rope_widen(__ldg(reinterpret_cast<const uint4*>(gain + hi)), own + 4);
             }
-            const __nv_bfloat16* gain = h < p.nq ? p.q_gain : h < p.nq + p.nkv ? p.k_gain : nullptr;
-            if (p.q_gain || p.k_gain) {   // (uniform: every lane of the warp takes part in the sums)
-                float ss = 0.f;
+            if (turn) {
 #pragma unroll
-                for (int k = 0; k < 16; ++k) ss = fmaf(x[k], x[k], ss);
-#pragma unroll
-                for (int o = GROUP / 2; o; o >>= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, o);
-                if (gain && here) {
-                    const float scale = 1.f / sqrtf(fmaf(ss, p.inv_d, p.eps));
-                    float g[16];
-                    rope_widen(__ldg(reinterpret_cast<const uint4*>(gain + lo)), g);
-                    rope_widen(__ldg(reinterpret_cast<const uint4*>(gain + hi)), g + 8);
-#pragma unroll
-                    for (int k = 0; k < 16; ++k) x[k] *= scale * g[k];
+                for (int k = 0; k < 4; ++k) {   // two pairs a step
+                    const int pair = NEIGHBOURS ? 4 * u + 2 * (k & 1) + (k < 2 ? 0 : 4 * p.turned) : 8 * u + 2 * k;
+                    const float2 c = *reinterpret_cast<const float2*>(&angles[warp][0][pair]), s = *reinterpret_cast<const float2*>(&angles[warp][1][pair]);
+                    if (NEIGHBOURS) {
+                        float2 &g0 = own[2 * k], &g1 = own[2 * k + 1];
+                        across[2 * k] = make_float2(-g0.y * s.x, g0.x * s.x);
+                        across[2 * k + 1] = make_float2(-g1.y * s.y, g1.x * s.y);
+                        g0 = sm::mul2(g0, make_float2(c.x, c.x));
+                        g1 = sm::mul2(g1, make_float2(c.y, c.y));
+                    } else {
+                        across[k] = sm::mul2(own[k + 4], make_float2(-s.x, -s.y));
+                        across[k + 4] = sm::mul2(own[k], s);
+                        own[k] = sm::mul2(own[k], c);
+                        own[k + 4] = sm::mul2(own[k + 4], c);
+                    }
                 }
             }
-            if (!here) continue;
-            if (turns && h < p.nq + p.nkv) {
+            const int apart = (hi - lo) * kSize;
+#pragma unroll 1
+            while (r < r1) {
+                if (have == 0) {   // the next copy
+                    if (!(ok = sm::bar_wait_warp(bar0 + 8u * at, phase, abort_word, p.status))) break;
+                    have = min(last - r, T::kRounds);
+                    chunk_head = head_of(r);
+                }
+                const int n = min(r1 - r, have);
+                const uint8_t* src = places + (warp * T::kDepth + at) * T::kPlace + ((head_of(r) - chunk_head + sub) * d + lo) * kSize;
+#pragma unroll 1
+                for (int i = 0; i < n; ++i, src += kHeads * d * kSize) {
+                    // (lanes without a head or a piece read their round's place, whatever is there, and store nothing)
+                    const int h = (r - r0 + i) * kHeads + sub;
+                    const bool here = live && h < heads;
+                    float2 x[8];
+                    if constexpr (F32) {
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    float &a = NEIGHBOURS ? x[2 * k] : x[k], &b = NEIGHBOURS ? x[2 * k + 1] : x[k + 8];
-                    const float c = cs[2 * k], s = cs[2 * k + 1], a0 = a;
-                    a = a0 * c - b * s;
-                    b = a0 * s + b * c;
+                        for (int k = 0; k < 2; ++k) {
+                            *reinterpret_cast<float4*>(x + 2 * k) = *reinterpret_cast<const float4*>(src + 16 * k);
+                            *reinterpret_cast<float4*>(x + 4 + 2 * k) = *reinterpret_cast<const float4*>(src + apart + 16 * k);
+                        }
+                    } else {
+                        rope_widen(*reinterpret_cast<const uint4*>(src), x);
+                        rope_widen(*reinterpret_cast<const uint4*>(src + apart), x + 4);
+                    }
+                    if (gain) {
+                        float2 s2 = make_float2(0.f, 0.f), s3 = s2;
+#pragma unroll
+                        for (int k = 0; k < 8; k += 2) {
+                            s2 = sm::fma2(x[k], x[k], s2);
+                            s3 = sm::fma2(x[k + 1], x[k + 1], s3);
+                        }
+                        float ss = here ? (s2.x + s3.x) + (s2.y + s3.y) : 0.f;
+#pragma unroll
+                        for (int o = GROUP / 2; o; o >>= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, o);
+                        const float scale = rsqrtf(fmaf(ss, p.inv_d, p.eps));
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) x[k] = sm::mul2(x[k], make_float2(scale, scale));
+                    }
+                    if (turn) {
+                        float2 y[8];
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            y[k] = sm::fma2(NEIGHBOURS ? make_float2(x[k].y, x[k].x) : x[k ^ 4], across[k], sm::mul2(x[k], own[k]));
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) x[k] = y[k];
+                    } else if (gain) {
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) x[k] = sm::mul2(x[k], own[k]);
+                    }
+                    if (here && writes) {
+                        __nv_bfloat16* dst = out + h * out_stride;
+                        *reinterpret_cast<uint4*>(dst + lo) = rope_pack(x);
+                        *reinterpret_cast<uint4*>(dst + hi) = rope_pack(x + 4);
+                    }
+                }
+                r += n;
+                have -= n;
+                if (have == 0) {
+                    if (++at == T::kDepth) { at = 0; phase ^= 1u; }
+                    __syncwarp();
+                    fetch();   // (into the place that was just read)
                 }
             }
-            __nv_bfloat16* dst;
-            if (h < p.nq) dst = p.q + int64_t(t) * p.q_stride + h * d;
-            else {
-                if (!stored) continue;
-                const bool is_k = h < p.nq + p.nkv;
-                dst = (is_k ? p.k : p.v) + cache + int64_t(h - p.nq - (is_k ? 0 : p.nkv)) * p.head_stride;
-            }
-            *reinterpret_cast<uint4*>(dst + lo) = rope_pack(x);
-            *reinterpret_cast<uint4*>(dst + hi) = rope_pack(x + 8);
         }
+    }
+    if (!ok && lane == 0) {   // a wait ran out: the copies still in flight end before the CTA does
+        const uint64_t t1 = sm::timer_ns();
+        while (sm::timer_ns() - t1 < 10000000ull) {}
     }
 }
 
-template <int GROUP, bool F32>
-static mk_status rope_launch(const RopeParams& p, bool neighbours, int64_t blocks, cudaStream_t stream) {
+template <int GROUP, bool F32, bool NEIGHBOURS>
+static mk_status rope_launch(const RopeParams& p, int device, int sms, cudaStream_t stream) {
+    static std::atomic<uint64_t> set{0};
+    const mk_status st = op_smem(reinterpret_cast<const void*>(&rope_kernel<GROUP, F32, NEIGHBOURS>), RopeTile<F32>::kSmem, device, &set);
+    if (st != MK_OK) return st;
+    constexpr int kWarps = kRopeThreads / 32;
+    const int64_t rounds = int64_t(p.tokens) * p.rounds;
     cudaLaunchConfig_t cfg{};
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -182,19 +277,20 @@ static mk_status rope_launch(const RopeParams& p, bool neighbours, int64_t block
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     cfg.stream = stream;
-    cfg.gridDim = dim3(unsigned(blocks));
+    cfg.gridDim = dim3(unsigned(std::min<int64_t>((rounds + kWarps - 1) / kWarps, int64_t(sms) * kRopeCtas)));
     cfg.blockDim = dim3(kRopeThreads);
-    MK_CK(neighbours ? cudaLaunchKernelEx(&cfg, &rope_kernel<GROUP, F32, true>, p) : cudaLaunchKernelEx(&cfg, &rope_kernel<GROUP, F32, false>, p));
+    cfg.dynamicSmemBytes = RopeTile<F32>::kSmem;
+    MK_CK(cudaLaunchKernelEx(&cfg, &rope_kernel<GROUP, F32, NEIGHBOURS>, p));
     return MK_OK;
 }
 template <int GROUP>
-static mk_status rope_launch(RopeParams& p, bool f32, bool neighbours, int sms, cudaStream_t stream) {
-    p.rounds = (p.heads + 32 / GROUP - 1) / (32 / GROUP);
-    // few tokens: a warp for every round; many: a warp takes a token
-    p.per = int64_t(p.tokens) * p.rounds <= 16 * int64_t(sms) ? 1 : p.rounds;
-    p.parts = (p.rounds + p.per - 1) / p.per;
-    const int64_t warps = int64_t(p.tokens) * p.parts, blocks = (warps + kRopeThreads / 32 - 1) / (kRopeThreads / 32);
-    return f32 ? rope_launch<GROUP, true>(p, neighbours, blocks, stream) : rope_launch<GROUP, false>(p, neighbours, blocks, stream);
+static mk_status rope_launch(RopeParams& p, bool f32, bool neighbours, int device, int sms, cudaStream_t stream) {
+    p.rounds_q = (p.nq + 32 / GROUP - 1) / (32 / GROUP);
+    p.rounds_k = (p.nkv + 32 / GROUP - 1) / (32 / GROUP);
+    p.rounds = p.rounds_q + 2 * p.rounds_k;
+    if (f32)
+        return neighbours ? rope_launch<GROUP, true, true>(p, device, sms, stream) : rope_launch<GROUP, true, false>(p, device, sms, stream);
+    return neighbours ? rope_launch<GROUP, false, true>(p, device, sms, stream) : rope_launch<GROUP, false, false>(p, device, sms, stream);
 }
 
 static mk_status rope_check(const mk_rope_args* a) {
@@ -277,7 +373,7 @@ extern "C" mk_status mk_rope_append(const mk_rope_args* a, void* stream) {
     if ((st = op_device(&device, &sms)) != MK_OK) return st;
     RopeParams p{};
     const int d = a->head_dim;
-    p.tokens = a->tokens; p.nq = a->n_q_heads; p.nkv = a->n_kv_heads; p.heads = p.nq + 2 * p.nkv;
+    p.tokens = a->tokens; p.nq = a->n_q_heads; p.nkv = a->n_kv_heads;
     p.units = d / 16; p.turned = a->rotary / 16;
     p.qkv = a->qkv; p.qkv_stride = a->qkv_stride;
     p.q_gain = static_cast<const __nv_bfloat16*>(a->q_gain);
@@ -306,9 +402,9 @@ extern "C" mk_status mk_rope_append(const mk_rope_args* a, void* stream) {
     }
     const bool f32 = a->qkv_dtype == MK_F32, nb = a->neighbours != 0;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (p.units <= 1) return rope_launch<1>(p, f32, nb, sms, s);
-    if (p.units <= 2) return rope_launch<2>(p, f32, nb, sms, s);
-    if (p.units <= 4) return rope_launch<4>(p, f32, nb, sms, s);
-    if (p.units <= 8) return rope_launch<8>(p, f32, nb, sms, s);
-    return rope_launch<16>(p, f32, nb, sms, s);
+    if (p.units <= 1) return rope_launch<1>(p, f32, nb, device, sms, s);
+    if (p.units <= 2) return rope_launch<2>(p, f32, nb, device, sms, s);
+    if (p.units <= 4) return rope_launch<4>(p, f32, nb, device, sms, s);
+    if (p.units <= 8) return rope_launch<8>(p, f32, nb, device, sms, s);
+    return rope_launch<16>(p, f32, nb, device, sms, s);
 }

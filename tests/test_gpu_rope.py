@@ -1,9 +1,9 @@
 """mk_rope_append against the formula in 64 bits: norms, rotated widths, pairs, axes, positions far along, caches of
 both layouts, padded batches.
 
-Tolerance per element: x, gains, cosines and sines enter in fp32 (an angle's error is at most 2^-23, the arithmetic of the norm
-and of the rotation about 12 roundings of 2^-24), so values are off by at most 2^-19 of the larger of the pair before the
-output's own rounding (half a step of bf16, 2^-8 of the value)."""
+Tolerance per element: x and gains enter in fp32; cosines and sines are off by at most 2^-20.9 (the special-function unit's bound
+on [-pi, pi]) and the rounding of the angle, 2^-22; the arithmetic of the norm and of the rotation is about 12 roundings of 2^-24.
+So values are off by at most 2^-19 of the pair's sum before the output's own rounding (half a step of bf16, 2^-8 of the value)."""
 import gc
 
 import pytest
