@@ -6,14 +6,13 @@
 
 namespace mk {
 
-constexpr int kLowThreads = 256, kLowWarps = kLowThreads / 32;
-constexpr int kLowRank = 32;        // columns of the rank at a time: 4 products of 8
+constexpr int kLowThreads = 256, kLowTokens = 16, kLowWarps = kLowThreads / 32;
 constexpr int kLowTile = 256;       // most tokens of a tile of the linear map
 
 struct LowParams {
     int rows, k, rank, n_adapters;
-    int tile, subs;                 // tokens of a tile of the linear map, blocks of kTokens tokens in it
-    int slots, items, f32;          // as LinearExtra; whether the output is fp32: three terms
+    int tile, subs;                 // tokens of a tile of the linear map, blocks of kLowTokens tokens in it
+    int slots, width, f32;          // as LinearExtra; whether the output is fp32: three parts
     const __nv_bfloat16* x;
     int64_t x_stride;
     const __nv_bfloat16* down;
@@ -21,8 +20,9 @@ struct LowParams {
     const int32_t* index;
     int32_t* count;
     int32_t* list;
-    __nv_bfloat16* terms;
-    int64_t terms_stride;
+    __nv_bfloat16* terms;           // [rows][blocks][2][32]: the first two parts
+    __nv_bfloat16* third;           // [rows][blocks][32]
+    int64_t blocks;
     int32_t* status;
 };
 
@@ -31,19 +31,25 @@ __device__ __forceinline__ void low_mma(float (&d)[4], uint32_t a0, uint32_t a1,
                  : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+__device__ __forceinline__ uint4 low_load(const __nv_bfloat16* p, bool wanted) {
+    return wanted ? __ldg(reinterpret_cast<const uint4*>(p)) : make_uint4(0, 0, 0, 0);
+}
 
-// A cluster works on `16 MT` neighbouring tokens of one tile of the linear map, for the tile's adapters y, y + gridDim.y, ..: those of
-// its tokens that name the adapter get their low-rank row, the others zeros.  x and down are read from global memory straight
-// into the operands of m16n8k16 products (a thread's 16 bytes of a row are the elements 2 i, 2 i + 1 of two products: the
-// contraction may take its elements in any order as long as both operands do), only rows that count.  The contraction is
-// shared out over the warps and the CTAs of the cluster in blocks of 32; the sums meet in shared memory, in a fixed order.
+// A cluster works on 16 neighbouring tokens of one tile of the linear map, for the tile's adapters y, y + gridDim.y, ..: those of
+// its tokens that name the adapter get their low-rank row, the others zeros.  8 NT columns of the rank at a time; x and down are
+// read from global memory straight into the operands of m16n8k16 products (a thread's 16 bytes of a row are the elements 2 i, 2 i + 1
+// of two products: the contraction may take its elements in any order as long as both operands do), only rows that count.  The
+// contraction is shared out over the warps and the CTAs of the cluster in blocks of 32; the sums meet in shared memory, in a
+// fixed order, once for all columns of the rank.
 // These products need no more than the reading of x and down does (they are 1/8 to 1/100 of the linear map's), so they stay on
 // mma.sync, with registers for operands and no staging.
-template <int MT>
+template <int NT>
 __global__ void __launch_bounds__(kLowThreads) low_rank_kernel(const __grid_constant__ LowParams p) {
-    constexpr int kTokens = 16 * MT;
-    __shared__ int name[kLowTile], list[kLowTile], warp_heads[kLowWarps];
-    __shared__ float part[kLowWarps][16][kLowRank], sums[kTokens][kLowRank];
+    constexpr int kCols = 8 * NT;
+    extern __shared__ float all_sums[];                 // [2][16][width], in turn for the adapters
+    __shared__ __align__(16) int name[kLowTile];
+    __shared__ int list[kLowTile], warp_heads[kLowWarps];
+    __shared__ float part[kLowWarps][16][kCols];
     // every kernel before this one is done when the next one may start: it reads x beside this one
     sm::pdl_wait();
     sm::pdl_trigger();
@@ -51,133 +57,139 @@ __global__ void __launch_bounds__(kLowThreads) low_rank_kernel(const __grid_cons
     const int split = int(gridDim.z), rank_z = int(blockIdx.z);
     const int m = int(blockIdx.x) / p.subs, sub = int(blockIdx.x) % p.subs, m0 = m * p.tile, tokens = min(p.tile, p.rows - m0);
     // the tile's adapters in the order in which its tokens name them
-    int mine = -1;
-    if (t < tokens) {
-        mine = p.index[m0 + t];
-        if (mine >= p.n_adapters) {
-            if (p.status) *p.status = MK_ERR_BOUNDS;
-            mine = -1;
-        }
-    }
-    name[t] = mine;
-    __syncthreads();
-    bool head = mine >= 0 && (t == 0 || name[t - 1] != mine);
-    for (int i = 0; head && i + 1 < t; ++i) head = name[i] != mine;
-    const uint32_t heads = __ballot_sync(0xFFFFFFFFu, head);
-    if (lane == 0) warp_heads[warp] = __popc(heads);
-    __syncthreads();
-    int before = __popc(heads & ((1u << lane) - 1)), count = 0;
 #pragma unroll
-    for (int w = 0; w < kLowWarps; ++w) {
-        if (w < warp) before += warp_heads[w];
-        count += warp_heads[w];
+    for (int i = t; i < kLowTile; i += kLowThreads) {
+        int mine = -1;
+        if (i < tokens) {
+            mine = p.index[m0 + i];
+            if (mine >= p.n_adapters) {
+                if (p.status) *p.status = MK_ERR_BOUNDS;
+                mine = -1;
+            }
+        }
+        name[i] = mine;
     }
-    if (head) list[before] = mine;
     __syncthreads();
+    int count = 0;
+    for (int from = 0; from < tokens; from += kLowThreads) {
+        const int i = from + t, mine = i < tokens ? name[i] : -1;
+        bool head = mine >= 0 && (i == 0 || name[i - 1] != mine);
+        if (head) {
+            bool seen = false;   // (four names a step, no step waiting for another)
+#pragma unroll 4
+            for (int j = 0; j < i; j += 4) {
+                const int4 n = *reinterpret_cast<const int4*>(name + j);
+                seen = seen || n.x == mine || (j + 1 < i && n.y == mine) || (j + 2 < i && n.z == mine) || (j + 3 < i && n.w == mine);
+            }
+            head = !seen;
+        }
+        const uint32_t heads = __ballot_sync(0xFFFFFFFFu, head);
+        if (lane == 0) warp_heads[warp] = __popc(heads);
+        __syncthreads();
+        int before = count + __popc(heads & ((1u << lane) - 1));
+#pragma unroll
+        for (int w = 0; w < kLowWarps; ++w) {
+            if (w < warp) before += warp_heads[w];
+            count += warp_heads[w];
+        }
+        if (head) list[before] = mine;
+        __syncthreads();
+    }
     if (sub == 0 && blockIdx.y == 0 && rank_z == 0) {
         if (t == 0) p.count[m] = count;
-        if (t < count) p.list[int64_t(m) * p.slots + t] = list[t];
+        for (int i = t; i < count; i += kLowThreads) p.list[int64_t(m) * p.slots + i] = list[i];
     }
 
-    const int row0 = sub * kTokens;                     // in the tile
+    const int row0 = sub * kLowTokens;                  // in the tile
     if (row0 >= tokens) return;                         // (all CTAs of the cluster)
     const int g = lane >> 2, q = lane & 3;              // a product's row, and its quarter of 32 elements
-    const int width = p.items * 16, blocks = (p.k + 31) / 32, item_cols = p.f32 ? 64 : 32;
+    const int blocks = (p.k + 31) / 32, width = p.width;
+    const __nv_bfloat16* x0 = p.x + int64_t(m0 + row0 + g) * p.x_stride + q * 8;
+    float* sums = all_sums;
+    bool reached = false;                               // whether a peer may still read this CTA's sums
     for (int slot = int(blockIdx.y); slot < count; slot += int(gridDim.y)) {
         const int adapter = list[slot];
-        bool any = false, use[MT][2];
+        const bool use[2] = {name[row0 + g] == adapter, name[row0 + 8 + g] == adapter};   // (names behind the last token are -1)
+        const bool any = __any_sync(0xFFFFFFFFu, use[0] || use[1]);                       // (every warp looks at every token)
+        if (any) {
+            const __nv_bfloat16* down0 = p.down + (int64_t(adapter) * p.rank + g) * p.k + q * 8;
+            for (int c0 = 0; c0 < width; c0 += kCols) {
+                const __nv_bfloat16* down = down0 + int64_t(c0) * p.k;
+                float acc[NT][4];
 #pragma unroll
-        for (int i = 0; i < MT; ++i)
+                for (int j = 0; j < NT; ++j)
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                use[i][h] = name[row0 + 16 * i + 8 * h + g] == adapter;   // (names behind the last token are -1)
-                any = any || use[i][h];
-            }
-        any = __any_sync(0xFFFFFFFFu, any);             // (every warp looks at every token)
-        const __nv_bfloat16* down = p.down + int64_t(adapter) * p.rank * p.k;
-        for (int c0 = 0; c0 < width; c0 += kLowRank) {
-            if (any) {
-                float acc[MT][4][4];
-#pragma unroll
-                for (int i = 0; i < MT; ++i)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-#pragma unroll
-                        for (int v = 0; v < 4; ++v) acc[i][j][v] = 0.f;
-#pragma unroll 2
+                    for (int v = 0; v < 4; ++v) acc[j][v] = 0.f;
+#pragma unroll 4
                 for (int b = rank_z * kLowWarps + warp; b < blocks; b += split * kLowWarps) {
-                    const int at = b * 32 + q * 8;
-                    const bool in = at < p.k;
-                    uint4 xs[MT][2], ds[4];
-                    const uint4 zero = make_uint4(0, 0, 0, 0);
+                    const bool in = b * 32 + q * 8 < p.k;
+                    uint4 xs[2], ds[NT];
 #pragma unroll
-                    for (int i = 0; i < MT; ++i)
+                    for (int j = 0; j < NT; ++j) ds[j] = low_load(down + int64_t(8 * j) * p.k + b * 32, in && c0 + 8 * j + g < p.rank);
 #pragma unroll
-                        for (int h = 0; h < 2; ++h)
-                            xs[i][h] = in && use[i][h] ? __ldg(reinterpret_cast<const uint4*>(p.x + int64_t(m0 + row0 + 16 * i + 8 * h + g) * p.x_stride + at)) : zero;
+                    for (int h = 0; h < 2; ++h) xs[h] = low_load(x0 + 8 * h * p.x_stride + b * 32, in && use[h]);
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        ds[j] = in && c0 + 8 * j + g < p.rank ? __ldg(reinterpret_cast<const uint4*>(down + int64_t(c0 + 8 * j + g) * p.k + at)) : zero;
-#pragma unroll
-                    for (int i = 0; i < MT; ++i)
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            low_mma(acc[i][j], xs[i][0].x, xs[i][1].x, xs[i][0].y, xs[i][1].y, ds[j].x, ds[j].y);
-                            low_mma(acc[i][j], xs[i][0].z, xs[i][1].z, xs[i][0].w, xs[i][1].w, ds[j].z, ds[j].w);
-                        }
-                }
-#pragma unroll
-                for (int i = 0; i < MT; ++i) {
-                    __syncthreads();
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-#pragma unroll
-                        for (int h = 0; h < 2; ++h)
-                            *reinterpret_cast<float2*>(&part[warp][g + 8 * h][8 * j + 2 * q]) = make_float2(acc[i][j][2 * h], acc[i][j][2 * h + 1]);
-                    __syncthreads();
-                    for (int e = t; e < 16 * kLowRank; e += kLowThreads) {
-                        float s = 0.f;
-#pragma unroll
-                        for (int w = 0; w < kLowWarps; ++w) s += part[w][e / kLowRank][e % kLowRank];
-                        sums[16 * i + e / kLowRank][e % kLowRank] = s;
+                    for (int j = 0; j < NT; ++j) {
+                        low_mma(acc[j], xs[0].x, xs[1].x, xs[0].y, xs[1].y, ds[j].x, ds[j].y);
+                        low_mma(acc[j], xs[0].z, xs[1].z, xs[0].w, xs[1].w, ds[j].z, ds[j].w);
                     }
                 }
-                __syncwarp();
-                if (split > 1) sm::cluster_sync();
-                else __syncthreads();
-            }
-            // the cluster's CTAs share out the pairs of columns; a token's row is complete over them
-            const float scale = p.scale ? p.scale[adapter] : 1.f;
-            for (int e = rank_z * kLowThreads + t; e < kTokens * kLowRank / 2; e += split * kLowThreads) {
-                const int r = e / (kLowRank / 2), c = e % (kLowRank / 2) * 2, col = c0 + c;
-                if (row0 + r >= tokens || col >= width) continue;
-                float v[2] = {0.f, 0.f};
-                if (any && name[row0 + r] == adapter) {
-                    const uint32_t src = sm::smem(&sums[r][c]);
-                    for (int z = 0; z < split; ++z) {
-                        const uint32_t peer = sm::cluster_addr(src, uint32_t(z));
-                        v[0] += sm::cluster_ld(peer);
-                        v[1] += sm::cluster_ld(peer + 4);
-                    }
-                    v[0] *= scale;
-                    v[1] *= scale;
-                }
-                __nv_bfloat16* dst = p.terms + int64_t(m0 + row0 + r) * p.terms_stride + int64_t(slot * p.items + col / 16) * item_cols + col % 16;
-                for (int term = 0; term < (p.f32 ? 3 : 2); ++term, dst += 16) {
-                    const __nv_bfloat16 h0 = __float2bfloat16_rn(v[0]), h1 = __float2bfloat16_rn(v[1]);
-                    __nv_bfloat162 pair;
-                    pair.x = h0;
-                    pair.y = h1;
-                    *reinterpret_cast<__nv_bfloat162*>(dst) = pair;
-                    // (an infinity, or a value that rounds to one, leaves no rest)
-                    v[0] = isinf(__bfloat162float(h0)) ? 0.f : v[0] - __bfloat162float(h0);
-                    v[1] = isinf(__bfloat162float(h1)) ? 0.f : v[1] - __bfloat162float(h1);
+                __syncthreads();                        // (the warps' sums of the columns before are read)
+#pragma unroll
+                for (int j = 0; j < NT; ++j)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+                        *reinterpret_cast<float2*>(&part[warp][g + 8 * h][8 * j + 2 * q]) = make_float2(acc[j][2 * h], acc[j][2 * h + 1]);
+                __syncthreads();
+                for (int e = t; e < 16 * kCols; e += kLowThreads) {
+                    float s = 0.f;
+#pragma unroll
+                    for (int w = 0; w < kLowWarps; ++w) s += part[w][e / kCols][e % kCols];
+                    if (c0 + e % kCols < width) sums[e / kCols * width + c0 + e % kCols] = s;
                 }
             }
             __syncwarp();
-            if (any && split > 1) sm::cluster_sync();   // (the sums are read before they are written again)
+            if (split > 1) sm::cluster_sync();
+            else __syncthreads();
+            reached = true;
         }
+        // the cluster's CTAs share out the pairs of columns
+        const float scale = any && p.scale ? p.scale[adapter] : 1.f;
+        for (int e = rank_z * kLowThreads + t; e < kLowTokens * width / 2; e += split * kLowThreads) {
+            const int r = 2 * e / width, c = 2 * e - r * width;
+            if (row0 + r >= tokens) break;
+            float v[2] = {0.f, 0.f};
+            if (any && name[row0 + r] == adapter) {
+                const uint32_t src = sm::smem(sums + r * width + c);
+                float2 got[8];   // (of all CTAs together: their way takes longer than everything else here)
+#pragma unroll
+                for (int z = 0; z < 8; ++z) got[z] = z < split ? sm::cluster_ld2(sm::cluster_addr(src, uint32_t(z))) : make_float2(0.f, 0.f);
+#pragma unroll
+                for (int z = 0; z < 8; ++z) {
+                    v[0] += got[z].x;
+                    v[1] += got[z].y;
+                }
+                v[0] *= scale;
+                v[1] *= scale;
+            }
+            const int col = slot * width + c;
+            const int64_t block = int64_t(m0 + row0 + r) * p.blocks + col / kAdaptCols;
+            __nv_bfloat16* dst = p.terms + block * (2 * kAdaptCols) + col % kAdaptCols;
+            for (int term = 0; term < (p.f32 ? 3 : 2); ++term) {
+                __nv_bfloat162 pair;
+                pair.x = __float2bfloat16_rn(v[0]);
+                pair.y = __float2bfloat16_rn(v[1]);
+                *reinterpret_cast<__nv_bfloat162*>(term == 2 ? p.third + block * kAdaptCols + col % kAdaptCols : dst + term * kAdaptCols) = pair;
+                const float h0 = __bfloat162float(pair.x), h1 = __bfloat162float(pair.y);
+                v[0] = isinf(h0) ? 0.f : v[0] - h0;   // (an infinity, or a value that rounds to one, leaves no rest)
+                v[1] = isinf(h1) ? 0.f : v[1] - h1;
+            }
+        }
+        // the next adapter's sums go to the other half; they are in this one again when every CTA has passed the next barrier
+        if (any) sums = sums == all_sums ? all_sums + 16 * width : all_sums;
     }
+    __syncwarp();
+    if (split > 1 && reached) sm::cluster_sync();
 }
 
 // A call is made in pieces of rows whose terms fit this; each at least a tile
@@ -185,9 +197,9 @@ constexpr int64_t kAdaptTermsBytes = 256ll << 20;
 
 struct AdaptPlan {
     LinearChoice<true> choice;
-    int slots, items, tiles;        // of a piece
-    int64_t rows, cols;             // tokens of a piece, columns of the terms
-    size_t terms, list, bytes;      // offsets of the terms and lists behind the counts; all
+    int slots, width, tiles;        // of a piece
+    int64_t rows, blocks;           // tokens of a piece, blocks of its adapters' columns
+    size_t list, terms, third, bytes;   // offsets of what lies behind the counts; all
 };
 
 static mk_status adapt_check(const mk_linear_args* a, const mk_adapters* ad, bool pointers) {
@@ -211,35 +223,41 @@ static mk_status adapt_check(const mk_linear_args* a, const mk_adapters* ad, boo
 static mk_status adapt_plan(const mk_linear_args* a, const mk_adapters* ad, AdaptPlan& pl) {
     LinearParams p{};
     const bool f32 = a->out_dtype == MK_F32;
-    pl.items = (ad->rank + 15) / 16;
+    pl.width = ad->rank <= 16 ? 16 : (ad->rank + kAdaptCols - 1) / kAdaptCols * kAdaptCols;
     // blocks of the adapters' part, for the estimate: few tokens name an adapter each, of many neighbours share theirs
     const int named = std::min({a->rows <= 64 ? a->rows : 4, ad->n_adapters, 64});
-    const int extra = f32 ? named * pl.items : (named * pl.items + 1) / 2;
+    const int extra = (named * pl.width + kAdaptCols - 1) / kAdaptCols;
     const mk_status st = linear_plan(a, extra, p, pl.choice);
     if (st != MK_OK) return st;
     const int tile = pl.choice.tokens;
     pl.slots = std::min({tile, ad->n_adapters, a->rows});
-    const int64_t items = int64_t(pl.slots) * pl.items;
-    pl.cols = (f32 ? items : (items + 1) / 2) * 64;
-    const int64_t all = (int64_t(a->rows) + tile - 1) / tile;
-    pl.tiles = int(std::min(all, std::max<int64_t>(1, kAdaptTermsBytes / (pl.cols * 2 * tile))));
+    pl.blocks = (int64_t(pl.slots) * pl.width + kAdaptCols - 1) / kAdaptCols;
+    const int64_t all = (int64_t(a->rows) + tile - 1) / tile, row = pl.blocks * kAdaptCols * 2;   // bytes of a part of a token
+    pl.tiles = int(std::min(all, std::max<int64_t>(1, kAdaptTermsBytes / (3 * row * tile))));
     pl.rows = std::min<int64_t>(a->rows, int64_t(pl.tiles) * tile);
     pl.list = align256(size_t(pl.tiles) * 4);
     pl.terms = pl.list + align256(size_t(pl.tiles) * size_t(pl.slots) * 4);
-    pl.bytes = pl.terms + align256(size_t(pl.rows) * size_t(pl.cols) * 2);
+    pl.third = pl.terms + align256(size_t(pl.rows * row) * 2);
+    pl.bytes = pl.third + (f32 ? align256(size_t(pl.rows * row)) : 0);
     return MK_OK;
 }
 
-template <int MT>
-static mk_status low_launch(LowParams& p, int sms, cudaStream_t stream) {
-    constexpr int kTokens = 16 * MT;
-    p.subs = (p.tile + kTokens - 1) / kTokens;
+#ifndef LROWS
+#define LROWS 512
+#define LCTAS 2
+#endif
+template <int NT>
+static mk_status low_launch(LowParams& p, int device, int sms, cudaStream_t stream) {
+    static std::atomic<uint64_t> set{0};
+    const mk_status st = op_smem(reinterpret_cast<const void*>(&low_rank_kernel<NT>), 2 * kLowTokens * MK_ADAPTERS_MAX_RANK * 4, device, &set);
+    if (st != MK_OK) return st;
+    p.subs = (p.tile + kLowTokens - 1) / kLowTokens;
     const int64_t subs = int64_t((p.rows + p.tile - 1) / p.tile) * p.subs;
-    // adapters of a tile side by side where there are few tokens, then the contraction over clusters of 2, 4 or 8 while two CTAs
+    // adapters of a tile side by side where there are few tokens, then the contraction over clusters of 2, 4 or 8 while LCTAS CTAs
     // an SM are not reached and each warp keeps a block of 32
-    const int lanes = p.rows <= 512 ? std::min({p.slots, 16}) : std::min(p.slots, 2);
+    const int lanes = p.rows <= LROWS ? std::min({p.slots, 16}) : 1;
     int split = 1;
-    while (split < 8 && subs * lanes * split * 2 <= 2 * sms && 2 * split * kLowWarps * 32 <= p.k) split *= 2;
+    while (split < 8 && 2 * subs * lanes * split <= int64_t(LCTAS) * sms && 2 * split * kLowWarps * 32 <= p.k) split *= 2;
     cudaLaunchConfig_t cfg{};
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -248,11 +266,12 @@ static mk_status low_launch(LowParams& p, int sms, cudaStream_t stream) {
     attr[1].val.clusterDim.x = attr[1].val.clusterDim.y = 1;
     attr[1].val.clusterDim.z = unsigned(split);
     cfg.attrs = attr;
-    cfg.numAttrs = 2;
+    cfg.numAttrs = split > 1 ? 2 : 1;
     cfg.stream = stream;
     cfg.gridDim = dim3(unsigned(subs), unsigned(lanes), unsigned(split));
     cfg.blockDim = dim3(kLowThreads);
-    MK_CK(cudaLaunchKernelEx(&cfg, &low_rank_kernel<MT>, p));
+    cfg.dynamicSmemBytes = size_t(2 * kLowTokens * p.width) * 4;
+    MK_CK(cudaLaunchKernelEx(&cfg, &low_rank_kernel<NT>, p));
     return MK_OK;
 }
 
@@ -287,7 +306,7 @@ extern "C" mk_status mk_linear_adapted(const mk_linear_args* a, const mk_adapter
         if (a->residual) c.residual = static_cast<const uint8_t*>(a->residual) + r0 * a->residual_stride * (a->residual_dtype == MK_F32 ? 4 : 2);
         LowParams low{};
         low.rows = c.rows; low.k = c.k; low.rank = ad->rank; low.n_adapters = ad->n_adapters;
-        low.tile = pl.choice.tokens; low.slots = pl.slots; low.items = pl.items; low.f32 = f32;
+        low.tile = pl.choice.tokens; low.slots = pl.slots; low.width = pl.width; low.f32 = f32;
         low.x = static_cast<const __nv_bfloat16*>(c.x);
         low.x_stride = c.rows == 1 ? c.k : c.x_stride;
         low.down = static_cast<const __nv_bfloat16*>(ad->down);
@@ -296,22 +315,29 @@ extern "C" mk_status mk_linear_adapted(const mk_linear_args* a, const mk_adapter
         low.count = reinterpret_cast<int32_t*>(ws);
         low.list = reinterpret_cast<int32_t*>(ws + pl.list);
         low.terms = reinterpret_cast<__nv_bfloat16*>(ws + pl.terms);
-        low.terms_stride = pl.cols;
+        low.third = reinterpret_cast<__nv_bfloat16*>(ws + pl.third);
+        low.blocks = pl.blocks;
         low.status = a->status;
-        if ((st = c.rows > 512 ? low_launch<4>(low, sms, s) : low_launch<1>(low, sms, s)) != MK_OK) return st;
+        if ((st = pl.width > 16 ? low_launch<4>(low, device, sms, s) : low_launch<2>(low, device, sms, s)) != MK_OK) return st;
         LinearExtra<true> e{};
+        e.index = low.index;
+        e.n_adapters = ad->n_adapters;
         e.count = low.count;
         e.list = low.list;
         e.slots = pl.slots;
-        e.items = pl.items;
+        e.width = pl.width;
         const int64_t w_rows = int64_t(c.n) * (c.activation == MK_ACT_SWIGLU ? 2 : 1);
         const cuuint64_t ud[3] = {cuuint64_t(ad->rank), cuuint64_t(w_rows), cuuint64_t(ad->n_adapters)};
         const cuuint64_t us[2] = {cuuint64_t(ad->rank) * 2, cuuint64_t(w_rows) * cuuint64_t(ad->rank) * 2};
-        const cuuint32_t ub[3] = {16, cuuint32_t(pl.choice.unit == 2 ? pl.choice.features / 2 : 128), 1};
+        const cuuint32_t ub[3] = {cuuint32_t(std::min(pl.width, kAdaptCols)), cuuint32_t(pl.choice.unit == 2 ? pl.choice.features / 2 : 128), 1};
         if ((st = op_tensor_map(&e.up, ad->up, 3, ud, us, ub)) != MK_OK) return st;
-        const cuuint64_t td[2] = {cuuint64_t(pl.cols), cuuint64_t(c.rows)}, ts[1] = {cuuint64_t(pl.cols) * 2};
-        const cuuint32_t tb[2] = {64, cuuint32_t(pl.choice.unit == 2 ? 128 : pl.choice.tokens)};
+        const cuuint32_t tile = cuuint32_t(pl.choice.unit == 2 ? 128 : pl.choice.tokens);
+        const cuuint64_t cols = cuuint64_t(pl.blocks) * kAdaptCols, td[2] = {2 * cols, cuuint64_t(c.rows)}, ts[1] = {cols * 4};
+        const cuuint32_t tb[2] = {2 * kAdaptCols, tile};
         if ((st = op_tensor_map(&e.terms, low.terms, 2, td, ts, tb)) != MK_OK) return st;
+        const cuuint64_t hd[2] = {cols, cuuint64_t(c.rows)}, hs[1] = {cols * 2};
+        const cuuint32_t hb[2] = {kAdaptCols, tile};
+        if (f32 && (st = op_tensor_map(&e.third, low.third, 2, hd, hs, hb)) != MK_OK) return st;
         // (the piece's own tiles: pieces are whole tiles but for the last)
         LinearParams p{};
         LinearPlan plan = pl.choice.plan;

@@ -25,46 +25,67 @@ struct LinearParams {
 // every adapter that a token of the tile names, against the tokens' low-rank rows scale x down^T, zero for the
 // tokens of other adapters (mk_adapt.cu works them out, and lists each tile's adapters).  So the weights of an adapter are
 // read once per tile of tokens, whoever names it, and the sums meet in the accumulators in front of the activation.
-// The low-rank rows are cut into `terms` bf16 parts (16 or 24 of fp32's 24 bits: an fp32 output shows what a single
-// rounding, 2^-9, leaves; two parts are off by 2^-18 of the adapter's share, far below a bf16 output's own rounding).  An item is 16 columns of an adapter's rank:
-// a block holds two items of up (kAdaptItemBytes each, rows of 32 bytes) and their two terms each as 64 columns, or one item and
-// its three terms, so that up is loaded once for all terms.
+// The low-rank rows are cut into bf16 parts, two (16 of fp32's 24 bits: off by 2^-18 of the adapter's share, far below a bf16
+// output's own rounding) or, for an fp32 output, three.  An adapter takes 16 columns of the rank, or a multiple of 32: a block is 32
+// columns of up (one adapter's, rows of 64 bytes, or two adapters', rows of 32) against the first two parts of the 32 columns
+// (64 columns of `terms`) and the third (32 columns of `third`): up is loaded once for all parts.
 template <bool ADAPT>
-struct LinearExtra {};
+struct LinearExtra {
+    static constexpr int32_t width = 0;
+};
 template <>
 struct LinearExtra<true> {
-    CUtensorMap up, terms;
-    const int32_t* count;   // [tiles of tokens]: adapters of the tile
-    const int32_t* list;    // [tiles of tokens][slots]: which
-    int32_t slots, items;   // items of an adapter
+    CUtensorMap up, terms, third;
+    const int32_t* index;      // [rows], -1 or n_adapters and more: none
+    const int32_t* count;      // [tiles of tokens]: adapters of the tile
+    const int32_t* list;       // [tiles of tokens][slots]: which, in the order in which its tokens name them
+    int32_t slots, width;      // columns of an adapter
+    int32_t n_adapters;
 };
-constexpr int kAdaptItemBytes = 128 * 16 * 2;
-// This CTA's share [b0, b1) of the adapters' blocks of the token tile `m`, for the role that asks
+constexpr int kAdaptCols = 32, kAdaptBytes = 128 * kAdaptCols * 2;   // of a block: columns, bytes of 128 rows of up
+// This CTA's share [b0, b1) of the adapters' blocks of a token tile, for the role that asks, and the adapters of its
+// columns: in shared memory for the CTA's first tile, in global memory for the others (behind the wait for the kernel that lists them)
 struct LinearShare {
-    int adapters, items, b0, b1;
+    const volatile int32_t* list;
+    int adapters, b0, b1;
+    __device__ __forceinline__ void cut(int width, int rank, int split) {
+        const int blocks = (adapters * width + kAdaptCols - 1) / kAdaptCols;
+        b0 = int(int64_t(blocks) * rank / split);
+        b1 = int(int64_t(blocks) * (rank + 1) / split);
+    }
 };
-template <bool F32>
-__device__ __forceinline__ LinearShare linear_share(const LinearExtra<true>& e, int m, int rank, int split) {
-    LinearShare s;
-    s.adapters = *reinterpret_cast<const volatile int32_t*>(e.count + m);
-    s.items = s.adapters * e.items;
-    const int blocks = F32 ? s.items : (s.items + 1) / 2;
-    s.b0 = int(int64_t(blocks) * rank / split);
-    s.b1 = int(int64_t(blocks) * (rank + 1) / split);
-    return s;
+struct LinearFirst {   // the first tile's adapters
+    int32_t list[256], count;
+    uint64_t ready;
+};
+// By one warp: the adapters that tokens [m0, m0 + tokens) name, in order
+__device__ __forceinline__ void linear_list(const LinearExtra<true>& e, int m0, int tokens, LinearFirst& first) {
+    const int lane = threadIdx.x & 31;
+    int count = 0;
+    for (int t = 0; t < tokens; t += 32) {
+        int name = t + lane < tokens ? e.index[m0 + t + lane] : -1;
+        if (name >= e.n_adapters) name = -1;
+        bool is_new = (__match_any_sync(0xFFFFFFFFu, name) & ((1u << lane) - 1)) == 0 && name >= 0;
+        for (int i = 0; i < count; ++i) is_new = is_new && first.list[i] != name;
+        const uint32_t all = __ballot_sync(0xFFFFFFFFu, is_new);
+        if (is_new) first.list[count + __popc(all & ((1u << lane) - 1))] = name;
+        count += __popc(all);
+        __syncwarp();
+    }
+    if (lane == 0) first.count = count;
 }
-// The adapters of consecutive items, 32 list entries at a time in the warp's lanes
-struct LinearAdapters {
-    const int32_t* list;
-    int adapters, from, mine;
-    __device__ __forceinline__ LinearAdapters(const int32_t* l, int n) : list(l), adapters(n), from(-32), mine(0) {}
-    __device__ __forceinline__ int operator()(int i) {   // (i is the same in every lane)
-        if (i < from || i >= from + 32 || from < 0) {
-            from = i;
-            const int at = i + int(threadIdx.x & 31);
-            mine = at < adapters ? *reinterpret_cast<const volatile int32_t*>(list + at) : 0;
-        }
-        return __shfl_sync(0xFFFFFFFFu, mine, i - from);
+// The adapter and its column of consecutive pieces of a tile's columns, for one lane: the next adapter's name is read ahead
+struct LinearColumns {
+    const volatile int32_t* list;
+    int adapters, width, at, column, name, ahead;
+    __device__ __forceinline__ LinearColumns(const LinearShare& s, int w, int first)
+        : list(s.list), adapters(s.adapters), width(w), at(first / w), column(first - at * w), name(read(at)), ahead(read(at + 1)) {}
+    __device__ __forceinline__ int read(int i) const { return i < adapters ? list[i] : 0; }
+    __device__ __forceinline__ void step(int by) {   // (never beyond an adapter's last column but to the next one's first)
+        if ((column += by) < width) return;
+        column = 0;
+        name = ahead;
+        ahead = read(++at + 1);
     }
 };
 
@@ -200,6 +221,7 @@ linear_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
     __shared__ uint64_t bars[2 * T::kStages + 5];
     __shared__ uint32_t tmem_at;
     __shared__ int abort_flag;
+    __shared__ std::conditional_t<ADAPT, LinearFirst, char> first_tile;
     volatile int* abort_word = &abort_flag;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t stage0 = (sm::smem(raw) + 1023u) & ~1023u;
@@ -213,6 +235,7 @@ linear_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
         for (int s = 0; s < T::kStages; ++s) { sm::bar_init(full(s), 1); sm::bar_init(empty(s), 1); }
         for (int s = 0; s < 2; ++s) { sm::bar_init(acc_full(s), 1); sm::bar_init(acc_empty(s), T::kWarps); }
         sm::bar_init(drained, 1);
+        if constexpr (ADAPT) sm::bar_init(sm::smem(&first_tile.ready), 1);
         abort_flag = 0;
         sm::bar_fence_init();
         sm::tma_prefetch_map(&map_w);
@@ -224,7 +247,7 @@ linear_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
     sm::tc_fence_after();
     const uint32_t tmem = tmem_at;
     sm::pdl_trigger();
-    if (!ADAPT || warp >= 2) sm::pdl_wait();
+    if constexpr (!ADAPT) sm::pdl_wait();
 
     // this CTA's tiles, and its share [kb0, kb1) of their contraction blocks
     const int rank = p.split > 1 ? int(sm::cluster_rank()) : 0;
@@ -236,6 +259,23 @@ linear_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
     auto place = [&](int tile, int& n0, int& m0) {
         n0 = tile / p.tiles_m * 128;
         m0 = tile % p.tiles_m * BN;
+    };
+    // (fails only as its wait does)
+    [[maybe_unused]] auto share = [&](int tile, LinearShare& s) {
+        if constexpr (ADAPT) {
+            const int m = tile % p.tiles_m;
+            if (tile == first) {
+                if (!sm::bar_wait_warp(sm::smem(&first_tile.ready), 0, abort_word, p.status)) return false;
+                s.list = first_tile.list;
+                s.adapters = *reinterpret_cast<const volatile int32_t*>(&first_tile.count);
+            } else {
+                sm::pdl_wait();
+                s.list = e.list + int64_t(m) * e.slots;
+                s.adapters = *reinterpret_cast<const volatile int32_t*>(e.count + m);
+            }
+            s.cut(e.width, rank, p.split);
+        }
+        return true;
     };
 
     if (warp == 0) {
@@ -259,29 +299,53 @@ linear_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
                 if (++s == T::kStages) { s = 0; phase ^= 1u; }
             }
             if constexpr (ADAPT) {
-                sm::pdl_wait();
-                const int m = tile % p.tiles_m;
-                const LinearShare sh = linear_share<F32>(e, m, rank, p.split);
-                LinearAdapters adapter(e.list + int64_t(m) * e.slots, sh.adapters);
-                constexpr int kItems = F32 ? 1 : 2;
-                for (int b = sh.b0; b < sh.b1 && ok; ++b, ++it) {
-                    if (!(ok = sm::bar_wait_warp(empty(s), phase, abort_word, p.status))) break;
-                    const uint32_t at = stage0 + s * T::kStageBytes;
-                    const int items = min(kItems, sh.items - b * kItems);
-                    if (issuer) {
-                        sm::bar_expect(full(s), uint32_t(items * T::kAccs * kAdaptItemBytes + T::kBBytes));
-                        sm::tma_load_2d(at + T::kAccs * T::kABytes, &e.terms, full(s), b * 64, m0);
-                    }
-                    for (int i = 0; i < items; ++i) {
-                        const int item = b * kItems + i, a = adapter(item / e.items), c = item % e.items * 16;
+                LinearShare sh{};
+                if (!ok || !(ok = share(tile, sh))) break;
+                // up first, as far as the stages go: it does not depend on the kernel in front, as the terms do
+                int given_s = s, given = sh.b0;   // (of the terms)
+                auto terms = [&](int upto) {
+                    for (; given < upto; ++given) {
+                        const uint32_t at = stage0 + given_s * T::kStageBytes;
                         if (issuer) {
-                            sm::tma_load_3d(at + i * kAdaptItemBytes, &e.up, full(s), c, n0, a);
-                            if (GATED) sm::tma_load_3d(at + T::kABytes + i * kAdaptItemBytes, &e.up, full(s), c, p.n + n0, a);
+                            sm::tma_load_2d(at + T::kAccs * T::kABytes, &e.terms, full(given_s), given * 2 * kAdaptCols, m0);
+                            if (F32) sm::tma_load_2d(at + kAdaptBytes, &e.third, full(given_s), given * kAdaptCols, m0);
+                        }
+                        if (++given_s == T::kStages) given_s = 0;
+                    }
+                };
+                const bool two = e.width == 16;
+                const int last = two && sh.adapters % 2 ? sh.adapters / 2 : -1;   // a block of one adapter's 16 columns
+                constexpr uint32_t kTerms = T::kBBytes + (F32 ? T::kBBytes / 2 : 0);
+                LinearColumns col(sh, e.width, sh.b0 * kAdaptCols);
+                int b = sh.b0;
+                for (; b < sh.b1; ++b, ++it) {
+                    if (b - sh.b0 >= T::kStages) {
+                        if (b - sh.b0 == T::kStages) sm::pdl_wait();
+                        terms(b);
+                    }
+                    if (!(ok = sm::bar_wait_warp(empty(s), phase, abort_word, p.status))) break;
+                    if (issuer) {
+                        const uint32_t at = stage0 + s * T::kStageBytes;
+                        sm::bar_expect(full(s), (b == last ? T::kAccs * (kAdaptBytes / 2) : T::kAccs * kAdaptBytes) + kTerms);
+                        sm::tma_load_3d(at, &e.up, full(s), col.column, n0, col.name);
+                        if (GATED) sm::tma_load_3d(at + T::kABytes, &e.up, full(s), col.column, p.n + n0, col.name);
+                        if (two) {
+                            col.step(16);
+                            if (b != last) {
+                                sm::tma_load_3d(at + kAdaptBytes / 2, &e.up, full(s), 0, n0, col.name);
+                                if (GATED) sm::tma_load_3d(at + T::kABytes + kAdaptBytes / 2, &e.up, full(s), 0, p.n + n0, col.name);
+                                col.step(16);
+                            }
+                        } else {
+                            col.step(kAdaptCols);
                         }
                     }
                     __syncwarp();
                     if (++s == T::kStages) { s = 0; phase ^= 1u; }
                 }
+                sm::pdl_wait();
+                terms(b);   // (after a wait that ran out too: every copy that a barrier expects is made)
+                __syncwarp();
             }
         }
         if (*abort_word && issuer)   // the copies in flight land before the CTA gives its shared memory back
@@ -295,19 +359,26 @@ linear_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
         uint32_t phase = 0;
         bool ok = true;
         // the adapters' blocks [x0, x1) into accumulators d: an item's products with each of its terms
+        const bool two = e.width == 16;
+        const uint64_t up0 = two ? sm::desc_k_sw32(stage0) : sm::desc_k_sw64(stage0), third0 = sm::desc_k_sw64(stage0 + kAdaptBytes);
+        const uint64_t step16 = two ? kAdaptBytes / 2 >> 4 : 2;
         [[maybe_unused]] auto adapters = [&](uint32_t d, const LinearShare& sh, int x0, int x1, bool fresh) {
             for (int b = x0; b < x1; ++b) {
                 if (!(ok = sm::bar_wait_warp(full(s), phase, abort_word, p.status))) break;
                 sm::tc_fence_after();
-                const uint64_t a = sm::desc_k_sw32(stage0 + uint32_t(s * T::kStageBytes)), t = b0 + uint64_t(s * (T::kStageBytes >> 4));
-                const int steps = F32 ? 3 : 2 * min(2, sh.items - 2 * b);
+                const uint64_t at = uint64_t(s * (T::kStageBytes >> 4)), t = b0 + at, t3 = third0 + at, a = up0 + at;
+                const int steps = two && 2 * b + 1 == sh.adapters ? 1 : 2;   // of 16 columns
                 if (leader) {
 #pragma unroll
-                    for (int kk = 0; kk < (F32 ? 3 : 4); ++kk) {
+                    for (int kk = 0; kk < 2; ++kk) {
                         if (kk >= steps) break;
-                        const uint64_t up = a + uint64_t((F32 ? 0 : kk / 2) * (kAdaptItemBytes >> 4));
-                        sm::mma_ss(d, up, t + 2 * kk, idesc, !fresh || b > x0 || kk > 0);
-                        if (GATED) sm::mma_ss(d + BN, up + (T::kABytes >> 4), t + 2 * kk, idesc, !fresh || b > x0 || kk > 0);
+                        const uint64_t up = a + kk * step16;
+#pragma unroll
+                        for (int term = 0; term < (F32 ? 3 : 2); ++term) {
+                            const uint64_t x = (term == 2 ? t3 : t + 4 * term) + 2 * kk;
+                            sm::mma_ss(d, up, x, idesc, !fresh || b > x0 || kk > 0 || term > 0);
+                            if (GATED) sm::mma_ss(d + BN, up + (T::kABytes >> 4), x, idesc, !fresh || b > x0 || kk > 0 || term > 0);
+                        }
                     }
                     sm::mma_commit(empty(s));
                 }
@@ -337,16 +408,15 @@ linear_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
                     if (++s == T::kStages) { s = 0; phase ^= 1u; }
                 }
                 if constexpr (ADAPT && !F32) {   // (the tile's only piece)
-                    sm::pdl_wait();
-                    const LinearShare sh = linear_share<F32>(e, tile % p.tiles_m, rank, p.split);
-                    if (ok) adapters(d, sh, sh.b0, sh.b1, false);
+                    LinearShare sh{};
+                    if (ok && (ok = share(tile, sh))) adapters(d, sh, sh.b0, sh.b1, false);
                 }
                 if (ok && leader) sm::mma_commit(acc_full(buf));
                 __syncwarp();
             }
             if constexpr (ADAPT && F32) {
-                sm::pdl_wait();
-                const LinearShare sh = linear_share<F32>(e, tile % p.tiles_m, rank, p.split);
+                LinearShare sh{};
+                ok = ok && share(tile, sh);
                 for (int x0 = sh.b0; x0 < sh.b1 && ok; x0 += kPromote, ++n) {
                     const int buf = n & 1;
                     if (n >= 2 && !(ok = sm::bar_wait_warp(acc_empty(buf), uint32_t(n / 2 - 1) & 1u, abort_word, p.status))) break;
@@ -362,6 +432,16 @@ linear_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
         const int quarter = warp & 3, row = quarter * 32 + lane, cols = (warp - 2) / 4 * T::kWidth;
         const uint32_t lanes = uint32_t(quarter * 32) << 16;
         const bool plain = !GATED && p.act == MK_ACT_NONE;
+        if constexpr (ADAPT) {
+            if (warp == 2 && first < tiles) {
+                int n0, m0;
+                place(first, n0, m0);
+                linear_list(e, m0, min(BN, p.rows - m0), first_tile);
+                __syncwarp();
+                if (lane == 0) sm::bar_arrive(sm::smem(&first_tile.ready));
+            }
+            sm::pdl_wait();
+        }
         float v[T::kWidth], u[GATED ? T::kWidth : 1];   // the thread's feature, its columns
         int n = 0;
         bool ok = true;
@@ -378,7 +458,8 @@ linear_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
             }
             int pieces = (kb1 - kb0 + piece - 1) / piece;
             if constexpr (ADAPT && F32) {
-                const LinearShare sh = linear_share<F32>(e, tile % p.tiles_m, rank, p.split);
+                LinearShare sh{};
+                if (!(ok = share(tile, sh))) break;
                 pieces += (sh.b1 - sh.b0 + kPromote - 1) / kPromote;
             }
 #pragma unroll 1
@@ -480,6 +561,7 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
     __shared__ uint64_t bars[2 * T::kStages + 4];
     __shared__ uint32_t tmem_at;
     __shared__ int abort_flag;
+    __shared__ std::conditional_t<ADAPT, LinearFirst, char> first_tile;
     volatile int* abort_word = &abort_flag;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t stage0 = (sm::smem(raw) + 1023u) & ~1023u;
@@ -493,6 +575,7 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
     if (threadIdx.x == 0) {
         for (int s = 0; s < T::kStages; ++s) { sm::bar_init(full(s), 1); sm::bar_init(empty(s), 1); }
         for (int s = 0; s < 2; ++s) { sm::bar_init(acc_full(s), 1); sm::bar_init(acc_empty(s), 16); }
+        if constexpr (ADAPT) sm::bar_init(sm::smem(&first_tile.ready), 1);
         abort_flag = 0;
         sm::bar_fence_init();
         sm::tma_prefetch_map(&map_w);
@@ -505,7 +588,7 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
     sm::tc_fence_after();
     const uint32_t tmem = tmem_at;
     sm::pdl_trigger();
-    if (!ADAPT || warp >= 2) sm::pdl_wait();
+    if constexpr (!ADAPT) sm::pdl_wait();
 
     const int cluster = 2 * p.split;
     const int first = int(blockIdx.x) / cluster, step = int(gridDim.x) / cluster;
@@ -518,6 +601,24 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
         const int width = min(8, p.tiles_m - group * 8);
         m0 = (group * 8 + in % width) * 256;
         n0 = in / width * (2 * T::kRows) + half * T::kRows;
+    };
+    // (fails only as its wait does)
+    [[maybe_unused]] auto share = [&](int tile, LinearShare& s) {
+        if constexpr (ADAPT) {
+            int n0, m0;
+            place(tile, n0, m0);
+            if (tile == first) {
+                if (!sm::bar_wait_warp(sm::smem(&first_tile.ready), 0, abort_word, p.status)) return false;
+                s.list = first_tile.list;
+                s.adapters = *reinterpret_cast<const volatile int32_t*>(&first_tile.count);
+            } else {
+                sm::pdl_wait();
+                s.list = e.list + int64_t(m0 / 256) * e.slots;
+                s.adapters = *reinterpret_cast<const volatile int32_t*>(e.count + m0 / 256);
+            }
+            s.cut(e.width, part, p.split);
+        }
+        return true;
     };
 
     if (warp == 0) {
@@ -541,29 +642,54 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
                 if (++s == T::kStages) { s = 0; phase ^= 1u; }
             }
             if constexpr (ADAPT) {
-                sm::pdl_wait();
-                const int m = m0 / 256;
-                const LinearShare sh = linear_share<F32>(e, m, part, p.split);
-                LinearAdapters adapter(e.list + int64_t(m) * e.slots, sh.adapters);
-                constexpr int kItems = F32 ? 1 : 2;
-                for (int b = sh.b0; b < sh.b1 && ok; ++b, ++it) {
-                    if (!(ok = sm::bar_wait_warp(empty(s), phase, abort_word, p.status))) break;
-                    const uint32_t at = stage0 + s * T::kStageBytes, bar = sm::cluster_addr(full(s), leader);
-                    const int items = min(kItems, sh.items - b * kItems);
-                    if (issuer) {
-                        if (half == 0) sm::bar_expect(full(s), uint32_t(2 * (items * kAdaptItemBytes + T::kHalfBytes)));
-                        sm::tma_load_2d_pair(at + T::kHalfBytes, &e.terms, bar, b * 64, m0 + half * 128);
-                    }
-                    for (int i = 0; i < items; ++i) {
-                        const int item = b * kItems + i, a = adapter(item / e.items), c = item % e.items * 16;
+                LinearShare sh{};
+                if (!ok || !(ok = share(tile, sh))) break;
+                // up first, as far as the stages go: it does not depend on the kernel in front, as the terms do
+                int given_s = s, given = sh.b0;   // (of the terms)
+                auto terms = [&](int upto) {
+                    for (; given < upto; ++given) {
+                        const uint32_t at = stage0 + given_s * T::kStageBytes, bar = sm::cluster_addr(full(given_s), leader);
                         if (issuer) {
-                            sm::tma_load_3d_pair(at + i * kAdaptItemBytes, &e.up, bar, c, n0, a);
-                            if (GATED) sm::tma_load_3d_pair(at + i * kAdaptItemBytes + kAdaptItemBytes / 2, &e.up, bar, c, p.n + n0, a);
+                            sm::tma_load_2d_pair(at + T::kHalfBytes, &e.terms, bar, given * 2 * kAdaptCols, m0 + half * 128);
+                            if (F32) sm::tma_load_2d_pair(at + kAdaptBytes, &e.third, bar, given * kAdaptCols, m0 + half * 128);
+                        }
+                        if (++given_s == T::kStages) given_s = 0;
+                    }
+                };
+                const bool two = e.width == 16;
+                const int last = two && sh.adapters % 2 ? sh.adapters / 2 : -1;   // a block of one adapter's 16 columns
+                constexpr uint32_t kTerms = T::kHalfBytes + (F32 ? T::kHalfBytes / 2 : 0);
+                const uint32_t up_rows = GATED ? (two ? kAdaptBytes / 4 : kAdaptBytes / 2) : 0;   // (behind the gate rows)
+                LinearColumns col(sh, e.width, sh.b0 * kAdaptCols);
+                int b = sh.b0;
+                for (; b < sh.b1; ++b, ++it) {
+                    if (b - sh.b0 >= T::kStages) {
+                        if (b - sh.b0 == T::kStages) sm::pdl_wait();
+                        terms(b);
+                    }
+                    if (!(ok = sm::bar_wait_warp(empty(s), phase, abort_word, p.status))) break;
+                    if (issuer) {
+                        const uint32_t at = stage0 + s * T::kStageBytes, bar = sm::cluster_addr(full(s), leader);
+                        if (half == 0) sm::bar_expect(full(s), 2 * ((b == last ? kAdaptBytes / 2 : kAdaptBytes) + kTerms));
+                        sm::tma_load_3d_pair(at, &e.up, bar, col.column, n0, col.name);
+                        if (GATED) sm::tma_load_3d_pair(at + up_rows, &e.up, bar, col.column, p.n + n0, col.name);
+                        if (two) {
+                            col.step(16);
+                            if (b != last) {
+                                sm::tma_load_3d_pair(at + kAdaptBytes / 2, &e.up, bar, 0, n0, col.name);
+                                if (GATED) sm::tma_load_3d_pair(at + kAdaptBytes / 2 + up_rows, &e.up, bar, 0, p.n + n0, col.name);
+                                col.step(16);
+                            }
+                        } else {
+                            col.step(kAdaptCols);
                         }
                     }
                     __syncwarp();
                     if (++s == T::kStages) { s = 0; phase ^= 1u; }
                 }
+                sm::pdl_wait();
+                terms(b);   // (after a wait that ran out too: every copy that a barrier expects is made)
+                __syncwarp();
             }
         }
         // the products' last arrivals on this CTA's barriers come before it leaves
@@ -583,29 +709,29 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
             int s = 0, n = 0;
             uint32_t phase = 0;
             bool ok = true;
+            const bool two = e.width == 16;
+            const uint64_t up0 = two ? sm::desc_k_sw32(stage0) : sm::desc_k_sw64(stage0), third0 = sm::desc_k_sw64(stage0 + kAdaptBytes);
+            const uint64_t step16 = two ? kAdaptBytes / 2 >> 4 : 2;
             [[maybe_unused]] auto adapters = [&](uint32_t d, const LinearShare& sh, int x0, int x1, bool fresh) {
                 for (int b = x0; b < x1; ++b) {
                     if (!(ok = sm::bar_wait_warp(full(s), phase, abort_word, p.status))) break;
                     sm::tc_fence_after();
-                    const uint64_t a = sm::desc_k_sw32(stage0 + uint32_t(s * T::kStageBytes)), t = b0 + uint64_t(s * (T::kStageBytes >> 4));
-                    const int steps = F32 ? 3 : 2 * min(2, sh.items - 2 * b);
+                    const uint64_t at = uint64_t(s * (T::kStageBytes >> 4)), t = b0 + at, t3 = third0 + at, a = up0 + at;
+                    const int steps = two && 2 * b + 1 == sh.adapters ? 1 : 2;   // of 16 columns
                     if (issuer) {
 #pragma unroll
-                        for (int kk = 0; kk < (F32 ? 3 : 4); ++kk) {
+                        for (int kk = 0; kk < 2; ++kk) {
                             if (kk >= steps) break;
-                            const uint64_t up = a + uint64_t((F32 ? 0 : kk / 2) * (kAdaptItemBytes >> 4));
-                            sm::mma_ss_pair(d, up, t + 2 * kk, idesc, !fresh || b > x0 || kk > 0);
+#pragma unroll
+                            for (int term = 0; term < (F32 ? 3 : 2); ++term)
+                                sm::mma_ss_pair(d, a + kk * step16, (term == 2 ? t3 : t + 4 * term) + 2 * kk, idesc,
+                                                !fresh || b > x0 || kk > 0 || term > 0);
                         }
                         sm::mma_commit_pair(empty(s), both);
                     }
                     __syncwarp();
                     if (++s == T::kStages) { s = 0; phase ^= 1u; }
                 }
-            };
-            [[maybe_unused]] auto token_tile = [&](int tile) {
-                int n0, m0;
-                place(tile, n0, m0);
-                return m0 / 256;
             };
             for (int tile = first; tile < tiles && ok; tile += step) {
                 for (int k0 = kb0; k0 < kb1 && ok; k0 += piece, ++n) {
@@ -627,16 +753,15 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
                         if (++s == T::kStages) { s = 0; phase ^= 1u; }
                     }
                     if constexpr (ADAPT && !F32) {   // (the tile's only piece)
-                        sm::pdl_wait();
-                        const LinearShare sh = linear_share<F32>(e, token_tile(tile), part, p.split);
-                        if (ok) adapters(d, sh, sh.b0, sh.b1, false);
+                        LinearShare sh{};
+                        if (ok && (ok = share(tile, sh))) adapters(d, sh, sh.b0, sh.b1, false);
                     }
                     if (ok && issuer) sm::mma_commit_pair(acc_full(buf), both);
                     __syncwarp();
                 }
                 if constexpr (ADAPT && F32) {
-                    sm::pdl_wait();
-                    const LinearShare sh = linear_share<F32>(e, token_tile(tile), part, p.split);
+                    LinearShare sh{};
+                    ok = ok && share(tile, sh);
                     for (int x0 = sh.b0; x0 < sh.b1 && ok; x0 += kPromote, ++n) {
                         const int buf = n & 1;
                         if (n >= 2 && !(ok = sm::bar_wait_warp(acc_empty(buf), uint32_t(n / 2 - 1) & 1u, abort_word, p.status))) break;
@@ -656,6 +781,16 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
         const int quarter = warp & 3, row = quarter * 32 + lane, cols = (warp - 2) / 4 * 128;
         const uint32_t lanes = uint32_t(quarter * 32) << 16;
         const bool up_row = GATED && row >= 64, plain = !GATED && p.act == MK_ACT_NONE;
+        if constexpr (ADAPT) {
+            if (warp == 2 && first < tiles) {
+                int n0, m0;
+                place(first, n0, m0);
+                linear_list(e, m0, min(256, p.rows - m0), first_tile);
+                __syncwarp();
+                if (lane == 0) sm::bar_arrive(sm::smem(&first_tile.ready));
+            }
+            sm::pdl_wait();
+        }
         float v[128];   // the thread's row of the tile, its 128 columns
         int n = 0;
         bool ok = true;
@@ -669,8 +804,9 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
                               p.bias && live ? __bfloat162float(p.bias[jb]) : 0.f, v);
             int pieces = (kb1 - kb0 + piece - 1) / piece;
             if constexpr (ADAPT && F32) {
-                const LinearShare sh = linear_share<F32>(e, m0 / 256, part, p.split);
-                pieces += (sh.b1 - sh.b0 + kPromote - 1) / kPromote;
+                LinearShare sh{};
+                ok = share(tile, sh);
+                pieces = ok ? pieces + (sh.b1 - sh.b0 + kPromote - 1) / kPromote : 0;
             }
 #pragma unroll 1
             for (int i = 0; i < pieces; ++i, ++n) {

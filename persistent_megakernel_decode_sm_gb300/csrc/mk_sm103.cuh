@@ -298,5 +298,11 @@ __device__ __forceinline__ float cluster_ld(uint32_t cluster_at) {   // a peer C
     return v;
 }
 
+__device__ __forceinline__ float2 cluster_ld2(uint32_t cluster_at) {
+    float2 v;
+    asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(cluster_at));
+    return v;
+}
+
 }  // namespace sm
 }  // namespace mk
