@@ -8,6 +8,7 @@ namespace mk {
 
 constexpr int kLowThreads = 256, kLowTokens = 16, kLowWarps = kLowThreads / 32;
 constexpr int kLowTile = 256;       // most tokens of a tile of the linear map
+constexpr int kLowFew = 512;        // tokens that are few: the work is in their adapters' rows, not in theirs
 
 struct LowParams {
     int rows, k, rank, n_adapters;
@@ -20,9 +21,8 @@ struct LowParams {
     const int32_t* index;
     int32_t* count;
     int32_t* list;
-    __nv_bfloat16* terms;           // [rows][blocks][2][32]: the first two parts
-    __nv_bfloat16* third;           // [rows][blocks][32]
-    int64_t blocks;
+    __nv_bfloat16* terms;           // [rows][parts][part columns]
+    int64_t part;
     int32_t* status;
 };
 
@@ -44,7 +44,7 @@ __device__ __forceinline__ uint4 low_load(const __nv_bfloat16* p, bool wanted) {
 // These products need no more than the reading of x and down does (they are 1/8 to 1/100 of the linear map's), so they stay on
 // mma.sync, with registers for operands and no staging.
 template <int NT>
-__global__ void __launch_bounds__(kLowThreads) low_rank_kernel(const __grid_constant__ LowParams p) {
+__global__ void __launch_bounds__(kLowThreads, 2) low_rank_kernel(const __grid_constant__ LowParams p) {
     constexpr int kCols = 8 * NT;
     extern __shared__ float all_sums[];                 // [2][16][width], in turn for the adapters
     __shared__ __align__(16) int name[kLowTile];
@@ -120,7 +120,7 @@ __global__ void __launch_bounds__(kLowThreads) low_rank_kernel(const __grid_cons
                 for (int j = 0; j < NT; ++j)
 #pragma unroll
                     for (int v = 0; v < 4; ++v) acc[j][v] = 0.f;
-#pragma unroll 4
+#pragma unroll NT == 8 ? 2 : 4
                 for (int b = rank_z * kLowWarps + warp; b < blocks; b += split * kLowWarps) {
                     const bool in = b * 32 + q * 8 < p.k;
                     uint4 xs[2], ds[NT];
@@ -172,14 +172,12 @@ __global__ void __launch_bounds__(kLowThreads) low_rank_kernel(const __grid_cons
                 v[0] *= scale;
                 v[1] *= scale;
             }
-            const int col = slot * width + c;
-            const int64_t block = int64_t(m0 + row0 + r) * p.blocks + col / kAdaptCols;
-            __nv_bfloat16* dst = p.terms + block * (2 * kAdaptCols) + col % kAdaptCols;
-            for (int term = 0; term < (p.f32 ? 3 : 2); ++term) {
+            __nv_bfloat16* dst = p.terms + int64_t(m0 + row0 + r) * (p.f32 ? 3 : 2) * p.part + slot * width + c;
+            for (int part = 0; part < (p.f32 ? 3 : 2); ++part, dst += p.part) {
                 __nv_bfloat162 pair;
                 pair.x = __float2bfloat16_rn(v[0]);
                 pair.y = __float2bfloat16_rn(v[1]);
-                *reinterpret_cast<__nv_bfloat162*>(term == 2 ? p.third + block * kAdaptCols + col % kAdaptCols : dst + term * kAdaptCols) = pair;
+                *reinterpret_cast<__nv_bfloat162*>(dst) = pair;
                 const float h0 = __bfloat162float(pair.x), h1 = __bfloat162float(pair.y);
                 v[0] = isinf(h0) ? 0.f : v[0] - h0;   // (an infinity, or a value that rounds to one, leaves no rest)
                 v[1] = isinf(h1) ? 0.f : v[1] - h1;
@@ -198,8 +196,8 @@ constexpr int64_t kAdaptTermsBytes = 256ll << 20;
 struct AdaptPlan {
     LinearChoice<true> choice;
     int slots, width, tiles;        // of a piece
-    int64_t rows, blocks;           // tokens of a piece, blocks of its adapters' columns
-    size_t list, terms, third, bytes;   // offsets of what lies behind the counts; all
+    int64_t rows, part;             // tokens of a piece, columns of a part of their terms
+    size_t list, terms, bytes;      // offsets of what lies behind the counts; all
 };
 
 static mk_status adapt_check(const mk_linear_args* a, const mk_adapters* ad, bool pointers) {
@@ -223,7 +221,7 @@ static mk_status adapt_check(const mk_linear_args* a, const mk_adapters* ad, boo
 static mk_status adapt_plan(const mk_linear_args* a, const mk_adapters* ad, AdaptPlan& pl) {
     LinearParams p{};
     const bool f32 = a->out_dtype == MK_F32;
-    pl.width = ad->rank <= 16 ? 16 : (ad->rank + kAdaptCols - 1) / kAdaptCols * kAdaptCols;
+    pl.width = ad->rank <= 16 ? 16 : ad->rank <= 32 ? 32 : (ad->rank + kAdaptCols - 1) / kAdaptCols * kAdaptCols;
     // blocks of the adapters' part, for the estimate: few tokens name an adapter each, of many neighbours share theirs
     const int named = std::min({a->rows <= 64 ? a->rows : 4, ad->n_adapters, 64});
     const int extra = (named * pl.width + kAdaptCols - 1) / kAdaptCols;
@@ -231,21 +229,16 @@ static mk_status adapt_plan(const mk_linear_args* a, const mk_adapters* ad, Adap
     if (st != MK_OK) return st;
     const int tile = pl.choice.tokens;
     pl.slots = std::min({tile, ad->n_adapters, a->rows});
-    pl.blocks = (int64_t(pl.slots) * pl.width + kAdaptCols - 1) / kAdaptCols;
-    const int64_t all = (int64_t(a->rows) + tile - 1) / tile, row = pl.blocks * kAdaptCols * 2;   // bytes of a part of a token
-    pl.tiles = int(std::min(all, std::max<int64_t>(1, kAdaptTermsBytes / (3 * row * tile))));
+    pl.part = (int64_t(pl.slots) * pl.width + kAdaptCols - 1) / kAdaptCols * kAdaptCols;
+    const int64_t all = (int64_t(a->rows) + tile - 1) / tile, row = pl.part * (f32 ? 3 : 2) * 2;   // bytes of a token's terms
+    pl.tiles = int(std::min(all, std::max<int64_t>(1, kAdaptTermsBytes / (row * tile))));
     pl.rows = std::min<int64_t>(a->rows, int64_t(pl.tiles) * tile);
     pl.list = align256(size_t(pl.tiles) * 4);
     pl.terms = pl.list + align256(size_t(pl.tiles) * size_t(pl.slots) * 4);
-    pl.third = pl.terms + align256(size_t(pl.rows * row) * 2);
-    pl.bytes = pl.third + (f32 ? align256(size_t(pl.rows * row)) : 0);
+    pl.bytes = pl.terms + align256(size_t(pl.rows * row));
     return MK_OK;
 }
 
-#ifndef LROWS
-#define LROWS 512
-#define LCTAS 2
-#endif
 template <int NT>
 static mk_status low_launch(LowParams& p, int device, int sms, cudaStream_t stream) {
     static std::atomic<uint64_t> set{0};
@@ -253,11 +246,12 @@ static mk_status low_launch(LowParams& p, int device, int sms, cudaStream_t stre
     if (st != MK_OK) return st;
     p.subs = (p.tile + kLowTokens - 1) / kLowTokens;
     const int64_t subs = int64_t((p.rows + p.tile - 1) / p.tile) * p.subs;
-    // adapters of a tile side by side where there are few tokens, then the contraction over clusters of 2, 4 or 8 while LCTAS CTAs
-    // an SM are not reached and each warp keeps a block of 32
-    const int lanes = p.rows <= LROWS ? std::min({p.slots, 16}) : 1;
+    // Adapters of a tile side by side where there are few tokens, then the contraction over clusters of 2, 4 or 8 while two CTAs an SM
+    // (what is resident) are not exceeded and each warp keeps a block of 32.  64 tokens with an adapter of rank 64 each (k 4096): 16 us
+    // in clusters of 4, in which 256 CTAs have work; of 2 21 us, and of 8, whose 512 CTAs come in rounds, 24
+    const int lanes = p.rows <= kLowFew ? std::min({p.slots, 16}) : 1;
     int split = 1;
-    while (split < 8 && 2 * subs * lanes * split <= int64_t(LCTAS) * sms && 2 * split * kLowWarps * 32 <= p.k) split *= 2;
+    while (split < 8 && 2 * subs * lanes * split <= 2 * sms && 2 * split * kLowWarps * 32 <= p.k) split *= 2;
     cudaLaunchConfig_t cfg{};
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -315,10 +309,11 @@ extern "C" mk_status mk_linear_adapted(const mk_linear_args* a, const mk_adapter
         low.count = reinterpret_cast<int32_t*>(ws);
         low.list = reinterpret_cast<int32_t*>(ws + pl.list);
         low.terms = reinterpret_cast<__nv_bfloat16*>(ws + pl.terms);
-        low.third = reinterpret_cast<__nv_bfloat16*>(ws + pl.third);
-        low.blocks = pl.blocks;
+        low.part = pl.part;
         low.status = a->status;
-        if ((st = pl.width > 16 ? low_launch<4>(low, device, sms, s) : low_launch<2>(low, device, sms, s)) != MK_OK) return st;
+        if ((st = pl.width > 32 && c.rows <= kLowFew ? low_launch<8>(low, device, sms, s)
+                  : pl.width > 16 ? low_launch<4>(low, device, sms, s)
+                                  : low_launch<2>(low, device, sms, s)) != MK_OK) return st;
         LinearExtra<true> e{};
         e.index = low.index;
         e.n_adapters = ad->n_adapters;
@@ -326,18 +321,18 @@ extern "C" mk_status mk_linear_adapted(const mk_linear_args* a, const mk_adapter
         e.list = low.list;
         e.slots = pl.slots;
         e.width = pl.width;
+        e.part = int32_t(pl.part);
         const int64_t w_rows = int64_t(c.n) * (c.activation == MK_ACT_SWIGLU ? 2 : 1);
         const cuuint64_t ud[3] = {cuuint64_t(ad->rank), cuuint64_t(w_rows), cuuint64_t(ad->n_adapters)};
         const cuuint64_t us[2] = {cuuint64_t(ad->rank) * 2, cuuint64_t(w_rows) * cuuint64_t(ad->rank) * 2};
-        const cuuint32_t ub[3] = {cuuint32_t(std::min(pl.width, kAdaptCols)), cuuint32_t(pl.choice.unit == 2 ? pl.choice.features / 2 : 128), 1};
+        const bool pair = pl.choice.unit == 2;
+        const int block = pair ? kPairCols : kAdaptCols;
+        const cuuint32_t ub[3] = {cuuint32_t(std::min(pl.width, block)), cuuint32_t(pair ? pl.choice.features / 2 : 128), 1};
         if ((st = op_tensor_map(&e.up, ad->up, 3, ud, us, ub)) != MK_OK) return st;
-        const cuuint32_t tile = cuuint32_t(pl.choice.unit == 2 ? 128 : pl.choice.tokens);
-        const cuuint64_t cols = cuuint64_t(pl.blocks) * kAdaptCols, td[2] = {2 * cols, cuuint64_t(c.rows)}, ts[1] = {cols * 4};
-        const cuuint32_t tb[2] = {2 * kAdaptCols, tile};
+        const cuuint32_t tile = cuuint32_t(pair ? 128 : pl.choice.tokens);
+        const cuuint64_t cols = cuuint64_t(pl.part) * (f32 ? 3 : 2), td[2] = {cols, cuuint64_t(c.rows)}, ts[1] = {cols * 2};
+        const cuuint32_t tb[2] = {cuuint32_t(block), tile};
         if ((st = op_tensor_map(&e.terms, low.terms, 2, td, ts, tb)) != MK_OK) return st;
-        const cuuint64_t hd[2] = {cols, cuuint64_t(c.rows)}, hs[1] = {cols * 2};
-        const cuuint32_t hb[2] = {kAdaptCols, tile};
-        if (f32 && (st = op_tensor_map(&e.third, low.third, 2, hd, hs, hb)) != MK_OK) return st;
         // (the piece's own tiles: pieces are whole tiles but for the last)
         LinearParams p{};
         LinearPlan plan = pl.choice.plan;

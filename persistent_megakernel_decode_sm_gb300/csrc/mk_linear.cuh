@@ -26,37 +26,43 @@ struct LinearParams {
 // tokens of other adapters (mk_adapt.cu works them out, and lists each tile's adapters).  So the weights of an adapter are
 // read once per tile of tokens, whoever names it, and the sums meet in the accumulators in front of the activation.
 // The low-rank rows are cut into bf16 parts, two (16 of fp32's 24 bits: off by 2^-18 of the adapter's share, far below a bf16
-// output's own rounding) or, for an fp32 output, three.  An adapter takes 16 columns of the rank, or a multiple of 32: a block is 32
-// columns of up (one adapter's, rows of 64 bytes, or two adapters', rows of 32) against the first two parts of the 32 columns
-// (64 columns of `terms`) and the third (32 columns of `third`): up is loaded once for all parts.
+// output's own rounding) or, for an fp32 output, three.  An adapter takes 16 columns of the rank, 32, or a multiple of 64; a piece is
+// up to 64 of them.  A block is 64 columns of up (four, two or one adapter's pieces, rows of 32, 64 or 128 bytes) in one
+// stage beside the first part of the terms' 64 columns, and the other parts in the stage after it: up is copied once for all parts,
+// and what a block costs by itself (waits, commits) is shared by 8 or 12 products.  A CTA pair, whose tiles name few adapters, takes
+// blocks of 32 columns in one stage each (4096 tokens through 2 x 8192 x 2048 168 us, with blocks over two stages 172).
 template <bool ADAPT>
 struct LinearExtra {
     static constexpr int32_t width = 0;
 };
 template <>
 struct LinearExtra<true> {
-    CUtensorMap up, terms, third;
+    CUtensorMap up, terms;     // terms: [rows][part][blocks][64]
     const int32_t* index;      // [rows], -1 or n_adapters and more: none
     const int32_t* count;      // [tiles of tokens]: adapters of the tile
     const int32_t* list;       // [tiles of tokens][slots]: which, in the order in which its tokens name them
     int32_t slots, width;      // columns of an adapter
+    int32_t part;              // columns of a part
     int32_t n_adapters;
 };
-constexpr int kAdaptCols = 32, kAdaptBytes = 128 * kAdaptCols * 2;   // of a block: columns, bytes of 128 rows of up
+constexpr int kAdaptCols = 64;   // of a block
+constexpr int kPairCols = 32, kPairBytes = 128 * kPairCols * 2;   // of a CTA pair's, all in one stage: columns, bytes of 128 rows
+__device__ __forceinline__ int adapt_piece(int width) { return min(width, kAdaptCols); }
 // This CTA's share [b0, b1) of the adapters' blocks of a token tile, for the role that asks, and the adapters of its
 // columns: in shared memory for the CTA's first tile, in global memory for the others (behind the wait for the kernel that lists them)
 struct LinearShare {
     const volatile int32_t* list;
-    int adapters, b0, b1;
-    __device__ __forceinline__ void cut(int width, int rank, int split) {
-        const int blocks = (adapters * width + kAdaptCols - 1) / kAdaptCols;
+    int adapters, pieces, b0, b1;
+    __device__ __forceinline__ void cut(int width, int cols, int rank, int split) {   // (cols: of a block)
+        pieces = width < cols ? adapters : adapters * (width / cols);
+        const int blocks = (adapters * width + cols - 1) / cols;
         b0 = int(int64_t(blocks) * rank / split);
         b1 = int(int64_t(blocks) * (rank + 1) / split);
     }
 };
-struct LinearFirst {   // the first tile's adapters
+struct LinearFirst {   // the first tile's adapters; stages given to a block of adapters, whose terms may be copied
     int32_t list[256], count;
-    uint64_t ready;
+    uint64_t ready, granted[10];
 };
 // By one warp: the adapters that tokens [m0, m0 + tokens) name, in order
 __device__ __forceinline__ void linear_list(const LinearExtra<true>& e, int m0, int tokens, LinearFirst& first) {
@@ -192,6 +198,7 @@ __device__ __forceinline__ void linear_join(const LinearParams& p, uint32_t stag
 // (3.4e-7); a bf16 output rounds a thousand times coarser and takes the whole contraction in one piece.
 constexpr int kLinK = 64;
 constexpr int kPromote = 8;
+constexpr int kAdaptPromote = 3;   // (blocks of adapters, of 12 products each, where those of w and x have 4)
 template <int BN, bool GATED>
 struct LinearTile {
     static constexpr int kAccs = GATED ? 2 : 1;
@@ -207,13 +214,13 @@ struct LinearTile {
     static_assert(kStages * kStageBytes >= kBufCols * 128 * 4);   // a split tile's partial sums are staged there
 };
 
-// Warp 0: TMA producer.  Warp 1: tensor memory and MMA issue.  The others: epilogue.
+// Warp 0: TMA producer.  Warp 1: tensor memory and MMA issue.  The others: epilogue; with adapters the last: copies of their terms.
 //
 // With adapters the kernel starts once every CTA of the kernel in front of it (mk_adapt.cu's, whose first act is to wait for the
-// kernels before it) has started: x and w are read at once, beside that kernel, and only who reads its results, the
-// residual or writes the output waits for its end.
+// kernels before it) has started: every kernel before that one is done, so x, w and the residual are read and sums taken at once,
+// beside that kernel, and only who copies its results waits for its end.
 template <int BN, bool GATED, bool F32, bool ADAPT>
-__global__ void __launch_bounds__(64 + 32 * LinearTile<BN, GATED>::kWarps, 1)
+__global__ void __launch_bounds__(64 + 32 * LinearTile<BN, GATED>::kWarps + (ADAPT ? 32 : 0), 1)
 linear_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x,
               const __grid_constant__ LinearParams p, const __grid_constant__ LinearExtra<ADAPT> e) {
     using T = LinearTile<BN, GATED>;
@@ -235,7 +242,11 @@ linear_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
         for (int s = 0; s < T::kStages; ++s) { sm::bar_init(full(s), 1); sm::bar_init(empty(s), 1); }
         for (int s = 0; s < 2; ++s) { sm::bar_init(acc_full(s), 1); sm::bar_init(acc_empty(s), T::kWarps); }
         sm::bar_init(drained, 1);
-        if constexpr (ADAPT) sm::bar_init(sm::smem(&first_tile.ready), 1);
+        if constexpr (ADAPT) {
+            static_assert(T::kStages <= 10);
+            sm::bar_init(sm::smem(&first_tile.ready), 1);
+            for (int s = 0; s < T::kStages; ++s) sm::bar_init(sm::smem(&first_tile.granted[s]), 1);
+        }
         abort_flag = 0;
         sm::bar_fence_init();
         sm::tma_prefetch_map(&map_w);
@@ -273,7 +284,7 @@ linear_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
                 s.list = e.list + int64_t(m) * e.slots;
                 s.adapters = *reinterpret_cast<const volatile int32_t*>(e.count + m);
             }
-            s.cut(e.width, rank, p.split);
+                s.cut(e.width, kAdaptCols, rank, p.split);
         }
         return true;
     };
@@ -301,51 +312,37 @@ linear_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
             if constexpr (ADAPT) {
                 LinearShare sh{};
                 if (!ok || !(ok = share(tile, sh))) break;
-                // up first, as far as the stages go: it does not depend on the kernel in front, as the terms do
-                int given_s = s, given = sh.b0;   // (of the terms)
-                auto terms = [&](int upto) {
-                    for (; given < upto; ++given) {
-                        const uint32_t at = stage0 + given_s * T::kStageBytes;
-                        if (issuer) {
-                            sm::tma_load_2d(at + T::kAccs * T::kABytes, &e.terms, full(given_s), given * 2 * kAdaptCols, m0);
-                            if (F32) sm::tma_load_2d(at + kAdaptBytes, &e.third, full(given_s), given * kAdaptCols, m0);
-                        }
-                        if (++given_s == T::kStages) given_s = 0;
-                    }
-                };
-                const bool two = e.width == 16;
-                const int last = two && sh.adapters % 2 ? sh.adapters / 2 : -1;   // a block of one adapter's 16 columns
-                constexpr uint32_t kTerms = T::kBBytes + (F32 ? T::kBBytes / 2 : 0);
+                // (up does not depend on the kernel in front: its copies are made as soon as there are stages; the last warp adds the terms)
+                const int span = adapt_piece(e.width), most = kAdaptCols / span;
+                const uint32_t bytes = uint32_t(span) * 256u;   // of a piece, 128 rows
                 LinearColumns col(sh, e.width, sh.b0 * kAdaptCols);
-                int b = sh.b0;
-                for (; b < sh.b1; ++b, ++it) {
-                    if (b - sh.b0 >= T::kStages) {
-                        if (b - sh.b0 == T::kStages) sm::pdl_wait();
-                        terms(b);
-                    }
+                auto next_stage = [&] {
+                    ++it;
+                    if (++s == T::kStages) { s = 0; phase ^= 1u; }
+                };
+                for (int b = sh.b0; b < sh.b1; ++b) {
                     if (!(ok = sm::bar_wait_warp(empty(s), phase, abort_word, p.status))) break;
                     if (issuer) {
-                        const uint32_t at = stage0 + s * T::kStageBytes;
-                        sm::bar_expect(full(s), (b == last ? T::kAccs * (kAdaptBytes / 2) : T::kAccs * kAdaptBytes) + kTerms);
-                        sm::tma_load_3d(at, &e.up, full(s), col.column, n0, col.name);
-                        if (GATED) sm::tma_load_3d(at + T::kABytes, &e.up, full(s), col.column, p.n + n0, col.name);
-                        if (two) {
-                            col.step(16);
-                            if (b != last) {
-                                sm::tma_load_3d(at + kAdaptBytes / 2, &e.up, full(s), 0, n0, col.name);
-                                if (GATED) sm::tma_load_3d(at + T::kABytes + kAdaptBytes / 2, &e.up, full(s), 0, p.n + n0, col.name);
-                                col.step(16);
-                            }
-                        } else {
-                            col.step(kAdaptCols);
+                        const int items = min(most, sh.pieces - b * most);
+                        sm::bar_expect(full(s), uint32_t(items * T::kAccs) * bytes + T::kBBytes);
+                        sm::bar_arrive(sm::smem(&first_tile.granted[s]));
+                        uint32_t at = stage0 + s * T::kStageBytes;
+                        for (int i = 0; i < items; ++i, at += bytes) {
+                            sm::tma_load_3d(at, &e.up, full(s), col.column, n0, col.name);
+                            if (GATED) sm::tma_load_3d(at + T::kABytes, &e.up, full(s), col.column, p.n + n0, col.name);
+                            col.step(span);
                         }
                     }
                     __syncwarp();
-                    if (++s == T::kStages) { s = 0; phase ^= 1u; }
+                    next_stage();
+                    if (!(ok = sm::bar_wait_warp(empty(s), phase, abort_word, p.status))) break;
+                    if (issuer) {
+                        sm::bar_expect(full(s), T::kBBytes * (F32 ? 2 : 1));
+                        sm::bar_arrive(sm::smem(&first_tile.granted[s]));
+                    }
+                    __syncwarp();
+                    next_stage();
                 }
-                sm::pdl_wait();
-                terms(b);   // (after a wait that ran out too: every copy that a barrier expects is made)
-                __syncwarp();
             }
         }
         if (*abort_word && issuer)   // the copies in flight land before the CTA gives its shared memory back
@@ -359,31 +356,36 @@ linear_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
         uint32_t phase = 0;
         bool ok = true;
         // the adapters' blocks [x0, x1) into accumulators d: an item's products with each of its terms
-        const bool two = e.width == 16;
-        const uint64_t up0 = two ? sm::desc_k_sw32(stage0) : sm::desc_k_sw64(stage0), third0 = sm::desc_k_sw64(stage0 + kAdaptBytes);
-        const uint64_t step16 = two ? kAdaptBytes / 2 >> 4 : 2;
+        const int span = adapt_piece(e.width);
+        const uint64_t up0 = span == 16 ? sm::desc_k_sw32(stage0) : span == 32 ? sm::desc_k_sw64(stage0) : a0;
+        const uint64_t odd = span == 16 ? 4096 >> 4 : 2, even = span == 64 ? 4 : 8192 >> 4;   // 16 columns further, 32
         [[maybe_unused]] auto adapters = [&](uint32_t d, const LinearShare& sh, int x0, int x1, bool fresh) {
             for (int b = x0; b < x1; ++b) {
-                if (!(ok = sm::bar_wait_warp(full(s), phase, abort_word, p.status))) break;
+                const int s1 = s + 1 == T::kStages ? 0 : s + 1;
+                if (!(ok = sm::bar_wait_warp(full(s), phase, abort_word, p.status)) ||
+                    !(ok = sm::bar_wait_warp(full(s1), phase ^ uint32_t(s1 == 0), abort_word, p.status)))
+                    break;
                 sm::tc_fence_after();
-                const uint64_t at = uint64_t(s * (T::kStageBytes >> 4)), t = b0 + at, t3 = third0 + at, a = up0 + at;
-                const int steps = two && 2 * b + 1 == sh.adapters ? 1 : 2;   // of 16 columns
+                const uint64_t at = uint64_t(s * (T::kStageBytes >> 4)), at1 = uint64_t(s1 * (T::kStageBytes >> 4));
+                const uint64_t x[3] = {b0 + at, b0 + at1, a0 + at1};   // the parts
+                const int steps = min(kAdaptCols, sh.pieces * span - b * kAdaptCols) / 16;
                 if (leader) {
 #pragma unroll
-                    for (int kk = 0; kk < 2; ++kk) {
+                    for (int kk = 0; kk < kAdaptCols / 16; ++kk) {
                         if (kk >= steps) break;
-                        const uint64_t up = a + kk * step16;
+                        const uint64_t up = up0 + at + kk / 2 * even + kk % 2 * odd;
 #pragma unroll
-                        for (int term = 0; term < (F32 ? 3 : 2); ++term) {
-                            const uint64_t x = (term == 2 ? t3 : t + 4 * term) + 2 * kk;
-                            sm::mma_ss(d, up, x, idesc, !fresh || b > x0 || kk > 0 || term > 0);
-                            if (GATED) sm::mma_ss(d + BN, up + (T::kABytes >> 4), x, idesc, !fresh || b > x0 || kk > 0 || term > 0);
+                        for (int part = 0; part < (F32 ? 3 : 2); ++part) {
+                            sm::mma_ss(d, up, x[part] + 2 * kk, idesc, !fresh || b > x0 || kk > 0 || part > 0);
+                            if (GATED) sm::mma_ss(d + BN, up + (T::kABytes >> 4), x[part] + 2 * kk, idesc, !fresh || b > x0 || kk > 0 || part > 0);
                         }
                     }
                     sm::mma_commit(empty(s));
+                    sm::mma_commit(empty(s1));
                 }
                 __syncwarp();
-                if (++s == T::kStages) { s = 0; phase ^= 1u; }
+                for (int i = 0; i < 2; ++i)
+                    if (++s == T::kStages) { s = 0; phase ^= 1u; }
             }
         };
         for (int tile = first; tile < tiles && ok; tile += step) {
@@ -417,10 +419,10 @@ linear_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
             if constexpr (ADAPT && F32) {
                 LinearShare sh{};
                 ok = ok && share(tile, sh);
-                for (int x0 = sh.b0; x0 < sh.b1 && ok; x0 += kPromote, ++n) {
+                for (int x0 = sh.b0; x0 < sh.b1 && ok; x0 += kAdaptPromote, ++n) {
                     const int buf = n & 1;
                     if (n >= 2 && !(ok = sm::bar_wait_warp(acc_empty(buf), uint32_t(n / 2 - 1) & 1u, abort_word, p.status))) break;
-                    adapters(tmem + buf * T::kBufCols, sh, x0, min(x0 + kPromote, sh.b1), true);
+                    adapters(tmem + buf * T::kBufCols, sh, x0, min(x0 + kAdaptPromote, sh.b1), true);
                     if (ok && leader) sm::mma_commit(acc_full(buf));
                     __syncwarp();
                 }
@@ -428,20 +430,42 @@ linear_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
         }
         if (*abort_word && leader) { sm::mma_commit(drained); sm::bar_drain(drained, 0); }
         __syncwarp();
+    } else if (ADAPT && warp == 2 + T::kWarps) {
+        if constexpr (ADAPT) {   // the first tile's adapters, then the terms
+            const bool issuer = sm::elect_one();
+            int n0, m0, s = 0;
+            place(first, n0, m0);
+            linear_list(e, m0, min(BN, p.rows - m0), first_tile);
+            __syncwarp();
+            if (issuer) sm::bar_arrive(sm::smem(&first_tile.ready));
+            __syncwarp();
+            sm::pdl_wait();
+            uint32_t phases = 0;   // of the grants of each stage
+            bool ok = true;
+            for (int tile = first; tile < tiles && ok; tile += step) {
+                LinearShare sh{};
+                if (!(ok = share(tile, sh))) break;
+                place(tile, n0, m0);
+                s = (s + kb1 - kb0) % T::kStages;
+                for (int i = 2 * sh.b0; i < 2 * sh.b1; ++i) {
+                    if (!(ok = sm::bar_wait_warp(sm::smem(&first_tile.granted[s]), phases >> s & 1u, abort_word, p.status))) break;
+                    phases ^= 1u << s;
+                    const uint32_t at = stage0 + s * T::kStageBytes;
+                    const int c = i / 2 * kAdaptCols;
+                    if (issuer) {
+                        sm::tma_load_2d(at + T::kAccs * T::kABytes, &e.terms, full(s), c + (i % 2 ? e.part : 0), m0);
+                        if (F32 && i % 2) sm::tma_load_2d(at, &e.terms, full(s), c + 2 * e.part, m0);
+                    }
+                    __syncwarp();
+                    if (++s == T::kStages) s = 0;
+                }
+            }
+        }
+        __syncwarp();
     } else {
         const int quarter = warp & 3, row = quarter * 32 + lane, cols = (warp - 2) / 4 * T::kWidth;
         const uint32_t lanes = uint32_t(quarter * 32) << 16;
         const bool plain = !GATED && p.act == MK_ACT_NONE;
-        if constexpr (ADAPT) {
-            if (warp == 2 && first < tiles) {
-                int n0, m0;
-                place(first, n0, m0);
-                linear_list(e, m0, min(BN, p.rows - m0), first_tile);
-                __syncwarp();
-                if (lane == 0) sm::bar_arrive(sm::smem(&first_tile.ready));
-            }
-            sm::pdl_wait();
-        }
         float v[T::kWidth], u[GATED ? T::kWidth : 1];   // the thread's feature, its columns
         int n = 0;
         bool ok = true;
@@ -460,7 +484,7 @@ linear_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
             if constexpr (ADAPT && F32) {
                 LinearShare sh{};
                 if (!(ok = share(tile, sh))) break;
-                pieces += (sh.b1 - sh.b0 + kPromote - 1) / kPromote;
+                pieces += (sh.b1 - sh.b0 + kAdaptPromote - 1) / kAdaptPromote;
             }
 #pragma unroll 1
             for (int i = 0; i < pieces; ++i, ++n) {
@@ -513,7 +537,7 @@ linear_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
         // the tile's columns are shared out over the cluster; each is summed over the CTAs in rank order
         __syncwarp();
         sm::cluster_sync();
-        if (warp >= 2 && !*abort_word) {
+        if (warp >= 2 && warp < 2 + T::kWarps && !*abort_word) {
             int n0, m0;
             place(first, n0, m0);
             const int t = threadIdx.x - 64, row = t & 127, j = n0 + row;
@@ -616,7 +640,7 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
                 s.list = e.list + int64_t(m0 / 256) * e.slots;
                 s.adapters = *reinterpret_cast<const volatile int32_t*>(e.count + m0 / 256);
             }
-            s.cut(e.width, part, p.split);
+            s.cut(e.width, kPairCols, part, p.split);
         }
         return true;
     };
@@ -649,9 +673,11 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
                 auto terms = [&](int upto) {
                     for (; given < upto; ++given) {
                         const uint32_t at = stage0 + given_s * T::kStageBytes, bar = sm::cluster_addr(full(given_s), leader);
+                        const int c = given * kPairCols;
                         if (issuer) {
-                            sm::tma_load_2d_pair(at + T::kHalfBytes, &e.terms, bar, given * 2 * kAdaptCols, m0 + half * 128);
-                            if (F32) sm::tma_load_2d_pair(at + kAdaptBytes, &e.third, bar, given * kAdaptCols, m0 + half * 128);
+                            sm::tma_load_2d_pair(at + T::kHalfBytes, &e.terms, bar, c, m0 + half * 128);
+                            sm::tma_load_2d_pair(at + T::kHalfBytes + kPairBytes, &e.terms, bar, c + e.part, m0 + half * 128);
+                            if (F32) sm::tma_load_2d_pair(at + kPairBytes, &e.terms, bar, c + 2 * e.part, m0 + half * 128);
                         }
                         if (++given_s == T::kStages) given_s = 0;
                     }
@@ -659,8 +685,8 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
                 const bool two = e.width == 16;
                 const int last = two && sh.adapters % 2 ? sh.adapters / 2 : -1;   // a block of one adapter's 16 columns
                 constexpr uint32_t kTerms = T::kHalfBytes + (F32 ? T::kHalfBytes / 2 : 0);
-                const uint32_t up_rows = GATED ? (two ? kAdaptBytes / 4 : kAdaptBytes / 2) : 0;   // (behind the gate rows)
-                LinearColumns col(sh, e.width, sh.b0 * kAdaptCols);
+                const uint32_t up_rows = GATED ? (two ? kPairBytes / 4 : kPairBytes / 2) : 0;   // (behind the gate rows)
+                LinearColumns col(sh, e.width, sh.b0 * kPairCols);
                 int b = sh.b0;
                 for (; b < sh.b1; ++b, ++it) {
                     if (b - sh.b0 >= T::kStages) {
@@ -670,18 +696,18 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
                     if (!(ok = sm::bar_wait_warp(empty(s), phase, abort_word, p.status))) break;
                     if (issuer) {
                         const uint32_t at = stage0 + s * T::kStageBytes, bar = sm::cluster_addr(full(s), leader);
-                        if (half == 0) sm::bar_expect(full(s), 2 * ((b == last ? kAdaptBytes / 2 : kAdaptBytes) + kTerms));
+                        if (half == 0) sm::bar_expect(full(s), 2 * ((b == last ? kPairBytes / 2 : kPairBytes) + kTerms));
                         sm::tma_load_3d_pair(at, &e.up, bar, col.column, n0, col.name);
                         if (GATED) sm::tma_load_3d_pair(at + up_rows, &e.up, bar, col.column, p.n + n0, col.name);
                         if (two) {
                             col.step(16);
                             if (b != last) {
-                                sm::tma_load_3d_pair(at + kAdaptBytes / 2, &e.up, bar, 0, n0, col.name);
-                                if (GATED) sm::tma_load_3d_pair(at + kAdaptBytes / 2 + up_rows, &e.up, bar, 0, p.n + n0, col.name);
+                                sm::tma_load_3d_pair(at + kPairBytes / 2, &e.up, bar, 0, n0, col.name);
+                                if (GATED) sm::tma_load_3d_pair(at + kPairBytes / 2 + up_rows, &e.up, bar, 0, p.n + n0, col.name);
                                 col.step(16);
                             }
                         } else {
-                            col.step(kAdaptCols);
+                            col.step(kPairCols);
                         }
                     }
                     __syncwarp();
@@ -710,13 +736,14 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
             uint32_t phase = 0;
             bool ok = true;
             const bool two = e.width == 16;
-            const uint64_t up0 = two ? sm::desc_k_sw32(stage0) : sm::desc_k_sw64(stage0), third0 = sm::desc_k_sw64(stage0 + kAdaptBytes);
-            const uint64_t step16 = two ? kAdaptBytes / 2 >> 4 : 2;
+            const uint64_t up0 = two ? sm::desc_k_sw32(stage0) : sm::desc_k_sw64(stage0);
+            const uint64_t part0[3] = {sm::desc_k_sw64(stage0 + T::kHalfBytes), sm::desc_k_sw64(stage0 + T::kHalfBytes + kPairBytes), sm::desc_k_sw64(stage0 + kPairBytes)};
+            const uint64_t step16 = two ? kPairBytes / 2 >> 4 : 2;
             [[maybe_unused]] auto adapters = [&](uint32_t d, const LinearShare& sh, int x0, int x1, bool fresh) {
                 for (int b = x0; b < x1; ++b) {
                     if (!(ok = sm::bar_wait_warp(full(s), phase, abort_word, p.status))) break;
                     sm::tc_fence_after();
-                    const uint64_t at = uint64_t(s * (T::kStageBytes >> 4)), t = b0 + at, t3 = third0 + at, a = up0 + at;
+                    const uint64_t at = uint64_t(s * (T::kStageBytes >> 4)), a = up0 + at;
                     const int steps = two && 2 * b + 1 == sh.adapters ? 1 : 2;   // of 16 columns
                     if (issuer) {
 #pragma unroll
@@ -724,7 +751,7 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
                             if (kk >= steps) break;
 #pragma unroll
                             for (int term = 0; term < (F32 ? 3 : 2); ++term)
-                                sm::mma_ss_pair(d, a + kk * step16, (term == 2 ? t3 : t + 4 * term) + 2 * kk, idesc,
+                                sm::mma_ss_pair(d, a + kk * step16, part0[term] + at + 2 * kk, idesc,
                                                 !fresh || b > x0 || kk > 0 || term > 0);
                         }
                         sm::mma_commit_pair(empty(s), both);
@@ -762,10 +789,10 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
                 if constexpr (ADAPT && F32) {
                     LinearShare sh{};
                     ok = ok && share(tile, sh);
-                    for (int x0 = sh.b0; x0 < sh.b1 && ok; x0 += kPromote, ++n) {
+                    for (int x0 = sh.b0; x0 < sh.b1 && ok; x0 += kAdaptPromote, ++n) {
                         const int buf = n & 1;
                         if (n >= 2 && !(ok = sm::bar_wait_warp(acc_empty(buf), uint32_t(n / 2 - 1) & 1u, abort_word, p.status))) break;
-                        adapters(tmem + buf * 256, sh, x0, min(x0 + kPromote, sh.b1), true);
+                        adapters(tmem + buf * 256, sh, x0, min(x0 + kAdaptPromote, sh.b1), true);
                         if (ok && issuer) sm::mma_commit_pair(acc_full(buf), both);
                         __syncwarp();
                     }
@@ -789,7 +816,6 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
                 __syncwarp();
                 if (lane == 0) sm::bar_arrive(sm::smem(&first_tile.ready));
             }
-            sm::pdl_wait();
         }
         float v[128];   // the thread's row of the tile, its 128 columns
         int n = 0;
@@ -806,7 +832,7 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
             if constexpr (ADAPT && F32) {
                 LinearShare sh{};
                 ok = share(tile, sh);
-                pieces = ok ? pieces + (sh.b1 - sh.b0 + kPromote - 1) / kPromote : 0;
+                pieces = ok ? pieces + (sh.b1 - sh.b0 + kAdaptPromote - 1) / kAdaptPromote : 0;
             }
 #pragma unroll 1
             for (int i = 0; i < pieces; ++i, ++n) {
@@ -969,7 +995,7 @@ struct LinearOne {
         if (st != MK_OK) return st;
         pl.tiles_n = (p.n + 127) / 128;
         pl.tiles_m = (p.rows + BN - 1) / BN;
-        LinearLaunch cfg(64 + 32 * T::kWarps, T::kSmem, nullptr);
+        LinearLaunch cfg(64 + 32 * T::kWarps + (ADAPT ? 32 : 0), T::kSmem, nullptr);
         return linear_split(fn, cfg, resident[device], 1, 8, (p.k + kLinK - 1) / kLinK, extra, kCycles, kFixed, kJoin, pl);
     }
     static mk_status launch(const mk_linear_args* a, LinearParams& p, const LinearExtra<ADAPT>& e, const LinearPlan& pl, cudaStream_t stream) {
@@ -977,7 +1003,7 @@ struct LinearOne {
         const mk_status st = linear_maps(a, p, int64_t(p.n) * T::kAccs, 128, BN, &map_w, &map_x);
         if (st != MK_OK) return st;
         p.tiles_n = pl.tiles_n; p.tiles_m = pl.tiles_m; p.split = pl.split;
-        LinearLaunch cfg(64 + 32 * T::kWarps, T::kSmem, stream);
+        LinearLaunch cfg(64 + 32 * T::kWarps + (ADAPT ? 32 : 0), T::kSmem, stream);
         cfg.shape(pl.split, pl.clusters);
         MK_CK(cudaLaunchKernelEx(&cfg.c, &linear_kernel<BN, GATED, F32, ADAPT>, map_w, map_x, p, e));
         return MK_OK;
