@@ -480,14 +480,14 @@ linear_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
 #pragma unroll
                 for (int i = 0; i < T::kWidth; ++i) u[GATED ? i : 0] = b;
             }
-            int pieces = (kb1 - kb0 + piece - 1) / piece;
+            int end = kb1;   // (of the loop over pieces: further by those of the adapters)
             if constexpr (ADAPT && F32) {
                 LinearShare sh{};
                 if (!(ok = share(tile, sh))) break;
-                pieces += (sh.b1 - sh.b0 + kAdaptPromote - 1) / kAdaptPromote;
+                end = kb0 + ((kb1 - kb0 + piece - 1) / piece + (sh.b1 - sh.b0 + kAdaptPromote - 1) / kAdaptPromote) * piece;
             }
 #pragma unroll 1
-            for (int i = 0; i < pieces; ++i, ++n) {
+            for (int k0 = kb0; k0 < end; k0 += piece, ++n) {
                 const int buf = n & 1;
                 if (!(ok = sm::bar_wait_warp(acc_full(buf), uint32_t(n / 2) & 1u, abort_word, p.status))) break;
                 sm::tc_fence_after();
@@ -828,14 +828,14 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
             const int jb = up_row ? p.n + j : j;   // (bias rows: gate rows, then up rows)
             linear_begin<128>(p, m0 + cols, j, live ? p.rows - m0 - cols : 0, part == 0, plain,
                               p.bias && live ? __bfloat162float(p.bias[jb]) : 0.f, v);
-            int pieces = (kb1 - kb0 + piece - 1) / piece;
+            int end = kb1;   // (of the loop over pieces: further by those of the adapters)
             if constexpr (ADAPT && F32) {
                 LinearShare sh{};
                 ok = share(tile, sh);
-                pieces = ok ? pieces + (sh.b1 - sh.b0 + kAdaptPromote - 1) / kAdaptPromote : 0;
+                end = ok ? kb0 + ((kb1 - kb0 + piece - 1) / piece + (sh.b1 - sh.b0 + kAdaptPromote - 1) / kAdaptPromote) * piece : kb0;
             }
 #pragma unroll 1
-            for (int i = 0; i < pieces; ++i, ++n) {
+            for (int k0 = kb0; k0 < end; k0 += piece, ++n) {
                 const int buf = n & 1;
                 if (!(ok = sm::bar_wait_warp(acc_full(buf), uint32_t(n / 2) & 1u, abort_word, p.status))) break;
                 sm::tc_fence_after();
