@@ -106,6 +106,10 @@ __global__ void __launch_bounds__(kLowThreads, 2) low_rank_kernel(const __grid_c
     const int blocks = (p.k + 31) / 32, width = p.width;
     const __nv_bfloat16* x0 = p.x + int64_t(m0 + row0 + g) * p.x_stride + q * 8;
     float* sums = all_sums;
+    // A warp's blocks in turn, from another one on in every cluster: neighbours mostly share an adapter, and with all of them at the same
+    // rows of down at the same time these come from few places of the L2
+    const int mine = max(0, (blocks - rank_z * kLowWarps - warp + split * kLowWarps - 1) / (split * kLowWarps));
+    const int first = mine > 0 ? int(blockIdx.x + blockIdx.y) % mine : 0;
     bool reached = false;                               // whether a peer may still read this CTA's sums
     for (int slot = int(blockIdx.y); slot < count; slot += int(gridDim.y)) {
         const int adapter = list[slot];
@@ -121,7 +125,8 @@ __global__ void __launch_bounds__(kLowThreads, 2) low_rank_kernel(const __grid_c
 #pragma unroll
                     for (int v = 0; v < 4; ++v) acc[j][v] = 0.f;
 #pragma unroll NT == 8 ? 2 : 4
-                for (int b = rank_z * kLowWarps + warp; b < blocks; b += split * kLowWarps) {
+                for (int i = 0; i < mine; ++i) {
+                    const int turn = i + first < mine ? i + first : i + first - mine, b = rank_z * kLowWarps + warp + turn * split * kLowWarps;
                     const bool in = b * 32 + q * 8 < p.k;
                     uint4 xs[2], ds[NT];
 #pragma unroll
