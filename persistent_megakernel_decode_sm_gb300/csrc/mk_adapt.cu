@@ -26,15 +26,6 @@ struct LowParams {
     int32_t* status;
 };
 
-__device__ __forceinline__ void low_mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-__device__ __forceinline__ uint4 low_load(const __nv_bfloat16* p, bool wanted) {
-    return wanted ? __ldg(reinterpret_cast<const uint4*>(p)) : make_uint4(0, 0, 0, 0);
-}
-
 // A cluster works on 16 neighbouring tokens of one tile of the linear map, for the tile's adapters y, y + gridDim.y, ..: those of
 // its tokens that name the adapter get their low-rank row, the others zeros.  8 NT columns of the rank at a time; x and down are
 // read from global memory straight into the operands of m16n8k16 products (a thread's 16 bytes of a row are the elements 2 i, 2 i + 1
@@ -130,13 +121,13 @@ __global__ void __launch_bounds__(kLowThreads, 2) low_rank_kernel(const __grid_c
                     const bool in = b * 32 + q * 8 < p.k;
                     uint4 xs[2], ds[NT];
 #pragma unroll
-                    for (int j = 0; j < NT; ++j) ds[j] = low_load(down + int64_t(8 * j) * p.k + b * 32, in && c0 + 8 * j + g < p.rank);
+                    for (int j = 0; j < NT; ++j) ds[j] = linear_load(down + int64_t(8 * j) * p.k + b * 32, in && c0 + 8 * j + g < p.rank);
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) xs[h] = low_load(x0 + 8 * h * p.x_stride + b * 32, in && use[h]);
+                    for (int h = 0; h < 2; ++h) xs[h] = linear_load(x0 + 8 * h * p.x_stride + b * 32, in && use[h]);
 #pragma unroll
                     for (int j = 0; j < NT; ++j) {
-                        low_mma(acc[j], xs[0].x, xs[1].x, xs[0].y, xs[1].y, ds[j].x, ds[j].y);
-                        low_mma(acc[j], xs[0].z, xs[1].z, xs[0].w, xs[1].w, ds[j].z, ds[j].w);
+                        linear_mma(acc[j], xs[0].x, xs[1].x, xs[0].y, xs[1].y, ds[j].x, ds[j].y);
+                        linear_mma(acc[j], xs[0].z, xs[1].z, xs[0].w, xs[1].w, ds[j].z, ds[j].w);
                     }
                 }
                 __syncthreads();                        // (the warps' sums of the columns before are read)
@@ -322,6 +313,12 @@ extern "C" mk_status mk_linear_adapted(const mk_linear_args* a, const mk_adapter
         LinearExtra<true> e{};
         e.index = low.index;
         e.n_adapters = ad->n_adapters;
+        e.rank = ad->rank;
+        e.x = low.x;
+        e.x_stride = low.x_stride;
+        e.w = static_cast<const __nv_bfloat16*>(c.w);
+        e.up_rows = static_cast<const __nv_bfloat16*>(ad->up);
+        e.term_rows = low.terms;
         e.count = low.count;
         e.list = low.list;
         e.slots = pl.slots;

@@ -43,7 +43,9 @@ struct LinearExtra<true> {
     const int32_t* list;       // [tiles of tokens][slots]: which, in the order in which its tokens name them
     int32_t slots, width;      // columns of an adapter
     int32_t part;              // columns of a part
-    int32_t n_adapters;
+    int32_t n_adapters, rank;
+    const __nv_bfloat16 *x, *w, *up_rows, *term_rows;   // what linear_alone reads
+    int64_t x_stride;
 };
 constexpr int kAdaptCols = 64;   // of a block
 constexpr int kPairCols = 32, kPairBytes = 128 * kPairCols * 2;   // of a CTA pair's, all in one stage: columns, bytes of 128 rows
@@ -163,13 +165,123 @@ __device__ __forceinline__ void linear_stores(const LinearParams& p, int r, int 
             else *dst = __float2bfloat16_rn(y[i]);
         }
 }
+__device__ __forceinline__ void linear_mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint4 linear_load(const __nv_bfloat16* p, bool wanted) {
+    return wanted ? __ldg(reinterpret_cast<const uint4*>(p)) : make_uint4(0, 0, 0, 0);
+}
+__device__ __forceinline__ void linear_widen(const uint4& u, float (&x)[8], bool add = false) {   // 8 bf16
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        x[2 * i] = (add ? x[2 * i] : 0.f) + __uint_as_float(w[i] << 16);
+        x[2 * i + 1] = (add ? x[2 * i + 1] : 0.f) + __uint_as_float(w[i] & 0xFFFF0000u);
+    }
+}
+// An adapter's infinity or NaN times a zero of another token's low-rank row is NaN: a tensor core cannot leave the product out.
+// Sums that came to NaN are therefore taken again here, with no adapter but the token's own (and as that one's parts may
+// be infinities of both signs, its value in one piece); what is NaN by itself stays so.  By a whole warp: 8 tokens m, m + step, ..
+// (the same of every lane, `left` from m on) of the lanes' features j, j + 1, .., stored where the lane wants its own.
+// x and w are read straight into m16n8k16 products (a thread's 16 bytes of a row are the elements 2 i, 2 i + 1 of two products),
+// summed 512 elements at a time; 16 features of 8 tokens take 3 loads a lane per 32 of the contraction.
+// Where no sum is NaN this is one comparison an output (0.1 to 0.3 us a call, 1.3 of 4096 tokens through 2 x 8192 x 2048).  Taking a
+// tile again is bound by the latencies of those loads: one adapter of NaN among 64 of 64 tokens (4096 x 6144) 330 us for 46, among
+// those of 4096 tokens (500 of whose share its tiles) 4.8 ms for 0.165; with the warp's lanes along the contraction 1850 and 33 ms.
+template <bool GATED, bool F32>
+__device__ __noinline__ void linear_alone(const LinearParams& p, const LinearExtra<true>& e, const volatile int32_t* list, int adapters,
+                                          int m, int step, int j, int left, bool wanted) {
+    constexpr unsigned kAll = 0xFFFFFFFFu;
+    const int lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
+    const unsigned all = __ballot_sync(kAll, wanted && left > 0);   // (a lane without a feature has nothing left)
+    if (!all) return;
+    const int most = __shfl_sync(kAll, left, __ffs(all) - 1), j0 = __shfl_sync(kAll, j, 0);
+    sm::pdl_wait();   // (the terms)
+    // a product's column is token g (behind the last: the last one's again), its sums are of tokens 2 q and 2 q + 1
+    const __nv_bfloat16* x = e.x + int64_t(m + min(g, (most - 1) / step) * step) * e.x_stride + q * 8;
+    int own[2], slot[2];   // their adapters, and where these are among the tile's
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        own[h] = (2 * q + h) * step < most ? e.index[m + (2 * q + h) * step] : -1;
+        slot[h] = -1;
+        if (own[h] >= 0)
+            for (int i = 0; i < adapters; ++i)
+                if (list[i] == own[h]) slot[h] = i;
+    }
+#pragma unroll 1
+    for (int half = 0; half < 32; half += 16) {
+        if (!(all >> half & 0xFFFFu)) continue;
+        int row[2];   // of w, less the gate rows
+#pragma unroll
+        for (int r = 0; r < 2; ++r) row[r] = min(j0 + half + g + 8 * r, p.n - 1);
+        float y[GATED ? 2 : 1][4];
+#pragma unroll
+        for (int part = 0; part < (GATED ? 2 : 1); ++part) {
+            const __nv_bfloat16 *w0 = e.w + (int64_t(part) * p.n + row[0]) * p.k + q * 8, *w1 = e.w + (int64_t(part) * p.n + row[1]) * p.k + q * 8;
+#pragma unroll
+            for (int v = 0; v < 4; ++v) y[part][v] = 0.f;
+#pragma unroll 1
+            for (int k0 = 0; k0 < p.k; k0 += 512) {
+                float acc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+                for (int c = k0; c < min(k0 + 512, p.k); c += 32) {
+                    const bool in = c + q * 8 < p.k;
+                    const uint4 a = linear_load(w0 + c, in), b = linear_load(w1 + c, in), t = linear_load(x + c, in);
+                    linear_mma(acc, a.x, b.x, a.y, b.y, t.x, t.y);
+                    linear_mma(acc, a.z, b.z, a.w, b.w, t.z, t.w);
+                }
+#pragma unroll
+                for (int v = 0; v < 4; ++v) y[part][v] += acc[v];
+            }
+#pragma unroll
+            for (int v = 0; v < 4; ++v) {   // (feature g + 8 (v / 2), token 2 q + v % 2)
+                if (slot[v & 1] >= 0) {
+                    const __nv_bfloat16* t = e.term_rows + int64_t(m + (2 * q + (v & 1)) * step) * (F32 ? 3 : 2) * e.part + slot[v & 1] * e.width;
+                    const __nv_bfloat16* u = e.up_rows + ((int64_t(own[v & 1]) * (GATED ? 2 : 1) + part) * p.n + row[v / 2]) * e.rank;
+#pragma unroll 1
+                    for (int c = 0; c < e.rank; c += 8) {
+                        float a[8], b[8];
+                        linear_widen(*reinterpret_cast<const uint4*>(t + c), a);
+                        linear_widen(*reinterpret_cast<const uint4*>(t + e.part + c), a, true);
+                        if (F32) linear_widen(*reinterpret_cast<const uint4*>(t + 2 * e.part + c), a, true);
+                        linear_widen(*reinterpret_cast<const uint4*>(u + c), b);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) y[part][v] = fmaf(a[i], b[i], y[part][v]);
+                    }
+                }
+                if (p.bias) y[part][v] += __bfloat162float(p.bias[part * p.n + row[v / 2]]);
+            }
+        }
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+            const int i = (2 * q + (v & 1)) * step, of = half + g + 8 * (v / 2);   // token, the lane whose feature it is
+            if (i >= most || !(all >> of & 1u)) continue;
+            float res[1];
+            linear_residuals<1>(p, true, m + i, j0 + of, 1, res);
+            const float out = linear_act(GATED ? MK_ACT_SWIGLU : p.act, y[0][v], GATED ? y[GATED ? 1 : 0][v] : 0.f) + res[0];
+            const int64_t at = (m + i) * p.out_stride + j0 + of;
+            if constexpr (F32) static_cast<float*>(p.out)[at] = out;
+            else static_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16_rn(out);
+        }
+    }
+}
+__device__ __forceinline__ bool linear_nan(const float (&y)[8]) {
+    bool nan = false;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) nan = nan || y[i] != y[i];
+    return nan;
+}
+
 // 8 columns c, c + STEP, .. (below c1) of a split tile: the partial sums of `split` CTAs (ranks
 // by * s + at), staged as [column][128 rows], added in order; the up sums lie `up_bytes` further
-template <int STEP, bool GATED, bool F32>
-__device__ __forceinline__ void linear_join(const LinearParams& p, uint32_t stage0, uint32_t up_bytes, int split, int by, int at,
-                                            int m0, int c, int c1, int row, int j) {
+template <int STEP, bool GATED, bool F32, bool ADAPT>
+__device__ __forceinline__ void linear_join(const LinearParams& p, const LinearExtra<ADAPT>& e, const std::conditional_t<ADAPT, LinearFirst, char>& tile, uint32_t stage0,
+                                            uint32_t up_bytes, int split, int by, int at, int m0, int c, int c1, int row, int j) {
     float y[8], u[8], res[8];
-    linear_residuals<8>(p, GATED || p.act != MK_ACT_NONE, m0 + c, j, c1 - c, res, STEP);
+    const int left = !ADAPT || j < p.n ? c1 - c : 0;   // (with adapters lanes without a feature come here too)
+    linear_residuals<8>(p, GATED || p.act != MK_ACT_NONE, m0 + c, j, left, res, STEP);
 #pragma unroll
     for (int i = 0; i < 8; ++i) y[i] = u[i] = 0.f;
     for (int s = 0; s < split; ++s) {
@@ -183,7 +295,12 @@ __device__ __forceinline__ void linear_join(const LinearParams& p, uint32_t stag
     }
 #pragma unroll
     for (int i = 0; i < 8; ++i) y[i] = linear_act(GATED ? MK_ACT_SWIGLU : p.act, y[i], u[i]) + res[i];
-    linear_stores<F32>(p, m0 + c, j, c1 - c, y, STEP);
+    if constexpr (ADAPT) {
+        const bool again = linear_nan(y);
+        if (__any_sync(0xFFFFFFFFu, again)) linear_alone<GATED, F32>(p, e, tile.list, tile.count, m0 + c, STEP, j, left, again);
+        if (again) return;
+    }
+    linear_stores<F32>(p, m0 + c, j, left, y, STEP);
 }
 
 // A tile is 128 output features (the MMA's M: rows of w, one per tensor-memory lane) by BN tokens
@@ -284,7 +401,7 @@ linear_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
                 s.list = e.list + int64_t(m) * e.slots;
                 s.adapters = *reinterpret_cast<const volatile int32_t*>(e.count + m);
             }
-                s.cut(e.width, kAdaptCols, rank, p.split);
+            s.cut(e.width, kAdaptCols, rank, p.split);
         }
         return true;
     };
@@ -522,6 +639,7 @@ linear_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
                 }
                 break;
             }
+            [[maybe_unused]] uint32_t again = 0;   // (a bit for each 8 tokens)
 #pragma unroll
             for (int c = 0; c < T::kWidth; c += 8) {
                 if (c >= p.rows - m0 - cols) break;
@@ -529,7 +647,17 @@ linear_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
                 linear_residuals(p, !plain, m0 + cols + c, j, left - c, res);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) y[i] = linear_act(GATED ? MK_ACT_SWIGLU : p.act, v[c + i], GATED ? u[GATED ? c + i : 0] : 0.f) + res[i];
-                linear_stores<F32>(p, m0 + cols + c, j, left - c, y);
+                if (ADAPT && linear_nan(y)) again |= 1u << (c / 8);
+                else linear_stores<F32>(p, m0 + cols + c, j, left - c, y);
+            }
+            if constexpr (ADAPT) {
+                if (__any_sync(0xFFFFFFFFu, again != 0)) {
+                    LinearShare sh{};
+                    const int end_c = share(tile, sh) ? T::kWidth : 0;
+#pragma unroll 1
+                    for (int c = 0; c < end_c; c += 8)
+                        linear_alone<GATED, F32>(p, e, sh.list, sh.adapters, m0 + cols + c, 1, j, left - c, again >> (c / 8) & 1);
+                }
             }
         }
     }
@@ -537,15 +665,15 @@ linear_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
         // the tile's columns are shared out over the cluster; each is summed over the CTAs in rank order
         __syncwarp();
         sm::cluster_sync();
-        if (warp >= 2 && warp < 2 + T::kWarps && !*abort_word) {
+        if (warp >= 2 && warp < 2 + T::kWarps && !(ADAPT ? __any_sync(0xFFFFFFFFu, *abort_word) : *abort_word)) {
             int n0, m0;
             place(first, n0, m0);
             const int t = threadIdx.x - 64, row = t & 127, j = n0 + row;
             constexpr int kGroups = T::kWarps / 4;
             const int c1 = min(BN * (rank + 1) / p.split, p.rows - m0);
-            if (j < p.n)
+            if (ADAPT ? n0 + (row & ~31) < p.n : j < p.n)
                 for (int c = BN * rank / p.split + t / 128; c < c1; c += 8 * kGroups)
-                    linear_join<kGroups, GATED, F32>(p, stage0, BN * 128 * 4, p.split, 1, 0, m0, c, c1, row, j);
+                    linear_join<kGroups, GATED, F32, ADAPT>(p, e, first_tile, stage0, BN * 128 * 4, p.split, 1, 0, m0, c, c1, row, j);
         }
         __syncwarp();
         sm::cluster_sync();   // no CTA leaves while a peer reads its partial sums
@@ -863,6 +991,7 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
             // 8 columns a step.  SwiGLU: 16 columns, of which the gate row keeps 0-7 and receives their up
             // values from its up row, which keeps 8-15 and receives their gate values; two buffers take turns
             constexpr int kStep = GATED ? 16 : 8;
+            [[maybe_unused]] uint32_t again = 0;   // (a bit for each step)
 #pragma unroll
             for (int c = 0; c < 128; c += kStep) {
                 const int m = m0 + cols + c + (up_row ? 8 : 0), left = live ? p.rows - m : 0;
@@ -887,7 +1016,19 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
 #pragma unroll
                     for (int i = 0; i < 8; ++i) y[i] = linear_act(p.act, v[c + i], 0.f) + res[i];
                 }
-                linear_stores<F32>(p, m, j, left, y);
+                if (ADAPT && linear_nan(y)) again |= 1u << (c / kStep);
+                else linear_stores<F32>(p, m, j, left, y);
+            }
+            if constexpr (ADAPT) {
+                if (__any_sync(0xFFFFFFFFu, again != 0)) {
+                    LinearShare sh{};
+                    const int end_c = share(tile, sh) ? 128 : 0;
+#pragma unroll 1
+                    for (int c = 0; c < end_c; c += kStep) {
+                        const int m = m0 + cols + c + (up_row ? 8 : 0);
+                        linear_alone<GATED, F32>(p, e, sh.list, sh.adapters, m, 1, j, live ? p.rows - m : 0, again >> (c / kStep) & 1);
+                    }
+                }
             }
         }
     }
@@ -895,15 +1036,15 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
         // the tile's columns are shared out over the pairs; each is summed in order of the contraction
         __syncwarp();
         sm::cluster_sync();
-        if (warp >= 2 && !*abort_word) {
+        if (warp >= 2 && !(ADAPT ? __any_sync(0xFFFFFFFFu, *abort_word) : *abort_word)) {
             int n0, m0;
             place(first, n0, m0);
             const int t = threadIdx.x - 64, row = t % T::kRows, j = n0 + row;
             constexpr int kGroups = 256 / T::kRows;
             const int width0 = 256 * part / p.split, c1 = min(256 * (part + 1) / p.split, p.rows - m0);
-            if (j < p.n)
+            if (ADAPT ? n0 + (row & ~31) < p.n : j < p.n)
                 for (int c = width0 + t / T::kRows; c < c1; c += 8 * kGroups)
-                    linear_join<kGroups, GATED, F32>(p, stage0, 64 * 4, p.split, 2, half, m0, c, c1, row, j);
+                    linear_join<kGroups, GATED, F32, ADAPT>(p, e, first_tile, stage0, 64 * 4, p.split, 2, half, m0, c, c1, row, j);
         }
         __syncwarp();
     }

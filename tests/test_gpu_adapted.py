@@ -169,6 +169,47 @@ def test_adapters_that_no_token_names_are_not_read_and_bad_entries_count_as_none
     mk.adapted_linear(x, w, ad, index)
 
 
+@pytest.mark.parametrize("rows,n,k,rank", [(5, 257, 136, 16), (12, 300, 2048, 8), (40, 130, 1032, 24), (70, 257, 136, 64), (130, 600, 2048, 16),
+                                           (300, 257, 264, 32), (700, 1000, 520, 16), (2100, 2048, 264, 40), (9000, 4096, 72, 8)])
+@pytest.mark.parametrize("act", [None, "silu", "swiglu"])
+@pytest.mark.parametrize("out_dtype", [BF, F32])
+def test_infinities_and_nan_of_an_adapter_stay_with_its_tokens(rows, n, k, rank, act, out_dtype):
+    f, count = 2 if act == "swiglu" else 1, 4
+    x, w, ad, index = randn((rows, k), 1), randn((f * n, k), 2, k ** -0.5), adapters(count, rank, k, f * n), index_of(rows, count, "any")
+    index[:5] = torch.tensor([1, 0, 2, -1, 3], dtype=torch.int32)
+    bias, residual = randn((f * n,), 3), randn((rows, n), 4, dtype=out_dtype)
+    want, bound = reference(x, w, ad, index, bias, act, residual, out_dtype)
+    down, up, scale = (t.clone() for t in ad)
+    up[1, ::3, rank - 1] = float("nan")
+    up[2, 1::4, 0] = float("inf")
+    up[2, 5, 1] = -float("inf")
+    down[3, 2, 5] = float("nan")
+    for out in (None, residual.clone()):   # (the second time in place)
+        got = mk.adapted_linear(x, w, (down, up, scale), index, bias, act, residual if out is None else out, out, out_dtype)
+        sound = (index <= 0).nonzero().reshape(-1)
+        off = (got[sound].double() - want[sound]).abs() / bound[sound]
+        assert torch.isfinite(got[sound]).all() and off.max().item() <= 1, off.max().item()
+        if act is None:   # theirs are what the formula gives, and finite elsewhere
+            x64 = x.double()
+            for a in (1, 2, 3):
+                mine = (index == a).nonzero().reshape(-1)
+                t = x64[mine] @ down[a].double().T
+                e = (t[:, None, :] * up[a].double()[None]).sum(2) if a < 3 else torch.full((len(mine), n), float("nan"), device="cuda").double()
+                assert torch.equal(got[mine].isnan(), e.isnan()) and torch.equal(got[mine].isposinf(), e.isposinf())
+                assert torch.equal(got[mine].isneginf(), e.isneginf())
+
+
+def test_tokens_that_are_not_finite_leave_the_others_alone():
+    rows, n, k = 60, 200, 264
+    x, w, ad, index = randn((rows, k), 1), randn((n, k), 2, k ** -0.5), adapters(3, 16, k, n), index_of(rows, 3, "any")
+    want = check(x, w, ad, index)
+    bad = x.clone()
+    bad[7, 3], bad[20], bad[21, 0] = float("nan"), float("inf"), -float("inf")
+    got = mk.adapted_linear(bad, w, ad, index)
+    rest = [i for i in range(rows) if i not in (7, 20, 21)]
+    assert torch.equal(got[rest], want[rest]) and not torch.isfinite(got[[7, 20]]).any()
+
+
 def test_large_and_tiny_low_rank_values():
     # a low-rank value near fp32's largest leaves no rest that is not finite; a tiny one keeps its parts
     x, w, index = randn((20, 64), 1), randn((40, 64), 2, 0.1), index_of(20, 2, "own")
@@ -255,6 +296,37 @@ def test_a_call_behind_kernels_that_make_its_inputs():
         for i in range(4):
             x = mk.adapted_linear(x, w, ad, index, out=(a, b)[i % 2])
         assert torch.equal(x, want[4])
+
+
+def test_adapters_past_2_to_the_32_elements():
+    # 65536 adapters of 16 x 4160: 4.4e9 elements of up; those that no token names hold whatever was there
+    count, rank, n, k, rows = 65536, 16, 4160, 24, 40
+    down, up = (torch.empty(shape, dtype=BF, device="cuda") for shape in ((count, rank, k), (count, n, rank)))
+    names = [0, 65535, 64600, 32768]
+    few = adapters(4, rank, k, n, scaled=False)
+    down[names], up[names] = few[0], few[1]
+    x, w, index = randn((rows, k), 1), randn((n, k), 2, k ** -0.5), index_of(rows, 4, "any")
+    far = torch.tensor(names + [-1], dtype=torch.int32, device="cuda")[index.long()]
+    assert torch.equal(mk.adapted_linear(x, w, (down, up), far), check(x, w, few, index))
+    one = torch.full((rows,), 65535, dtype=torch.int32, device="cuda")
+    assert torch.equal(mk.adapted_linear(x, w, (down, up), one, out_dtype=F32), check(x, w, few, torch.ones_like(one), out_dtype=F32))
+
+
+def test_two_captured_graphs_of_one_workspace():
+    rows, n, k = 30, 264, 512
+    x, w, index = randn((rows, k), 1), randn((n, k), 2, 0.05), index_of(rows, 9, "any")
+    sets = [adapters(9, 16, k, n, seed=s) for s in (50, 70)]
+    ws = torch.empty(1 << 22, dtype=torch.uint8, device="cuda")
+    want = [check(x, w, ad, index) for ad in sets]
+    graphs, outs = [torch.cuda.CUDAGraph() for _ in sets], []
+    torch.cuda.synchronize()
+    for g, ad in zip(graphs, sets):
+        with torch.cuda.graph(g):
+            outs.append(mk.adapted_linear(x, w, ad, index, workspace=ws))
+    for i in (0, 1, 1, 0, 1):
+        outs[i].zero_()
+        graphs[i].replay()
+        assert torch.equal(outs[i], want[i])
 
 
 def test_refusals():

@@ -219,6 +219,67 @@ def test_captured_and_replayed_in_place():
         same(ends, [pool.front, len(pool.free), 0])
 
 
+def test_slots_and_lengths_up_to_2_to_the_31():
+    block, columns, n_blocks = 1 << 20, 2047, 2047
+    ring = torch.full((n_blocks,), -7, dtype=torch.int32, device="cuda")
+    ring[2046], ring[0] = 2046, 5
+    table = torch.full((2, columns), -7, dtype=torch.int32, device="cuda")
+    table[0, 2045], table[1, 0] = 2045, 3
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    most = columns * block
+    lens, new = (torch.tensor(x, dtype=torch.int32, device="cuda") for x in ([most - block - 3, 7], [most - block + 2, block + 1]))
+    ends = torch.tensor([2046, 2, 0], dtype=torch.int32, device="cuda")
+    total = 5 + block + 1 - 7
+    slots, pos, seq, first = mk.assign_pages(ring, ends, table, lens, new, block, total + 1, status=status)
+    assert status.item() == 0 and ends.tolist() == [1, 0, 0] and table[0, 2046].item() == 2046 and table[1, 1].item() == 5
+    a = torch.arange(most - block - 3, most - block + 2, device="cuda")
+    b = torch.arange(7, block + 1, device="cuda")
+    assert torch.equal(slots[:5].long(), a.where(a < most - block, 2046 * block + (a - (most - block)))) and torch.equal(pos[:5].long(), a)
+    assert torch.equal(slots[5:-1].long(), torch.where(b < block, 3 * block + b, 5 * block + (b - block))) and torch.equal(pos[5:-1].long(), b)
+    assert slots[-1] == -1 and first.tolist() == [0, 5, total] and seq[:5].sum() == 0 and (seq[5:-1] == 1).all()
+
+
+def test_the_c_call_without_what_may_be_null():
+    import ctypes
+    pool = Pool(4, 8, 9, 40, front=35)
+    ring, ends, table, lens = pool.device()
+    new = [20, 0, 61, 8]
+    target, slots = torch.tensor(new, dtype=torch.int32, device="cuda"), torch.full((100,), 9, dtype=torch.int32, device="cuda")
+    args = mk.mk_pages_args(4, 8, 9, 40, 0, 100, ring.data_ptr(), ends.data_ptr(), ends.data_ptr(), table.data_ptr(), lens.data_ptr(),
+                            target.data_ptr(), slots.data_ptr(), None, None, None, None)
+    assert mk.lib.mk_assign_pages(ctypes.addressof(args), torch.cuda.current_stream().cuda_stream) == 0
+    same(slots, pool.step(new, 100)[0])
+    lens.copy_(target)
+    target.zero_()
+    args.max_tokens, args.slots = 0, None            # only takes blocks and gives them back
+    assert mk.lib.mk_assign_pages(ctypes.addressof(args), torch.cuda.current_stream().cuda_stream) == 0
+    pool.step([0] * 4, 0)
+    same(ends, [pool.front, len(pool.free), 0])
+    same(ring.roll(-pool.front)[:len(pool.free)], pool.free)
+
+
+def test_two_pools_on_two_streams_at_once():
+    pools = [Pool(64, 16, 400, 24000, front=i, seed=i) for i in range(2)]
+    states = [p.device() for p in pools]
+    streams = [torch.cuda.Stream() for _ in pools]
+    r = random.Random(2)
+    torch.cuda.synchronize()
+    got, want = [], []
+    for _ in range(12):
+        new = [[min(n + r.choice([1, 40, 700]), 6400) if r.random() < 0.8 else 0 for n in p.lens] for p in pools]
+        targets = [torch.tensor(n, dtype=torch.int32, device="cuda") for n in new]
+        torch.cuda.synchronize()
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got.append(mk.assign_pages(*states[i], targets[i], 16, 50000))
+                states[i][3] = targets[i]
+        want += [p.step(n, 50000) for p, n in zip(pools, new)]
+    torch.cuda.synchronize()
+    for g, w in zip(got, want):
+        for a, b in zip(g, w):
+            same(a, b)
+
+
 def test_refusals():
     pool = Pool(3, 8, 4, 20)
     ring, ends, table, lens = pool.device()

@@ -226,6 +226,44 @@ def test_streams_and_graphs():
         assert torch.equal(q, want) and torch.equal(kv.k[:, :, slots.long()], other.k[:, :, slots.long()])
 
 
+@pytest.mark.parametrize("nq,nkv,d", [(4094, 1, 16), (4094, 1, 256), (2, 2047, 32)])
+def test_the_most_heads(nq, nkv, d):
+    check(3, nq, nkv, d, d)
+    check(3, nq, nkv, d, 16, dtype=F32, paged=4)
+
+
+def test_two_tokens_of_one_slot_leave_either_ones_values():
+    t, nq, nkv, d = 200, 4, 2, 64
+    qkv, at = randn((t, 8 * d), 1), torch.arange(t, dtype=torch.int32, device="cuda")
+    kv, each = (KVCache(*(torch.zeros(1, nkv, t, d, dtype=BF, device="cuda") for _ in range(2))) for _ in range(2))
+    want = mk.rope_append(qkv, each, at, at, freqs_of(d))
+    got = mk.rope_append(qkv, kv, at, torch.full_like(at, 7), freqs_of(d))
+    assert torch.equal(got, want)
+    for c, e in ((kv.k, each.k), (kv.v, each.v)):
+        assert (c[:, :, 7:8] == e).any(2).all()          # (of every element some token's)
+        c[:, :, 7] = 0
+        assert not c.any()
+
+
+def test_calls_on_two_streams_at_once():
+    t, nq, nkv, d = 3000, 8, 2, 128
+    qkv, at = randn((t, 12 * d), 1), torch.arange(t, dtype=torch.int32, device="cuda")
+    gain = randn((d,), 2)
+    caches = [KVCache(*(torch.zeros(1, nkv, t, d, dtype=BF, device="cuda") for _ in range(2))) for _ in range(3)]
+    want = mk.rope_append(qkv, caches[2], at, at, freqs_of(d), q_gain=gain, k_gain=gain)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    outs = []
+    for _ in range(8):
+        for s, c in zip(streams, caches):
+            with torch.cuda.stream(s):
+                outs.append(mk.rope_append(qkv, c, at, at, freqs_of(d), q_gain=gain, k_gain=gain))
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, want) for o in outs)
+    for c in caches[:2]:
+        assert torch.equal(c.k, caches[2].k) and torch.equal(c.v, caches[2].v)
+
+
 def test_refusals():
     nkv, d, t = 2, 32, 4
     kv = KVCache(*(torch.zeros(1, 1, nkv, 8, d, dtype=BF, device="cuda") for _ in range(2)))
