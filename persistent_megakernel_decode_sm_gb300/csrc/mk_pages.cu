@@ -151,6 +151,7 @@ __global__ void __launch_bounds__(kPagesThreads) pages_kernel(const __grid_const
     };
     auto new_block = [&](int k) -> const int* { return k < free ? a.ring + wrap((long long)(front) + k) : given_back(k - free); };
     const int self = int(blockIdx.x) * kPagesThreads + t, threads = int(gridDim.x) * kPagesThreads;
+    // (there may be 2^31 - 1 tokens and as many moved blocks: bounds are taken as differences, steps in 64 bits)
     // a warp takes 128 neighbouring tokens, a lane four of them: mostly of one request and one block, else one after the other
     auto block_of = [&](int b, int j) -> const int* {
         return j < s.held[b] ? a.table + int64_t(b) * a.max_blocks + j : new_block(s.taken[b] + (j - s.held[b]));
@@ -159,12 +160,12 @@ __global__ void __launch_bounds__(kPagesThreads) pages_kernel(const __grid_const
         const long long at = run + 4 * lane;
         int slot[4] = {-1, -1, -1, -1}, pos[4] = {0, 0, 0, 0}, seq[4] = {-1, -1, -1, -1};
         if (run < tokens) {
-            const int b0 = pages_warp_owner(s.tokens, a.batch, int(run)), b1 = pages_warp_owner(s.tokens, a.batch, min(int(run) + kRun, tokens) - 1);
+            const int b0 = pages_warp_owner(s.tokens, a.batch, int(run)), b1 = pages_warp_owner(s.tokens, a.batch, int(run) + min(kRun, tokens - int(run)) - 1);
             if (at < tokens) {
                 const int token = int(at);
                 int b = pages_owner(s.tokens, b0, b1 + 1, token), x = s.len[b] + (token - s.tokens[b]);
                 int j = pages_divide(p, x), off = x - j * a.block_size;
-                if (token + 4 <= s.tokens[b + 1] && off + 4 <= a.block_size) {
+                if (s.tokens[b + 1] - token >= 4 && a.block_size - off >= 4) {
                     const int id = *block_of(b, j);
                     const bool good = unsigned(id) < unsigned(a.n_blocks);
                     if (!good && a.status) *a.status = MK_ERR_BOUNDS;
@@ -178,7 +179,7 @@ __global__ void __launch_bounds__(kPagesThreads) pages_kernel(const __grid_const
                     int id[4];
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {   // (the loads of all four are in flight together)
-                        if (token + i >= tokens) break;
+                        if (i >= tokens - token) break;
                         while (token + i >= s.tokens[b + 1]) ++b;   // (ends: token + i < tokens, the last sum)
                         x = s.len[b] + (token + i - s.tokens[b]);
                         j = pages_divide(p, x);
@@ -211,13 +212,13 @@ __global__ void __launch_bounds__(kPagesThreads) pages_kernel(const __grid_const
     }
     // the moved blocks, from the last thread on (which has no tokens where the first ones suffice)
     const int back = threads - 1 - self;
-    for (int j = back; j < returned; j += threads) {
+    for (long long j = back; j < returned; j += threads) {
         const int at = wrap((long long)(front) + free);
-        a.ring[wrap((long long)(at) + j)] = *given_back(j);
+        a.ring[wrap(at + j)] = *given_back(int(j));
     }
-    for (int k = back; k < taken; k += threads) {
-        const int b = pages_owner(s.taken, 0, a.batch, k);
-        a.table[int64_t(b) * a.max_blocks + s.held[b] + (k - s.taken[b])] = *new_block(k);
+    for (long long k = back; k < taken; k += threads) {
+        const int b = pages_owner(s.taken, 0, a.batch, int(k));
+        a.table[int64_t(b) * a.max_blocks + s.held[b] + (k - s.taken[b])] = *new_block(int(k));
     }
     if (a.first)
         for (int b = back; b <= a.batch; b += threads) a.first[b] = st == MK_OK ? s.tokens[b] : 0;
