@@ -66,12 +66,20 @@ struct LinearFirst {   // the first tile's adapters; stages given to a block of 
     int32_t list[256], count;
     uint64_t ready, granted[10];
 };
+// What the linear kernel with adapters reads before its own wait is whole: the kernel in front starts it behind its wait for
+// everything before.  But that wait orders the other kernel's reads, not this one's; read at the L2 (L2 true), where every
+// earlier kernel's writes have arrived, such a value cannot be one that an SM's L1 still holds.
+template <bool L2, typename T>
+__device__ __forceinline__ T linear_get(const T* at) {
+    if constexpr (L2) return __ldcg(at);
+    else return *at;
+}
 // By one warp: the adapters that tokens [m0, m0 + tokens) name, in order
 __device__ __forceinline__ void linear_list(const LinearExtra<true>& e, int m0, int tokens, LinearFirst& first) {
     const int lane = threadIdx.x & 31;
     int count = 0;
     for (int t = 0; t < tokens; t += 32) {
-        int name = t + lane < tokens ? e.index[m0 + t + lane] : -1;
+        int name = t + lane < tokens ? linear_get<true>(e.index + m0 + t + lane) : -1;
         if (name >= e.n_adapters) name = -1;
         bool is_new = (__match_any_sync(0xFFFFFFFFu, name) & ((1u << lane) - 1)) == 0 && name >= 0;
         for (int i = 0; i < count; ++i) is_new = is_new && first.list[i] != name;
@@ -126,7 +134,7 @@ __device__ __forceinline__ float linear_act(int act, float y, float up) {
     return act == MK_ACT_SWIGLU ? s * up : s;
 }
 // The residuals of the tokens r, r + 1, .. of feature j, of which `left` exist (zeros where not wanted)
-template <int N>
+template <bool L2, int N>
 __device__ __forceinline__ void linear_residuals(const LinearParams& p, bool wanted, int r, int j, int left, float (&res)[N], int step = 1) {
     const int64_t at = r * p.residual_stride + j, by = p.residual_stride * step;
 #pragma unroll
@@ -136,19 +144,19 @@ __device__ __forceinline__ void linear_residuals(const LinearParams& p, bool wan
         const float* src = static_cast<const float*>(p.residual) + at;
 #pragma unroll
         for (int i = 0; i < N; ++i, src += by)
-            if (i * step < left) res[i] = *src;
+            if (i * step < left) res[i] = linear_get<L2>(src);
     } else {
         const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(p.residual) + at;
 #pragma unroll
         for (int i = 0; i < N; ++i, src += by)
-            if (i * step < left) res[i] = __bfloat162float(*src);
+            if (i * step < left) res[i] = __bfloat162float(linear_get<L2>(src));
     }
 }
 // What the sums of a thread's columns start from: the bias and, where no activation comes between,
 // the residual (in one of the CTAs that share the contraction)
-template <int N>
+template <bool L2, int N>
 __device__ __forceinline__ void linear_begin(const LinearParams& p, int r, int j, int left, bool mine, bool plain, float bias, float (&v)[N]) {
-    linear_residuals<N>(p, mine && plain, r, j, left, v);
+    linear_residuals<L2>(p, mine && plain, r, j, left, v);
     if (mine)
 #pragma unroll
         for (int i = 0; i < N; ++i) v[i] += bias;
@@ -251,7 +259,7 @@ __device__ __noinline__ void linear_alone(const LinearParams& p, const LinearExt
                         for (int i = 0; i < 8; ++i) y[part][v] = fmaf(a[i], b[i], y[part][v]);
                     }
                 }
-                if (p.bias) y[part][v] += __bfloat162float(p.bias[part * p.n + row[v / 2]]);
+                if (p.bias) y[part][v] += __bfloat162float(linear_get<true>(p.bias + part * p.n + row[v / 2]));
             }
         }
 #pragma unroll
@@ -259,7 +267,7 @@ __device__ __noinline__ void linear_alone(const LinearParams& p, const LinearExt
             const int i = (2 * q + (v & 1)) * step, of = half + g + 8 * (v / 2);   // token, the lane whose feature it is
             if (i >= most || !(all >> of & 1u)) continue;
             float res[1];
-            linear_residuals<1>(p, true, m + i, j0 + of, 1, res);
+            linear_residuals<true>(p, true, m + i, j0 + of, 1, res);
             const float out = linear_act(GATED ? MK_ACT_SWIGLU : p.act, y[0][v], GATED ? y[GATED ? 1 : 0][v] : 0.f) + res[0];
             const int64_t at = (m + i) * p.out_stride + j0 + of;
             if constexpr (F32) static_cast<float*>(p.out)[at] = out;
@@ -281,7 +289,7 @@ __device__ __forceinline__ void linear_join(const LinearParams& p, const LinearE
                                             uint32_t up_bytes, int split, int by, int at, int m0, int c, int c1, int row, int j) {
     float y[8], u[8], res[8];
     const int left = !ADAPT || j < p.n ? c1 - c : 0;   // (with adapters lanes without a feature come here too)
-    linear_residuals<8>(p, GATED || p.act != MK_ACT_NONE, m0 + c, j, left, res, STEP);
+    linear_residuals<ADAPT>(p, GATED || p.act != MK_ACT_NONE, m0 + c, j, left, res, STEP);
 #pragma unroll
     for (int i = 0; i < 8; ++i) y[i] = u[i] = 0.f;
     for (int s = 0; s < split; ++s) {
@@ -591,9 +599,9 @@ linear_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
             place(tile, n0, m0);
             const int j = n0 + row, left = j < p.n ? p.rows - m0 - cols : 0;
             // bias, and without an activation the residual, enter the sums first: their loads are hidden
-            linear_begin<T::kWidth>(p, m0 + cols, j, left, rank == 0, plain, p.bias && j < p.n ? __bfloat162float(p.bias[j]) : 0.f, v);
+            linear_begin<ADAPT>(p, m0 + cols, j, left, rank == 0, plain, p.bias && j < p.n ? __bfloat162float(linear_get<ADAPT>(p.bias + j)) : 0.f, v);
             if (GATED) {
-                const float b = rank == 0 && p.bias && j < p.n ? __bfloat162float(p.bias[p.n + j]) : 0.f;
+                const float b = rank == 0 && p.bias && j < p.n ? __bfloat162float(linear_get<ADAPT>(p.bias + p.n + j)) : 0.f;
 #pragma unroll
                 for (int i = 0; i < T::kWidth; ++i) u[GATED ? i : 0] = b;
             }
@@ -644,7 +652,7 @@ linear_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
             for (int c = 0; c < T::kWidth; c += 8) {
                 if (c >= p.rows - m0 - cols) break;
                 float y[8], res[8];
-                linear_residuals(p, !plain, m0 + cols + c, j, left - c, res);
+                linear_residuals<ADAPT>(p, !plain, m0 + cols + c, j, left - c, res);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) y[i] = linear_act(GATED ? MK_ACT_SWIGLU : p.act, v[c + i], GATED ? u[GATED ? c + i : 0] : 0.f) + res[i];
                 if (ADAPT && linear_nan(y)) again |= 1u << (c / 8);
@@ -954,8 +962,8 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
             const int j = n0 + (GATED ? row & 63 : row);
             const bool live = j < p.n;
             const int jb = up_row ? p.n + j : j;   // (bias rows: gate rows, then up rows)
-            linear_begin<128>(p, m0 + cols, j, live ? p.rows - m0 - cols : 0, part == 0, plain,
-                              p.bias && live ? __bfloat162float(p.bias[jb]) : 0.f, v);
+            linear_begin<ADAPT>(p, m0 + cols, j, live ? p.rows - m0 - cols : 0, part == 0, plain,
+                              p.bias && live ? __bfloat162float(linear_get<ADAPT>(p.bias + jb)) : 0.f, v);
             int end = kb1;   // (of the loop over pieces: further by those of the adapters)
             if constexpr (ADAPT && F32) {
                 LinearShare sh{};
@@ -997,7 +1005,7 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
                 const int m = m0 + cols + c + (up_row ? 8 : 0), left = live ? p.rows - m : 0;
                 if (m0 + cols + c >= p.rows) break;   // (the same for both warps of an exchange: they share cols)
                 float y[8], res[8];
-                linear_residuals<8>(p, !plain, m, j, left, res);
+                linear_residuals<ADAPT>(p, !plain, m, j, left, res);
                 if constexpr (GATED) {
                     const uint32_t at = stage0 + T::kStages * T::kStageBytes + uint32_t(((c / 16 & 1) * 2 + cols / 128) * (8 * 128 * 4));
 #pragma unroll
