@@ -26,6 +26,18 @@ struct LowParams {
     int32_t* status;
 };
 
+// Two low-rank values' next bf16 part, and what it leaves.  A part that is not the last stays finite: a value that would round to
+// an infinity takes bf16's largest, and so do infinities and NaN, which are then in every rest and become the last part.
+__device__ __forceinline__ __nv_bfloat162 low_part(float (&v)[2], bool last) {
+    constexpr float kMost = 3.3895313892515355e38f;   // (2 - 2^-7) 2^127
+    __nv_bfloat162 h;
+    h.x = __float2bfloat16_rn(last ? v[0] : fminf(fmaxf(v[0], -kMost), kMost));
+    h.y = __float2bfloat16_rn(last ? v[1] : fminf(fmaxf(v[1], -kMost), kMost));
+    v[0] -= __bfloat162float(h.x);
+    v[1] -= __bfloat162float(h.y);
+    return h;
+}
+
 // A cluster works on 16 neighbouring tokens of one tile of the linear map, for the tile's adapters y, y + gridDim.y, ..: those of
 // its tokens that name the adapter get their low-rank row, the others zeros.  8 NT columns of the rank at a time; x and down are
 // read from global memory straight into the operands of m16n8k16 products (a thread's 16 bytes of a row are the elements 2 i, 2 i + 1
@@ -155,7 +167,7 @@ __global__ void __launch_bounds__(kLowThreads, 2) low_rank_kernel(const __grid_c
             const int r = 2 * e / width, c = 2 * e - r * width;
             if (row0 + r >= tokens) break;
             float v[2] = {0.f, 0.f};
-            if (any && name[row0 + r] == adapter) {
+            if (any && name[row0 + r] == adapter && c < p.rank) {   // (columns behind the rank stay zero whatever x and the scale are)
                 const uint32_t src = sm::smem(sums + r * width + c);
                 float2 got[8];   // (of all CTAs together: their way takes longer than everything else here)
 #pragma unroll
@@ -169,15 +181,9 @@ __global__ void __launch_bounds__(kLowThreads, 2) low_rank_kernel(const __grid_c
                 v[1] *= scale;
             }
             __nv_bfloat16* dst = p.terms + int64_t(m0 + row0 + r) * (p.f32 ? 3 : 2) * p.part + slot * width + c;
-            for (int part = 0; part < (p.f32 ? 3 : 2); ++part, dst += p.part) {
-                __nv_bfloat162 pair;
-                pair.x = __float2bfloat16_rn(v[0]);
-                pair.y = __float2bfloat16_rn(v[1]);
-                *reinterpret_cast<__nv_bfloat162*>(dst) = pair;
-                const float h0 = __bfloat162float(pair.x), h1 = __bfloat162float(pair.y);
-                v[0] = isinf(h0) ? 0.f : v[0] - h0;   // (an infinity, or a value that rounds to one, leaves no rest)
-                v[1] = isinf(h1) ? 0.f : v[1] - h1;
-            }
+            *reinterpret_cast<__nv_bfloat162*>(dst) = low_part(v, false);
+            if (p.f32) *reinterpret_cast<__nv_bfloat162*>(dst += p.part) = low_part(v, false);
+            *reinterpret_cast<__nv_bfloat162*>(dst + p.part) = low_part(v, true);
         }
         // the next adapter's sums go to the other half; they are in this one again when every CTA has passed the next barrier
         if (any) sums = sums == all_sums ? all_sums + 16 * width : all_sums;
