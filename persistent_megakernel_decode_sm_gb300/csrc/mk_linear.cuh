@@ -173,6 +173,22 @@ __device__ __forceinline__ void linear_stores(const LinearParams& p, int r, int 
             else *dst = __float2bfloat16_rn(y[i]);
         }
 }
+// The same but for sums that came to NaN: a bit for each of these
+template <bool F32>
+__device__ __forceinline__ uint32_t linear_stores_sound(const LinearParams& p, int r, int j, int left, const float (&y)[8], int step = 1) {
+    using Out = std::conditional_t<F32, float, __nv_bfloat16>;
+    Out* dst = static_cast<Out*>(p.out) + (r * p.out_stride + j);
+    const int64_t by = p.out_stride * step;
+    uint32_t nan = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i, dst += by)
+        if (i * step < left) {
+            if (y[i] != y[i]) nan |= 1u << i;
+            else if constexpr (F32) *dst = y[i];
+            else *dst = __float2bfloat16_rn(y[i]);
+        }
+    return nan;
+}
 __device__ __forceinline__ void linear_mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
     asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
                  : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
@@ -189,24 +205,112 @@ __device__ __forceinline__ void linear_widen(const uint4& u, float (&x)[8], bool
         x[2 * i + 1] = (add ? x[2 * i + 1] : 0.f) + __uint_as_float(w[i] & 0xFFFF0000u);
     }
 }
+// Whether 8 bf16 are all finite
+__device__ __forceinline__ bool linear_finite(const uint4& u) {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+    bool ok = true;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) ok = ok && (w[i] & 0x7F80u) != 0x7F80u && (w[i] & 0x7F800000u) != 0x7F800000u;
+    return ok;
+}
+// What a lane has found out about its feature: the tile's adapters whose up rows of it are not finite (how many, the last of them),
+// and the adapter that it last looked up among the tile's
+struct LinearSuspects {
+    int bad = -1, last = -1;
+    int name = -1, slot = -1;
+};
+// Of the tokens m + i step (bits i of `nan`) whose outputs of feature j came to NaN, those that have to be taken again: another
+// token's adapter is not finite there, or the token's own makes an infinity in a part.  The others are NaN in their own right.
+template <bool GATED, bool F32>
+__device__ __noinline__ uint32_t linear_suspects(const LinearParams& p, const LinearExtra<true>& e, const volatile int32_t* list, int adapters,
+                                                 int m, int step, int j, uint32_t nan, LinearSuspects& s) {
+    constexpr int kRows = GATED ? 2 : 1;
+    const int64_t next = int64_t(p.n) * e.rank;   // from gate to up rows
+    auto row = [&](int adapter) { return e.up_rows + (int64_t(adapter) * kRows * p.n + j) * e.rank; };
+    if (s.bad < 0) {
+        s.bad = 0;
+        for (int i = 0; i < adapters; ++i) {
+            const __nv_bfloat16* u = row(list[i]);
+            bool ok = true;
+#pragma unroll 2
+            for (int c = 0; c < e.rank; c += 8)
+#pragma unroll
+                for (int part = 0; part < kRows; ++part) ok = linear_finite(__ldg(reinterpret_cast<const uint4*>(u + part * next + c))) && ok;
+            if (!ok) {
+                ++s.bad;
+                s.last = i;
+            }
+        }
+    }
+    uint32_t again = 0;
+    for (uint32_t left = nan; left; left &= left - 1) {
+        const int i = __ffs(left) - 1, token = m + i * step, own = e.index[token];
+        if (own != s.name) {
+            s.name = own;
+            s.slot = -1;
+            for (int at = 0; at < adapters && own >= 0; ++at)
+                if (list[at] == own) s.slot = at;
+        }
+        bool redo = s.bad > 1 || (s.bad == 1 && s.last != s.slot), in_parts = false;
+        if (s.slot >= 0) {   // (most often a token whose x is not finite, and its first sum NaN)
+            const __nv_bfloat16 *t = e.term_rows + int64_t(token) * (F32 ? 3 : 2) * e.part + s.slot * e.width, *u = row(own);
+            float sum[kRows], parts[kRows];
+#pragma unroll
+            for (int r = 0; r < kRows; ++r) sum[r] = parts[r] = 0.f;
+            bool is_nan = false;
+#pragma unroll 1
+            for (int c = 0; c < e.rank && !is_nan; c += 8) {
+                float h[F32 ? 3 : 2][8], b[8];
+#pragma unroll
+                for (int k = 0; k < (F32 ? 3 : 2); ++k) linear_widen(*reinterpret_cast<const uint4*>(t + k * e.part + c), h[k]);
+#pragma unroll
+                for (int r = 0; r < kRows; ++r) {
+                    linear_widen(*reinterpret_cast<const uint4*>(u + r * next + c), b);
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        sum[r] = fmaf(F32 ? h[0][k] + h[1][k] + h[F32 ? 2 : 1][k] : h[0][k] + h[1][k], b[k], sum[r]);
+#pragma unroll
+                        for (int q = 0; q < (F32 ? 3 : 2); ++q) parts[r] += fabsf(h[q][k] * b[k]);
+                    }
+                    is_nan = is_nan || sum[r] != sum[r];
+                }
+            }
+            if (is_nan) continue;
+#pragma unroll
+            for (int r = 0; r < kRows; ++r) in_parts = in_parts || !isfinite(parts[r]);
+        }
+        if (redo || in_parts) again |= 1u << i;
+    }
+    return again;
+}
 // An adapter's infinity or NaN times a zero of another token's low-rank row is NaN: a tensor core cannot leave the product out.
-// Sums that came to NaN are therefore taken again here, with no adapter but the token's own (and as that one's parts may
-// be infinities of both signs, its value in one piece); what is NaN by itself stays so.  By a whole warp: 8 tokens m, m + step, ..
-// (the same of every lane, `left` from m on) of the lanes' features j, j + 1, .., stored where the lane wants its own.
+// Sums that came to NaN so are taken again here, with no adapter but the token's own (and as that one's parts may
+// be infinities of both signs, its value in one piece); what is NaN by itself is stored as that.  By a whole warp: the tokens
+// m + i step (bits i of a lane's `nan`, of 8 that are the same of every lane, `left` from m on) of the lanes' features j, j + 1, ...
 // x and w are read straight into m16n8k16 products (a thread's 16 bytes of a row are the elements 2 i, 2 i + 1 of two products),
 // summed 512 elements at a time; 16 features of 8 tokens take 3 loads a lane per 32 of the contraction.
-// Where no sum is NaN this is one comparison an output (0.1 to 0.3 us a call, 1.3 of 4096 tokens through 2 x 8192 x 2048).  Taking a
-// tile again is bound by the latencies of those loads: one adapter of NaN among 64 of 64 tokens (4096 x 6144) 330 us for 46, among
-// those of 4096 tokens (500 of whose share its tiles) 4.8 ms for 0.165; with the warp's lanes along the contraction 1850 and 33 ms.
+// Where no sum is NaN this is one comparison an output (0.1 to 0.3 us a call, 1.3 of 4096 tokens through 2 x 8192 x 2048).  Where some
+// are in their own right, finding that out reads the up rows of the tile's adapters: 512 of those 4096 tokens of NaN 370 us for 168,
+// all of them 910, 64 tokens of 64 adapters of rank 64 (4096 x 6144) 200 for 46 (with all of these taken again 2.9 ms, 9.2 ms and
+// 340 us).  Taking a tile again is bound by the latencies of x's and w's loads: one adapter of NaN among those 64 510 us, among those of
+// the 4096 tokens, 60 of which name it, 3.1 ms.
 template <bool GATED, bool F32>
 __device__ __noinline__ void linear_alone(const LinearParams& p, const LinearExtra<true>& e, const volatile int32_t* list, int adapters,
-                                          int m, int step, int j, int left, bool wanted) {
+                                          int m, int step, int j, int left, uint32_t nan, LinearSuspects& suspects) {
+    using Out = std::conditional_t<F32, float, __nv_bfloat16>;
     constexpr unsigned kAll = 0xFFFFFFFFu;
     const int lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
-    const unsigned all = __ballot_sync(kAll, wanted && left > 0);   // (a lane without a feature has nothing left)
+    if (!__any_sync(kAll, nan != 0)) return;
+    sm::pdl_wait();   // (the terms)
+    uint32_t mine = 0;
+    if (nan) {
+        mine = linear_suspects<GATED, F32>(p, e, list, adapters, m, step, j, nan, suspects);
+        for (uint32_t stays = nan & ~mine; stays; stays &= stays - 1)
+            static_cast<Out*>(p.out)[(m + (__ffs(stays) - 1) * step) * p.out_stride + j] = Out(__uint_as_float(0x7FFFFFFFu));
+    }
+    const unsigned all = __ballot_sync(kAll, mine != 0);   // (a lane without a feature has stored nothing, and has no bits)
     if (!all) return;
     const int most = __shfl_sync(kAll, left, __ffs(all) - 1), j0 = __shfl_sync(kAll, j, 0);
-    sm::pdl_wait();   // (the terms)
     // a product's column is token g (behind the last: the last one's again), its sums are of tokens 2 q and 2 q + 1
     const __nv_bfloat16* x = e.x + int64_t(m + min(g, (most - 1) / step) * step) * e.x_stride + q * 8;
     int own[2], slot[2];   // their adapters, and where these are among the tile's
@@ -265,13 +369,11 @@ __device__ __noinline__ void linear_alone(const LinearParams& p, const LinearExt
 #pragma unroll
         for (int v = 0; v < 4; ++v) {
             const int i = (2 * q + (v & 1)) * step, of = half + g + 8 * (v / 2);   // token, the lane whose feature it is
-            if (i >= most || !(all >> of & 1u)) continue;
+            if (!(__shfl_sync(kAll, mine, of) >> (2 * q + (v & 1)) & 1u)) continue;
             float res[1];
             linear_residuals<true>(p, true, m + i, j0 + of, 1, res);
             const float out = linear_act(GATED ? MK_ACT_SWIGLU : p.act, y[0][v], GATED ? y[GATED ? 1 : 0][v] : 0.f) + res[0];
-            const int64_t at = (m + i) * p.out_stride + j0 + of;
-            if constexpr (F32) static_cast<float*>(p.out)[at] = out;
-            else static_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16_rn(out);
+            static_cast<Out*>(p.out)[(m + i) * p.out_stride + j0 + of] = Out(out);
         }
     }
 }
@@ -286,7 +388,8 @@ __device__ __forceinline__ bool linear_nan(const float (&y)[8]) {
 // by * s + at), staged as [column][128 rows], added in order; the up sums lie `up_bytes` further
 template <int STEP, bool GATED, bool F32, bool ADAPT>
 __device__ __forceinline__ void linear_join(const LinearParams& p, const LinearExtra<ADAPT>& e, const std::conditional_t<ADAPT, LinearFirst, char>& tile, uint32_t stage0,
-                                            uint32_t up_bytes, int split, int by, int at, int m0, int c, int c1, int row, int j) {
+                                            uint32_t up_bytes, int split, int by, int at, int m0, int c, int c1, int row, int j,
+                                            [[maybe_unused]] LinearSuspects& suspects) {
     float y[8], u[8], res[8];
     const int left = !ADAPT || j < p.n ? c1 - c : 0;   // (with adapters lanes without a feature come here too)
     linear_residuals<ADAPT>(p, GATED || p.act != MK_ACT_NONE, m0 + c, j, left, res, STEP);
@@ -304,9 +407,11 @@ __device__ __forceinline__ void linear_join(const LinearParams& p, const LinearE
 #pragma unroll
     for (int i = 0; i < 8; ++i) y[i] = linear_act(GATED ? MK_ACT_SWIGLU : p.act, y[i], u[i]) + res[i];
     if constexpr (ADAPT) {
-        const bool again = linear_nan(y);
-        if (__any_sync(0xFFFFFFFFu, again)) linear_alone<GATED, F32>(p, e, tile.list, tile.count, m0 + c, STEP, j, left, again);
-        if (again) return;
+        if (__any_sync(0xFFFFFFFFu, linear_nan(y))) {
+            const uint32_t nan = linear_stores_sound<F32>(p, m0 + c, j, left, y, STEP);
+            linear_alone<GATED, F32>(p, e, tile.list, tile.count, m0 + c, STEP, j, left, nan, suspects);
+            return;
+        }
     }
     linear_stores<F32>(p, m0 + c, j, left, y, STEP);
 }
@@ -647,7 +752,7 @@ linear_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
                 }
                 break;
             }
-            [[maybe_unused]] uint32_t again = 0;   // (a bit for each 8 tokens)
+            [[maybe_unused]] uint32_t nan[(T::kWidth + 31) / 32] = {};   // (a bit for each token)
 #pragma unroll
             for (int c = 0; c < T::kWidth; c += 8) {
                 if (c >= p.rows - m0 - cols) break;
@@ -655,16 +760,21 @@ linear_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
                 linear_residuals<ADAPT>(p, !plain, m0 + cols + c, j, left - c, res);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) y[i] = linear_act(GATED ? MK_ACT_SWIGLU : p.act, v[c + i], GATED ? u[GATED ? c + i : 0] : 0.f) + res[i];
-                if (ADAPT && linear_nan(y)) again |= 1u << (c / 8);
+                if (ADAPT && linear_nan(y)) nan[c / 32] |= linear_stores_sound<F32>(p, m0 + cols + c, j, left - c, y) << (c % 32);
                 else linear_stores<F32>(p, m0 + cols + c, j, left - c, y);
             }
             if constexpr (ADAPT) {
-                if (__any_sync(0xFFFFFFFFu, again != 0)) {
-                    LinearShare sh{};
-                    const int end_c = share(tile, sh) ? T::kWidth : 0;
+                bool any = false;
+#pragma unroll
+                for (uint32_t word : nan) any = any || word != 0;
+                LinearShare sh{};
+                if (__any_sync(0xFFFFFFFFu, any) && share(tile, sh)) {
+                    LinearSuspects suspects;
+#pragma unroll
+                    for (int c = 0; c < T::kWidth; c += 32)
 #pragma unroll 1
-                    for (int c = 0; c < end_c; c += 8)
-                        linear_alone<GATED, F32>(p, e, sh.list, sh.adapters, m0 + cols + c, 1, j, left - c, again >> (c / 8) & 1);
+                        for (int i = 0; i < min(32, T::kWidth); i += 8)
+                            linear_alone<GATED, F32>(p, e, sh.list, sh.adapters, m0 + cols + c + i, 1, j, left - c - i, nan[c / 32] >> i & 0xFFu, suspects);
                 }
             }
         }
@@ -679,9 +789,10 @@ linear_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
             const int t = threadIdx.x - 64, row = t & 127, j = n0 + row;
             constexpr int kGroups = T::kWarps / 4;
             const int c1 = min(BN * (rank + 1) / p.split, p.rows - m0);
+            LinearSuspects suspects;
             if (ADAPT ? n0 + (row & ~31) < p.n : j < p.n)
                 for (int c = BN * rank / p.split + t / 128; c < c1; c += 8 * kGroups)
-                    linear_join<kGroups, GATED, F32, ADAPT>(p, e, first_tile, stage0, BN * 128 * 4, p.split, 1, 0, m0, c, c1, row, j);
+                    linear_join<kGroups, GATED, F32, ADAPT>(p, e, first_tile, stage0, BN * 128 * 4, p.split, 1, 0, m0, c, c1, row, j, suspects);
         }
         __syncwarp();
         sm::cluster_sync();   // no CTA leaves while a peer reads its partial sums
@@ -999,7 +1110,7 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
             // 8 columns a step.  SwiGLU: 16 columns, of which the gate row keeps 0-7 and receives their up
             // values from its up row, which keeps 8-15 and receives their gate values; two buffers take turns
             constexpr int kStep = GATED ? 16 : 8;
-            [[maybe_unused]] uint32_t again = 0;   // (a bit for each step)
+            [[maybe_unused]] uint32_t nan[kStep == 8 ? 4 : 2] = {};   // (a bit for each token: 8 of a step)
 #pragma unroll
             for (int c = 0; c < 128; c += kStep) {
                 const int m = m0 + cols + c + (up_row ? 8 : 0), left = live ? p.rows - m : 0;
@@ -1024,18 +1135,23 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
 #pragma unroll
                     for (int i = 0; i < 8; ++i) y[i] = linear_act(p.act, v[c + i], 0.f) + res[i];
                 }
-                if (ADAPT && linear_nan(y)) again |= 1u << (c / kStep);
+                if (ADAPT && linear_nan(y)) nan[c / kStep / 4] |= linear_stores_sound<F32>(p, m, j, left, y) << (c / kStep % 4 * 8);
                 else linear_stores<F32>(p, m, j, left, y);
             }
             if constexpr (ADAPT) {
-                if (__any_sync(0xFFFFFFFFu, again != 0)) {
-                    LinearShare sh{};
-                    const int end_c = share(tile, sh) ? 128 : 0;
+                bool any = false;
+#pragma unroll
+                for (uint32_t word : nan) any = any || word != 0;
+                LinearShare sh{};
+                if (__any_sync(0xFFFFFFFFu, any) && share(tile, sh)) {
+                    LinearSuspects suspects;
+#pragma unroll
+                    for (int w = 0; w < (kStep == 8 ? 4 : 2); ++w)
 #pragma unroll 1
-                    for (int c = 0; c < end_c; c += kStep) {
-                        const int m = m0 + cols + c + (up_row ? 8 : 0);
-                        linear_alone<GATED, F32>(p, e, sh.list, sh.adapters, m, 1, j, live ? p.rows - m : 0, again >> (c / kStep) & 1);
-                    }
+                        for (int i = 0; i < 4; ++i) {
+                            const int m = m0 + cols + (4 * w + i) * kStep + (up_row ? 8 : 0);
+                            linear_alone<GATED, F32>(p, e, sh.list, sh.adapters, m, 1, j, live ? p.rows - m : 0, nan[w] >> (8 * i) & 0xFFu, suspects);
+                        }
                 }
             }
         }
@@ -1050,9 +1166,10 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
             const int t = threadIdx.x - 64, row = t % T::kRows, j = n0 + row;
             constexpr int kGroups = 256 / T::kRows;
             const int width0 = 256 * part / p.split, c1 = min(256 * (part + 1) / p.split, p.rows - m0);
+            LinearSuspects suspects;
             if (ADAPT ? n0 + (row & ~31) < p.n : j < p.n)
                 for (int c = width0 + t / T::kRows; c < c1; c += 8 * kGroups)
-                    linear_join<kGroups, GATED, F32, ADAPT>(p, e, first_tile, stage0, 64 * 4, p.split, 2, half, m0, c, c1, row, j);
+                    linear_join<kGroups, GATED, F32, ADAPT>(p, e, first_tile, stage0, 64 * 4, p.split, 2, half, m0, c, c1, row, j, suspects);
         }
         __syncwarp();
     }
