@@ -503,8 +503,8 @@ typedef struct {
     const float* scale;
     const int32_t* index;
 } mk_adapters;
-/* Workspace bytes of mk_linear_adapted for these arguments (0 where they are not valid, or with no rows; nothing is read
- * through pointers). */
+/* Workspace bytes of mk_linear_adapted for these arguments: 0 with no rows, or where sizes, activation or types are not valid.
+ * No pointer in them is looked at but `residual` (null or not: its type counts), so buffers need not exist yet. */
 size_t mk_linear_adapted_workspace(const mk_linear_args* a, const mk_adapters* ad);
 mk_status mk_linear_adapted(const mk_linear_args* a, const mk_adapters* ad, void* workspace, size_t workspace_bytes, void* stream);
 

@@ -277,7 +277,7 @@ using namespace mk;
 
 extern "C" size_t mk_linear_adapted_workspace(const mk_linear_args* a, const mk_adapters* ad) {
     AdaptPlan pl{};
-    if (linear_check(a) != MK_OK || adapt_check(a, ad, false) != MK_OK || a->rows == 0 || adapt_plan(a, ad, pl) != MK_OK) return 0;
+    if (linear_check_shape(a) != MK_OK || adapt_check(a, ad, false) != MK_OK || a->rows == 0 || adapt_plan(a, ad, pl) != MK_OK) return 0;
     return pl.bytes;
 }
 

@@ -1329,7 +1329,8 @@ static mk_status linear_choose(const LinearParams& p, int extra, int device, Lin
     return st;
 }
 
-static mk_status linear_check(const mk_linear_args* a) {
+// What a plan depends on: sizes, activation, types
+static mk_status linear_check_shape(const mk_linear_args* a) {
     if (!a) return fail(MK_ERR_ARG, "null argument");
     if (a->rows < 0 || a->rows > (1 << 30) || a->n < 1 || a->n > (1 << 30) || a->k < 8 || a->k % 8)
         return fail(MK_ERR_ARG, "linear: rows %d, n %d, k %d (rows in [0, 2^30], n in [1, 2^30], k a multiple of 8)", a->rows, a->n, a->k);
@@ -1338,8 +1339,12 @@ static mk_status linear_check(const mk_linear_args* a) {
     if ((a->out_dtype != MK_BF16 && a->out_dtype != MK_F32) ||
         (a->residual && a->residual_dtype != MK_BF16 && a->residual_dtype != MK_F32))
         return fail(MK_ERR_ARG, "linear: unknown data type");
+    return MK_OK;
+}
+static mk_status linear_check(const mk_linear_args* a) {
+    const mk_status st = linear_check_shape(a);
+    if (st != MK_OK || a->rows == 0) return st;
     const bool gated = a->activation == MK_ACT_SWIGLU;
-    if (a->rows == 0) return MK_OK;
     const int64_t os = a->out_dtype == MK_F32 ? 4 : 2, rs = a->residual_dtype == MK_F32 ? 4 : 2;
     if (!a->x || !a->w || !a->out) return fail(MK_ERR_ARG, "linear: null pointer");
     if (!op_aligned(a->x, 16) || !op_aligned(a->w, 16)) return fail(MK_ERR_ARG, "linear: x and w must be 16-byte aligned");
