@@ -513,8 +513,8 @@ mk_status mk_linear_adapted(const mk_linear_args* a, const mk_adapters* ad, void
  *   y = x / sqrt(mean(x^2) + eps) * gain                     q and k, where their gain is given
  *   (y_i, y_j) -> (y_i c - y_j s, y_i s + y_j c)             q and k: pair p = 0 .. rotary / 2 - 1 of elements i, j,
  *                                                            c, s = cos, sin of positions[axis(p)][t] * freqs[p]
- * all in fp32 (angles exactly reduced, whatever the position), rounded once to bf16.  Elements behind `rotary` and v pass
- * as they are (rounded).
+ * all in fp32, rounded once to bf16; angles are exactly reduced, whatever the position, their sines and cosines off by at most
+ * 2^-20.9 (of 1, not of themselves).  Elements behind `rotary` and v pass as they are (rounded).
  *  tokens         may be 0 (nothing is done); at most 2^30
  *  head_dim       a multiple of 16, at most 256; n_q_heads + 2 n_kv_heads at most 4096
  *  qkv            of qkv_dtype, token t at qkv + t * qkv_stride elements; 16-byte aligned, qkv_stride a multiple of 8
@@ -534,7 +534,8 @@ mk_status mk_linear_adapted(const mk_linear_args* a, const mk_adapters* ad, void
  *  kv, layer      the cache as in mk_attend, of `sequences` sequences (1: a pool, or a single one)
  *  q              bf16, token t's heads at q + t * q_stride elements (a multiple of 8; 16-byte aligned).  It may be the
  *                 q part of a bf16 qkv itself (the same pointer and stride); else it overlaps no input and not the cache
- * Errors: MK_ERR_ARG, MK_ERR_CUDA; status: MK_ERR_BOUNDS. */
+ * Errors: MK_ERR_ARG, MK_ERR_CUDA; status: MK_ERR_BOUNDS, and MK_ERR_TIMEOUT where a copy did not arrive within its limit: q and the
+ * cache then lack heads. */
 typedef struct {
     int32_t tokens, n_q_heads, n_kv_heads, head_dim;
     const void* qkv;

@@ -785,7 +785,8 @@ def rope_append(qkv, kv, positions, slots, freqs, layer: int = 0, sections: Opti
     bf16 qkv).  Returns out.
 
     status: a CUDA int32 tensor of one element, zeroed by the caller, that receives MK_ERR_BOUNDS for a slot behind the
-    cache (not stored).  No gradients are recorded."""
+    cache (not stored), or MK_ERR_TIMEOUT where a copy did not arrive within its limit (out and the cache then lack heads).  No
+    gradients are recorded."""
     q = (_fast or _setup()).rope_append(qkv, kv.k, kv.v, positions, slots, freqs, layer, sections, neighbours, q_gain, k_gain, eps, out,
                                         status)
     if q is not None:
