@@ -489,9 +489,11 @@ mk_status mk_attend(const mk_attend_args* a, void* workspace, size_t workspace_b
  *                    followed: it counts as none and status receives MK_ERR_BOUNDS
  * down and up are 16-byte aligned, scale and index 4-byte aligned; out overlaps none of them.  What holds for mk_linear
  * holds here; sums are fp32, scale[a] x down[a]^T enters the second product in two bf16 parts (16 bits; three parts, 24 bits, for an
- * fp32 output).  Infinities and NaN of an adapter reach only the tokens that name it: outputs of other tokens that would come
- * to NaN beside it are taken again, 3 to 20 times as long as the call where many are.  Outputs that are NaN in their own right (x, w,
- * bias, residual or the token's own adapter) are left as they are, up to 6 times.  Adapters that no token names are not read.
+ * fp32 output).  The same call gives the same bits; a token's may differ in the last places between calls that hold it in another
+ * row, or beside other tokens (the order of the fp32 sums).  Infinities and NaN of an adapter reach only the tokens that name it:
+ * outputs of other tokens that would come to NaN beside it are taken again, 3 to 20 times as long as the call where many are.
+ * Outputs that are NaN in their own right (x, w, bias, residual or the token's own adapter) are left as they are, up to 6 times.
+ * Adapters that no token names are not read.
  * workspace: mk_linear_adapted_workspace bytes of device memory, 256-byte aligned, which depend on the current device; calls that
  * may overlap need workspaces of their own.  Errors: MK_ERR_ARG, MK_ERR_CAPACITY (the workspace is too small), MK_ERR_CUDA;
  * status: MK_ERR_BOUNDS, MK_ERR_TIMEOUT. */

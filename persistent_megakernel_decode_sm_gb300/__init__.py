@@ -744,6 +744,7 @@ def adapted_linear(x, weight, adapters, index, bias=None, activation: Optional[s
     [rows], each token's adapter, negative for none.  The other operands are linear()'s.  workspace: at least
     mk_linear_adapted_workspace bytes (allocated by default).  Returns out.
 
+    The same call gives the same bits; a token's may differ in the last places where it stands in another row or beside others.
     status: as in linear(), and MK_ERR_BOUNDS for an index of n_adapters or more, which counts as none.  No gradients are
     recorded."""
     down, up, scale = adapters if len(adapters) == 3 else (*adapters, None)

@@ -66,3 +66,15 @@ def test_operands_written_right_in_front(rows, n, k, act, captured):
         run()
         for i, out in enumerate(outs):
             assert torch.equal(out, want[i % sets])
+
+
+@pytest.mark.parametrize("rows,n,k,rank,count", [(64, 514, 2048, 64, 64), (300, 257, 688, 24, 5), (1024, 512, 264, 16, 40)])
+@pytest.mark.parametrize("out_dtype", [BF, F32])
+def test_rows_in_another_order(rows, n, k, rank, count, out_dtype):
+    """Each order is within its bound, and the same again; bits may differ between them."""
+    from test_gpu_adapted import adapters, check, index_of
+    x, w, ad, index = randn((rows, k), 1), randn((n, k), 2, k ** -0.5), adapters(count, rank, k, n), index_of(rows, count, "any")
+    for seed in range(3):
+        order = torch.randperm(rows, generator=torch.Generator().manual_seed(seed)).cuda()
+        got = check(x[order], w, ad, index[order], out_dtype=out_dtype)
+        assert torch.equal(got, mk.adapted_linear(x[order], w, ad, index[order], out_dtype=out_dtype))
