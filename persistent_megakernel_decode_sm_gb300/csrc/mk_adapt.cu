@@ -224,10 +224,7 @@ static mk_status adapt_plan(const mk_linear_args* a, const mk_adapters* ad, Adap
     LinearParams p{};
     const bool f32 = a->out_dtype == MK_F32;
     pl.width = ad->rank <= 16 ? 16 : ad->rank <= 32 ? 32 : (ad->rank + kAdaptCols - 1) / kAdaptCols * kAdaptCols;
-    // blocks of the adapters' part, for the estimate: few tokens name an adapter each, of many neighbours share theirs
-    const int named = std::min({a->rows <= 64 ? a->rows : 4, ad->n_adapters, 64});
-    const int extra = (named * pl.width + kAdaptCols - 1) / kAdaptCols;
-    const mk_status st = linear_plan(a, extra, p, pl.choice);
+    const mk_status st = linear_plan(a, LinearNamed{ad->n_adapters, pl.width}, p, pl.choice);
     if (st != MK_OK) return st;
     const int tile = pl.choice.tokens;
     pl.slots = std::min({tile, ad->n_adapters, a->rows});

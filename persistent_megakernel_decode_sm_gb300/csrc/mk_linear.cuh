@@ -5,6 +5,7 @@
 #include "mk_ops.h"
 #include "mk_sm103.cuh"
 
+#include <algorithm>
 #include <type_traits>
 
 namespace mk {
@@ -1216,13 +1217,28 @@ struct LinearPlan {
     int64_t clusters;   // of the grid
     int64_t cost;       // estimated cycles
 };
+// With adapters a tile counts more blocks, 1.6 for each 64 columns of the adapters that its tokens name (8 or 12 products, where a
+// block of w and x has 4).  Who names which is not known here: each of up to 512 tokens is taken to have its own adapter, of
+// more rows / 512 neighbours share one.  The low-rank kernel in front is seen more of by pairs, which need an SM's whole shared memory, and
+// by split tiles, whose parts all end behind it: kAdaptPair and kAdaptSplit cycles.  us as planned so, and without the two and with four adapters
+// a tile whatever its width: tokens with an adapter each of 256 (4096 x 4096), 128 of rank 64 45.7 and 51.9, 256 73 and 81, 512 of rank 16
+// 57 and 80, of rank 64 135 and 155, fp32 158 and 197; 2048 of rank 64, fp32 (2048 x 2048) 308 and 399; 100 tokens of 8 adapters in
+// runs, 1024 x 8192, SwiGLU 14.6 and 18.3.  Runs of 128 of 512 tokens, 128 adapters loaded, take 31 either way, with tiles of 128 28.
+constexpr int kAdaptPair = 6000, kAdaptSplit = 2000;
+struct LinearNamed {
+    int adapters = 0, width = 0;   // loaded; columns of each
+    int blocks(int tokens, int rows) const {
+        const int each = (rows + 511) / 512, named = std::min({(tokens + each - 1) / each, adapters, rows});
+        return (named * width + kAdaptCols - 1) / kAdaptCols * 8 / 5;
+    }
+};
 // Times by rounds of the clusters that run at once: a round's blocks of the contraction at `cycles` each, a fixed
 // part (set-up, the first copies' way, the epilogue) and, where the contraction is cut over `split` units of `unit`
 // CTAs, the exchange of partial sums (`join`).  Unsplit tiles go to a persistent grid whose fixed part shows once.
 // Clusters of 8 leave SMs out (15 run at once on 152 SMs, 36 of 4, 76 of 2): 16 tiles over 8 CTAs each took two
 // rounds, 46.7 us against 38.8 with 4 (512 x 2048 x 8192).
 static mk_status linear_split(const void* fn, LinearLaunch& cfg, std::atomic<int> (&resident)[8], int unit, int most, int blocks, int extra,
-                              int cycles, int fixed, int join, LinearPlan& pl) {
+                              int cycles, int fixed, int join, int more, LinearPlan& pl) {
     const int64_t tiles = int64_t(pl.tiles_n) * pl.tiles_m;
     if (tiles > (1 << 28)) return fail(MK_ERR_ARG, "linear: %lld tiles", static_cast<long long>(tiles));
     pl.cost = INT64_MAX;
@@ -1237,7 +1253,7 @@ static mk_status linear_split(const void* fn, LinearLaunch& cfg, std::atomic<int
         if (fit < 1) break;
         const int64_t rounds = (tiles + fit - 1) / fit, part = int64_t((blocks + extra + s - 1) / s) * cycles;
         const bool even = (s & (s - 1)) == 0;   // (else the shares of a tile's columns come out uneven)
-        const int64_t t = s == 1 ? rounds * part + fixed : rounds * (part + fixed + (even ? join : 2 * join));
+        const int64_t t = s == 1 ? rounds * part + fixed : rounds * (part + fixed + more + (even ? join : 2 * join));
         if (t < pl.cost) { pl.cost = t; pl.split = s; pl.clusters = s > 1 || tiles < fit ? tiles : fit; }
     }
     return MK_OK;
@@ -1269,7 +1285,7 @@ struct LinearOne {
         pl.tiles_n = (p.n + 127) / 128;
         pl.tiles_m = (p.rows + BN - 1) / BN;
         LinearLaunch cfg(64 + 32 * T::kWarps + (ADAPT ? 32 : 0), T::kSmem, nullptr);
-        return linear_split(fn, cfg, resident[device], 1, 8, (p.k + kLinK - 1) / kLinK, extra, kCycles, kFixed, kJoin, pl);
+        return linear_split(fn, cfg, resident[device], 1, 8, (p.k + kLinK - 1) / kLinK, extra, kCycles, kFixed, kJoin, ADAPT ? kAdaptSplit : 0, pl);
     }
     static mk_status launch(const mk_linear_args* a, LinearParams& p, const LinearExtra<ADAPT>& e, const LinearPlan& pl, cudaStream_t stream) {
         CUtensorMap map_w, map_x;
@@ -1295,7 +1311,8 @@ struct LinearPair {
         pl.tiles_n = (p.n + 2 * T::kRows - 1) / (2 * T::kRows);
         pl.tiles_m = (p.rows + 255) / 256;
         LinearLaunch cfg(320, T::kSmem, nullptr);
-        return linear_split(fn, cfg, resident[device], 2, 4, (p.k + kLinK - 1) / kLinK, extra, 515, GATED ? 20000 : 15000, 2500, pl);
+        return linear_split(fn, cfg, resident[device], 2, 4, (p.k + kLinK - 1) / kLinK, extra, 515, (GATED ? 20000 : 15000) + (ADAPT ? kAdaptPair : 0), 2500,
+                            ADAPT ? kAdaptSplit : 0, pl);
     }
     static mk_status launch(const mk_linear_args* a, LinearParams& p, const LinearExtra<ADAPT>& e, const LinearPlan& pl, cudaStream_t stream) {
         CUtensorMap map_w, map_x;
@@ -1319,13 +1336,13 @@ struct LinearChoice {
     mk_status (*launch)(const mk_linear_args*, LinearParams&, const LinearExtra<ADAPT>&, const LinearPlan&, cudaStream_t);
 };
 template <bool GATED, bool F32, bool ADAPT>
-static mk_status linear_choose(const LinearParams& p, int extra, int device, LinearChoice<ADAPT>& best) {
+static mk_status linear_choose(const LinearParams& p, const LinearNamed& named, int device, LinearChoice<ADAPT>& best) {
     LinearPlan pl{};
     best = LinearChoice<ADAPT>{};
     mk_status st = MK_OK;
     auto offer = [&](auto kernel, bool wanted) {
         using K = decltype(kernel);
-        if (st != MK_OK || !wanted || (st = K::plan(p, extra, device, pl)) != MK_OK) return;
+        if (st != MK_OK || !wanted || (st = K::plan(p, named.blocks(K::kTokens, p.rows), device, pl)) != MK_OK) return;
         if (!best.launch || pl.cost < best.plan.cost) best = {pl, K::kTokens, K::kFeatures, K::kUnit, &K::launch};
     };
     offer(LinearOne<16, GATED, F32, ADAPT>{}, p.rows <= 64);
@@ -1374,7 +1391,7 @@ static mk_status linear_check(const mk_linear_args* a) {
 
 // The parameters of a checked call, and its plan on the current device
 template <bool ADAPT>
-static mk_status linear_plan(const mk_linear_args* a, int extra, LinearParams& p, LinearChoice<ADAPT>& choice) {
+static mk_status linear_plan(const mk_linear_args* a, const LinearNamed& named, LinearParams& p, LinearChoice<ADAPT>& choice) {
     p.rows = a->rows; p.n = a->n; p.k = a->k; p.act = a->activation;
     p.bias = static_cast<const __nv_bfloat16*>(a->bias);
     p.residual = a->residual;
@@ -1388,8 +1405,8 @@ static mk_status linear_plan(const mk_linear_args* a, int extra, LinearParams& p
     const mk_status st = op_device(&device, &sms);
     if (st != MK_OK) return st;
     if (a->activation == MK_ACT_SWIGLU)
-        return p.out_f32 ? linear_choose<true, true, ADAPT>(p, extra, device, choice) : linear_choose<true, false, ADAPT>(p, extra, device, choice);
-    return p.out_f32 ? linear_choose<false, true, ADAPT>(p, extra, device, choice) : linear_choose<false, false, ADAPT>(p, extra, device, choice);
+        return p.out_f32 ? linear_choose<true, true, ADAPT>(p, named, device, choice) : linear_choose<true, false, ADAPT>(p, named, device, choice);
+    return p.out_f32 ? linear_choose<false, true, ADAPT>(p, named, device, choice) : linear_choose<false, false, ADAPT>(p, named, device, choice);
 }
 
 }  // namespace mk
