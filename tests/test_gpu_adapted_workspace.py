@@ -1,5 +1,6 @@
 """mk_linear_adapted_workspace before any buffer exists: the size of a call is that of its sizes, activation and types."""
 import ctypes
+import gc
 
 import pytest
 import torch
@@ -10,6 +11,13 @@ if not torch.cuda.is_available():
     pytest.skip("needs a CUDA GPU", allow_module_level=True)
 
 import persistent_megakernel_decode_sm_gb300 as mk  # noqa: E402
+
+
+@pytest.fixture(scope="module", autouse=True)
+def nothing_left_behind():
+    """A later module's tests look at the memory."""
+    yield
+    gc.collect()
 
 
 def size(linear, adapters):
