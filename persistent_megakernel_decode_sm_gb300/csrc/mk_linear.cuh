@@ -31,7 +31,7 @@ struct LinearParams {
 // up to 64 of them.  A block is 64 columns of up (four, two or one adapter's pieces, rows of 32, 64 or 128 bytes) in one
 // stage beside the first part of the terms' 64 columns, and the other parts in the stage after it: up is copied once for all parts,
 // and what a block costs by itself (waits, commits) is shared by 8 or 12 products.  A CTA pair, whose tiles name few adapters, takes
-// blocks of 32 columns in one stage each (4096 tokens through 2 x 8192 x 2048 168 us, with blocks over two stages 172).
+// blocks of 32 columns in one stage each (4096 tokens through 2 x 8192 x 2048 165 us, with blocks over two stages 2.5% more).
 template <bool ADAPT>
 struct LinearExtra {
     static constexpr int32_t width = 0;
@@ -298,9 +298,9 @@ __device__ __noinline__ uint32_t linear_suspects(const LinearParams& p, const Li
 // x and w are read straight into m16n8k16 products (a thread's 16 bytes of a row are the elements 2 i, 2 i + 1 of two products),
 // summed 512 elements at a time; 16 features of 8 tokens take 3 loads a lane per 32 of the contraction.
 // Where no sum is NaN this is one comparison an output (0.1 to 0.3 us a call, 1.3 of 4096 tokens through 2 x 8192 x 2048).  Where some
-// are in their own right, finding that out reads the up rows of the tile's adapters: 512 of those 4096 tokens of NaN 370 us for 168,
-// all of them 910, 64 tokens of 64 adapters of rank 64 (4096 x 6144) 200 for 46 (with all of these taken again 2.9 ms, 9.2 ms and
-// 340 us).  Taking a tile again is bound by the latencies of x's and w's loads: one adapter of NaN among those 64 510 us, among those of
+// are in their own right, finding that out reads the up rows of the tile's adapters: 512 of those 4096 tokens of NaN 370 us for 165,
+// all of them 920, 64 tokens of 64 adapters of rank 64 (4096 x 6144) 208 for 46 (with all of these taken again 2.9 ms, 9.2 ms and
+// 340 us).  Taking a tile again is bound by the latencies of x's and w's loads: one adapter of NaN among those 64 515 us, among those of
 // the 4096 tokens, 60 of which name it, 3.1 ms.
 template <bool GATED, bool F32>
 __device__ __noinline__ void linear_alone(const LinearParams& p, const LinearExtra<true>& e, const volatile int32_t* list, int adapters,
@@ -1221,9 +1221,9 @@ struct LinearPlan {
 // block of w and x has 4).  Who names which is not known here: each of up to 512 tokens is taken to have its own adapter, of
 // more rows / 512 neighbours share one.  The low-rank kernel in front is seen more of by pairs, which need an SM's whole shared memory, and
 // by split tiles, whose parts all end behind it: kAdaptPair and kAdaptSplit cycles.  us as planned so, and without the two and with four adapters
-// a tile whatever its width: tokens with an adapter each of 256 (4096 x 4096), 128 of rank 64 45.7 and 51.9, 256 73 and 81, 512 of rank 16
-// 57 and 80, of rank 64 135 and 155, fp32 158 and 197; 2048 of rank 64, fp32 (2048 x 2048) 308 and 399; 100 tokens of 8 adapters in
-// runs, 1024 x 8192, SwiGLU 14.6 and 18.3.  Runs of 128 of 512 tokens, 128 adapters loaded, take 31 either way, with tiles of 128 28.
+// a tile whatever its width: tokens with an adapter each of 256 (4096 x 4096), 128 of rank 64 45.5 and 51.0, 256 73 and 80, 512 of rank 16
+// 56 and 81, of rank 64 132 and 153, fp32 153 and 193; 2048 of rank 64, fp32 (2048 x 2048) 306 and 382; 100 tokens of 8 adapters in
+// runs, 1024 x 8192, SwiGLU 14.7 and 18.1.  Runs of 128 of 512 tokens, 128 adapters loaded, take 31 either way, with tiles of 128 28.
 constexpr int kAdaptPair = 6000, kAdaptSplit = 2000;
 struct LinearNamed {
     int adapters = 0, width = 0;   // loaded; columns of each
