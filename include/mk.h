@@ -492,7 +492,7 @@ mk_status mk_attend(const mk_attend_args* a, void* workspace, size_t workspace_b
  * fp32 output).  The same call gives the same bits; a token's may differ in the last places between calls that hold it in another
  * row, or beside other tokens (the order of the fp32 sums).  Infinities and NaN of an adapter reach only the tokens that name it:
  * outputs of other tokens that would come to NaN beside it are taken again, 3 to 20 times as long as the call where many are.
- * Outputs that are NaN in their own right (x, w, bias, residual or the token's own adapter) are left as they are, up to 6 times.
+ * Outputs that are NaN in their own right (x, w, bias, residual or the token's own adapter) are left as they are, up to 8 times.
  * Adapters that no token names are not read.
  * workspace: mk_linear_adapted_workspace bytes of device memory, 256-byte aligned, which depend on the current device; calls that
  * may overlap need workspaces of their own.  Errors: MK_ERR_ARG, MK_ERR_CAPACITY (the workspace is too small), MK_ERR_CUDA;
